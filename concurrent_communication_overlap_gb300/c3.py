@@ -25,6 +25,10 @@ C3_SMK_AUTO, C3_SMK_VEC, C3_SMK_BULK = 0, 1, 2
 C3_L2_NORMAL, C3_L2_EVICT_FIRST = 0, 1
 C3_CE_PER_SEGMENT, C3_CE_STRIDED, C3_CE_GRAPH, C3_CE_GRAPH_PARALLEL, C3_CE_HOST_STAGED = 0, 1, 2, 3, 4
 C3_FAULT_NONE, C3_FAULT_GEMM_LAUNCH, C3_FAULT_SM_COLL_LAUNCH, C3_FAULT_MEMCPY, C3_FAULT_DEVICE_INIT = 0, 1, 2, 3, 4
+C3_F32, C3_BF16 = 0, 1
+C3_SCORE_SOFTMAX, C3_SCORE_SIGMOID = 0, 1
+C3_FP4_MX, C3_FP4_NV = 0, 1
+C3_TILE_ROWS = 128
 CLASS_NAMES = {0: "G-long", 1: "GC-equal", 2: "C-long"}
 
 _i64, _int, _vp, _sz = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
@@ -81,6 +85,17 @@ class C3RpTable(ctypes.Structure):
                 ("gemm_memory", ctypes.c_double * C3_RP_MAX), ("coll", ctypes.c_double * C3_RP_MAX)]
 
 
+class C3Router(ctypes.Structure):
+    _fields_ = [("bias", _vp), ("experts", _int), ("topk", _int), ("groups", _int), ("topk_groups", _int),
+                ("group_best", _int), ("score", _int), ("renorm", _int), ("logits_type", _int),
+                ("scale", ctypes.c_float)]
+
+
+class C3Fp4(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp), ("tensor_scale", _vp), ("rows", _i64), ("cols", _i64),
+                ("count", _int), ("format", _int)]
+
+
 class C3Error(RuntimeError):
     def __init__(self, status, where, detail):
         super().__init__(f"{where}: {status} ({c3_strerror(status)}): {detail}")
@@ -118,10 +133,30 @@ def _load():
         "c3_gemm_plan": [_i64, _i64, _i64, _int, ctypes.POINTER(_int), ctypes.POINTER(_int), ctypes.POINTER(_int)],
         "c3_cta_windows": [_int, ctypes.POINTER(C3CtaWindow), _int, ctypes.POINTER(_int)],
     }
+    router, fp4 = ctypes.POINTER(C3Router), ctypes.POINTER(C3Fp4)
+    sig |= {
+        "c3_route": [router, _vp, _i64, _i64, _vp, _vp, _vp],
+        "c3_route_backward": [router, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp],
+        "c3_moe_rows": [_i64, _int, _int],
+        "c3_moe_order_bytes": [_i64, _int, _int],
+        "c3_moe_order": [_vp, _i64, _int, _int, _vp, _vp, _i64, _vp, _vp, _vp, _sz, _vp],
+        "c3_fp4_code_bytes": [_i64, _i64],
+        "c3_fp4_scale_bytes": [_i64, _i64, _int],
+        "c3_fp4_quantize": [_vp, _int, _i64, _i64, _i64, _int, _vp, fp4, _vp],
+        "c3_fp4_dequantize": [fp4, _vp, _int, _i64, _vp],
+        "c3_fp4_gemm": [fp4, fp4, _vp, _int, _int, _vp],
+        "c3_fp4_gemm_experts": [fp4, fp4, _vp, _vp, _vp, _int, _int, _vp],
+        "c3_moe_combine": [_vp, _int, _i64, _i64, _vp, _vp, _i64, _int, _vp, _int, _vp],
+        "c3_moe_combine_backward": [_vp, _int, _vp, _int, _i64, _i64, _vp, _vp, _i64, _int, _vp, _vp, _vp],
+    }
     for name, args in sig.items():
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = _int
+    lib.c3_moe_rows.restype = _i64
+    lib.c3_moe_order_bytes.restype = _sz
+    lib.c3_fp4_code_bytes.restype = _sz
+    lib.c3_fp4_scale_bytes.restype = _sz
     lib.c3_kernel_launches.argtypes = []
     lib.c3_kernel_launches.restype = ctypes.c_uint64
     lib.c3_strerror.restype = ctypes.c_char_p
@@ -133,7 +168,10 @@ _lib = _load()
 EXPORTED = ("c3_get_device_info", "c3_strerror", "c3_last_error", "c3_status_check", "c3_shutdown",
             "c3_gemm", "c3_allgather", "c3_alltoall", "c3_allreduce", "c3_run", "c3_time", "c3_l2_flush", "c3_kernel_launches",
             "c3_gemm_noalloc", "c3_gemm_plan", "c3_selftest_wait", "c3_inject_fault", "c3_sp_predict",
-            "c3_rp_predict", "c3_rp_predict_elastic", "c3_cta_windows")
+            "c3_rp_predict", "c3_rp_predict_elastic", "c3_cta_windows",
+            "c3_route", "c3_route_backward", "c3_moe_rows", "c3_moe_order_bytes", "c3_moe_order",
+            "c3_fp4_code_bytes", "c3_fp4_scale_bytes", "c3_fp4_quantize", "c3_fp4_dequantize", "c3_fp4_gemm",
+            "c3_fp4_gemm_experts", "c3_moe_combine", "c3_moe_combine_backward")
 
 
 def lib():
@@ -319,3 +357,104 @@ def c3_time(problem: Problem, mode, sm_split=0, priority=0, warmup=3, reps=9, ch
     if check:
         _check(rc, "c3_time")
     return [arr[i].as_dict() for i in range(reps)]
+
+
+class Router:
+    """Owns a c3_router record and keeps the bias tensor alive."""
+
+    def __init__(self, experts, topk, score=C3_SCORE_SOFTMAX, groups=1, topk_groups=None, group_best=1,
+                 renorm=False, scale=1.0, bias=None, logits_type=C3_F32):
+        self._bias = bias
+        self.rec = C3Router(_ptr(bias), int(experts), int(topk), int(groups),
+                            int(groups if topk_groups is None else topk_groups), int(group_best), int(score),
+                            int(bool(renorm)), int(logits_type), float(scale))
+        self.ref = ctypes.byref(self.rec)
+
+
+class Fp4:
+    """Owns a c3_fp4 record and keeps its tensors alive."""
+
+    def __init__(self, rows, cols, format, codes, scales, tensor_scale=None, count=1):
+        self._keep = (codes, scales, tensor_scale)
+        self.rows, self.cols, self.count, self.format = int(rows), int(cols), int(count), int(format)
+        self.rec = C3Fp4(_ptr(codes), _ptr(scales), _ptr(tensor_scale), self.rows, self.cols, self.count,
+                         self.format)
+        self.ref = ctypes.byref(self.rec)
+
+
+def _done(rc, where, check):
+    return _check(rc, where) if check else rc
+
+
+def c3_route(router, logits, ld, tokens, idx, weights, stream=None, check=True):
+    rc = _lib.c3_route(router.ref, _ptr(logits), ld, tokens, _ptr(idx), _ptr(weights), _stream(stream))
+    return _done(rc, "c3_route", check)
+
+
+def c3_route_backward(router, logits, ld, tokens, idx, dweights, dlogits, dld, stream=None, check=True):
+    rc = _lib.c3_route_backward(router.ref, _ptr(logits), ld, tokens, _ptr(idx), _ptr(dweights), _ptr(dlogits), dld,
+                                _stream(stream))
+    return _done(rc, "c3_route_backward", check)
+
+
+def c3_moe_rows(tokens, topk, experts):
+    """Rows that the sorted choices can need at most."""
+    rows = int(_lib.c3_moe_rows(int(tokens), int(topk), int(experts)))
+    if rows < 0:
+        _check(rows, "c3_moe_rows")
+    return rows
+
+
+def c3_moe_order_bytes(tokens, topk, experts):
+    return int(_lib.c3_moe_order_bytes(int(tokens), int(topk), int(experts)))
+
+
+def c3_moe_order(idx, tokens, topk, experts, slot, row_of, rows, offsets, counts, work, work_bytes=None, stream=None,
+                 check=True):
+    """work: a tensor (its size is taken from it) or an address with work_bytes."""
+    if work_bytes is None:
+        work_bytes = 0 if work is None else work.numel() * work.element_size()
+    rc = _lib.c3_moe_order(_ptr(idx), tokens, topk, experts, _ptr(slot), _ptr(row_of), rows, _ptr(offsets),
+                           _ptr(counts), _ptr(work), work_bytes, _stream(stream))
+    return _done(rc, "c3_moe_order", check)
+
+
+def c3_fp4_code_bytes(rows, cols):
+    return int(_lib.c3_fp4_code_bytes(int(rows), int(cols)))
+
+
+def c3_fp4_scale_bytes(rows, cols, format):
+    return int(_lib.c3_fp4_scale_bytes(int(rows), int(cols), int(format)))
+
+
+def c3_fp4_quantize(x, x_type, x_rows, x_cols, q, ld=None, transpose=False, row_of=None, stream=None, check=True):
+    rc = _lib.c3_fp4_quantize(_ptr(x), x_type, x_rows, x_cols, x_cols if ld is None else ld, int(transpose),
+                              _ptr(row_of), q.ref, _stream(stream))
+    return _done(rc, "c3_fp4_quantize", check)
+
+
+def c3_fp4_dequantize(q, x, x_type, ld, stream=None, check=True):
+    return _done(_lib.c3_fp4_dequantize(q.ref, _ptr(x), x_type, ld, _stream(stream)), "c3_fp4_dequantize", check)
+
+
+def c3_fp4_gemm(a, b, C, c_type, sm_budget=0, stream=None, check=True):
+    return _done(_lib.c3_fp4_gemm(a.ref, b.ref, _ptr(C), c_type, sm_budget, _stream(stream)), "c3_fp4_gemm", check)
+
+
+def c3_fp4_gemm_experts(x, w, offsets, counts, C, c_type, sm_budget=0, stream=None, check=True):
+    rc = _lib.c3_fp4_gemm_experts(x.ref, w.ref, _ptr(offsets), _ptr(counts), _ptr(C), c_type, sm_budget,
+                                  _stream(stream))
+    return _done(rc, "c3_fp4_gemm_experts", check)
+
+
+def c3_moe_combine(y, y_type, rows, cols, slot, weights, tokens, topk, out, out_type, stream=None, check=True):
+    rc = _lib.c3_moe_combine(_ptr(y), y_type, rows, cols, _ptr(slot), _ptr(weights), tokens, topk, _ptr(out),
+                             out_type, _stream(stream))
+    return _done(rc, "c3_moe_combine", check)
+
+
+def c3_moe_combine_backward(dout, dout_type, y, y_type, rows, cols, slot, weights, tokens, topk, dy, dweights,
+                            stream=None, check=True):
+    rc = _lib.c3_moe_combine_backward(_ptr(dout), dout_type, _ptr(y), y_type, rows, cols, _ptr(slot), _ptr(weights),
+                                      tokens, topk, _ptr(dy), _ptr(dweights), _stream(stream))
+    return _done(rc, "c3_moe_combine_backward", check)

@@ -26,6 +26,10 @@ enum WaitSite : int {
     kSiteBulkLoad = 5,
     kSiteBulkDrain = 6,
     kSiteSelfTest = 7,
+    kSiteFp4Producer = 8,
+    kSiteFp4Mma = 9,
+    kSiteFp4Epilogue = 10,
+    kSiteFp4Drain = 11,
 };
 
 __device__ __forceinline__ unsigned long long globaltimer() {

@@ -192,6 +192,54 @@ enum { kFaultGemmLaunch = 1, kFaultSmCollLaunch = 2, kFaultMemcpy = 3, kFaultDev
 bool take_fault(int site);
 void ce_release_graphs(int device);
 
+// ---------------------------------------------------------------- routing and 4-bit operators
+// The arguments have been checked (ops_api.cpp); each call is one or two
+// kernels on `s` and returns 0 or a negative c3_status.
+
+// A router (c3_router).  by_score: keys are the softmax scores themselves and
+// not the logits, which order alike without a bias or sums over groups.
+struct RouteArgs {
+    const float* bias;
+    int experts, topk, groups, topk_groups, group_best, score, renorm, by_score;
+    float scale;
+};
+int route_launch(const void* logits, int bf16, int64_t ld, int64_t tokens, const RouteArgs& a, int32_t* idx,
+                 float* weights, cudaStream_t s);
+int route_backward_launch(const void* logits, int bf16, int64_t ld, int64_t tokens, const RouteArgs& a,
+                          const int32_t* idx, const float* dweights, void* dlogits, int64_t dld, cudaStream_t s);
+
+constexpr int kTileRows = 128;  // rows of a scale tile; an expert's rows start at a multiple of it
+int64_t order_rows(int64_t tokens, int topk, int experts);
+size_t order_bytes(int64_t tokens, int topk, int experts);
+int order_launch(const int32_t* idx, int64_t tokens, int topk, int experts, int32_t* slot, int32_t* row_of,
+                 int64_t rows, int32_t* offsets, int32_t* counts, void* work, cudaStream_t s);
+int combine_launch(const void* y, int y_bf16, int64_t rows, int64_t cols, const int32_t* slot, const float* weights,
+                   int64_t tokens, int topk, void* out, int out_bf16, cudaStream_t s);
+int combine_backward_launch(const void* dout, int dout_bf16, const void* y, int y_bf16, int64_t rows, int64_t cols,
+                            const int32_t* slot, const float* weights, int64_t tokens, int topk, void* dy,
+                            float* dweights, cudaStream_t s);
+
+// A 4-bit matrix (c3_fp4): `count` matrices of rows x cols, one after the other.
+struct Fp4 {
+    uint8_t* codes;            // [count][rows][pitch]
+    uint8_t* scales;           // [count][row tiles][k tiles][512]
+    const float* tensor_scale; // [count], or NULL
+    int64_t rows, cols;
+    int count;
+    int nv;                    // 0: blocks of 32 with power-of-two scales; 1: blocks of 16 with e4m3 scales
+    int64_t pitch() const { return (cols + 31) / 32 * 16; }
+    int64_t row_tiles() const { return (rows + kTileRows - 1) / kTileRows; }
+    int64_t k_tiles() const { return nv ? (cols + 63) / 64 : (cols + 127) / 128; }
+    int64_t scale_bytes() const { return row_tiles() * k_tiles() * 512; }
+};
+int fp4_quantize_launch(const void* x, int bf16, int64_t x_rows, int64_t ld, int transpose, const int32_t* row_of,
+                        const Fp4& q, cudaStream_t s);
+int fp4_dequantize_launch(const Fp4& q, void* x, int bf16, int64_t ld, cudaStream_t s);
+// offsets/counts: the experts' rows of a (device), or NULL for one plain product.
+int fp4_gemm_launch(const Fp4& a, const Fp4& b, const int32_t* offsets, const int32_t* counts, void* C, int bf16,
+                    int sm_budget, cudaStream_t s, DevStatus* st);
+int fp4_gemm_init_device();
+
 int status_reset_launch(DevStatus* st, cudaStream_t s);
 int selftest_wait_launch(DevStatus* st, unsigned long long limit_ns, int arrive, cudaStream_t s);
 int zero_fill_launch(void* buf, size_t bytes, cudaStream_t s);

@@ -93,6 +93,8 @@ static int init_device(DeviceState& ds, int dev) {
     if (rc) return rc;
     rc = copy_init_device(ds.smem_per_block);
     if (rc) return rc;
+    rc = fp4_gemm_init_device();
+    if (rc) return rc;
     ds.ready = true;
     return 0;
 }

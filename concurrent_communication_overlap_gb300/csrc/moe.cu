@@ -1,0 +1,372 @@
+// moe.cu -- what stands between a router and the experts' products: the rows
+// of the tokens sorted by expert, and the experts' outputs put together again,
+// forward and backward.
+#include "c3_device.cuh"
+#include "c3_internal.h"
+
+#include <cuda_bf16.h>
+
+namespace c3 {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kOrderThreads = 256;
+constexpr int kOrderWarps = kOrderThreads / 32;
+constexpr int kOrderChunk = 4096;       // choices of one CTA: each warp takes a consecutive eighth
+constexpr int kMaxExperts = 1024;
+
+// ---------------------------------------------------------------- order
+//
+// A stable counting sort of the choices by expert.  A choice's row is
+//   offsets[e] + (choices of e before it),
+// the sum of three counts: of the CTAs before, of the warps before in this CTA,
+// and of the choices before in this warp.  The first kernel counts per CTA, the
+// second adds up and places.  No atomics on global memory: the rows do not
+// depend on the order in which CTAs run.
+
+__device__ __forceinline__ int choice_expert(const int32_t* idx, int64_t i, int64_t n, int experts) {
+    if (i >= n) return -1;
+    const int e = idx[i];
+    return (e >= 0 && e < experts) ? e : -1;
+}
+
+// Counts of the CTA's choices: hist[warp][e] in shared memory, one counter set a warp.
+__device__ __forceinline__ void count_chunk(const int32_t* __restrict__ idx, int64_t n, int experts, int64_t first,
+                                            int* hist) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < kOrderWarps * experts; i += kOrderThreads) hist[i] = 0;
+    __syncthreads();
+    const int64_t at = first + (int64_t)warp * (kOrderChunk / kOrderWarps);
+    for (int j = 0; j < kOrderChunk / kOrderWarps; j += 32) {
+        if (at + j >= n) break;
+        const int e = choice_expert(idx, at + j + lane, n, experts);
+        const unsigned same = __match_any_sync(kAll, e);
+        if (e >= 0 && (same & ((1u << lane) - 1)) == 0) hist[warp * experts + e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(kOrderThreads)
+    order_count_kernel(const int32_t* __restrict__ idx, int64_t n, int experts, int* __restrict__ per_cta) {
+    extern __shared__ int hist[];
+    count_chunk(idx, n, experts, (int64_t)blockIdx.x * kOrderChunk, hist);
+    for (int e = threadIdx.x; e < experts; e += kOrderThreads) {
+        int c = 0;
+        for (int w = 0; w < kOrderWarps; ++w) c += hist[w * experts + e];
+        per_cta[(size_t)blockIdx.x * experts + e] = c;
+    }
+}
+
+__global__ void __launch_bounds__(kOrderThreads)
+    order_place_kernel(const int32_t* __restrict__ idx, int64_t n, int topk, int experts,
+                       const int* __restrict__ per_cta, int32_t* __restrict__ slot, int32_t* __restrict__ row_of,
+                       int64_t rows, int32_t* __restrict__ offsets, int32_t* __restrict__ counts) {
+    extern __shared__ int hist[];            // [warps][experts], then total[experts], start[experts + 1]
+    int* total = hist + kOrderWarps * experts;
+    int* start = total + experts;
+    __shared__ int warp_sums[kOrderWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t first = (int64_t)blockIdx.x * kOrderChunk;
+    count_chunk(idx, n, experts, first, hist);
+    // The choices of each expert in the CTAs before this one, and in all.
+    for (int e = threadIdx.x; e < experts; e += kOrderThreads) {
+        int before = 0, all = 0;
+        if (gridDim.x == 1) {
+            for (int w = 0; w < kOrderWarps; ++w) all += hist[w * experts + e];
+        } else {
+            for (unsigned b = 0; b < gridDim.x; ++b) {
+                const int c = __ldg(per_cta + (size_t)b * experts + e);
+                if (b < blockIdx.x) before += c;
+                all += c;
+            }
+        }
+        total[e] = all;
+        // hist becomes the count before each warp's choices
+        int run = before;
+        for (int w = 0; w < kOrderWarps; ++w) {
+            const int c = hist[w * experts + e];
+            hist[w * experts + e] = run;
+            run += c;
+        }
+    }
+    __syncthreads();
+    // Each expert's first row: an exclusive sum of the counts rounded up to whole tiles.
+    constexpr int kPer = kMaxExperts / kOrderThreads;
+    int mine[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x * kPer + i;
+        mine[i] = e < experts ? (total[e] + kTileRows - 1) / kTileRows * kTileRows : 0;
+        sum += mine[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    int base = incl - sum;
+    for (int w = 0; w < warp; ++w) base += warp_sums[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x * kPer + i;
+        if (e < experts) start[e] = base;
+        base += mine[i];
+        if (e == experts - 1) start[experts] = base;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= experts; e += kOrderThreads) {
+            offsets[e] = start[e];
+            if (e < experts) counts[e] = total[e];
+        }
+    // The rows of this CTA's choices.
+    const int64_t at = first + (int64_t)warp * (kOrderChunk / kOrderWarps);
+    for (int j = 0; j < kOrderChunk / kOrderWarps; j += 32) {
+        if (at + j >= n) break;
+        const int64_t i = at + j + lane;
+        const int e = choice_expert(idx, i, n, experts);
+        const unsigned same = __match_any_sync(kAll, e);
+        int row = -1;
+        if (e >= 0) row = start[e] + hist[warp * experts + e] + __popc(same & ((1u << lane) - 1));
+        __syncwarp();
+        if (e >= 0 && (same & ((1u << lane) - 1)) == 0) hist[warp * experts + e] += __popc(same);
+        __syncwarp();
+        if (i < n) {
+            slot[i] = row;
+            if (row >= 0) row_of[row] = (int32_t)(i / topk);
+        }
+    }
+    // Rows that no choice takes: each expert's last tile, and what is left of the buffer.
+    for (int e = blockIdx.x; e < experts; e += gridDim.x) {
+        const int from = start[e] + total[e], to = start[e + 1];
+        for (int r = from + (int)threadIdx.x; r < to; r += kOrderThreads) row_of[r] = -1;
+    }
+    for (int64_t r = start[experts] + (int64_t)blockIdx.x * kOrderThreads + threadIdx.x; r < rows;
+         r += (int64_t)gridDim.x * kOrderThreads)
+        row_of[r] = -1;
+}
+
+int64_t order_rows(int64_t tokens, int topk, int experts) {
+    const int64_t n = tokens * topk;
+    const int64_t busy = n < experts ? n : experts;
+    return (n + (kTileRows - 1) * busy) / kTileRows * kTileRows;
+}
+
+static int64_t order_ctas(int64_t n) { return (n + kOrderChunk - 1) / kOrderChunk; }
+
+size_t order_bytes(int64_t tokens, int topk, int experts) {
+    return (size_t)order_ctas(tokens * topk) * (size_t)experts * sizeof(int);
+}
+
+int order_launch(const int32_t* idx, int64_t tokens, int topk, int experts, int32_t* slot, int32_t* row_of,
+                 int64_t rows, int32_t* offsets, int32_t* counts, void* work, cudaStream_t s) {
+    const int64_t n = tokens * topk;
+    const int ctas = n ? (int)order_ctas(n) : 1;
+    const size_t smem = sizeof(int) * (size_t)experts * (kOrderWarps + 2) + sizeof(int);
+    if (ctas > 1) {
+        order_count_kernel<<<ctas, kOrderThreads, sizeof(int) * (size_t)experts * kOrderWarps, s>>>(
+            idx, n, experts, static_cast<int*>(work));
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return set_cuda_error(e, "order count kernel launch");
+        count_launch();
+    }
+    order_place_kernel<<<ctas, kOrderThreads, smem, s>>>(idx, n, topk, experts, static_cast<const int*>(work), slot,
+                                                         row_of, rows, offsets, counts);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return set_cuda_error(e, "order kernel launch");
+    count_launch();
+    return 0;
+}
+
+// ---------------------------------------------------------------- combine
+
+// Eight consecutive values as fp32, whatever the type.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+constexpr int kCombineThreads = 256;
+
+// out[t] = sum_j w[t][j] y[slot[t][j]], in fp32, j ascending.  A CTA takes one
+// token and a span of columns; VEC: rows are 16-byte aligned, 8 columns a thread.
+template <typename Ty, typename To, bool VEC>
+__global__ void __launch_bounds__(kCombineThreads)
+    combine_kernel(const Ty* __restrict__ y, int64_t rows, int64_t cols, const int32_t* __restrict__ slot,
+                   const float* __restrict__ weights, int64_t tokens, int topk, To* __restrict__ out) {
+    constexpr int kW = VEC ? 8 : 1;
+    const int64_t spans = (cols + kCombineThreads * kW - 1) / (kCombineThreads * kW);
+    for (int64_t job = blockIdx.x; job < tokens * spans; job += gridDim.x) {
+        const int64_t t = job / spans;
+        const int64_t c = ((job - t * spans) * kCombineThreads + threadIdx.x) * kW;
+        if (c >= cols) continue;
+        float acc[kW] = {};
+        for (int j = 0; j < topk; ++j) {
+            const int r = __ldg(slot + t * topk + j);
+            if (r < 0 || r >= rows) continue;
+            const float w = weights ? __ldg(weights + t * topk + j) : 1.0f;
+            float v[kW];
+            if constexpr (VEC)
+                load8(y + (int64_t)r * cols + c, v);
+            else
+                v[0] = load1(y + (int64_t)r * cols + c);
+#pragma unroll
+            for (int i = 0; i < kW; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+        }
+        if constexpr (VEC)
+            store8(out + t * cols + c, acc);
+        else
+            store1(out + t * cols + c, acc[0]);
+    }
+}
+
+// dy[slot] = w dout[t] and dw = <dout[t], y[slot]>: one CTA a choice.
+template <typename Td, typename Ty, bool VEC>
+__global__ void __launch_bounds__(kCombineThreads)
+    combine_backward_kernel(const Td* __restrict__ dout, const Ty* __restrict__ y, int64_t rows, int64_t cols,
+                            const int32_t* __restrict__ slot, const float* __restrict__ weights, int64_t tokens,
+                            int topk, Ty* __restrict__ dy, float* __restrict__ dweights) {
+    constexpr int kW = VEC ? 8 : 1;
+    __shared__ float part[kCombineThreads / 32];
+    for (int64_t job = blockIdx.x; job < tokens * topk; job += gridDim.x) {
+        const int64_t t = job / topk;
+        const int r = slot[job];
+        float dot = 0.0f;
+        if (r >= 0 && r < rows) {
+            const float w = weights ? weights[job] : 1.0f;
+            for (int64_t c = (int64_t)threadIdx.x * kW; c < cols; c += kCombineThreads * kW) {
+                float d[kW], v[kW];
+                if constexpr (VEC) {
+                    load8(dout + t * cols + c, d);
+                    if (dweights) load8(y + (int64_t)r * cols + c, v);
+                } else {
+                    d[0] = load1(dout + t * cols + c);
+                    if (dweights) v[0] = load1(y + (int64_t)r * cols + c);
+                }
+#pragma unroll
+                for (int i = 0; i < kW; ++i) {
+                    if (dweights) dot = fmaf(d[i], v[i], dot);
+                    d[i] *= w;
+                }
+                if constexpr (VEC)
+                    store8(dy + (int64_t)r * cols + c, d);
+                else
+                    store1(dy + (int64_t)r * cols + c, d[0]);
+            }
+        }
+        if (dweights) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
+            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                float sum = 0.0f;
+                for (int i = 0; i < kCombineThreads / 32; ++i) sum += part[i];
+                dweights[job] = sum;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+static int combine_grid(int64_t jobs) {
+    DeviceState* ds = device_state();
+    if (!ds) return 0;
+    const int64_t most = (int64_t)ds->sm_count * 64;
+    return (int)(jobs < most ? jobs : most);
+}
+
+static bool rows_vec(const void* p, int64_t cols, int bf16) {
+    return ((uintptr_t)p & 15u) == 0 && cols % 8 == 0 && (cols * (bf16 ? 2 : 4)) % 16 == 0;
+}
+
+template <typename Ty, typename To>
+static int combine_go(const void* y, int64_t rows, int64_t cols, const int32_t* slot, const float* weights,
+                      int64_t tokens, int topk, void* out, bool vec, cudaStream_t s) {
+    const int64_t per = kCombineThreads * (vec ? 8 : 1);
+    const int grid = combine_grid(tokens * ((cols + per - 1) / per));
+    if (grid == 0) return -3;
+    const Ty* yy = static_cast<const Ty*>(y);
+    To* oo = static_cast<To*>(out);
+    if (vec)
+        combine_kernel<Ty, To, true><<<grid, kCombineThreads, 0, s>>>(yy, rows, cols, slot, weights, tokens, topk, oo);
+    else
+        combine_kernel<Ty, To, false><<<grid, kCombineThreads, 0, s>>>(yy, rows, cols, slot, weights, tokens, topk, oo);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return set_cuda_error(e, "combine kernel launch");
+    count_launch();
+    return 0;
+}
+
+int combine_launch(const void* y, int y_bf16, int64_t rows, int64_t cols, const int32_t* slot, const float* weights,
+                   int64_t tokens, int topk, void* out, int out_bf16, cudaStream_t s) {
+    const bool vec = rows_vec(y, cols, y_bf16) && rows_vec(out, cols, out_bf16);
+    if (y_bf16)
+        return out_bf16 ? combine_go<__nv_bfloat16, __nv_bfloat16>(y, rows, cols, slot, weights, tokens, topk, out, vec, s)
+                        : combine_go<__nv_bfloat16, float>(y, rows, cols, slot, weights, tokens, topk, out, vec, s);
+    return out_bf16 ? combine_go<float, __nv_bfloat16>(y, rows, cols, slot, weights, tokens, topk, out, vec, s)
+                    : combine_go<float, float>(y, rows, cols, slot, weights, tokens, topk, out, vec, s);
+}
+
+template <typename Td, typename Ty>
+static int combine_back_go(const void* dout, const void* y, int64_t rows, int64_t cols, const int32_t* slot,
+                           const float* weights, int64_t tokens, int topk, void* dy, float* dweights, bool vec,
+                           cudaStream_t s) {
+    const int grid = combine_grid(tokens * topk);
+    if (grid == 0) return -3;
+    const Td* dd = static_cast<const Td*>(dout);
+    const Ty* yy = static_cast<const Ty*>(y);
+    Ty* oo = static_cast<Ty*>(dy);
+    if (vec)
+        combine_backward_kernel<Td, Ty, true>
+            <<<grid, kCombineThreads, 0, s>>>(dd, yy, rows, cols, slot, weights, tokens, topk, oo, dweights);
+    else
+        combine_backward_kernel<Td, Ty, false>
+            <<<grid, kCombineThreads, 0, s>>>(dd, yy, rows, cols, slot, weights, tokens, topk, oo, dweights);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return set_cuda_error(e, "combine backward kernel launch");
+    count_launch();
+    return 0;
+}
+
+int combine_backward_launch(const void* dout, int dout_bf16, const void* y, int y_bf16, int64_t rows, int64_t cols,
+                            const int32_t* slot, const float* weights, int64_t tokens, int topk, void* dy,
+                            float* dweights, cudaStream_t s) {
+    const bool vec = rows_vec(dout, cols, dout_bf16) && rows_vec(dy, cols, y_bf16) && (!dweights || rows_vec(y, cols, y_bf16));
+    if (dout_bf16)
+        return y_bf16 ? combine_back_go<__nv_bfloat16, __nv_bfloat16>(dout, y, rows, cols, slot, weights, tokens, topk, dy, dweights, vec, s)
+                      : combine_back_go<__nv_bfloat16, float>(dout, y, rows, cols, slot, weights, tokens, topk, dy, dweights, vec, s);
+    return y_bf16 ? combine_back_go<float, __nv_bfloat16>(dout, y, rows, cols, slot, weights, tokens, topk, dy, dweights, vec, s)
+                  : combine_back_go<float, float>(dout, y, rows, cols, slot, weights, tokens, topk, dy, dweights, vec, s);
+}
+
+}  // namespace c3

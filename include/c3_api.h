@@ -556,6 +556,184 @@ int c3_cta_windows(int kernel, c3_cta_window *out, int max, int *n);
  * bytes >= 2 x L2.  Two SM kernels, asynchronous on `s`. */
 int c3_l2_flush(void *buf, size_t bytes, c3_stream s);
 
+/* ------------------------------------------------------------------------
+ * Operators of sparse layers and 4-bit numerics: what makes the payload of
+ * the all-to-all and of the weight all-gather, and what consumes it.  The
+ * pages have no counterpart of these entry points.  The conventions above
+ * hold: the caller owns every buffer and workspace, calls are asynchronous on
+ * `s`, nothing is launched on an argument error, and empty problems (no
+ * tokens, no rows) are C3_OK.  Tensors are row-major; an `ld` is the distance
+ * between rows in elements.  Pointers are aligned to their element (else
+ * C3_EALIGN); codes, scales and products' outputs to 16 bytes.
+ * ------------------------------------------------------------------------ */
+typedef enum { C3_F32 = 0, C3_BF16 = 1 } c3_type;
+typedef enum { C3_SCORE_SOFTMAX = 0, C3_SCORE_SIGMOID = 1 } c3_score;
+
+/* A router: how logits become a choice of experts and weights.
+ *   score s_e: softmax over the experts whose logit is above -inf, or
+ *     1 / (1 + exp(-x_e)).
+ *   key: s_e + bias_e (bias may be NULL).  With softmax, no bias and
+ *     group_best 1 the logits are compared themselves: they order as the
+ *     scores do.  An expert with a logit or a key of -inf or NaN is not
+ *     eligible.
+ *   groups: consecutive experts / groups experts form a group; its score is
+ *     the sum of its best group_best eligible keys (one, where it has only
+ *     one).  Experts outside the best topk_groups groups are not eligible.
+ *   The topk best keys are chosen, in descending order; equal keys, and equal
+ *     groups, go to the lowest number.  A token with fewer eligible experts
+ *     has idx -1 and weight 0 in the places that are left.
+ *   weight: scale * s_e; with renorm scale * s_e / (sum of the chosen s),
+ *     for the softmax as a softmax over the chosen logits, which never
+ *     divides by zero; for the sigmoid 0 where the sum is 0.
+ * A NaN logit makes all weights of its token NaN, and so does +inf with the
+ * softmax. */
+typedef struct {
+    const float *bias;  /* device, [experts], or NULL */
+    int experts;        /* 1..1024 */
+    int topk;           /* 1..32, at most topk_groups * experts / groups */
+    int groups;         /* 1.., divides experts */
+    int topk_groups;    /* 1..groups */
+    int group_best;     /* 1 or 2 (2 needs at least two experts a group) */
+    int score;          /* c3_score */
+    int renorm;         /* 0 or 1 */
+    int logits_type;    /* c3_type */
+    float scale;        /* finite */
+} c3_router;
+
+/*
+ * Routing:  logits [tokens][experts] (row distance ld >= experts) to
+ *   idx      int32 [tokens][topk]
+ *   weights  fp32  [tokens][topk]
+ */
+int c3_route(const c3_router *r, const void *logits, int64_t ld, int64_t tokens, int32_t *idx,
+             float *weights, c3_stream s);
+
+/*
+ * Gradient of the weights of c3_route with respect to the logits, for the
+ * choice idx that c3_route made (the choice itself has none, nor has the
+ * bias, which only moves the choice):
+ *   dlogits[t][e] = sum_j dweights[t][j] d weights[t][j] / d logits[t][e],
+ * in the logits' type, row distance dld, every entry written (zeros where the
+ * weights do not depend on an expert).  Entries of idx outside 0..experts-1
+ * count as none.
+ */
+int c3_route_backward(const c3_router *r, const void *logits, int64_t ld, int64_t tokens,
+                      const int32_t *idx, const float *dweights, void *dlogits, int64_t dld,
+                      c3_stream s);
+
+/*
+ * The rows of a sparse layer, sorted by expert.  Each expert's rows start at
+ * a multiple of 128 (C3_TILE_ROWS); within an expert they are in the order of
+ * the choices (token, then j).  The result does not depend on timing.
+ *   idx      int32 [tokens][topk]; entries outside 0..experts-1 take no row
+ *   slot     int32 [tokens][topk]: the choice's row, -1 for none
+ *   row_of   int32 [rows]: the token of a row, -1 where no choice has it
+ *   rows     at least c3_moe_rows(tokens, topk, experts) (else C3_EINVAL)
+ *   offsets  int32 [experts + 1]: first row of each expert; the last entry is
+ *            the first row that no expert has
+ *   counts   int32 [experts]: choices of each expert
+ *   work     c3_moe_order_bytes(...) bytes, device, scratch
+ *   topk 1..32, experts 1..1024
+ * c3_moe_rows: the most rows that any choice can need (tokens * topk plus
+ * padding), or C3_EINVAL; C3_EUNSUP from 2^31 rows on.  c3_moe_order_bytes: 0
+ * for bad arguments.  Both are host only.
+ */
+#define C3_TILE_ROWS 128
+int64_t c3_moe_rows(int64_t tokens, int topk, int experts);
+size_t c3_moe_order_bytes(int64_t tokens, int topk, int experts);
+int c3_moe_order(const int32_t *idx, int64_t tokens, int topk, int experts, int32_t *slot,
+                 int32_t *row_of, int64_t rows, int32_t *offsets, int32_t *counts, void *work,
+                 size_t work_bytes, c3_stream s);
+
+/*
+ * Microscaled 4-bit matrices.  A code is one of 0 .5 1 1.5 2 3 4 6 with a sign
+ * (bit 3); consecutive columns share a scale:
+ *   C3_FP4_MX  32 columns, a power of two 2^(b - 127), b one byte (255: NaN)
+ *   C3_FP4_NV  16 columns, an e4m3 number, and one fp32 number for the matrix
+ *              (tensor_scale; NULL stands for 1)
+ * value = code * scale * tensor_scale.
+ *   codes   [count][rows][pitch] bytes, pitch = 16 * ceil(cols / 32): two codes
+ *           a byte, the even column in the low half, zeros past cols
+ *   scales  [count][ceil(rows / 128)][k tiles][512] bytes, a k tile being four
+ *           blocks (128 columns MX, 64 NV): the scale of row r and block b of a
+ *           tile is byte (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4.  Blocks
+ *           past cols have scale byte 0; rows past `rows` are never used.
+ * `count` matrices of one size lie one after the other (the experts of a
+ * layer), each with its own tensor_scale[i].  c3_fp4_code_bytes and
+ * c3_fp4_scale_bytes give the sizes for count = 1 (0 for bad arguments). */
+typedef enum { C3_FP4_MX = 0, C3_FP4_NV = 1 } c3_fp4_format;
+typedef struct {
+    void *codes;
+    void *scales;
+    const float *tensor_scale; /* device, [count], or NULL (C3_FP4_MX: NULL) */
+    int64_t rows, cols;        /* rows >= 0, cols >= 1 */
+    int count;                 /* 1.. */
+    int format;                /* c3_fp4_format */
+} c3_fp4;
+size_t c3_fp4_code_bytes(int64_t rows, int64_t cols);
+size_t c3_fp4_scale_bytes(int64_t rows, int64_t cols, int format);
+
+/*
+ * Quantises x (x_type, [count][x_rows][x_cols], row distance ld >= x_cols) into q.
+ *   Scales: MX the smallest power of two with max|x| <= 6 * scale (no element
+ *   saturates); NV e4m3(max|y| / 6), to nearest even and at most 448, of
+ *   y = x * (1 / tensor_scale).  Codes: to the nearest value of x / scale, ties
+ *   to the even code.  A block of zeros has scale 0 (byte 0); a block with a
+ *   NaN or an infinity has a NaN scale and stands for NaNs.
+ *   transpose  0, or 1 to quantise the transpose of x: q has x_cols rows and
+ *              x_rows columns, and the blocks run along x's columns (the
+ *              operands of a product's gradients)
+ *   row_of     NULL, or q->rows row numbers of x, device (count 1, no
+ *              transpose): row r of q is row row_of[r] of x; where that is
+ *              outside 0..x_rows-1 the row of q is left as it was
+ * The gradient of quantised values is passed through unchanged by convention,
+ * so there is no backward entry point.
+ */
+int c3_fp4_quantize(const void *x, int x_type, int64_t x_rows, int64_t x_cols, int64_t ld,
+                    int transpose, const int32_t *row_of, const c3_fp4 *q, c3_stream s);
+/* The values of q, as x_type, [count][rows][cols] with row distance ld >= cols. */
+int c3_fp4_dequantize(const c3_fp4 *q, void *x, int x_type, int64_t ld, c3_stream s);
+
+/*
+ * C[m][n] = sum_k a[m][k] * b[n][k] of two 4-bit matrices of one format and
+ * equal cols (count 1), accumulated in fp32 on the tensor cores, rounded once
+ * to c_type (C: a->rows x b->rows, 16-byte aligned).  sm_budget as for c3_gemm.
+ * The gradients of a product are products of the same kind: of the output's
+ * gradient with the transposed operand, quantised along the other axis.
+ */
+int c3_fp4_gemm(const c3_fp4 *a, const c3_fp4 *b, void *C, int c_type, int sm_budget, c3_stream s);
+
+/*
+ * The experts' products: row r of expert e, offsets[e] <= r < offsets[e] +
+ * counts[e] (device, as c3_moe_order writes them), becomes
+ *   C[r][n] = sum_k x[r][k] * w[e][n][k]
+ * with w->count experts (1..1024).  Rows of C that no expert has are left as
+ * they were.  An expert whose offset is no multiple of 128, or whose rows do
+ * not lie within x, is skipped.
+ */
+int c3_fp4_gemm_experts(const c3_fp4 *x, const c3_fp4 *w, const int32_t *offsets,
+                        const int32_t *counts, void *C, int c_type, int sm_budget, c3_stream s);
+
+/*
+ * The experts' outputs of each token put together, in fp32, rounded once:
+ *   out[t] = sum_j weights[t][j] * y[slot[t][j]]      (j ascending)
+ * y [rows][cols] and out [tokens][cols] are dense; slots outside 0..rows-1
+ * add nothing; weights NULL stands for ones (the gradient of a gather of
+ * tokens into rows).  topk 1..32.
+ */
+int c3_moe_combine(const void *y, int y_type, int64_t rows, int64_t cols, const int32_t *slot,
+                   const float *weights, int64_t tokens, int topk, void *out, int out_type,
+                   c3_stream s);
+/*
+ * Its gradients:  dy[slot[t][j]] = weights[t][j] * dout[t]  (dy in y's type;
+ * rows that no slot names are left as they were; two slots of one row are an
+ * error of the caller)  and  dweights[t][j] = <dout[t], y[slot[t][j]]>, 0 for
+ * slots outside 0..rows-1.  dweights may be NULL (then y may be too).
+ */
+int c3_moe_combine_backward(const void *dout, int dout_type, const void *y, int y_type, int64_t rows,
+                            int64_t cols, const int32_t *slot, const float *weights, int64_t tokens,
+                            int topk, void *dy, float *dweights, c3_stream s);
+
 #ifdef __cplusplus
 }
 #endif
