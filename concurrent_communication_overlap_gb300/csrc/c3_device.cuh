@@ -30,6 +30,7 @@ enum WaitSite : int {
     kSiteFp4Mma = 9,
     kSiteFp4Epilogue = 10,
     kSiteFp4Drain = 11,
+    kSiteFp4Scales = 12,
 };
 
 __device__ __forceinline__ unsigned long long globaltimer() {

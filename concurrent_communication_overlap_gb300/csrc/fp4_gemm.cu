@@ -25,30 +25,12 @@ namespace c3 {
 
 constexpr int kFM = 128;             // rows of A in a tile
 constexpr int kFK = 256;             // columns of a stage: 128 bytes of codes
-constexpr int kFThreads = 192;
 constexpr int kFGroupM = 16;
 constexpr int kFSmemLimit = 232448;  // 227 KiB
+constexpr int kFHalfSmem = 115712;   // two CTAs on an SM: half of 228 KiB less 1 KiB each
 constexpr int kFMaxExperts = 1024;
 
-template <bool NV, int BN>
-struct Fp4Cfg {
-    static constexpr int kKT = NV ? 4 : 2;                    // scale tiles along a stage's columns
-    static constexpr uint32_t kABytes = kFM * 128;
-    static constexpr uint32_t kBBytes = BN * 128;
-    static constexpr uint32_t kSfa = kKT * 512;
-    static constexpr uint32_t kSfb = kKT * 512 * (BN / 128);
-    static constexpr uint32_t kStage = kABytes + kBBytes + (kSfa + kSfb + 1023) / 1024 * 1024;
-    static constexpr int kExtra = 1024 + 512 + 4 * (kFMaxExperts + 1);
-    static constexpr int kStages = (kFSmemLimit - kExtra) / (int)kStage > 8 ? 8 : (kFSmemLimit - kExtra) / (int)kStage;
-    static constexpr int kAccBufs = 2;
-    static constexpr int kSfCol = kAccBufs * BN;              // scales behind the accumulators
-    static constexpr int kSmem = kStages * (int)kStage + kExtra;
-    static_assert(kSfCol + kKT * 4 * (1 + BN / 128) <= 512, "TMEM");
-};
-
 struct Fp4GemmArgs {
-    const uint8_t* sfa;
-    const uint8_t* sfb;
     const float* ga;
     const float* gb;
     const int32_t* offsets;  // experts' rows of A, or NULL
@@ -57,7 +39,6 @@ struct Fp4GemmArgs {
     int64_t M;
     int N, K;
     int experts;
-    int k_tiles;             // scale tiles along K
     int b_row_tiles;         // scale tiles along one matrix of B
     int num_m, num_n, num_kb;
 };
@@ -71,32 +52,50 @@ __device__ __forceinline__ uint64_t code_desc(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+// One lane of a converged warp.  The warps that issue tensor-core work stay
+// together and predicate the instruction alone: their addresses and descriptors
+// then live in uniform registers (one lane branching off to issue took 640
+// cycles for a stage of four MMAs, 400 this way).
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
 }
-
-// Instruction descriptor: E2M1 codes (bits 7-9, 10-11 = 1), both K-major, N >> 3
-// at bits 17-22, power-of-two scales at bit 23, M >> 7 at bits 27-28; the scale
-// factors' byte within their column (0 or 2) at bits 4-5 (B) and 29-30 (A).
-template <bool NV, int BN>
-__device__ __forceinline__ uint32_t fp4_idesc() {
-    return (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | (NV ? 0u : 1u << 23) | (1u << 27);
+// GROUP: CTAs that share the tile (1 or 2).
+template <int GROUP, bool NV>
+__device__ __forceinline__ void mma_fp4(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate) {
+#define C3_MMA(G_, KIND_, VEC_)                                                                                      \
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"                     \
+                 "@q tcgen05.mma.cta_group::" G_ ".kind::" KIND_ ".block_scale.scale_vec::" VEC_                      \
+                 " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb),  \
+                 "r"(accumulate), "r"(lead)                                                                          \
+                 : "memory")
+    if constexpr (GROUP == 2 && NV) C3_MMA("2", "mxf4nvf4", "4X");
+    else if constexpr (GROUP == 2) C3_MMA("2", "mxf4", "2X");
+    else if constexpr (NV) C3_MMA("1", "mxf4nvf4", "4X");
+    else C3_MMA("1", "mxf4", "2X");
+#undef C3_MMA
 }
-template <bool NV>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                        uint32_t accumulate) {
-    if constexpr (NV)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
+// 128 rows x 4 scales from shared memory to four TMEM columns, in every lane quarter.
+template <int GROUP>
+__device__ __forceinline__ void copy_scales(uint32_t lead, uint32_t taddr, uint64_t sdesc) {
+#define C3_CP(G_)                                                                                    \
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q tcgen05.cp.cta_group::" G_       \
+                 ".32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(sdesc), "r"(lead) : "memory")
+    if constexpr (GROUP == 2) C3_CP("2");
+    else C3_CP("1");
+#undef C3_CP
+}
+// Arrive on this CTA's `bar` once all that the thread issued has completed.
+template <int GROUP>
+__device__ __forceinline__ void commit_local(uint32_t lead, uint32_t bar) {
+#define C3_COMMIT(G_)                                                                                \
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q tcgen05.commit.cta_group::" G_   \
+                 ".mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead) : "memory")
+    if constexpr (GROUP == 2) C3_COMMIT("2");
+    else C3_COMMIT("1");
+#undef C3_COMMIT
 }
 
 // One output tile: its expert, rows and columns.
@@ -107,7 +106,7 @@ struct Fp4Tile {
     int nb;
 };
 
-template <int BN>
+template <int ROWS>
 __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4GemmArgs& g, const int* prefix, int t) {
     Fp4Tile r;
     if (g.offsets == nullptr) {
@@ -115,8 +114,8 @@ __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4GemmArgs& g, const int* pre
         const int gm = min(g.num_m - first, kFGroupM), in = t - grp * per;
         const int mb = first + in % gm;
         r.expert = 0;
-        r.row0 = (int64_t)mb * kFM;
-        r.rows = (int)min((int64_t)kFM, g.M - r.row0);
+        r.row0 = (int64_t)mb * ROWS;
+        r.rows = (int)min((int64_t)ROWS, g.M - r.row0);
         r.nb = in / gm;
         return r;
     }
@@ -131,29 +130,506 @@ __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4GemmArgs& g, const int* pre
     const int mb = in % mt;
     r.expert = lo;
     r.nb = in / mt;
-    r.row0 = (int64_t)g.offsets[lo] + (int64_t)mb * kFM;
-    r.rows = min(kFM, g.counts[lo] - mb * kFM);
+    r.row0 = (int64_t)g.offsets[lo] + (int64_t)mb * ROWS;
+    r.rows = min(ROWS, g.counts[lo] - mb * ROWS);
     return r;
 }
 
-template <bool NV, int BN, typename TC>
-__global__ void __launch_bounds__(kFThreads, 1)
-    fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Fp4GemmArgs g,
-                    DevStatus* st) {
-    using Cfg = Fp4Cfg<NV, BN>;
-    constexpr int S = Cfg::kStages;
-    constexpr int KT = Cfg::kKT;
+// Row tiles before each expert, by one warp.  An expert whose rows do not lie in
+// A, or do not start at a whole scale tile, has none: nothing out of range is touched.
+template <int ROWS>
+__device__ __forceinline__ void expert_tiles(const Fp4GemmArgs& g, int* prefix, int lane) {
+    int run = 0;
+    for (int e0 = 0; e0 < g.experts; e0 += 32) {
+        const int e = e0 + lane;
+        int mt = 0;
+        if (e < g.experts) {
+            const int64_t off = g.offsets[e], c = g.counts[e];
+            if (off >= 0 && c > 0 && off % kTileRows == 0 && off + c <= g.M) mt = (int)((c + ROWS - 1) / ROWS);
+        }
+        int incl = mt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (e < g.experts) prefix[e + 1] = run + incl;
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) prefix[0] = 0;
+}
+
+// ---------------------------------------------------------------- two SMs on one tile
+//
+// The form for many rows.  A cluster of two CTAs shares one tile of MSUB x 256
+// rows by 192 columns (cta_group::2): each CTA brings in its 128 rows of A of
+// every 256, half of B's rows and all of the tile's scales of B, and holds the
+// accumulators of its own rows.  A 4-bit MMA at full rate eats its operands
+// four times as fast as a bf16 one, so what an SM has to take in per MMA cycle
+// decides: 128 x 128 tiles on one SM need 126 bytes a cycle, 256 x 192 on two
+// 78, 512 x 192 on two 61.  192 columns, because a tile's scales have to begin
+// at an even TMEM column (a multiple of 64 rows of B) and two accumulator sets
+// of 256 columns would leave TMEM no room for scales.
+//
+// The leader (rank 0) issues every MMA.  Its full barriers count the bytes of
+// both CTAs' loads; a commit frees a stage, or publishes a tile, in both.  The
+// epilogue's eight warps in each CTA read 32 x 32 pieces out of TMEM one ahead,
+// turn them through 2 KB of shared memory each, and write whole 64-byte pieces
+// of rows.
+constexpr int kPN = 192;
+constexpr int kPThreads = 384;
+constexpr int kPEpiWarps = 8;
+
+template <bool NV, int MSUB, typename TC>
+struct Fp4PairCfg {
+    static constexpr int kKT = NV ? 4 : 2;
+    static constexpr int kBN2 = kPN / 2;
+    static constexpr uint32_t kABytes = MSUB * kFM * 128;
+    static constexpr uint32_t kBBytes = kBN2 * 128;
+    static constexpr uint32_t kSfa = MSUB * kKT * 512;
+    static constexpr uint32_t kSfb = 2 * kKT * 512;   // 192 rows from a multiple of 64 on lie in two scale tiles
+    static constexpr uint32_t kStage = kABytes + kBBytes + kSfa + kSfb;
+    static constexpr uint32_t kStaging = kPEpiWarps * 2048;
+    // 512 rows: one matrix only
+    static constexpr int kExtra = 1024 + 512 + (MSUB == 1 ? 4 * (kFMaxExperts + 1) : 0) + (int)kStaging;
+    static constexpr int kFit = (kFSmemLimit - kExtra) / (int)kStage;
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
+    static constexpr int kSmem = kStages * (int)kStage + kExtra;
+    static constexpr int kAccBufs = MSUB == 2 ? 1 : 2;
+    static constexpr int kSetCols = (MSUB + 2) * 4;   // TMEM columns of one k tile's scales
+    static_assert(kStage % 1024 == 0, "the codes need 1024-byte alignment");
+    static constexpr int kSets = NV ? 2 : 4;          // stages whose scales TMEM holds
+    static_assert(kStages >= kSets && 2 * kPN + kSets * kKT * kSetCols <= 512, "pair configuration");
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t leader_addr(uint32_t local) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(local));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A wait whose phase another CTA of the cluster may complete.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort) return false;
+            if (globaltimer() - t0 > kWaitLimitNs) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y,
+                                                 uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"((uint16_t)3), "r"(lead)
+        : "memory");
+}
+
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t* v) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 16 fp32 values of this lane's row to 64 bytes (fp32) or 32 values to 64 bytes
+// (bf16) of shared memory, then the warp's 32 rows to C, a quarter warp a row.
+// Chunk j of row r lies at chunk j ^ ((r >> 1) & 3): no bank conflicts either way.
+template <typename TC>
+__device__ __forceinline__ void store_rows(uint32_t blk, int lane, const uint32_t* v, TC* C, int64_t row0, int rows,
+                                           int col0, int N) {
+    constexpr int kPer = 16 / sizeof(TC);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        st_shared_v4(blk + (uint32_t)lane * 64u + (uint32_t)((j ^ ((lane >> 1) & 3)) << 4), v[4 * j], v[4 * j + 1],
+                     v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), j = lane & 3;
+        uint32_t u[4];
+        ld_shared_v4(blk + (uint32_t)r * 64u + (uint32_t)((j ^ ((r >> 1) & 3)) << 4), u);
+        const int col = col0 + j * kPer;
+        if (r < rows && col < N)
+            *reinterpret_cast<uint4*>(C + (row0 + r) * (int64_t)N + col) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    __syncwarp();
+}
+
+// A 32 x 32 piece, already rounded to TC, to C; columns past N and rows past
+// `rows` are left alone.  vec: rows of C are whole 16-byte units.
+template <typename TC>
+__device__ __forceinline__ void store_piece(const uint32_t* v, uint32_t blk, int lane, bool vec, TC* C, int64_t row0,
+                                            int rows, int col0, int N) {
+    if (vec) {
+#pragma unroll
+        for (int h = 0; h < (int)sizeof(TC) / 2; ++h)
+            store_rows<TC>(blk, lane, v + 16 * h, C, row0, rows, col0 + 16 * h, N);
+    } else if (lane < rows) {
+        TC* crow = C + (row0 + lane) * (int64_t)N;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (col0 + j < N) {
+                if constexpr (sizeof(TC) == 2)
+                    crow[col0 + j] = __ushort_as_bfloat16((unsigned short)(v[j / 2] >> (16 * (j & 1))));
+                else
+                    crow[col0 + j] = __uint_as_float(v[j]);
+            }
+    }
+    __syncwarp();
+}
+
+// tmA, tmB: codes; tmSA, tmSB: scales as [row tiles][k tiles * 64] 64-bit words.
+template <bool NV, int MSUB, typename TC>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
+    fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                         Fp4GemmArgs g, DevStatus* st) {
+    using Cfg = Fp4PairCfg<NV, MSUB, TC>;
+    constexpr int S = Cfg::kStages, KT = Cfg::kKT, NB = Cfg::kAccBufs;
+    constexpr int kRows = 256 * MSUB;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const uint32_t staging = base + S * Cfg::kStage;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(gbase + S * Cfg::kStage + Cfg::kStaging);
+    // stage full [0, S), empty [S, 2S), its scales in TMEM too [2S, 3S), accumulator full 3S..,
+    // empty 3S+2.., drain 3S+4
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 5);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* prefix = reinterpret_cast<int*>(gbase + S * Cfg::kStage + Cfg::kStaging + 512);
+    auto bar = [&](int i) { return smem_addr(&bars[i]); };
+    const int SREADY = 2 * S, TFULL = 3 * S, TEMPTY = 3 * S + 2, DRAIN = 3 * S + 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < S; ++i) {
+            mbar_init(bar(i), 1);
+            mbar_init(bar(S + i), 1);
+            mbar_init(bar(SREADY + i), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar(TFULL + b), 1);
+            mbar_init(bar(TEMPTY + b), 2 * kPEpiWarps);
+        }
+        mbar_init(bar(DRAIN), 1);
+        fence_barrier_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tmSA);
+        prefetch_tensormap(&tmSB);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (MSUB == 1 && g.offsets && warp == 2) expert_tiles<kRows>(g, prefix, lane);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers are ready before either signals the other's
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int total = MSUB == 1 && g.offsets ? prefix[g.experts] * g.num_n : g.num_m * g.num_n;
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol_a = policy_evict_last(), pol_b = policy_evict_normal();
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = first; ok && t < total; t += step) {
+                const Fp4Tile tile = fp4_tile<kRows>(g, prefix, t);
+                const int arow = (int)tile.row0 + (int)rank * 128;
+                const int n0 = tile.nb * kPN;
+                const int brow = tile.expert * g.N + n0 + (int)rank * Cfg::kBN2;
+                const int sbrow = tile.expert * g.b_row_tiles + n0 / 128;
+                for (int kb = 0; kb < g.num_kb; ++kb) {
+                    if (!mbar_wait_cluster(bar(S + stage), phase ^ 1u, abort_flag)) {
+                        report_error(st, -4, kSiteFp4Producer);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sb = base + (uint32_t)stage * Cfg::kStage;
+                    const uint32_t full = leader_addr(bar(stage));
+                    const uint32_t sf = sb + Cfg::kABytes + Cfg::kBBytes;
+                    if (rank == 0) mbar_arrive_expect_tx(bar(stage), 2 * Cfg::kStage);
+#pragma unroll
+                    for (int i = 0; i < MSUB; ++i)
+                        tma_load_2d_pair(sf + (uint32_t)i * KT * 512u, &tmSA, full, kb * KT * 64, arow / 128 + i * 2, pol_a);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        tma_load_2d_pair(sf + Cfg::kSfa + (uint32_t)i * KT * 512u, &tmSB, full, kb * KT * 64, sbrow + i, pol_b);
+#pragma unroll
+                    for (int i = 0; i < MSUB; ++i)
+                        tma_load_2d_pair(sb + (uint32_t)i * kFM * 128u, &tmA, full, kb * 128, arow + i * 256, pol_a);
+                    tma_load_2d_pair(sb + Cfg::kABytes, &tmB, full, kb * 128, brow, pol_b);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // The pair's loads have all landed once every stage that was filled has been
+            // freed (its MMAs follow its loads): wait for that before the CTA may end.
+            // After a wait gave up, the leader's full barriers tell it instead.
+            volatile int no_abort = 0;
+            for (int i = 0; (ok || rank == 0) && i < S; ++i)
+                if (!mbar_wait_cluster(bar(ok ? S + i : i), (i < stage) ? phase : (phase ^ 1u), &no_abort))
+                    report_error(st, -4, kSiteFp4Drain);
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const uint32_t lead = elect_lane();
+            const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(kPN >> 3) << 17) | (NV ? 0u : 1u << 23) | (2u << 27);
+            const uint64_t code0 = code_desc(base);
+            int stage = 0, local = 0, set = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = first; ok && t < total; t += step, ++local) {
+                // odd tiles begin at row 64 of a scale tile: two columns
+                const uint32_t shift = (uint32_t)(fp4_tile<kRows>(g, prefix, t).nb & 1) * 2u;
+                const int buf = local % NB;
+                if (!mbar_wait_cluster(bar(TEMPTY + buf), ((uint32_t)(local / NB) & 1u) ^ 1u, abort_flag)) {
+                    report_error(st, -4, kSiteFp4Mma);
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(buf * kPN);
+                for (int kb = 0; kb < g.num_kb; ++kb) {
+                    if (!mbar_wait_cluster(bar(SREADY + stage), phase, abort_flag)) {
+                        report_error(st, -4, kSiteFp4Mma);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = code0 + (uint64_t)((uint32_t)stage * (Cfg::kStage >> 4));
+                    const uint64_t bd = ad + (Cfg::kABytes >> 4);
+                    const int steps = min(4, (g.K - kb * kFK + 63) / 64);
+                    const uint32_t tsf0 = tmem + 2u * kPN + (uint32_t)(set * KT * Cfg::kSetCols);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t go = k < steps ? lead : 0u;
+                        const uint32_t tsf = tsf0 + (uint32_t)((NV ? k : k >> 1) * Cfg::kSetCols);
+                        const uint32_t id = NV ? 0u : (uint32_t)(k & 1) * 2u;
+#pragma unroll
+                        for (int i = 0; i < MSUB; ++i)
+                            mma_fp4<2, NV>(go, d + (uint32_t)(i * kPN), ad + (uint64_t)(i * (kFM * 128 >> 4) + 2 * k),
+                                             bd + (uint64_t)(2 * k), idesc | (id << 4) | (id << 29), tsf + (uint32_t)i * 4,
+                                             tsf + (uint32_t)MSUB * 4 + shift, k > 0 ? 1u : (uint32_t)(kb > 0));
+                    }
+                    commit_pair(lead, bar(S + stage));
+                    set = set + 1 == Cfg::kSets ? 0 : set + 1;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) commit_pair(lead, bar(TFULL + buf));
+            }
+            // no MMA may still run when TMEM is freed
+            commit_local<2>(lead, bar(DRAIN));
+            volatile int no_abort = 0;
+            if (!mbar_wait(bar(DRAIN), 0, &no_abort)) report_error(st, -4, kSiteFp4Drain);
+        }
+    } else if (warp < 4) {
+        if (warp == 2 && rank == 0) {
+            // ---------------- scales from shared memory to TMEM, in both CTAs
+            const uint32_t lead = elect_lane();
+            const uint64_t scale0 = scale_desc(base + Cfg::kABytes + Cfg::kBBytes);
+            int stage = 0, set = 0, old_stage = 0;  // old_stage: the stage whose MMAs used this set last
+            uint32_t phase = 0, old_phase = 0;
+            int done = 0;
+            bool ok = true;
+            for (int t = first; ok && t < total; t += step)
+                for (int kb = 0; kb < g.num_kb; ++kb) {
+                    ok = mbar_wait_cluster(bar(stage), phase, abort_flag);
+                    if (ok && done >= Cfg::kSets) ok = mbar_wait_cluster(bar(S + old_stage), old_phase, abort_flag);
+                    if (!ok) {
+                        report_error(st, -4, kSiteFp4Scales);
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t from = scale0 + (uint64_t)((uint32_t)stage * (Cfg::kStage >> 4));
+                    const uint32_t to = tmem + 2u * kPN + (uint32_t)(set * KT * Cfg::kSetCols);
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                        for (int i = 0; i < MSUB + 2; ++i)
+                            copy_scales<2>(lead, to + (uint32_t)(kt * Cfg::kSetCols + i * 4),
+                                                  from + (uint64_t)((i * KT + kt) * (512 >> 4)));
+                    commit_local<2>(lead, bar(SREADY + stage));
+                    if (++done > Cfg::kSets && ++old_stage == S) {
+                        old_stage = 0;
+                        old_phase ^= 1u;
+                    }
+                    set = set + 1 == Cfg::kSets ? 0 : set + 1;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+        }
+    } else {
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t blk = staging + (uint32_t)(warp - 4) * 2048u;
+        const bool vec = ((int64_t)g.N * (int)sizeof(TC)) % 16 == 0;
+        const float ga = g.ga ? *g.ga : 1.0f;
+        int local = 0;
+        for (int t = first; t < total; t += step, ++local) {
+            const Fp4Tile tile = fp4_tile<kRows>(g, prefix, t);
+            const int buf = local % NB;
+            const bool ready = mbar_wait_cluster(bar(TFULL + buf), (uint32_t)(local / NB) & 1u, abort_flag);
+            if (!__all_sync(0xffffffffu, ready)) {
+                report_error(st, -4, kSiteFp4Epilogue);
+                break;
+            }
+            tc_fence_after();
+            const float alpha = ga * (g.gb ? g.gb[tile.expert] : 1.0f);
+            // This warp's columns: with two row blocks all of one block's, else half of them.
+            constexpr int kPieces = kPN / 32 / (MSUB == 2 ? 1 : 2);
+            constexpr int kWords = 8 * sizeof(TC);
+            constexpr int kBatch = kPieces * kWords <= 96 ? kPieces : 96 / kWords;
+            const int sub = MSUB == 2 ? half : 0;
+            const int r0 = sub * 256 + (int)rank * 128 + q * 32;  // the warp's first row in the tile
+            const int c0 = MSUB == 2 ? 0 : half * kPieces * 32;
+            const int rows = tile.rows - r0, col0 = tile.nb * kPN + c0;
+            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((buf + sub) * kPN + c0);
+            // Read out and rounded first: the accumulator is free again before anything is stored.
+#pragma unroll
+            for (int b = 0; b < kPieces; b += kBatch) {
+                uint32_t v[kBatch * kWords];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    uint32_t r[32];
+                    tmem_ld32(taddr + (uint32_t)((b + i) * 32), r);
+                    tmem_ld_wait();
+                    if constexpr (sizeof(TC) == 2) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(alpha * __uint_as_float(r[2 * j]),
+                                                                           alpha * __uint_as_float(r[2 * j + 1]));
+                            v[i * kWords + j] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[i * kWords + j] = __float_as_uint(alpha * __uint_as_float(r[j]));
+                    }
+                }
+                if (b + kBatch >= kPieces) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(leader_addr(bar(TEMPTY + buf)));
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    store_piece<TC>(&v[i * kWords], blk, lane, vec, static_cast<TC*>(g.C), tile.row0 + r0, rows,
+                                    col0 + (b + i) * 32, g.N);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // nothing of this CTA's is signalled or read by the other any more
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- few rows
+//
+// The form for few rows of A (a serving step's tokens, an expert's handful): the
+// weights' bytes decide, so the roles are swapped.  B's rows (the output's
+// columns) take the MMA's 128 rows and A's rows its columns, NT of them: nothing
+// of a tile is padding that has to be brought in, and a warp stores 32
+// neighbours of one row of C.
+//
+// Two CTAs fit an SM: one's start and end hide behind the other's stream.  Where
+// there are fewer tiles than CTAs to fill the machine, a cluster of `split` CTAs
+// takes one tile, each a part of K; their fp32 parts meet in shared memory, each
+// CTA adding up its share of A's rows in the order of the ranks.
+constexpr int kRThreads = 256;
+
+template <bool NV, int NT>
+struct Fp4RowsCfg {
+    static constexpr int kKT = NV ? 4 : 2;
+    static constexpr uint32_t kWBytes = 128 * 128;
+    static constexpr uint32_t kTBytes = NT * 128;
+    static constexpr uint32_t kSf = kKT * 512;
+    static constexpr uint32_t kStage = kWBytes + kTBytes + 2 * kSf;
+    static constexpr int kExtra = 1024 + 512 + (NT == 64 ? 4 * (kFMaxExperts + 1) : 0);  // experts: 64 rows
+    static constexpr int kStages = (kFHalfSmem - kExtra) / (int)kStage;
+    static constexpr int kSmem = kStages * (int)kStage + kExtra;
+    static constexpr int kAccBufs = NT == 128 ? 1 : 2;
+    static constexpr int kSetCols = 8;
+    static constexpr int kSets = 128 / (kKT * kSetCols) > 4 ? 4 : 128 / (kKT * kSetCols);
+    static_assert(kStage % 1024 == 0 && kStages >= 3, "few-rows configuration");
+    static_assert(kStages * kStage >= NT * 512, "the parts meet in the ring");
+};
+
+__device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+
+template <bool NV, int NT, typename TC>
+__global__ void __launch_bounds__(kRThreads, 2)
+    fp4_gemm_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                         Fp4GemmArgs g, int split, DevStatus* st) {
+    using Cfg = Fp4RowsCfg<NV, NT>;
+    constexpr int S = Cfg::kStages, KT = Cfg::kKT, NB = Cfg::kAccBufs;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw);
     uint64_t* bars = reinterpret_cast<uint64_t*>(gbase + S * Cfg::kStage);
-    // full [0, S), empty [S, 2S), accumulator full [2S, 2S+2), empty [2S+2, 2S+4), drain 2S+4
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+    // stage full [0, S), empty [S, 2S), its scales in TMEM [2S, 3S), accumulator full 3S.., empty 3S+2.., drain 3S+4
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* prefix = reinterpret_cast<int*>(gbase + S * Cfg::kStage + 512);
     auto bar = [&](int i) { return smem_addr(&bars[i]); };
-    const int TFULL = 2 * S, TEMPTY = 2 * S + 2, DRAIN = 2 * S + 4;
+    const int SREADY = 2 * S, TFULL = 3 * S, TEMPTY = 3 * S + 2, DRAIN = 3 * S + 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -161,207 +637,239 @@ __global__ void __launch_bounds__(kFThreads, 1)
         for (int i = 0; i < S; ++i) {
             mbar_init(bar(i), 1);
             mbar_init(bar(S + i), 1);
+            mbar_init(bar(SREADY + i), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar(TFULL + b), 1);
-            mbar_init(bar(TEMPTY + b), 4 * 32);
+            mbar_init(bar(TEMPTY + b), 4);
         }
         mbar_init(bar(DRAIN), 1);
         fence_barrier_init();
         prefetch_tensormap(&tmA);
         prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tmSA);
+        prefetch_tensormap(&tmSB);
     }
     if (warp == 1) {
-        tmem_alloc(smem_addr(tmem_slot), 512);
+        tmem_alloc(smem_addr(tmem_slot), 256);
         tmem_relinquish();
     }
-    if (g.offsets && warp == 2) {
-        // Row tiles before each expert.  An expert whose rows do not lie in A, or
-        // do not start at a whole tile, has none: nothing out of range is touched.
-        int run = 0;
-        for (int e0 = 0; e0 < g.experts; e0 += 32) {
-            const int e = e0 + lane;
-            int mt = 0;
-            if (e < g.experts) {
-                const int64_t off = g.offsets[e], c = g.counts[e];
-                if (off >= 0 && c > 0 && off % kTileRows == 0 && off + c <= g.M) mt = (int)((c + kFM - 1) / kFM);
-            }
-            int incl = mt;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            if (e < g.experts) prefix[e + 1] = run + incl;
-            run += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        if (lane == 0) prefix[0] = 0;
-    }
+    if (NT == 64 && g.offsets && warp == 2) expert_tiles<NT>(g, prefix, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int total = g.offsets ? prefix[g.experts] * g.num_n : g.num_m * g.num_n;
+    const int total = NT == 64 && g.offsets ? prefix[g.experts] * g.num_n : g.num_m * g.num_n;
+    const uint32_t rank = split > 1 ? cluster_rank() : 0u;
+    const int first = split > 1 ? blockIdx.x / split : blockIdx.x;
+    const int step = split > 1 ? total : gridDim.x;  // a cluster takes one tile
+    const int kb0 = (int)((int64_t)g.num_kb * (int)rank / split), kb1 = (int)((int64_t)g.num_kb * ((int)rank + 1) / split);
 
     if (warp == 0) {
         if (lane == 0) {
+            // weights that one tile alone reads do not stay in L2
+            const uint64_t pol_w = g.num_m > 1 ? policy_evict_normal() : policy_evict_first(), pol_t = policy_evict_last();
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-                const Fp4Tile tile = fp4_tile<BN>(g, prefix, t);
-                const uint8_t* sfa = g.sfa + (tile.row0 / kTileRows) * g.k_tiles * 512;
-                const int rt0 = tile.nb * (BN / 128);
-                const uint8_t* sfb = g.sfb + ((int64_t)tile.expert * g.b_row_tiles + rt0) * g.k_tiles * 512;
-                const int nrt = min(BN / 128, g.b_row_tiles - rt0);
-                const int arow = (int)tile.row0, brow = tile.expert * g.N + tile.nb * BN;
-                for (int kb = 0; kb < g.num_kb; ++kb) {
+            for (int t = first; ok && t < total; t += step) {
+                const Fp4Tile tile = fp4_tile<NT>(g, prefix, t);
+                const int trow = (int)tile.row0, wrow = tile.expert * g.N + tile.nb * 128;
+                const int swrow = tile.expert * g.b_row_tiles + tile.nb;
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(bar(S + stage), phase ^ 1u, abort_flag)) {
                         report_error(st, -4, kSiteFp4Producer);
                         ok = false;
                         break;
                     }
                     const uint32_t sb = base + (uint32_t)stage * Cfg::kStage;
-                    const uint32_t sf = sb + Cfg::kABytes + Cfg::kBBytes;
-                    const uint32_t part = (uint32_t)min(KT, g.k_tiles - kb * KT) * 512u;
-                    mbar_arrive_expect_tx(bar(stage), Cfg::kABytes + Cfg::kBBytes + part * (uint32_t)(1 + nrt));
-                    tma_load_2d(sb, &tmA, bar(stage), kb * 128, arow, policy_evict_last());
-                    tma_load_2d(sb + Cfg::kABytes, &tmB, bar(stage), kb * 128, brow, policy_evict_normal());
-                    bulk_load(sf, sfa + (int64_t)kb * KT * 512, part, bar(stage));
-                    for (int i = 0; i < nrt; ++i)
-                        bulk_load(sf + Cfg::kSfa + (uint32_t)i * KT * 512u, sfb + ((int64_t)i * g.k_tiles + kb * KT) * 512,
-                                  part, bar(stage));
+                    const uint32_t sf = sb + Cfg::kWBytes + Cfg::kTBytes;
+                    mbar_arrive_expect_tx(bar(stage), Cfg::kStage);
+                    tma_load_2d(sb, &tmB, bar(stage), kb * 128, wrow, pol_w);
+                    tma_load_2d(sb + Cfg::kWBytes, &tmA, bar(stage), kb * 128, trow, pol_t);
+                    tma_load_2d(sf, &tmSB, bar(stage), kb * KT * 64, swrow, pol_w);
+                    tma_load_2d(sf + Cfg::kSf, &tmSA, bar(stage), kb * KT * 64, trow / 128, pol_t);
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            // Every load must have landed before the CTA ends (see the bf16 kernel).
+            // Every load must have landed before the CTA ends.
             volatile int no_abort = 0;
             for (int i = 0; i < S; ++i)
                 if (!mbar_wait(bar(i), (i < stage) ? phase : (phase ^ 1u), &no_abort))
                     report_error(st, -4, kSiteFp4Drain);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = fp4_idesc<NV, BN>();
-            const uint32_t tsfa = tmem + (uint32_t)Cfg::kSfCol, tsfb = tsfa + KT * 4;
-            int stage = 0, local = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++local) {
-                const int buf = local & 1;
-                if (!mbar_wait(bar(TEMPTY + buf), ((uint32_t)(local >> 1) & 1u) ^ 1u, abort_flag)) {
+        const uint32_t lead = elect_lane();
+        const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(NT >> 3) << 17) | (NV ? 0u : 1u << 23) | (1u << 27);
+        const uint64_t code0 = code_desc(base);
+        int stage = 0, local = 0, set = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = first; ok && t < total; t += step, ++local) {
+            const uint32_t shift = (uint32_t)(fp4_tile<NT>(g, prefix, t).row0 % 128) / 32;  // 0 or 2
+            const int buf = local % NB;
+            if (!mbar_wait(bar(TEMPTY + buf), ((uint32_t)(local / NB) & 1u) ^ 1u, abort_flag)) {
+                report_error(st, -4, kSiteFp4Mma);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + (uint32_t)(buf * NT);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(bar(SREADY + stage), phase, abort_flag)) {
                     report_error(st, -4, kSiteFp4Mma);
+                    ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(buf * BN);
-                for (int kb = 0; kb < g.num_kb; ++kb) {
-                    if (!mbar_wait(bar(stage), phase, abort_flag)) {
-                        report_error(st, -4, kSiteFp4Mma);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sb = base + (uint32_t)stage * Cfg::kStage;
-                    const uint32_t sf = sb + Cfg::kABytes + Cfg::kBBytes;
-                    const int steps = min(4, (g.K - kb * kFK + 63) / 64);
-                    const int parts = min(KT, g.k_tiles - kb * KT);
-                    for (int i = 0; i < parts; ++i) {
-                        tmem_copy_scales(tsfa + (uint32_t)i * 4, scale_desc(sf + (uint32_t)i * 512u));
+                const uint64_t wd = code0 + (uint64_t)((uint32_t)stage * (Cfg::kStage >> 4));
+                const uint64_t td = wd + (Cfg::kWBytes >> 4);
+                const int steps = min(4, (g.K - kb * kFK + 63) / 64);
+                const uint32_t tsf0 = tmem + 128u + (uint32_t)(set * KT * Cfg::kSetCols);
 #pragma unroll
-                        for (int j = 0; j < BN / 128; ++j)
-                            tmem_copy_scales(tsfb + (uint32_t)(i * (BN / 128) + j) * 4,
-                                             scale_desc(sf + Cfg::kSfa + (uint32_t)(j * KT + i) * 512u));
-                    }
-                    const uint64_t ad = code_desc(sb), bd = code_desc(sb + Cfg::kABytes);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k >= steps) break;
-                        const int kt = NV ? k : k >> 1;
-                        const uint32_t id = NV ? 0u : (uint32_t)(k & 1) * 2u;
-                        mma_fp4<NV>(d, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc | (id << 4) | (id << 29),
-                                    tsfa + (uint32_t)kt * 4, tsfb + (uint32_t)(kt * (BN / 128)) * 4,
-                                    (kb > 0 || k > 0) ? 1u : 0u);
-                    }
-                    tc_commit(bar(S + stage));
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t tsf = tsf0 + (uint32_t)((NV ? k : k >> 1) * Cfg::kSetCols);
+                    const uint32_t id = NV ? 0u : (uint32_t)(k & 1) * 2u;
+                    mma_fp4<1, NV>(k < steps ? lead : 0u, d, wd + (uint64_t)(2 * k), td + (uint64_t)(2 * k),
+                                   idesc | (id << 4) | (id << 29), tsf, tsf + 4u + shift, k > 0 ? 1u : (uint32_t)(kb > kb0));
                 }
-                if (ok) tc_commit(bar(TFULL + buf));
+                commit_local<1>(lead, bar(S + stage));
+                set = set + 1 == Cfg::kSets ? 0 : set + 1;
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
-            tc_commit(bar(DRAIN));
-            volatile int no_abort = 0;
-            if (!mbar_wait(bar(DRAIN), 0, &no_abort)) report_error(st, -4, kSiteFp4Drain);
+            if (ok) commit_local<1>(lead, bar(TFULL + buf));
         }
-    } else {
+        // no MMA may still run when TMEM is freed
+        commit_local<1>(lead, bar(DRAIN));
+        volatile int no_abort = 0;
+        if (!mbar_wait(bar(DRAIN), 0, &no_abort)) report_error(st, -4, kSiteFp4Drain);
+    } else if (warp == 2) {
+        // ---------------- scales from shared memory to TMEM (see the pair kernel)
+        const uint32_t lead = elect_lane();
+        const uint64_t scale0 = scale_desc(base + Cfg::kWBytes + Cfg::kTBytes);
+        int stage = 0, set = 0, old_stage = 0;
+        uint32_t phase = 0, old_phase = 0;
+        int done = 0;
+        bool ok = true;
+        for (int t = first; ok && t < total; t += step)
+            for (int kb = kb0; kb < kb1; ++kb) {
+                ok = mbar_wait(bar(stage), phase, abort_flag);
+                if (ok && done >= Cfg::kSets) ok = mbar_wait(bar(S + old_stage), old_phase, abort_flag);
+                if (!ok) {
+                    report_error(st, -4, kSiteFp4Scales);
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t from = scale0 + (uint64_t)((uint32_t)stage * (Cfg::kStage >> 4));
+                const uint32_t to = tmem + 128u + (uint32_t)(set * KT * Cfg::kSetCols);
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        copy_scales<1>(lead, to + (uint32_t)(kt * Cfg::kSetCols + i * 4),
+                                       from + (uint64_t)((i * KT + kt) * (512 >> 4)));
+                commit_local<1>(lead, bar(SREADY + stage));
+                if (++done > Cfg::kSets && ++old_stage == S) {
+                    old_stage = 0;
+                    old_phase ^= 1u;
+                }
+                set = set + 1 == Cfg::kSets ? 0 : set + 1;
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+    } else if (warp >= 4 && split == 1) {
         const int q = warp & 3;
-        const bool vec = ((int64_t)g.N * (int)sizeof(TC)) % 16 == 0;
         const float ga = g.ga ? *g.ga : 1.0f;
         int local = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x, ++local) {
-            const Fp4Tile tile = fp4_tile<BN>(g, prefix, t);
-            const int buf = local & 1;
-            const bool ready = mbar_wait(bar(TFULL + buf), (uint32_t)(local >> 1) & 1u, abort_flag);
-            if (!__all_sync(0xffffffffu, ready)) {
+        for (int t = first; t < total; t += step, ++local) {
+            const Fp4Tile tile = fp4_tile<NT>(g, prefix, t);
+            const int buf = local % NB;
+            const bool go = mbar_wait(bar(TFULL + buf), (uint32_t)(local / NB) & 1u, abort_flag);
+            if (!__all_sync(0xffffffffu, go)) {
                 report_error(st, -4, kSiteFp4Epilogue);
                 break;
             }
             tc_fence_after();
             const float alpha = ga * (g.gb ? g.gb[tile.expert] : 1.0f);
-            const int row = q * 32 + lane;
-            TC* crow = static_cast<TC*>(g.C) + (tile.row0 + row) * (int64_t)g.N;
-            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
+            const int n = tile.nb * 128 + q * 32 + lane;
+            TC* c = static_cast<TC*>(g.C) + tile.row0 * (int64_t)g.N + n;
+            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * NT);
 #pragma unroll 1
-            for (int c = 0; c < BN / 32; ++c) {
-                const int col0 = tile.nb * BN + c * 32;
-                if (col0 >= g.N) break;
+            for (int j0 = 0; j0 < NT && j0 < tile.rows; j0 += 32) {
                 uint32_t r[32];
-                tmem_ld32(taddr + (uint32_t)(c * 32), r);
+                tmem_ld32(taddr + (uint32_t)j0, r);
                 tmem_ld_wait();
-                if (row >= tile.rows) {
-                    // not a row of this expert: left as it was
-                } else if (vec && col0 + 32 <= g.N) {
-                    if constexpr (sizeof(TC) == 4) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            reinterpret_cast<float4*>(crow + col0)[j] =
-                                make_float4(alpha * __uint_as_float(r[4 * j]), alpha * __uint_as_float(r[4 * j + 1]),
-                                            alpha * __uint_as_float(r[4 * j + 2]), alpha * __uint_as_float(r[4 * j + 3]));
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t u[4];
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                const __nv_bfloat162 b2 =
-                                    __floats2bfloat162_rn(alpha * __uint_as_float(r[8 * j + 2 * h]),
-                                                          alpha * __uint_as_float(r[8 * j + 2 * h + 1]));
-                                u[h] = *reinterpret_cast<const uint32_t*>(&b2);
-                            }
-                            reinterpret_cast<uint4*>(crow + col0)[j] = make_uint4(u[0], u[1], u[2], u[3]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (col0 + j < g.N) crow[col0 + j] = (TC)(alpha * __uint_as_float(r[j]));
-                }
+                for (int j = 0; j < 32; ++j)
+                    if (j0 + j < tile.rows && n < g.N) c[(int64_t)(j0 + j) * g.N] = (TC)(alpha * __uint_as_float(r[j]));
                 __syncwarp();
             }
             tc_fence_before();
-            mbar_arrive(bar(TEMPTY + buf));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(TEMPTY + buf));
+        }
+    }
+    __syncwarp();
+    if (split > 1) {
+        // The parts of a tile: share s of A's rows (NT / split of them) is added up by
+        // rank s, from the parts that every rank writes into its ring, which is idle:
+        // all MMAs and loads of the cluster are done at the first barrier.
+        const int share = NT / split;
+        const bool live = first < total;
+        const int q = warp & 3;
+        bool go = true;
+        if (warp >= 4 && live) {
+            go = mbar_wait(bar(TFULL), 0u, abort_flag);
+            go = __all_sync(0xffffffffu, go);
+            if (!go) report_error(st, -4, kSiteFp4Epilogue);
+        }
+        cluster_sync_all();
+        if (warp >= 4 && live && go) {
+            tc_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16);
+            const uint32_t mine = base + (uint32_t)(rank * share * 128 + q * 32 + lane) * 4u;
+#pragma unroll 1
+            for (int j0 = 0; j0 < NT; j0 += 32) {
+                uint32_t r[32];
+                tmem_ld32(taddr + (uint32_t)j0, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const int to = (j0 + j) / share, at = (j0 + j) - to * share;
+                    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(peer_addr(mine + (uint32_t)at * 512u, (uint32_t)to)),
+                                 "r"(r[j])
+                                 : "memory");
+                }
+            }
+            tc_fence_before();
+        }
+        cluster_sync_all();
+        if (warp >= 4 && live && go) {
+            const Fp4Tile tile = fp4_tile<NT>(g, prefix, first);
+            const float alpha = (g.ga ? *g.ga : 1.0f) * (g.gb ? g.gb[tile.expert] : 1.0f);
+            const int n = tile.nb * 128 + q * 32 + lane;
+            const float* part = reinterpret_cast<const float*>(gbase) + q * 32 + lane;
+            for (int at = 0; at < share; ++at) {
+                const int j = (int)rank * share + at;
+                if (j >= tile.rows || n >= g.N) break;
+                float sum = 0.0f;
+                for (int s = 0; s < split; ++s) sum += part[(s * share + at) * 128];
+                static_cast<TC*>(g.C)[(tile.row0 + j) * (int64_t)g.N + n] = (TC)(alpha * sum);
+            }
         }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, 256);
     }
 }
 
@@ -400,19 +908,116 @@ static int code_map(CUtensorMap* map, const Fp4& q, int box_rows) {
     return 0;
 }
 
-template <bool NV, int BN, typename TC>
+// The scales of all matrices as rows of 64-bit words, one row tile a row; what lies past the last k tile reads as zeros.
+static int scale_map(CUtensorMap* map, const Fp4& q) {
+    EncodeTiledFn fn = fp4_encode_fn();
+    if (!fn) return set_error(-3, "cuTensorMapEncodeTiled entry point unavailable");
+    cuuint64_t dims[2] = {(cuuint64_t)q.k_tiles() * 64, (cuuint64_t)q.row_tiles() * (cuuint64_t)q.count};
+    cuuint64_t strides[1] = {(cuuint64_t)q.k_tiles() * 512};
+    cuuint32_t box[2] = {q.nv ? 256u : 128u, 1};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, q.scales, dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return set_error(-3, "cuTensorMapEncodeTiled (4-bit scales) failed");
+    return 0;
+}
+
+template <typename K>
+static cudaError_t allow_smem(K kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <bool NV, typename TC>
 static cudaError_t fp4_attr() {
-    return cudaFuncSetAttribute(fp4_gemm_kernel<NV, BN, TC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Fp4Cfg<NV, BN>::kSmem);
+    cudaError_t e = allow_smem(fp4_gemm_pair_kernel<NV, 1, TC>, Fp4PairCfg<NV, 1, TC>::kSmem);
+    if (e == cudaSuccess) e = allow_smem(fp4_gemm_pair_kernel<NV, 2, TC>, Fp4PairCfg<NV, 2, TC>::kSmem);
+    if (e == cudaSuccess) e = allow_smem(fp4_gemm_rows_kernel<NV, 32, TC>, Fp4RowsCfg<NV, 32>::kSmem);
+    if (e == cudaSuccess) e = allow_smem(fp4_gemm_rows_kernel<NV, 64, TC>, Fp4RowsCfg<NV, 64>::kSmem);
+    if (e == cudaSuccess) e = allow_smem(fp4_gemm_rows_kernel<NV, 128, TC>, Fp4RowsCfg<NV, 128>::kSmem);
+    return e;
 }
 
 int fp4_gemm_init_device() {
-    cudaError_t e = fp4_attr<false, 128, float>();
-    if (e == cudaSuccess) e = fp4_attr<false, 128, __nv_bfloat16>();
-    if (e == cudaSuccess) e = fp4_attr<true, 128, float>();
-    if (e == cudaSuccess) e = fp4_attr<true, 128, __nv_bfloat16>();
+    cudaError_t e = fp4_attr<false, float>();
+    if (e == cudaSuccess) e = fp4_attr<false, __nv_bfloat16>();
+    if (e == cudaSuccess) e = fp4_attr<true, float>();
+    if (e == cudaSuccess) e = fp4_attr<true, __nv_bfloat16>();
     if (e != cudaSuccess) return set_cuda_error(e, "cudaFuncSetAttribute(4-bit gemm)");
     return 0;
+}
+
+// How a product runs: rows of A in a tile (512 or 256 on two SMs; 128, 64 or 32
+// with the roles swapped), and over how many CTAs a tile's K is split.
+struct Fp4Plan {
+    int rows, cols, split, ctas;
+};
+
+static Fp4Plan fp4_plan(int64_t M, int64_t N, int64_t K, int experts, bool grouped, int cap, int sms) {
+    Fp4Plan p{};
+    const int64_t kb = (K + kFK - 1) / kFK;
+    auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    // rows an expert has on average, were they dealt evenly
+    const int64_t per = grouped ? up(M, experts) : M;
+    if (cap >= 2 && per > 128) {
+        // Cycles of the busiest pair, as measured: a stage of 256 columns takes 1070
+        // with 512 rows and 660 with 256; 512 rows end a tile with 1500 unhidden.
+        const int64_t pairs = cap / 2, n = up(N, kPN);
+        const int64_t t2 = up(up(M, 512) * n, pairs) * (kb * 1070 + 1500);
+        const int64_t t1 = up(up(M, 256) * n, pairs) * (kb * 660 + 300) + 1500;
+        p.rows = !grouped && t2 < t1 ? 512 : 256;
+        p.cols = kPN;
+        p.split = 1;
+        const int64_t tiles = (up(M, p.rows) + (grouped ? experts : 0)) * n;
+        p.ctas = 2 * (int)(tiles < pairs ? tiles : pairs);
+        return p;
+    }
+    p.rows = grouped ? 64 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
+    p.cols = 128;
+    const int64_t n = up(N, 128);
+    // An expert with any row has whole scale tiles to itself, so busy experts are at
+    // most M / 128 and tiles of 64 rows at most M / 64.
+    const int64_t tiles = up(M, p.rows) * n;
+    const int64_t busy = grouped ? (experts < up(M, kTileRows) ? experts : up(M, kTileRows)) * n : tiles;
+    // A budget below the whole machine is kept to the letter: one CTA for each SM of it.
+    const int64_t slots = cap < sms ? cap : 2 * (int64_t)cap;
+    p.split = 1;
+    while (p.split < 8 && busy * p.split * 2 <= slots && kb >= 4 * p.split && !(grouped && cap < sms)) p.split *= 2;
+    p.ctas = p.split > 1 ? (int)(tiles * p.split) : (int)(grouped || slots < tiles ? slots : tiles);
+    return p;
+}
+
+template <bool NV, int MSUB, typename TC>
+static cudaError_t go_pair(const Fp4Plan& p, const CUtensorMap* m, const Fp4GemmArgs& g, cudaStream_t s, DevStatus* st) {
+    fp4_gemm_pair_kernel<NV, MSUB, TC><<<p.ctas, kPThreads, Fp4PairCfg<NV, MSUB, TC>::kSmem, s>>>(m[0], m[1], m[2], m[3], g, st);
+    return cudaGetLastError();
+}
+
+template <bool NV, int NT, typename TC>
+static cudaError_t go_rows(const Fp4Plan& p, const CUtensorMap* m, const Fp4GemmArgs& g, cudaStream_t s, DevStatus* st) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)p.ctas);
+    c.blockDim = dim3(kRThreads);
+    c.dynamicSmemBytes = Fp4RowsCfg<NV, NT>::kSmem;
+    c.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)p.split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    c.attrs = &attr;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, fp4_gemm_rows_kernel<NV, NT, TC>, m[0], m[1], m[2], m[3], g, p.split, st);
+}
+
+template <bool NV, typename TC>
+static cudaError_t go_any(const Fp4Plan& p, const CUtensorMap* m, const Fp4GemmArgs& g, cudaStream_t s, DevStatus* st) {
+    switch (p.rows) {
+        case 512: return go_pair<NV, 2, TC>(p, m, g, s, st);
+        case 256: return go_pair<NV, 1, TC>(p, m, g, s, st);
+        case 128: return go_rows<NV, 128, TC>(p, m, g, s, st);
+        case 64: return go_rows<NV, 64, TC>(p, m, g, s, st);
+        default: return go_rows<NV, 32, TC>(p, m, g, s, st);
+    }
 }
 
 int fp4_gemm_launch(const Fp4& a, const Fp4& b, const int32_t* offsets, const int32_t* counts, void* C, int bf16,
@@ -421,10 +1026,8 @@ int fp4_gemm_launch(const Fp4& a, const Fp4& b, const int32_t* offsets, const in
     if (!ds) return -3;
     if (take_fault(kFaultGemmLaunch)) return set_error(-3, "injected failure: GEMM launch");
     const int cap = (sm_budget <= 0 || sm_budget > ds->sm_count) ? ds->sm_count : sm_budget;
-    constexpr int BN = 128;
+    const Fp4Plan p = fp4_plan(a.rows, b.rows, a.cols, b.count, offsets != nullptr, cap, ds->sm_count);
     Fp4GemmArgs g;
-    g.sfa = a.scales;
-    g.sfb = b.scales;
     g.ga = a.tensor_scale;
     g.gb = b.tensor_scale;
     g.offsets = offsets;
@@ -434,26 +1037,24 @@ int fp4_gemm_launch(const Fp4& a, const Fp4& b, const int32_t* offsets, const in
     g.N = (int)b.rows;
     g.K = (int)a.cols;
     g.experts = b.count;
-    g.k_tiles = (int)a.k_tiles();
     g.b_row_tiles = (int)b.row_tiles();
-    g.num_m = (int)((a.rows + kFM - 1) / kFM);
-    g.num_n = (int)((b.rows + BN - 1) / BN);
+    g.num_m = (int)((a.rows + p.rows - 1) / p.rows);
+    g.num_n = (int)((b.rows + p.cols - 1) / p.cols);
     g.num_kb = (int)((a.cols + kFK - 1) / kFK);
-    const int64_t tiles = (int64_t)g.num_m * g.num_n;  // an upper bound for experts
-    if (tiles > 0x7FFFFFFF) return set_error(-5, "4-bit product has more than 2^31 tiles");
-    const int grid = (int)(tiles < cap ? tiles : cap);
-    CUtensorMap ma, mb;
-    int rc = code_map(&ma, a, kFM);
-    if (rc) return rc;
-    if ((rc = code_map(&mb, b, BN))) return rc;
-#define C3_GO(NV_, T_) fp4_gemm_kernel<NV_, BN, T_><<<grid, kFThreads, Fp4Cfg<NV_, BN>::kSmem, s>>>(ma, mb, g, st)
-    if (a.nv && bf16) C3_GO(true, __nv_bfloat16);
-    else if (a.nv) C3_GO(true, float);
-    else if (bf16) C3_GO(false, __nv_bfloat16);
-    else C3_GO(false, float);
-#undef C3_GO
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return set_cuda_error(e, "4-bit gemm kernel launch");
+    // For experts a bound: each may end inside a tile.
+    if (((int64_t)g.num_m + (offsets ? b.count : 0)) * g.num_n * p.split > 0x7FFFFFFF)
+        return set_error(-5, "4-bit product has more than 2^31 tiles");
+    const bool pair = p.rows > 128;
+    CUtensorMap m[4];
+    int rc = code_map(&m[0], a, pair ? kFM : p.rows);
+    if (rc || (rc = code_map(&m[1], b, pair ? kPN / 2 : 128)) || (rc = scale_map(&m[2], a)) || (rc = scale_map(&m[3], b)))
+        return rc;
+    const cudaError_t e = a.nv ? (bf16 ? go_any<true, __nv_bfloat16>(p, m, g, s, st) : go_any<true, float>(p, m, g, s, st))
+                               : (bf16 ? go_any<false, __nv_bfloat16>(p, m, g, s, st) : go_any<false, float>(p, m, g, s, st));
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return set_cuda_error(e, "4-bit gemm kernel launch");
+    }
     count_launch();
     return 0;
 }

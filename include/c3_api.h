@@ -707,8 +707,8 @@ int c3_fp4_gemm(const c3_fp4 *a, const c3_fp4 *b, void *C, int c_type, int sm_bu
  * The experts' products: row r of expert e, offsets[e] <= r < offsets[e] +
  * counts[e] (device, as c3_moe_order writes them), becomes
  *   C[r][n] = sum_k x[r][k] * w[e][n][k]
- * with w->count experts (1..1024).  Rows of C that no expert has are left as
- * they were.  An expert whose offset is no multiple of 128, or whose rows do
+ * with w->count experts (1..1024), whose rows do not overlap.  Rows of C that
+ * no expert has are left as they were.  An expert whose offset is no multiple of 128, or whose rows do
  * not lie within x, is skipped.
  */
 int c3_fp4_gemm_experts(const c3_fp4 *x, const c3_fp4 *w, const int32_t *offsets,
