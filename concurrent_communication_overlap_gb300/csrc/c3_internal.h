@@ -239,6 +239,7 @@ int fp4_dequantize_launch(const Fp4& q, void* x, int bf16, int64_t ld, cudaStrea
 int fp4_gemm_launch(const Fp4& a, const Fp4& b, const int32_t* offsets, const int32_t* counts, void* C, int bf16,
                     int sm_budget, cudaStream_t s, DevStatus* st);
 int fp4_gemm_init_device();
+int order_init_device();
 
 int status_reset_launch(DevStatus* st, cudaStream_t s);
 int selftest_wait_launch(DevStatus* st, unsigned long long limit_ns, int arrive, cudaStream_t s);

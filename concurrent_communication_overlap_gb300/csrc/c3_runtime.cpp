@@ -95,6 +95,8 @@ static int init_device(DeviceState& ds, int dev) {
     if (rc) return rc;
     rc = fp4_gemm_init_device();
     if (rc) return rc;
+    rc = order_init_device();
+    if (rc) return rc;
     ds.ready = true;
     return 0;
 }

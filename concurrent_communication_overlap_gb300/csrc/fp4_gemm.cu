@@ -957,8 +957,9 @@ static Fp4Plan fp4_plan(int64_t M, int64_t N, int64_t K, int experts, bool group
     Fp4Plan p{};
     const int64_t kb = (K + kFK - 1) / kFK;
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    // rows an expert has on average, were they dealt evenly
-    const int64_t per = grouped ? up(M, experts) : M;
+    // Rows an expert has on average: the buffer's, less the padding that it has room for (c3_moe_rows).
+    const int64_t pad = (int64_t)(kTileRows - 1) * experts;
+    const int64_t per = !grouped ? M : M > pad ? (M - pad) / experts : 0;
     if (cap >= 2 && per > 128) {
         // Cycles of the busiest pair, as measured: a stage of 256 columns takes 1070
         // with 512 rows and 660 with 256; 512 rows end a tile with 1500 unhidden.

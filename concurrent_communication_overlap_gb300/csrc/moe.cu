@@ -9,19 +9,22 @@
 namespace c3 {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kOrderThreads = 256;
-constexpr int kOrderWarps = kOrderThreads / 32;
-constexpr int kOrderChunk = 4096;       // choices of one CTA: each warp takes a consecutive eighth
 constexpr int kMaxExperts = 1024;
 
 // ---------------------------------------------------------------- order
 //
 // A stable counting sort of the choices by expert.  A choice's row is
-//   offsets[e] + (choices of e before it),
-// the sum of three counts: of the CTAs before, of the warps before in this CTA,
-// and of the choices before in this warp.  The first kernel counts per CTA, the
-// second adds up and places.  No atomics on global memory: the rows do not
-// depend on the order in which CTAs run.
+//   start[e] + (choices of e before its CTA's) + (before its warp's) + (before it in its warp),
+// whole-number sums, so that the rows do not depend on the order in which CTAs or
+// atomics run.
+//
+// Up to kOneLaunch choices, one launch: every CTA counts all choices itself (64 a
+// thread at most, from L2) and places 1024 of them, one a thread.  Above, counting
+// again in every CTA would cost more than two small launches: one that counts each
+// CTA's 4096 choices, one that adds the counts up along the CTAs.
+constexpr int kOrderThreads = 1024;
+constexpr int kOrderWarps = kOrderThreads / 32;
+constexpr int64_t kOneLaunch = 65536;
 
 __device__ __forceinline__ int choice_expert(const int32_t* idx, int64_t i, int64_t n, int experts) {
     if (i >= n) return -1;
@@ -29,124 +32,134 @@ __device__ __forceinline__ int choice_expert(const int32_t* idx, int64_t i, int6
     return (e >= 0 && e < experts) ? e : -1;
 }
 
-// Counts of the CTA's choices: hist[warp][e] in shared memory, one counter set a warp.
-__device__ __forceinline__ void count_chunk(const int32_t* __restrict__ idx, int64_t n, int experts, int64_t first,
-                                            int* hist) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < kOrderWarps * experts; i += kOrderThreads) hist[i] = 0;
+// Counts of choices [first, first + per_cta) of each CTA.
+__global__ void __launch_bounds__(kOrderThreads)
+    order_count_kernel(const int32_t* __restrict__ idx, int64_t n, int experts, int per_cta, int* __restrict__ counts) {
+    __shared__ int c[kMaxExperts];
+    for (int e = threadIdx.x; e < experts; e += kOrderThreads) c[e] = 0;
     __syncthreads();
-    const int64_t at = first + (int64_t)warp * (kOrderChunk / kOrderWarps);
-    for (int j = 0; j < kOrderChunk / kOrderWarps; j += 32) {
-        if (at + j >= n) break;
-        const int e = choice_expert(idx, at + j + lane, n, experts);
-        const unsigned same = __match_any_sync(kAll, e);
-        if (e >= 0 && (same & ((1u << lane) - 1)) == 0) hist[warp * experts + e] += __popc(same);
-        __syncwarp();
+    const int64_t first = (int64_t)blockIdx.x * per_cta;
+    for (int i = threadIdx.x; i < per_cta; i += kOrderThreads) {
+        const int e = choice_expert(idx, first + i, n, experts);
+        if (e >= 0) atomicAdd(&c[e], 1);
     }
     __syncthreads();
+    for (int e = threadIdx.x; e < experts; e += kOrderThreads) counts[(size_t)blockIdx.x * experts + e] = c[e];
 }
 
-__global__ void __launch_bounds__(kOrderThreads)
-    order_count_kernel(const int32_t* __restrict__ idx, int64_t n, int experts, int* __restrict__ per_cta) {
-    extern __shared__ int hist[];
-    count_chunk(idx, n, experts, (int64_t)blockIdx.x * kOrderChunk, hist);
-    for (int e = threadIdx.x; e < experts; e += kOrderThreads) {
-        int c = 0;
-        for (int w = 0; w < kOrderWarps; ++w) c += hist[w * experts + e];
-        per_cta[(size_t)blockIdx.x * experts + e] = c;
+// counts[cta][e] to the sum over the CTAs before, and the sum over all behind the last; a warp an expert.
+__global__ void __launch_bounds__(256) order_sum_kernel(int* __restrict__ counts, int ctas, int experts) {
+    const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (e >= experts) return;
+    int run = 0;
+    for (int b0 = 0; b0 < ctas; b0 += 32) {
+        const int c = b0 + lane < ctas ? counts[(size_t)(b0 + lane) * experts + e] : 0;
+        int incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kAll, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (b0 + lane < ctas) counts[(size_t)(b0 + lane) * experts + e] = run + incl - c;
+        run += __shfl_sync(kAll, incl, 31);
     }
+    if (lane == 0) counts[(size_t)ctas * experts + e] = run;
 }
 
+// sums: order_sum_kernel's, or NULL where every CTA counts for itself.
 __global__ void __launch_bounds__(kOrderThreads)
-    order_place_kernel(const int32_t* __restrict__ idx, int64_t n, int topk, int experts,
-                       const int* __restrict__ per_cta, int32_t* __restrict__ slot, int32_t* __restrict__ row_of,
+    order_place_kernel(const int32_t* __restrict__ idx, int64_t n, int topk, int experts, int per_cta, int place_ctas,
+                       const int* __restrict__ sums, int32_t* __restrict__ slot, int32_t* __restrict__ row_of,
                        int64_t rows, int32_t* __restrict__ offsets, int32_t* __restrict__ counts) {
-    extern __shared__ int hist[];            // [warps][experts], then total[experts], start[experts + 1]
-    int* total = hist + kOrderWarps * experts;
-    int* start = total + experts;
+    extern __shared__ int shared[];
+    int* total = shared;              // [experts] choices of each expert
+    int* before = total + experts;    // [experts] those of the CTAs before
+    int* start = before + experts;    // [experts + 1] first row
+    int* hist = start + experts + 1;  // [warps][experts] of this CTA
     __shared__ int warp_sums[kOrderWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t first = (int64_t)blockIdx.x * kOrderChunk;
-    count_chunk(idx, n, experts, first, hist);
-    // The choices of each expert in the CTAs before this one, and in all.
+    const int64_t first = (int64_t)blockIdx.x * per_cta;
+    const bool places = (int)blockIdx.x < place_ctas;
     for (int e = threadIdx.x; e < experts; e += kOrderThreads) {
-        int before = 0, all = 0;
-        if (gridDim.x == 1) {
-            for (int w = 0; w < kOrderWarps; ++w) all += hist[w * experts + e];
-        } else {
-            for (unsigned b = 0; b < gridDim.x; ++b) {
-                const int c = __ldg(per_cta + (size_t)b * experts + e);
-                if (b < blockIdx.x) before += c;
-                all += c;
+        total[e] = sums ? sums[(size_t)place_ctas * experts + e] : 0;
+        before[e] = sums && places ? sums[(size_t)blockIdx.x * experts + e] : 0;
+    }
+    if (places)
+        for (int i = threadIdx.x; i < kOrderWarps * experts; i += kOrderThreads) hist[i] = 0;
+    __syncthreads();
+    if (!sums)
+        for (int64_t i = threadIdx.x; i < n; i += kOrderThreads) {
+            const int e = choice_expert(idx, i, n, experts);
+            if (e >= 0) {
+                atomicAdd(&total[e], 1);
+                if (i < first) atomicAdd(&before[e], 1);
             }
         }
-        total[e] = all;
-        // hist becomes the count before each warp's choices
-        int run = before;
-        for (int w = 0; w < kOrderWarps; ++w) {
-            const int c = hist[w * experts + e];
-            hist[w * experts + e] = run;
-            run += c;
+    // A warp's choices are consecutive: counted first, so that each warp knows what lies before it.
+    const int per_warp = per_cta / kOrderWarps;
+    const int64_t mine = first + (int64_t)warp * per_warp;
+    if (places)
+        for (int j = 0; j < per_warp; j += 32) {
+            const int e = choice_expert(idx, mine + j + lane, n, experts);
+            const unsigned same = __match_any_sync(kAll, e);
+            if (e >= 0 && (same & ((1u << lane) - 1)) == 0) hist[warp * experts + e] += __popc(same);
+            __syncwarp();
         }
-    }
     __syncthreads();
-    // Each expert's first row: an exclusive sum of the counts rounded up to whole tiles.
-    constexpr int kPer = kMaxExperts / kOrderThreads;
-    int mine[kPer], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x * kPer + i;
-        mine[i] = e < experts ? (total[e] + kTileRows - 1) / kTileRows * kTileRows : 0;
-        sum += mine[i];
-    }
-    int incl = sum;
+    // Each expert's first row: an exclusive sum of the counts rounded up to whole tiles, a thread an expert.
+    static_assert(kMaxExperts <= kOrderThreads, "a thread an expert");
+    const int up = (int)threadIdx.x < experts ? (total[threadIdx.x] + kTileRows - 1) / kTileRows * kTileRows : 0;
+    int incl = up;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(kAll, incl, o);
         if (lane >= o) incl += v;
     }
     if (lane == 31) warp_sums[warp] = incl;
-    __syncthreads();
-    int base = incl - sum;
-    for (int w = 0; w < warp; ++w) base += warp_sums[w];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x * kPer + i;
-        if (e < experts) start[e] = base;
-        base += mine[i];
-        if (e == experts - 1) start[experts] = base;
-    }
-    __syncthreads();
-    if (blockIdx.x == 0)
-        for (int e = threadIdx.x; e <= experts; e += kOrderThreads) {
-            offsets[e] = start[e];
-            if (e < experts) counts[e] = total[e];
-        }
-    // The rows of this CTA's choices.
-    const int64_t at = first + (int64_t)warp * (kOrderChunk / kOrderWarps);
-    for (int j = 0; j < kOrderChunk / kOrderWarps; j += 32) {
-        if (at + j >= n) break;
-        const int64_t i = at + j + lane;
-        const int e = choice_expert(idx, i, n, experts);
-        const unsigned same = __match_any_sync(kAll, e);
-        int row = -1;
-        if (e >= 0) row = start[e] + hist[warp * experts + e] + __popc(same & ((1u << lane) - 1));
-        __syncwarp();
-        if (e >= 0 && (same & ((1u << lane) - 1)) == 0) hist[warp * experts + e] += __popc(same);
-        __syncwarp();
-        if (i < n) {
-            slot[i] = row;
-            if (row >= 0) row_of[row] = (int32_t)(i / topk);
+    if (places && (int)threadIdx.x < experts) {
+        int run = before[threadIdx.x];
+        for (int w = 0; w < kOrderWarps; ++w) {
+            const int c = hist[w * experts + threadIdx.x];
+            hist[w * experts + threadIdx.x] = run;
+            run += c;
         }
     }
-    // Rows that no choice takes: each expert's last tile, and what is left of the buffer.
-    for (int e = blockIdx.x; e < experts; e += gridDim.x) {
-        const int from = start[e] + total[e], to = start[e + 1];
-        for (int r = from + (int)threadIdx.x; r < to; r += kOrderThreads) row_of[r] = -1;
+    __syncthreads();
+    const int lower = lane < warp ? warp_sums[lane] : 0;
+    const int base = __reduce_add_sync(kAll, lower) + incl - up;
+    if ((int)threadIdx.x < experts) start[threadIdx.x] = base;
+    if ((int)threadIdx.x == experts - 1) start[experts] = base + up;
+    __syncthreads();
+    if (blockIdx.x == 0 && (int)threadIdx.x < experts) {
+        offsets[threadIdx.x] = base;
+        counts[threadIdx.x] = total[threadIdx.x];
+        if ((int)threadIdx.x == experts - 1) offsets[experts] = base + up;
     }
-    for (int64_t r = start[experts] + (int64_t)blockIdx.x * kOrderThreads + threadIdx.x; r < rows;
-         r += (int64_t)gridDim.x * kOrderThreads)
-        row_of[r] = -1;
+    if (places)
+        for (int j = 0; j < per_warp; j += 32) {
+            const int64_t i = mine + j + lane;
+            const int e = choice_expert(idx, i, n, experts);
+            const unsigned same = __match_any_sync(kAll, e);
+            int row = -1;
+            if (e >= 0) row = start[e] + hist[warp * experts + e] + __popc(same & ((1u << lane) - 1));
+            __syncwarp();
+            if (e >= 0 && (same & ((1u << lane) - 1)) == 0) hist[warp * experts + e] += __popc(same);
+            __syncwarp();
+            if (i < n) {
+                slot[i] = row;
+                if (row >= 0) row_of[row] = (int32_t)((unsigned)i / (unsigned)topk);
+            }
+        }
+    // Rows that no choice takes: past an expert's count in its last tile, and past the last expert.
+    for (int64_t r = (int64_t)blockIdx.x * kOrderThreads + threadIdx.x; r < rows; r += (int64_t)gridDim.x * kOrderThreads) {
+        int lo = 0, hi = experts;  // the last expert that starts at r or before
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (start[mid] <= r) lo = mid;
+            else hi = mid;
+        }
+        if (r >= start[lo] + (int64_t)total[lo]) row_of[r] = -1;
+    }
 }
 
 int64_t order_rows(int64_t tokens, int topk, int experts) {
@@ -155,28 +168,45 @@ int64_t order_rows(int64_t tokens, int topk, int experts) {
     return (n + (kTileRows - 1) * busy) / kTileRows * kTileRows;
 }
 
-static int64_t order_ctas(int64_t n) { return (n + kOrderChunk - 1) / kOrderChunk; }
+static int order_per_cta(int64_t n) { return n <= kOneLaunch ? kOrderThreads : 4 * kOrderThreads; }
 
 size_t order_bytes(int64_t tokens, int topk, int experts) {
-    return (size_t)order_ctas(tokens * topk) * (size_t)experts * sizeof(int);
+    const int64_t n = tokens * topk;
+    if (n <= kOneLaunch) return sizeof(int);
+    return (size_t)((n + order_per_cta(n) - 1) / order_per_cta(n) + 1) * (size_t)experts * sizeof(int);
+}
+
+int order_init_device() {
+    cudaError_t e = cudaFuncSetAttribute(order_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(int) * ((kOrderWarps + 3) * kMaxExperts + 1));
+    return e == cudaSuccess ? 0 : set_cuda_error(e, "cudaFuncSetAttribute(order)");
 }
 
 int order_launch(const int32_t* idx, int64_t tokens, int topk, int experts, int32_t* slot, int32_t* row_of,
                  int64_t rows, int32_t* offsets, int32_t* counts, void* work, cudaStream_t s) {
+    DeviceState* ds = device_state();
+    if (!ds) return -3;
     const int64_t n = tokens * topk;
-    const int ctas = n ? (int)order_ctas(n) : 1;
-    const size_t smem = sizeof(int) * (size_t)experts * (kOrderWarps + 2) + sizeof(int);
-    if (ctas > 1) {
-        order_count_kernel<<<ctas, kOrderThreads, sizeof(int) * (size_t)experts * kOrderWarps, s>>>(
-            idx, n, experts, static_cast<int*>(work));
-        cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return set_cuda_error(e, "order count kernel launch");
+    const int per = order_per_cta(n);
+    const int place = (int)((n + per - 1) / per);
+    int* sums = n <= kOneLaunch ? nullptr : static_cast<int*>(work);
+    cudaError_t e;
+    if (sums) {
+        order_count_kernel<<<place, kOrderThreads, 0, s>>>(idx, n, experts, per, sums);
+        if ((e = cudaGetLastError()) != cudaSuccess) return set_cuda_error(e, "order count kernel launch");
+        count_launch();
+        order_sum_kernel<<<(experts + 7) / 8, 256, 0, s>>>(sums, place, experts);
+        if ((e = cudaGetLastError()) != cudaSuccess) return set_cuda_error(e, "order sum kernel launch");
         count_launch();
     }
-    order_place_kernel<<<ctas, kOrderThreads, smem, s>>>(idx, n, topk, experts, static_cast<const int*>(work), slot,
-                                                         row_of, rows, offsets, counts);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return set_cuda_error(e, "order kernel launch");
+    // CTAs beyond those that place choices only help to mark unused rows
+    const int64_t fill = (rows + kOrderThreads - 1) / kOrderThreads;
+    const int64_t most = fill < 8 ? (fill > 0 ? fill : 1) : 8;
+    const int grid = place > most ? place : (int)most;
+    const size_t smem = sizeof(int) * ((size_t)(kOrderWarps + 3) * experts + 1);
+    order_place_kernel<<<grid, kOrderThreads, smem, s>>>(idx, n, topk, experts, per, place, sums, slot, row_of, rows,
+                                                         offsets, counts);
+    if ((e = cudaGetLastError()) != cudaSuccess) return set_cuda_error(e, "order kernel launch");
     count_launch();
     return 0;
 }
