@@ -161,33 +161,37 @@ __device__ __forceinline__ void expert_tiles(const Fp4GemmArgs& g, int* prefix, 
 
 // ---------------------------------------------------------------- two SMs on one tile
 //
-// The form for many rows.  A cluster of two CTAs shares one tile of MSUB x 256
-// rows by 192 columns (cta_group::2): each CTA brings in its 128 rows of A of
-// every 256, half of B's rows and all of the tile's scales of B, and holds the
-// accumulators of its own rows.  A 4-bit MMA at full rate eats its operands
-// four times as fast as a bf16 one, so what an SM has to take in per MMA cycle
-// decides: 128 x 128 tiles on one SM need 126 bytes a cycle, 256 x 192 on two
-// 78, 512 x 192 on two 61.  192 columns, because a tile's scales have to begin
-// at an even TMEM column (a multiple of 64 rows of B) and two accumulator sets
-// of 256 columns would leave TMEM no room for scales.
+// The form for many rows.  A cluster of two CTAs shares one tile (cta_group::2):
+// each CTA brings in half of A's rows, half of B's and all of the tile's scales of
+// B, and holds the accumulators of its own rows.  A 4-bit MMA at full rate eats
+// its operands four times as fast as a bf16 one, so what an SM has to take in per
+// MMA cycle decides: 128 x 128 tiles on one SM need 126 bytes a cycle, 256 x 192
+// on two 78, 512 x 192 or 256 x 384 on two 61.  Accumulators are 192 columns,
+// because a tile's scales have to begin at an even TMEM column (a multiple of 64
+// rows of B) and 2 x 256 columns would leave TMEM no room for scales; there are
+// two: one above the other (512 rows), side by side (384 columns), or in turn for
+// tiles of 256 x 192, whose read-out then hides behind the next tile.
 //
 // The leader (rank 0) issues every MMA.  Its full barriers count the bytes of
 // both CTAs' loads; a commit frees a stage, or publishes a tile, in both.  The
 // epilogue's eight warps in each CTA read 32 x 32 pieces out of TMEM one ahead,
 // turn them through 2 KB of shared memory each, and write whole 64-byte pieces
 // of rows.
-constexpr int kPN = 192;
+constexpr int kPN = 192;  // columns of one accumulator
 constexpr int kPThreads = 384;
 constexpr int kPEpiWarps = 8;
 
-template <bool NV, int MSUB, typename TC>
+template <bool NV, int MSUB, int NSUB, typename TC>
 struct Fp4PairCfg {
     static constexpr int kKT = NV ? 4 : 2;
+    static constexpr int kRows = MSUB * 256, kCols = NSUB * kPN;
     static constexpr int kBN2 = kPN / 2;
+    static constexpr int kSfbTiles = NSUB + 1;  // scale tiles that the columns lie in
+    static constexpr int kSub = MSUB * NSUB;    // accumulators of a tile
     static constexpr uint32_t kABytes = MSUB * kFM * 128;
-    static constexpr uint32_t kBBytes = kBN2 * 128;
+    static constexpr uint32_t kBBytes = NSUB * kBN2 * 128;
     static constexpr uint32_t kSfa = MSUB * kKT * 512;
-    static constexpr uint32_t kSfb = 2 * kKT * 512;   // 192 rows from a multiple of 64 on lie in two scale tiles
+    static constexpr uint32_t kSfb = kSfbTiles * kKT * 512;
     static constexpr uint32_t kStage = kABytes + kBBytes + kSfa + kSfb;
     static constexpr uint32_t kStaging = kPEpiWarps * 2048;
     // 512 rows: one matrix only
@@ -195,8 +199,8 @@ struct Fp4PairCfg {
     static constexpr int kFit = (kFSmemLimit - kExtra) / (int)kStage;
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kSmem = kStages * (int)kStage + kExtra;
-    static constexpr int kAccBufs = MSUB == 2 ? 1 : 2;
-    static constexpr int kSetCols = (MSUB + 2) * 4;   // TMEM columns of one k tile's scales
+    static constexpr int kAccBufs = kSub == 2 ? 1 : 2;
+    static constexpr int kSetCols = (MSUB + kSfbTiles) * 4;   // TMEM columns of one k tile's scales
     static_assert(kStage % 1024 == 0, "the codes need 1024-byte alignment");
     static constexpr int kSets = NV ? 2 : 4;          // stages whose scales TMEM holds
     static_assert(kStages >= kSets && 2 * kPN + kSets * kKT * kSetCols <= 512, "pair configuration");
@@ -314,14 +318,14 @@ __device__ __forceinline__ void store_piece(const uint32_t* v, uint32_t blk, int
 }
 
 // tmA, tmB: codes; tmSA, tmSB: scales as [row tiles][k tiles * 64] 64-bit words.
-template <bool NV, int MSUB, typename TC>
+template <bool NV, int MSUB, int NSUB, typename TC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                          Fp4GemmArgs g, DevStatus* st) {
-    using Cfg = Fp4PairCfg<NV, MSUB, TC>;
+    using Cfg = Fp4PairCfg<NV, MSUB, NSUB, TC>;
     constexpr int S = Cfg::kStages, KT = Cfg::kKT, NB = Cfg::kAccBufs;
-    constexpr int kRows = 256 * MSUB;
+    constexpr int kRows = Cfg::kRows;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -378,8 +382,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             bool ok = true;
             for (int t = first; ok && t < total; t += step) {
                 const Fp4Tile tile = fp4_tile<kRows>(g, prefix, t);
-                const int arow = (int)tile.row0 + (int)rank * 128;
-                const int n0 = tile.nb * kPN;
+                const int arow = (int)tile.row0 + (int)rank * (kRows / 2);
+                const int n0 = tile.nb * Cfg::kCols;
                 const int brow = tile.expert * g.N + n0 + (int)rank * Cfg::kBN2;
                 const int sbrow = tile.expert * g.b_row_tiles + n0 / 128;
                 for (int kb = 0; kb < g.num_kb; ++kb) {
@@ -392,16 +396,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                     const uint32_t full = leader_addr(bar(stage));
                     const uint32_t sf = sb + Cfg::kABytes + Cfg::kBBytes;
                     if (rank == 0) mbar_arrive_expect_tx(bar(stage), 2 * Cfg::kStage);
+                    tma_load_2d_pair(sf, &tmSA, full, kb * KT * 64, arow / 128, pol_a);
+                    tma_load_2d_pair(sf + Cfg::kSfa, &tmSB, full, kb * KT * 64, sbrow, pol_b);
+                    tma_load_2d_pair(sb, &tmA, full, kb * 128, arow, pol_a);
 #pragma unroll
-                    for (int i = 0; i < MSUB; ++i)
-                        tma_load_2d_pair(sf + (uint32_t)i * KT * 512u, &tmSA, full, kb * KT * 64, arow / 128 + i * 2, pol_a);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        tma_load_2d_pair(sf + Cfg::kSfa + (uint32_t)i * KT * 512u, &tmSB, full, kb * KT * 64, sbrow + i, pol_b);
-#pragma unroll
-                    for (int i = 0; i < MSUB; ++i)
-                        tma_load_2d_pair(sb + (uint32_t)i * kFM * 128u, &tmA, full, kb * 128, arow + i * 256, pol_a);
-                    tma_load_2d_pair(sb + Cfg::kABytes, &tmB, full, kb * 128, brow, pol_b);
+                    for (int j = 0; j < NSUB; ++j)
+                        tma_load_2d_pair(sb + Cfg::kABytes + (uint32_t)j * Cfg::kBN2 * 128u, &tmB, full, kb * 128, brow + j * kPN, pol_b);
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
@@ -425,8 +425,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             uint32_t phase = 0;
             bool ok = true;
             for (int t = first; ok && t < total; t += step, ++local) {
-                // odd tiles begin at row 64 of a scale tile: two columns
-                const uint32_t shift = (uint32_t)(fp4_tile<kRows>(g, prefix, t).nb & 1) * 2u;
+                // 192 columns: odd tiles begin at row 64 of a scale tile, two TMEM columns on
+                const uint32_t shift = NSUB == 2 ? 0u : (uint32_t)(fp4_tile<kRows>(g, prefix, t).nb & 1) * 2u;
                 const int buf = local % NB;
                 if (!mbar_wait_cluster(bar(TEMPTY + buf), ((uint32_t)(local / NB) & 1u) ^ 1u, abort_flag)) {
                     report_error(st, -4, kSiteFp4Mma);
@@ -452,9 +452,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                         const uint32_t id = NV ? 0u : (uint32_t)(k & 1) * 2u;
 #pragma unroll
                         for (int i = 0; i < MSUB; ++i)
-                            mma_fp4<2, NV>(go, d + (uint32_t)(i * kPN), ad + (uint64_t)(i * (kFM * 128 >> 4) + 2 * k),
-                                             bd + (uint64_t)(2 * k), idesc | (id << 4) | (id << 29), tsf + (uint32_t)i * 4,
-                                             tsf + (uint32_t)MSUB * 4 + shift, k > 0 ? 1u : (uint32_t)(kb > 0));
+#pragma unroll
+                            for (int j = 0; j < NSUB; ++j)
+                                mma_fp4<2, NV>(go, d + (uint32_t)((i + j) * kPN), ad + (uint64_t)(i * (kFM * 128 >> 4) + 2 * k),
+                                               bd + (uint64_t)(j * (Cfg::kBN2 * 128 >> 4) + 2 * k), idesc | (id << 4) | (id << 29),
+                                               tsf + (uint32_t)i * 4, tsf + (uint32_t)(MSUB * 4 + j * (kPN / 32)) + shift,
+                                               k > 0 ? 1u : (uint32_t)(kb > 0));
                     }
                     commit_pair(lead, bar(S + stage));
                     set = set + 1 == Cfg::kSets ? 0 : set + 1;
@@ -493,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 #pragma unroll
                     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                        for (int i = 0; i < MSUB + 2; ++i)
+                        for (int i = 0; i < MSUB + Cfg::kSfbTiles; ++i)
                             copy_scales<2>(lead, to + (uint32_t)(kt * Cfg::kSetCols + i * 4),
                                                   from + (uint64_t)((i * KT + kt) * (512 >> 4)));
                     commit_local<2>(lead, bar(SREADY + stage));
@@ -524,14 +527,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             }
             tc_fence_after();
             const float alpha = ga * (g.gb ? g.gb[tile.expert] : 1.0f);
-            // This warp's columns: with two row blocks all of one block's, else half of them.
-            constexpr int kPieces = kPN / 32 / (MSUB == 2 ? 1 : 2);
+            // This warp's columns: all of one accumulator's where there are two, else half.
+            constexpr int kPieces = kPN / 32 / (Cfg::kSub == 2 ? 1 : 2);
             constexpr int kWords = 8 * sizeof(TC);
             constexpr int kBatch = kPieces * kWords <= 96 ? kPieces : 96 / kWords;
-            const int sub = MSUB == 2 ? half : 0;
-            const int r0 = sub * 256 + (int)rank * 128 + q * 32;  // the warp's first row in the tile
-            const int c0 = MSUB == 2 ? 0 : half * kPieces * 32;
-            const int rows = tile.rows - r0, col0 = tile.nb * kPN + c0;
+            const int sub = Cfg::kSub == 2 ? half : 0;
+            const int r0 = (int)rank * (kRows / 2) + (MSUB == 2 ? sub * 128 : 0) + q * 32;  // the warp's first row in the tile
+            const int c0 = Cfg::kSub == 2 ? 0 : half * kPieces * 32;
+            const int rows = tile.rows - r0, col0 = tile.nb * Cfg::kCols + (NSUB == 2 ? sub * kPN : 0) + c0;
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((buf + sub) * kPN + c0);
             // Read out and rounded first: the accumulator is free again before anything is stored.
 #pragma unroll
@@ -909,12 +912,12 @@ static int code_map(CUtensorMap* map, const Fp4& q, int box_rows) {
 }
 
 // The scales of all matrices as rows of 64-bit words, one row tile a row; what lies past the last k tile reads as zeros.
-static int scale_map(CUtensorMap* map, const Fp4& q) {
+static int scale_map(CUtensorMap* map, const Fp4& q, int box_rows) {
     EncodeTiledFn fn = fp4_encode_fn();
     if (!fn) return set_error(-3, "cuTensorMapEncodeTiled entry point unavailable");
     cuuint64_t dims[2] = {(cuuint64_t)q.k_tiles() * 64, (cuuint64_t)q.row_tiles() * (cuuint64_t)q.count};
     cuuint64_t strides[1] = {(cuuint64_t)q.k_tiles() * 512};
-    cuuint32_t box[2] = {q.nv ? 256u : 128u, 1};
+    cuuint32_t box[2] = {q.nv ? 256u : 128u, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, q.scales, dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -930,8 +933,9 @@ static cudaError_t allow_smem(K kernel, int bytes) {
 
 template <bool NV, typename TC>
 static cudaError_t fp4_attr() {
-    cudaError_t e = allow_smem(fp4_gemm_pair_kernel<NV, 1, TC>, Fp4PairCfg<NV, 1, TC>::kSmem);
-    if (e == cudaSuccess) e = allow_smem(fp4_gemm_pair_kernel<NV, 2, TC>, Fp4PairCfg<NV, 2, TC>::kSmem);
+    cudaError_t e = allow_smem(fp4_gemm_pair_kernel<NV, 1, 1, TC>, Fp4PairCfg<NV, 1, 1, TC>::kSmem);
+    if (e == cudaSuccess) e = allow_smem(fp4_gemm_pair_kernel<NV, 2, 1, TC>, Fp4PairCfg<NV, 2, 1, TC>::kSmem);
+    if (e == cudaSuccess) e = allow_smem(fp4_gemm_pair_kernel<NV, 1, 2, TC>, Fp4PairCfg<NV, 1, 2, TC>::kSmem);
     if (e == cudaSuccess) e = allow_smem(fp4_gemm_rows_kernel<NV, 32, TC>, Fp4RowsCfg<NV, 32>::kSmem);
     if (e == cudaSuccess) e = allow_smem(fp4_gemm_rows_kernel<NV, 64, TC>, Fp4RowsCfg<NV, 64>::kSmem);
     if (e == cudaSuccess) e = allow_smem(fp4_gemm_rows_kernel<NV, 128, TC>, Fp4RowsCfg<NV, 128>::kSmem);
@@ -947,8 +951,9 @@ int fp4_gemm_init_device() {
     return 0;
 }
 
-// How a product runs: rows of A in a tile (512 or 256 on two SMs; 128, 64 or 32
-// with the roles swapped), and over how many CTAs a tile's K is split.
+// How a product runs: rows and columns of a tile (512 x 192, 256 x 384 or 256 x 192
+// on two SMs; 128, 64 or 32 x 128 with the roles swapped), and over how many CTAs a
+// tile's K is split.
 struct Fp4Plan {
     int rows, cols, split, ctas;
 };
@@ -961,15 +966,26 @@ static Fp4Plan fp4_plan(int64_t M, int64_t N, int64_t K, int experts, bool group
     const int64_t pad = (int64_t)(kTileRows - 1) * experts;
     const int64_t per = !grouped ? M : M > pad ? (M - pad) / experts : 0;
     if (cap >= 2 && per > 128) {
-        // Cycles of the busiest pair, as measured: a stage of 256 columns takes 1070
-        // with 512 rows and 660 with 256; 512 rows end a tile with 1500 unhidden.
-        const int64_t pairs = cap / 2, n = up(N, kPN);
-        const int64_t t2 = up(up(M, 512) * n, pairs) * (kb * 1070 + 1500);
-        const int64_t t1 = up(up(M, 256) * n, pairs) * (kb * 660 + 300) + 1500;
-        p.rows = !grouped && t2 < t1 ? 512 : 256;
-        p.cols = kPN;
+        // Cycles of the busiest pair, from 8192 x 28672 x 8192 in each form (637, 579 and
+        // 569 us): a stage of 256 columns of K takes 620 with one accumulator and 1080 with
+        // two, whose read-out, 1500, nothing hides, nor the store of the last (256 x 28672 x
+        // 8192: 32.8 us in two waves of 192 columns, 34.6 in one of 384).
+        const int64_t pairs = cap / 2;
+        int64_t best = 0;
+        for (int form = 0; form < 3; ++form) {
+            const int rows = form == 1 ? 512 : 256, cols = form == 2 ? 2 * kPN : kPN;
+            if (grouped && form == 1) continue;  // an expert's last tile would be mostly empty
+            // of an expert's rows, half a tile on average is past its count
+            const int64_t tiles = grouped ? experts * up(per + rows / 2, rows) : up(M, rows);
+            const int64_t cost = up(tiles * up(N, cols), pairs) * (form ? kb * 1080 + 1500 : kb * 620 + 300) + (form ? 6000 : 1200);
+            if (best == 0 || cost < best) {
+                best = cost;
+                p.rows = rows;
+                p.cols = cols;
+            }
+        }
         p.split = 1;
-        const int64_t tiles = (up(M, p.rows) + (grouped ? experts : 0)) * n;
+        const int64_t tiles = (up(M, p.rows) + (grouped ? experts : 0)) * up(N, p.cols);
         p.ctas = 2 * (int)(tiles < pairs ? tiles : pairs);
         return p;
     }
@@ -988,9 +1004,10 @@ static Fp4Plan fp4_plan(int64_t M, int64_t N, int64_t K, int experts, bool group
     return p;
 }
 
-template <bool NV, int MSUB, typename TC>
+template <bool NV, int MSUB, int NSUB, typename TC>
 static cudaError_t go_pair(const Fp4Plan& p, const CUtensorMap* m, const Fp4GemmArgs& g, cudaStream_t s, DevStatus* st) {
-    fp4_gemm_pair_kernel<NV, MSUB, TC><<<p.ctas, kPThreads, Fp4PairCfg<NV, MSUB, TC>::kSmem, s>>>(m[0], m[1], m[2], m[3], g, st);
+    constexpr int kSmem = Fp4PairCfg<NV, MSUB, NSUB, TC>::kSmem;
+    fp4_gemm_pair_kernel<NV, MSUB, NSUB, TC><<<p.ctas, kPThreads, kSmem, s>>>(m[0], m[1], m[2], m[3], g, st);
     return cudaGetLastError();
 }
 
@@ -1013,8 +1030,8 @@ static cudaError_t go_rows(const Fp4Plan& p, const CUtensorMap* m, const Fp4Gemm
 template <bool NV, typename TC>
 static cudaError_t go_any(const Fp4Plan& p, const CUtensorMap* m, const Fp4GemmArgs& g, cudaStream_t s, DevStatus* st) {
     switch (p.rows) {
-        case 512: return go_pair<NV, 2, TC>(p, m, g, s, st);
-        case 256: return go_pair<NV, 1, TC>(p, m, g, s, st);
+        case 512: return go_pair<NV, 2, 1, TC>(p, m, g, s, st);
+        case 256: return p.cols == kPN ? go_pair<NV, 1, 1, TC>(p, m, g, s, st) : go_pair<NV, 1, 2, TC>(p, m, g, s, st);
         case 128: return go_rows<NV, 128, TC>(p, m, g, s, st);
         case 64: return go_rows<NV, 64, TC>(p, m, g, s, st);
         default: return go_rows<NV, 32, TC>(p, m, g, s, st);
@@ -1047,8 +1064,9 @@ int fp4_gemm_launch(const Fp4& a, const Fp4& b, const int32_t* offsets, const in
         return set_error(-5, "4-bit product has more than 2^31 tiles");
     const bool pair = p.rows > 128;
     CUtensorMap m[4];
-    int rc = code_map(&m[0], a, pair ? kFM : p.rows);
-    if (rc || (rc = code_map(&m[1], b, pair ? kPN / 2 : 128)) || (rc = scale_map(&m[2], a)) || (rc = scale_map(&m[3], b)))
+    int rc = code_map(&m[0], a, pair ? p.rows / 2 : p.rows);
+    if (rc || (rc = code_map(&m[1], b, pair ? kPN / 2 : 128)) || (rc = scale_map(&m[2], a, pair ? p.rows / 256 : 1)) ||
+        (rc = scale_map(&m[3], b, pair ? p.cols / kPN + 1 : 1)))
         return rc;
     const cudaError_t e = a.nv ? (bf16 ? go_any<true, __nv_bfloat16>(p, m, g, s, st) : go_any<true, float>(p, m, g, s, st))
                                : (bf16 ? go_any<false, __nv_bfloat16>(p, m, g, s, st) : go_any<false, float>(p, m, g, s, st));

@@ -308,6 +308,78 @@ def test_route_backward(c3, r, ty):
     assert (np.abs(slope - along) <= room).all()
 
 
+SMALL = [
+    dict(E=1, k=1, score="softmax"),
+    dict(E=5, k=2, score="sigmoid", renorm=True, bias=True),
+    dict(E=8, k=8, score="softmax", renorm=True, scale=2.5),
+    dict(E=60, k=6, score="softmax"),
+    dict(E=64, k=8, score="sigmoid"),
+    dict(E=33, k=3, score="softmax", bias=True),
+]
+
+
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("T", [8192, 8237])
+@pytest.mark.parametrize("r", SMALL, ids=lambda r: "_".join(f"{k}{v}" for k, v in r.items()))
+def test_route_many_tokens(c3, r, T, ty):
+    """Few experts and many tokens take a form of their own: the same results as for few tokens, and the definition's."""
+    rng = np.random.default_rng(T + r["E"])
+    E, k = r["E"], r["k"]
+    x = grid_logits(rng, T, E)
+    x[5] = -np.inf
+    x[6, : E // 2] = -np.inf
+    x[7, E - 1] = np.nan
+    x[8] = 0.0
+    x[T - 1, 0] = -0.0
+    bias = rng.integers(-8, 9, E) / 16.0 if r.get("bias") else None
+    idx, w, router, wide = run_route(c3, r, x, ty, bias, extra=3)
+    few_idx, few_w = torch.empty_like(idx), torch.empty_like(w)
+    for at in range(0, T, 4096):
+        n = min(4096, T - at)
+        c3.c3_route(router, wide[at:], E + 3, n, few_idx[at:], few_w[at:])
+    dw = cuda(rng.standard_normal((T, k)).astype(np.float32))
+    dx, few_dx = Guarded((T, E + 1), TD[ty], 5.0), torch.full((T, E + 1), 5.0, dtype=TD[ty], device="cuda")
+    c3.c3_route_backward(router, wide, E + 3, T, idx, dw, dx.t, E + 1)
+    for at in range(0, T, 4096):
+        n = min(4096, T - at)
+        c3.c3_route_backward(router, wide[at:], E + 3, n, idx[at:], dw[at:], few_dx[at:], E + 1)
+    torch.cuda.synchronize()
+    assert dx.intact() and bool((dx.t[:, E:] == 5.0).all())
+    by_logit = r["score"] == "softmax" and bias is None
+    if by_logit or r["score"] == "sigmoid":   # keys that no sum over the row enters
+        assert torch.equal(idx, few_idx)
+    same = (idx == few_idx).all(1)
+    assert bool(same.float().mean() > 0.99)
+    # both forms are 128 u off the definition at most (weights), 256 u of the largest term (gradients)
+    fine = same & ~torch.isnan(few_w).any(1)
+    assert torch.equal(torch.isnan(w[same]), torch.isnan(few_w[same]))
+    assert bool(((w - few_w)[fine].abs() <= 256 * U * few_w[fine].abs()).all())
+    some = np.r_[0:40, T - 40:T]
+    ref_idx, ref_w = route_oracle(x[some], E, k, r["score"], bias, **oracle_args(r))
+    got_idx, got_w = idx.cpu().numpy()[some], f64(w)[some]
+    if by_logit:
+        assert np.array_equal(got_idx, ref_idx)
+    rows = (got_idx == ref_idx).all(1)
+    assert rows.mean() > 0.9
+    assert np.array_equal(np.isnan(got_w[rows]), np.isnan(ref_w[rows]))
+    err = np.abs(got_w - ref_w)[rows]
+    assert (err[~np.isnan(err)] <= (128 * U * np.abs(ref_w)[rows])[~np.isnan(err)]).all()
+    some = some[(some != 7)]
+    ref = route_grad_oracle(x[some], idx.cpu().numpy()[some], dw.cpu().numpy().astype(np.float64)[some], r)
+    tol = 256 * U * 4 * r.get("scale", 1.0)
+    if r["score"] == "sigmoid" and r.get("renorm"):
+        sel = idx.cpu().numpy()[some]
+        s = np.where(sel >= 0, 1 / (1 + np.exp(-np.take_along_axis(x[some], np.maximum(sel, 0), 1))), 0)
+        tol = tol / np.maximum(s.sum(1, keepdims=True), 1e-3)
+    if ty:
+        tol = tol + H * np.abs(ref)
+    assert (np.abs(f64(dx.t)[some, :E] - ref) <= tol).all()
+    other = torch.ones(T, dtype=torch.bool, device="cuda")
+    other[7] = False
+    a, b = dx.t.float()[other], few_dx.float()[other]
+    assert bool(((a - b).abs() <= 2 * 256 * U * 4 * r.get("scale", 1.0) * (20 if r.get("renorm") else 1) + 2 * H * b.abs()).all())
+
+
 # ----------------------------------------------------------------------------- order
 
 def order_oracle(idx, E, rows):
@@ -327,7 +399,8 @@ def order_oracle(idx, E, rows):
 
 
 @pytest.mark.parametrize("T,k,E", [(0, 2, 4), (1, 1, 1), (3, 2, 5), (100, 4, 7), (513, 8, 256), (4096, 1, 3),
-                                   (2000, 3, 1024), (5000, 6, 60), (20011, 2, 33)])
+                                   (2000, 3, 1024), (5000, 6, 60), (20011, 2, 33),
+                                   (8192, 8, 16), (8193, 8, 16), (70001, 1, 1000), (40000, 3, 7)])
 def test_order(c3, T, k, E):
     rng = np.random.default_rng(T + E)
     idx = rng.integers(-1, E, (T, k))
