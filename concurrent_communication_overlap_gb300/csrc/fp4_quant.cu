@@ -15,13 +15,12 @@
 #include "c3_internal.h"
 
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 namespace c3 {
 
 constexpr int kQRows = 32;                 // rows of a CTA's tile: one row group of a scale tile
 constexpr int kQCols = 256;                // columns of a CTA's tile
-constexpr int kQThreads = kQRows * kQCols / 32;  // a thread takes twice 16 columns of a row
+constexpr int kQThreads = 256;             // eight threads a row, 16 columns each
 
 // Eight signed values to eight codes, the first in the lowest four bits.
 __device__ __forceinline__ uint32_t to_codes(const float* v) {
@@ -76,6 +75,13 @@ __device__ __forceinline__ float max_abs_nan(float a, float b) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t mx_byte(uint32_t u, bool bad) {
+    // amax = m 2^E, m in [1, 2): 6 2^e holds it with e = E - 2 up to m = 1.5, with E - 1 above.
+    // The biased exponent of a subnormal is 0: what follows clamps at 0 anyway.
+    const int e = (int)(u >> 23) - 2 + ((u & 0x7fffffu) > 0x400000u ? 1 : 0);
+    return bad ? 0xffu : (uint32_t)min(max(e, 0), 253);
+}
+
 // Scale byte and codes of 16 columns a thread.  MX: the thread's neighbour (lane ^ 1) holds the block's other half.
 template <bool NV>
 __device__ __forceinline__ void encode16(float (&v)[16], uint32_t& byte, uint2& codes) {
@@ -85,16 +91,11 @@ __device__ __forceinline__ void encode16(float (&v)[16], uint32_t& byte, uint2& 
     if (!NV) amax = max_abs_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     const bool bad = !(amax <= 3.402823466e38f);
     if (!NV) {
-        // amax = m 2^E, m in [1, 2): 6 2^e holds it with e = E - 2 up to m = 1.5, with E - 1 above.
-        // The biased exponent of a subnormal is 0: what follows clamps at 0 anyway.
-        const uint32_t u = __float_as_uint(amax);
-        const int e = (int)(u >> 23) - 2 + ((u & 0x7fffffu) > 0x400000u ? 1 : 0);
-        byte = (uint32_t)min(max(e, 0), 253);
-        const float inv = __uint_as_float((254u - byte) << 23);  // 2^-e
+        byte = mx_byte(__float_as_uint(amax), bad);
+        const float inv = __uint_as_float((254u - min(byte, 253u)) << 23);  // 2^-e
         const uint64_t i2 = pack2(inv, inv);
 #pragma unroll
         for (int i = 0; i < 16; i += 2) unpack2(mul2(pack2(v[i], v[i + 1]), i2), v[i], v[i + 1]);
-        if (bad) byte = 0xffu;
     } else {
         byte = to_e4m3(__fdiv_rn(amax, 6.0f));
         const float s = from_e4m3(byte);
@@ -115,69 +116,145 @@ __device__ __forceinline__ void encode16(float (&v)[16], uint32_t& byte, uint2& 
     if (NV && byte == 0u) codes.x = codes.y = 0u;
 }
 
-__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
+// ---- bf16 rows to MX codes, two values an instruction
+//
+// The conversion instruction to 4-bit codes is slow: alone it bounds the
+// quantisation of 8192 x 8192 at about 29 us.  Half the columns take it, the other
+// half the same rounding in packed bf16 arithmetic, so that neither pipe waits for
+// the other.  With a = |x / scale| <= 6, exact in bf16, and p the power of two below
+// max(a, 1): codes step by p / 2 around a, and so do bf16 numbers around 96 p, so
+// r = a + 96 p is rounded to nearest even at the right place, and
+//   code = (r's low three bits) + 2 log2(p), the latter in r's exponent.
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t bmax2_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Two codes, in the low four bits of either half.
+__device__ __forceinline__ uint32_t two_codes(uint32_t y) {
+    const uint32_t a = y & 0x7fff7fffu;
+    const uint32_t p = bmax2(a, 0x3f803f80u) & 0x7f807f80u;
+    const uint32_t r = bfma2(p, 0x42c042c0u, a);  // 96; the exponent's low bits are 1 + log2(p)
+    return ((r & 0x00070007u) + ((r >> 6) & 0x00060006u) - 0x00020002u) | ((y >> 12) & 0x00080008u);
+}
+// Eight values in memory order, as four words of two, times `inv`, to eight codes.
+__device__ __forceinline__ uint32_t eight_codes(const uint32_t* w, uint32_t inv) {
+    // (0, 4) (1, 5) (2, 6) (3, 7): the halves of the result then hold 0..3 and 4..7
+    uint32_t r = two_codes(bmul2(__byte_perm(w[0], w[2], 0x5410), inv));
+    r |= two_codes(bmul2(__byte_perm(w[0], w[2], 0x7632), inv)) << 4;
+    r |= two_codes(bmul2(__byte_perm(w[1], w[3], 0x5410), inv)) << 8;
+    r |= two_codes(bmul2(__byte_perm(w[1], w[3], 0x7632), inv)) << 12;
+    return r;
+}
+// Scale byte and codes of 16 columns a thread; its neighbour (lane ^ 1) holds the block's other half.
+__device__ __forceinline__ void encode16_mx_bf16(const uint32_t (&w)[8], uint32_t& byte, uint2& codes) {
+    uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = bmax2_nan(m, w[i] & 0x7fff7fffu);
+    m = bmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = bmax2_nan(m, m >> 16);
+    const uint32_t u = m << 16;  // the low half as fp32
+    byte = mx_byte(u, u >= 0x7f800000u);
+    const uint32_t inv = ((254u - min(byte, 253u)) << 7) * 0x00010001u;  // 2^-e in both halves
+    codes.x = eight_codes(w, inv);
+    float v[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float4 a = reinterpret_cast<const float4*>(p)[i];
-        v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
+        const uint32_t y = bmul2(w[4 + i], inv);
+        v[2 * i] = __uint_as_float(y << 16);
+        v[2 * i + 1] = __uint_as_float(y & 0xffff0000u);
     }
+    codes.y = to_codes(v);
 }
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[16]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint4 a = reinterpret_cast<const uint4*>(p)[h];
-        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[8 * h + 2 * i] = __uint_as_float(u[i] << 16);
-            v[8 * h + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
-    }
-}
+
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// Columns c .. c + 15 of row r, encoded, to their places; every lane of the warp takes part.
+// The codes and the scale byte of columns c .. c + 15 of row r to their places; every lane of the warp takes part.
 template <bool NV>
-__device__ __forceinline__ void put16(float (&v)[16], bool have, float inv_t, const Fp4& q, int64_t mat_row, uint8_t* tile_row,
+__device__ __forceinline__ void put16(uint32_t byte, uint2 codes, bool have, const Fp4& q, int64_t mat_row, uint8_t* tile_row,
                                       int64_t c, int64_t pitch, int64_t k_tiles) {
-    if (NV) {
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) unpack2(mul2(pack2(v[j], v[j + 1]), pack2(inv_t, inv_t)), v[j], v[j + 1]);
-    }
-    uint32_t byte;
-    uint2 codes;
-    encode16<NV>(v, byte, codes);
     // The four scales of a tile's row as one word: from lanes 2 apart (MX) or neighbours (NV).
     constexpr int kStep = NV ? 1 : 2;
     const int lane = threadIdx.x & 31;
     const int lead = NV ? (lane & ~3) : (lane & ~7);
-    uint32_t word = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) word |= __shfl_sync(0xffffffffu, byte, lead + j * kStep) << (8 * j);
+    uint32_t word = byte << (8 * ((lane / kStep) & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, kStep);
+    word |= __shfl_xor_sync(0xffffffffu, word, 2 * kStep);
     if (!have) return;
     if (c < pitch * 2) *reinterpret_cast<uint2*>(q.codes + mat_row * pitch + c / 2) = codes;
     const int64_t kt = c / (NV ? 64 : 128);
     if (lane == lead && kt < k_tiles) *reinterpret_cast<uint32_t*>(tile_row + kt * 512) = word;
 }
 
-// One CTA: 32 rows of one matrix, 256 columns at a time, two spans of 16 columns
-// a thread, both loaded before either is encoded.  `across` CTAs share a row
-// tile's columns.  TRANS: the matrix is the transpose of what lies in memory,
-// and a tile goes through shared memory.
-template <typename T, bool NV, bool TRANS>
+// 16 columns of a row as they lie in memory: 8 words of bf16 pairs or 16 of fp32; zeros past `most`.
+template <typename T>
+struct Raw16 {
+    static constexpr int kWords = 4 * sizeof(T);
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const T* p, int64_t most, bool vec) {
+        if (vec && most >= 16) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 a = reinterpret_cast<const uint4*>(p)[i];
+                w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+            }
+        } else if constexpr (sizeof(T) == 2) {
+            const uint16_t* s = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i] = (2 * i < most ? s[2 * i] : 0u) | (2 * i + 1 < most ? (uint32_t)s[2 * i + 1] << 16 : 0u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = i < most ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[16]) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[i] = __uint_as_float(sizeof(T) == 4 ? w[i & (kWords - 1)]
+                                                  : (i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+};
+
+template <bool NV>
+__device__ __forceinline__ void encode_scaled(float (&v)[16], float inv_t, uint32_t& byte, uint2& codes) {
+    if (NV) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) unpack2(mul2(pack2(v[j], v[j + 1]), pack2(inv_t, inv_t)), v[j], v[j + 1]);
+    }
+    encode16<NV>(v, byte, codes);
+}
+
+// One CTA: 32 rows of one matrix, 128 columns at a time, `across` CTAs a row tile;
+// a thread's next 16 columns are on their way while these are encoded.
+template <typename T, bool NV>
 __global__ void __launch_bounds__(kQThreads)
     fp4_quantize_kernel(const T* __restrict__ x, int64_t x_rows, int64_t ld, int vec, const int32_t* __restrict__ row_of,
-                        Fp4 q, int64_t pitch, int64_t k_tiles, int64_t scale_bytes, int64_t x_stride, unsigned col_tiles,
+                        Fp4 q, int64_t pitch, int64_t k_tiles, int64_t scale_bytes, int64_t x_stride, unsigned spans,
                         unsigned across) {
     const int i = threadIdx.x >> 3, g = threadIdx.x & 7;
     const unsigned rt = blockIdx.x / across;
     const int64_t r = (int64_t)rt * kQRows + i;
     const int mat = blockIdx.y;
-    x += (int64_t)mat * x_stride;
     bool have = r < q.rows;
     int64_t src = r;
-    if (!TRANS && row_of) {
+    if (row_of) {
         if (have) {
             src = row_of[r];
             have = src >= 0 && src < x_rows;
@@ -187,147 +264,179 @@ __global__ void __launch_bounds__(kQThreads)
     const float inv_t = NV && q.tensor_scale ? __fdiv_rn(1.0f, q.tensor_scale[mat]) : 1.0f;
     uint8_t* tile_row = q.scales + (int64_t)mat * scale_bytes + (r / kTileRows) * k_tiles * 512 + (r % 32) * 16 +
                         (r % kTileRows) / 32 * 4;
-    for (unsigned ct = blockIdx.x - rt * across; ct < col_tiles; ct += across) {
-        const int64_t c0 = (int64_t)ct * kQCols, c = c0 + g * 16;
-        float v[2][16];
-        if constexpr (TRANS) {
-            // rows of shared memory are columns of the matrix; 32 values and one of padding each
-            __shared__ float tile[kQCols][kQRows + 1];
-            const int rr = threadIdx.x & 31;
-            const int64_t row = (int64_t)rt * kQRows + rr;
-            const T* from = x + c0 * ld + row;
-            const int most = (int)min((int64_t)kQCols, q.cols - c0);
-#pragma unroll 16
-            for (int cc = threadIdx.x >> 5; cc < kQCols; cc += kQThreads / 32)
-                tile[cc][rr] = (cc < most && row < q.rows) ? load1(from + cc * ld) : 0.0f;
-            __syncthreads();
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[h][j] = tile[h * 128 + g * 16 + j][i];
-            __syncthreads();
+    const T* xr = x + (int64_t)mat * x_stride + src * ld;
+    unsigned u = blockIdx.x - rt * across;
+    int64_t c = (int64_t)u * 128 + g * 16;
+    Raw16<T> now;
+    now.load(xr + c, have ? q.cols - c : 0, vec);
+    for (; u < spans; u += across) {
+        const int64_t next = c + (int64_t)across * 128;
+        Raw16<T> ahead;
+        ahead.load(xr + next, have && u + across < spans ? q.cols - next : 0, vec);
+        uint32_t byte;
+        uint2 codes;
+        if constexpr (!NV && sizeof(T) == 2) {
+            encode16_mx_bf16(now.w, byte, codes);
         } else {
-            const T* xr = x + src * ld + c;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (have && vec && c + h * 128 + 16 <= q.cols) {
-                    load16(xr + h * 128, v[h]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        v[h][j] = (have && c + h * 128 + j < q.cols) ? load1(xr + h * 128 + j) : 0.0f;
-                }
-            }
+            float v[16];
+            now.values(v);
+            encode_scaled<NV>(v, inv_t, byte, codes);
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            put16<NV>(v[h], have, inv_t, q, (int64_t)mat * q.rows + r, tile_row, c + h * 128, pitch, k_tiles);
+        put16<NV>(byte, codes, have, q, (int64_t)mat * q.rows + r, tile_row, c, pitch, k_tiles);
+        now = ahead;
+        c = next;
     }
 }
 
-// Eight codes, the first in the lowest four bits, as fp32.
-__device__ __forceinline__ void from_codes(uint32_t w, float* v) {
-    uint32_t h[4];
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
+// The transpose of what lies in memory: 32 rows x 256 columns, turned in shared
+// memory, whose rows are the matrix's columns, 32 values and one of padding each.
+template <typename T, bool NV>
+__global__ void __launch_bounds__(kQThreads)
+    fp4_quantize_turned_kernel(const T* __restrict__ x, int64_t ld, Fp4 q, int64_t pitch, int64_t k_tiles,
+                               int64_t scale_bytes, int64_t x_stride, unsigned col_tiles) {
+    __shared__ float tile[kQCols][kQRows + 1];
+    const int i = threadIdx.x >> 3, g = threadIdx.x & 7;
+    const unsigned rt = blockIdx.x / col_tiles;
+    const int64_t c0 = (int64_t)(blockIdx.x - rt * col_tiles) * kQCols, c = c0 + g * 16;
+    const int64_t r = (int64_t)rt * kQRows + i;
+    const int mat = blockIdx.y;
+    const int rr = threadIdx.x & 31;
+    const int64_t row = (int64_t)rt * kQRows + rr;
+    const T* from = x + (int64_t)mat * x_stride + c0 * ld + row;
+    const int most = (int)min((int64_t)kQCols, q.cols - c0);
+#pragma unroll 16
+    for (int cc = threadIdx.x >> 5; cc < kQCols; cc += kQThreads / 32)
+        tile[cc][rr] = (cc < most && row < q.rows) ? load1(from + cc * ld) : 0.0f;
+    __syncthreads();
+    const float inv_t = NV && q.tensor_scale ? __fdiv_rn(1.0f, q.tensor_scale[mat]) : 1.0f;
+    uint8_t* tile_row = q.scales + (int64_t)mat * scale_bytes + (r / kTileRows) * k_tiles * 512 + (r % 32) * 16 +
+                        (r % kTileRows) / 32 * 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    for (int h = 0; h < 2; ++h) {
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = tile[h * 128 + g * 16 + j][i];
+        uint32_t byte;
+        uint2 codes;
+        encode_scaled<NV>(v, inv_t, byte, codes);
+        put16<NV>(byte, codes, r < q.rows, q, (int64_t)mat * q.rows + r, tile_row, c + h * 128, pitch, k_tiles);
+    }
+}
+
+// Eight codes, the first in the lowest four bits, as bf16 pairs in order.  A
+// code's three magnitude bits pick the two bytes of its bf16 number out of tables
+// in registers (0 .5 1 1.5 2 3 4 6 are 0000 3f00 3f80 3fc0 4000 4040 4080 40c0); the
+// sign, the selector's top bit, spreads the sign bit of a table of 80s to ff.
+__device__ __forceinline__ void from_codes(uint32_t w, uint32_t (&v)[4]) {
+    const uint32_t m = w & 0x77777777u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t sel = h ? m >> 16 : m & 0xffffu, all = h ? w >> 16 : w & 0xffffu;
+        const uint32_t hi = __byte_perm(0x3f3f3f00u, 0x40404040u, sel);
+        const uint32_t lo = __byte_perm(0xc0800000u, 0xc0804000u, sel);
+        uint32_t sign;  // the intrinsic masks the replicating bit of its selector, the instruction does not
+        asm("prmt.b32 %0, %1, %1, %2;" : "=r"(sign) : "r"(0x80808080u), "r"(all));
+        const uint32_t top = hi | ((sign << 1) & 0x80808080u);
+        v[2 * h] = __byte_perm(lo, top, 0x5140);
+        v[2 * h + 1] = __byte_perm(lo, top, 0x7362);
     }
 }
 
 __device__ __forceinline__ void store_v(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_v(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-__device__ __forceinline__ void store16(float* dst, const float (&v)[16]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        reinterpret_cast<float4*>(dst)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+__device__ __forceinline__ void store8(float* dst, const float (&v)[8]) {
+    reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
-__device__ __forceinline__ void store16(__nv_bfloat16* dst, const float (&v)[16]) {
-    uint32_t u[8];
+__device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&v)[8]) {
+    uint32_t u[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
         u[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    *reinterpret_cast<uint4*>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// The same tiles and the same places of a thread as the quantisation.  VEC:
-// rows of x are whole 16-byte units and a thread stores its own columns; else the
-// tile goes through shared memory and a warp stores 32 neighbours at a time.
+// One CTA: 32 rows x 256 columns.  A warp takes four rows, a lane 8 columns of
+// each, so that a warp reads and writes whole runs.  VEC: rows of x are whole
+// 16-byte units; else a row goes through shared memory and out a value a lane.
 template <typename T, bool NV, bool VEC>
 __global__ void __launch_bounds__(kQThreads)
     fp4_dequantize_kernel(Fp4 q, int64_t pitch, int64_t k_tiles, int64_t scale_bytes, T* __restrict__ x, int64_t ld,
                           unsigned col_tiles) {
-    const int i = threadIdx.x >> 3, g = threadIdx.x & 7;
+    constexpr int kWarps = kQThreads / 32, kRows = kQRows / kWarps;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned rt = blockIdx.x / col_tiles;
-    const int64_t c0 = (int64_t)(blockIdx.x - rt * col_tiles) * kQCols, c = c0 + g * 16;
-    const int64_t r = (int64_t)rt * kQRows + i;
+    const int64_t c0 = (int64_t)(blockIdx.x - rt * col_tiles) * kQCols, c = c0 + lane * 8;
+    const int64_t row0 = (int64_t)rt * kQRows;
     const int mat = blockIdx.y;
-    const uint8_t* codes = q.codes + ((int64_t)mat * q.rows + r) * pitch + c / 2;
-    const uint8_t* tile_row = q.scales + (int64_t)mat * scale_bytes + (r / kTileRows) * k_tiles * 512 + (r % 32) * 16 +
-                              (r % kTileRows) / 32 * 4;
-    constexpr int kBlock = NV ? 16 : 32;
-    uint2 w[2] = {};
-    uint32_t byte[2] = {};
+    const bool in = c < q.cols;
+    const uint8_t* codes = q.codes + ((int64_t)mat * q.rows + row0) * pitch + c / 2;
+    const int64_t blk = c / (NV ? 16 : 32);
+    const uint8_t* scales = q.scales + (int64_t)mat * scale_bytes + ((row0 / kTileRows) * k_tiles + blk / 4) * 512 +
+                            (row0 % kTileRows) / 32 * 4 + blk % 4;
+    uint32_t w[kRows], byte[kRows];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        if (r < q.rows && c + h * 128 < q.cols) {
-            w[h] = __ldcs(reinterpret_cast<const uint2*>(codes + h * 64));
-            const int64_t blk = (c + h * 128) / kBlock;
-            byte[h] = tile_row[blk / 4 * 512 + blk % 4];
-        }
+    for (int i = 0; i < kRows; ++i) {
+        const int r = warp + i * kWarps;
+        const bool have = in && row0 + r < q.rows;
+        w[i] = have ? __ldcs(reinterpret_cast<const uint32_t*>(codes + r * pitch)) : 0u;
+        byte[i] = have ? scales[r * 16] : 0u;
+    }
     const float t = q.tensor_scale ? q.tensor_scale[mat] : 1.0f;
-    T* dst = x + ((int64_t)mat * q.rows + r) * ld + c;
-    __shared__ T tile[VEC ? 1 : kQRows][VEC ? 1 : kQCols + 2];
+    __shared__ __align__(16) T turn[VEC ? 1 : kWarps][VEC ? 8 : kQCols];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const float s = NV ? from_e4m3(byte[h])
-                           : byte[h] == 255u ? NAN : __uint_as_float(byte[h] ? byte[h] << 23 : 1u << 22);
-        float v[16];
-        from_codes(w[h].x, v);
-        from_codes(w[h].y, v + 8);
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t r = row0 + warp + i * kWarps;
+        if (r >= q.rows) break;
+        uint32_t p[4];
+        from_codes(w[i], p);
+        T* row = x + ((int64_t)mat * q.rows + r) * ld;
+        if constexpr (!NV && sizeof(T) == 2) {
+            // a code times a power of two is a bf16 number: no rounding, no detour by fp32
+            const uint32_t s = byte[i] == 255u ? 0x7fc0u : byte[i] ? byte[i] << 7 : 0x40u;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = v[j] * s * t;
+            for (int j = 0; j < 4; ++j) p[j] = bmul2(p[j], s * 0x00010001u);
+            if (VEC && c + 8 <= q.cols) {
+                *reinterpret_cast<uint4*>(row + c) = make_uint4(p[0], p[1], p[2], p[3]);
+                continue;
+            }
+        }
+        float v[8];
+        const float s = NV ? from_e4m3(byte[i])
+                           : sizeof(T) == 2 ? 1.0f
+                           : byte[i] == 255u ? NAN : __uint_as_float(byte[i] ? byte[i] << 23 : 1u << 22);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(p[j] << 16) * s * t;
+            v[2 * j + 1] = __uint_as_float(p[j] & 0xffff0000u) * s * t;
+        }
         if constexpr (VEC) {
-            if (r < q.rows && c + h * 128 + 16 <= q.cols) {
-                store16(dst + h * 128, v);
-            } else if (r < q.rows) {
+            if (c + 8 <= q.cols) {
+                store8(row + c, v);
+            } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (c + h * 128 + j < q.cols) store_v(dst + h * 128 + j, v[j]);
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < q.cols) store_v(row + c + j, v[j]);
             }
         } else {
+            store8(&turn[warp][lane * 8], v);
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) store_v(&tile[i][h * 128 + g * 16 + j], v[j]);
-        }
-    }
-    if constexpr (!VEC) {
-        __syncthreads();
-        const int lane = threadIdx.x & 31;
-        for (int rr = threadIdx.x >> 5; rr < kQRows && (int64_t)rt * kQRows + rr < q.rows; rr += kQThreads / 32) {
-            T* row = x + ((int64_t)mat * q.rows + (int64_t)rt * kQRows + rr) * ld + c0;
-#pragma unroll
-            for (int cc = lane; cc < kQCols; cc += 32)
-                if (c0 + cc < q.cols) row[cc] = tile[rr][cc];
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j * 32 + lane < q.cols) row[c0 + j * 32 + lane] = turn[warp][j * 32 + lane];
+            __syncwarp();
         }
     }
 }
 
 // ---------------------------------------------------------------- host side
 
-// CTAs along the columns of a row tile: all column tiles, or `most` of them.
-static int fp4_grid(const Fp4& q, int64_t cols_padded, int64_t most, dim3* grid, unsigned* col_tiles, unsigned* across) {
-    *col_tiles = (unsigned)((cols_padded + kQCols - 1) / kQCols);
-    *across = *col_tiles > most ? (unsigned)most : *col_tiles;
-    const int64_t n = (q.rows + kQRows - 1) / kQRows * *across;
+// `per_row` CTAs for each 32 rows of each matrix.
+static int fp4_grid(const Fp4& q, int64_t per_row, dim3* grid) {
+    const int64_t n = (q.rows + kQRows - 1) / kQRows * per_row;
     if (n > 0x7fffffff || q.count > 65535) return set_error(-5, "4-bit matrix has too many tiles for one launch");
     *grid = dim3((unsigned)n, (unsigned)q.count);
     return 0;
@@ -340,29 +449,39 @@ static bool vec_ok(const void* p, int64_t ld, int bf16) {
 int fp4_quantize_launch(const void* x, int bf16, int64_t x_rows, int64_t ld, int transpose, const int32_t* row_of,
                         const Fp4& q, cudaStream_t s) {
     dim3 grid;
-    unsigned col_tiles, across;
-    // A k tile's padding is written too: MX tiles are 128 columns wide, NV tiles 64.
-    // Gathered rows are mostly absent when each expert has a handful, and a CTA that
-    // finds none of its 32 leaves: four CTAs a row tile instead of one each 256 columns
-    // (8256 x 4096 with 192 rows present: 11 us against 18; all 32768 present: 69 against 91).
-    int rc = fp4_grid(q, q.k_tiles() * (q.nv ? 64 : 128), row_of ? 4 : 1 << 30, &grid, &col_tiles, &across);
-    if (rc) return rc;
+    // a k tile's padding is written too: MX tiles are 128 columns wide, NV tiles 64
+    const int64_t cols = q.k_tiles() * (q.nv ? 64 : 128);
     const int64_t stride = (transpose ? q.cols : x_rows) * ld;
-    const int vec = vec_ok(x, ld, bf16) && (q.count == 1 || (stride * (bf16 ? 2 : 4)) % 16 == 0);
-#define C3_GO(T_, NV_, TR_)                                                                                       \
-    fp4_quantize_kernel<T_, NV_, TR_><<<grid, kQThreads, 0, s>>>(static_cast<const T_*>(x), x_rows, ld, vec, row_of, q, \
-                                                                 q.pitch(), q.k_tiles(), q.scale_bytes(), stride, col_tiles, across)
-#define C3_PICK(T_)                                       \
-    do {                                                  \
-        if (q.nv && transpose) C3_GO(T_, true, true);     \
-        else if (q.nv) C3_GO(T_, true, false);            \
-        else if (transpose) C3_GO(T_, false, true);       \
-        else C3_GO(T_, false, false);                     \
-    } while (0)
-    if (bf16) C3_PICK(__nv_bfloat16);
-    else C3_PICK(float);
-#undef C3_PICK
+    int rc;
+    if (transpose) {
+        const unsigned col_tiles = (unsigned)((cols + kQCols - 1) / kQCols);
+        if ((rc = fp4_grid(q, col_tiles, &grid))) return rc;
+#define C3_GO(T_, NV_)                                                                                            \
+    fp4_quantize_turned_kernel<T_, NV_><<<grid, kQThreads, 0, s>>>(static_cast<const T_*>(x), ld, q, q.pitch(),    \
+                                                                   q.k_tiles(), q.scale_bytes(), stride, col_tiles)
+        if (bf16 && q.nv) C3_GO(__nv_bfloat16, true);
+        else if (bf16) C3_GO(__nv_bfloat16, false);
+        else if (q.nv) C3_GO(float, true);
+        else C3_GO(float, false);
 #undef C3_GO
+    } else {
+        // Eight spans of 128 columns a CTA, so that loads run ahead; a single CTA a span
+        // where rows are few.  Gathered rows are mostly absent when each expert has a
+        // handful, and a CTA that finds none of its 32 leaves.
+        const unsigned spans = (unsigned)((cols + 127) / 128);
+        const int64_t tiles = (q.rows + kQRows - 1) / kQRows * q.count;
+        const unsigned across = tiles >= 256 || row_of ? (spans + 7) / 8 : spans;
+        if ((rc = fp4_grid(q, across, &grid))) return rc;
+        const int vec = vec_ok(x, ld, bf16) && (q.count == 1 || (stride * (bf16 ? 2 : 4)) % 16 == 0);
+#define C3_GO(T_, NV_)                                                                                                \
+    fp4_quantize_kernel<T_, NV_><<<grid, kQThreads, 0, s>>>(static_cast<const T_*>(x), x_rows, ld, vec, row_of, q,    \
+                                                            q.pitch(), q.k_tiles(), q.scale_bytes(), stride, spans, across)
+        if (bf16 && q.nv) C3_GO(__nv_bfloat16, true);
+        else if (bf16) C3_GO(__nv_bfloat16, false);
+        else if (q.nv) C3_GO(float, true);
+        else C3_GO(float, false);
+#undef C3_GO
+    }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return set_cuda_error(e, "4-bit quantise kernel launch");
     count_launch();
@@ -371,8 +490,8 @@ int fp4_quantize_launch(const void* x, int bf16, int64_t x_rows, int64_t ld, int
 
 int fp4_dequantize_launch(const Fp4& q, void* x, int bf16, int64_t ld, cudaStream_t s) {
     dim3 grid;
-    unsigned col_tiles, across;
-    int rc = fp4_grid(q, q.cols, 1 << 30, &grid, &col_tiles, &across);
+    const unsigned col_tiles = (unsigned)((q.cols + kQCols - 1) / kQCols);
+    int rc = fp4_grid(q, col_tiles, &grid);
     if (rc) return rc;
     const bool vec = vec_ok(x, ld, bf16);
 #define C3_GO(T_, NV_, VEC_)                                                                                     \
