@@ -365,6 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    chain_wait();
     if (MSUB == 1 && g.offsets && warp == 2) expert_tiles<kRows>(g, prefix, lane);
     tc_fence_before();
     __syncthreads();
@@ -657,6 +658,7 @@ __global__ void __launch_bounds__(kRThreads, 2)
         tmem_alloc(smem_addr(tmem_slot), 256);
         tmem_relinquish();
     }
+    chain_wait();
     if (NT == 64 && g.offsets && warp == 2) expert_tiles<NT>(g, prefix, lane);
     tc_fence_before();
     __syncthreads();
@@ -1006,25 +1008,14 @@ static Fp4Plan fp4_plan(int64_t M, int64_t N, int64_t K, int experts, bool group
 
 template <bool NV, int MSUB, int NSUB, typename TC>
 static cudaError_t go_pair(const Fp4Plan& p, const CUtensorMap* m, const Fp4GemmArgs& g, cudaStream_t s, DevStatus* st) {
-    constexpr int kSmem = Fp4PairCfg<NV, MSUB, NSUB, TC>::kSmem;
-    fp4_gemm_pair_kernel<NV, MSUB, NSUB, TC><<<p.ctas, kPThreads, kSmem, s>>>(m[0], m[1], m[2], m[3], g, st);
-    return cudaGetLastError();
+    return launch_chained(fp4_gemm_pair_kernel<NV, MSUB, NSUB, TC>, dim3(p.ctas), kPThreads,
+                          Fp4PairCfg<NV, MSUB, NSUB, TC>::kSmem, s, 1, m[0], m[1], m[2], m[3], g, st);
 }
 
 template <bool NV, int NT, typename TC>
 static cudaError_t go_rows(const Fp4Plan& p, const CUtensorMap* m, const Fp4GemmArgs& g, cudaStream_t s, DevStatus* st) {
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)p.ctas);
-    c.blockDim = dim3(kRThreads);
-    c.dynamicSmemBytes = Fp4RowsCfg<NV, NT>::kSmem;
-    c.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)p.split;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    c.attrs = &attr;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, fp4_gemm_rows_kernel<NV, NT, TC>, m[0], m[1], m[2], m[3], g, p.split, st);
+    return launch_chained(fp4_gemm_rows_kernel<NV, NT, TC>, dim3(p.ctas), kRThreads, Fp4RowsCfg<NV, NT>::kSmem, s,
+                          (unsigned)p.split, m[0], m[1], m[2], m[3], g, p.split, st);
 }
 
 template <bool NV, typename TC>
@@ -1070,10 +1061,7 @@ int fp4_gemm_launch(const Fp4& a, const Fp4& b, const int32_t* offsets, const in
         return rc;
     const cudaError_t e = a.nv ? (bf16 ? go_any<true, __nv_bfloat16>(p, m, g, s, st) : go_any<true, float>(p, m, g, s, st))
                                : (bf16 ? go_any<false, __nv_bfloat16>(p, m, g, s, st) : go_any<false, float>(p, m, g, s, st));
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return set_cuda_error(e, "4-bit gemm kernel launch");
-    }
+    if (e != cudaSuccess) return set_cuda_error(e, "4-bit gemm kernel launch");
     count_launch();
     return 0;
 }

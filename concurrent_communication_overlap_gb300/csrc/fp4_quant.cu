@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(kQThreads)
     const int mat = blockIdx.y;
     bool have = r < q.rows;
     int64_t src = r;
+    chain_wait();
     if (row_of) {
         if (have) {
             src = row_of[r];
@@ -304,6 +305,7 @@ __global__ void __launch_bounds__(kQThreads)
     const int64_t row = (int64_t)rt * kQRows + rr;
     const T* from = x + (int64_t)mat * x_stride + c0 * ld + row;
     const int most = (int)min((int64_t)kQCols, q.cols - c0);
+    chain_wait();
 #pragma unroll 16
     for (int cc = threadIdx.x >> 5; cc < kQCols; cc += kQThreads / 32)
         tile[cc][rr] = (cc < most && row < q.rows) ? load1(from + cc * ld) : 0.0f;
@@ -378,6 +380,7 @@ __global__ void __launch_bounds__(kQThreads)
     const uint8_t* scales = q.scales + (int64_t)mat * scale_bytes + ((row0 / kTileRows) * k_tiles + blk / 4) * 512 +
                             (row0 % kTileRows) / 32 * 4 + blk % 4;
     uint32_t w[kRows], byte[kRows];
+    chain_wait();
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int r = warp + i * kWarps;
@@ -453,12 +456,13 @@ int fp4_quantize_launch(const void* x, int bf16, int64_t x_rows, int64_t ld, int
     const int64_t cols = q.k_tiles() * (q.nv ? 64 : 128);
     const int64_t stride = (transpose ? q.cols : x_rows) * ld;
     int rc;
+    cudaError_t e;
     if (transpose) {
         const unsigned col_tiles = (unsigned)((cols + kQCols - 1) / kQCols);
         if ((rc = fp4_grid(q, col_tiles, &grid))) return rc;
-#define C3_GO(T_, NV_)                                                                                            \
-    fp4_quantize_turned_kernel<T_, NV_><<<grid, kQThreads, 0, s>>>(static_cast<const T_*>(x), ld, q, q.pitch(),    \
-                                                                   q.k_tiles(), q.scale_bytes(), stride, col_tiles)
+#define C3_GO(T_, NV_)                                                                                       \
+    e = launch_chained(fp4_quantize_turned_kernel<T_, NV_>, grid, kQThreads, 0, s, 1, static_cast<const T_*>(x), \
+                       ld, q, q.pitch(), q.k_tiles(), q.scale_bytes(), stride, col_tiles)
         if (bf16 && q.nv) C3_GO(__nv_bfloat16, true);
         else if (bf16) C3_GO(__nv_bfloat16, false);
         else if (q.nv) C3_GO(float, true);
@@ -473,16 +477,15 @@ int fp4_quantize_launch(const void* x, int bf16, int64_t x_rows, int64_t ld, int
         const unsigned across = tiles >= 256 || row_of ? (spans + 7) / 8 : spans;
         if ((rc = fp4_grid(q, across, &grid))) return rc;
         const int vec = vec_ok(x, ld, bf16) && (q.count == 1 || (stride * (bf16 ? 2 : 4)) % 16 == 0);
-#define C3_GO(T_, NV_)                                                                                                \
-    fp4_quantize_kernel<T_, NV_><<<grid, kQThreads, 0, s>>>(static_cast<const T_*>(x), x_rows, ld, vec, row_of, q,    \
-                                                            q.pitch(), q.k_tiles(), q.scale_bytes(), stride, spans, across)
+#define C3_GO(T_, NV_)                                                                                           \
+    e = launch_chained(fp4_quantize_kernel<T_, NV_>, grid, kQThreads, 0, s, 1, static_cast<const T_*>(x), x_rows,    \
+                       ld, vec, row_of, q, q.pitch(), q.k_tiles(), q.scale_bytes(), stride, spans, across)
         if (bf16 && q.nv) C3_GO(__nv_bfloat16, true);
         else if (bf16) C3_GO(__nv_bfloat16, false);
         else if (q.nv) C3_GO(float, true);
         else C3_GO(float, false);
 #undef C3_GO
     }
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return set_cuda_error(e, "4-bit quantise kernel launch");
     count_launch();
     return 0;
@@ -494,9 +497,10 @@ int fp4_dequantize_launch(const Fp4& q, void* x, int bf16, int64_t ld, cudaStrea
     int rc = fp4_grid(q, col_tiles, &grid);
     if (rc) return rc;
     const bool vec = vec_ok(x, ld, bf16);
-#define C3_GO(T_, NV_, VEC_)                                                                                     \
-    fp4_dequantize_kernel<T_, NV_, VEC_><<<grid, kQThreads, 0, s>>>(q, q.pitch(), q.k_tiles(), q.scale_bytes(),   \
-                                                                    static_cast<T_*>(x), ld, col_tiles)
+    cudaError_t e;
+#define C3_GO(T_, NV_, VEC_)                                                                                 \
+    e = launch_chained(fp4_dequantize_kernel<T_, NV_, VEC_>, grid, kQThreads, 0, s, 1, q, q.pitch(), q.k_tiles(), \
+                       q.scale_bytes(), static_cast<T_*>(x), ld, col_tiles)
 #define C3_PICK(T_)                                  \
     do {                                             \
         if (q.nv && vec) C3_GO(T_, true, true);      \
@@ -508,7 +512,6 @@ int fp4_dequantize_launch(const Fp4& q, void* x, int bf16, int64_t ld, cudaStrea
     else C3_PICK(float);
 #undef C3_PICK
 #undef C3_GO
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return set_cuda_error(e, "4-bit dequantise kernel launch");
     count_launch();
     return 0;

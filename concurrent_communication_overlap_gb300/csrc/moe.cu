@@ -36,6 +36,7 @@ __device__ __forceinline__ int choice_expert(const int32_t* idx, int64_t i, int6
 __global__ void __launch_bounds__(kOrderThreads)
     order_count_kernel(const int32_t* __restrict__ idx, int64_t n, int experts, int per_cta, int* __restrict__ counts) {
     __shared__ int c[kMaxExperts];
+    chain_wait();
     for (int e = threadIdx.x; e < experts; e += kOrderThreads) c[e] = 0;
     __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * per_cta;
@@ -50,6 +51,7 @@ __global__ void __launch_bounds__(kOrderThreads)
 // counts[cta][e] to the sum over the CTAs before, and the sum over all behind the last; a warp an expert.
 __global__ void __launch_bounds__(256) order_sum_kernel(int* __restrict__ counts, int ctas, int experts) {
     const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    chain_wait();
     if (e >= experts) return;
     int run = 0;
     for (int b0 = 0; b0 < ctas; b0 += 32) {
@@ -80,6 +82,7 @@ __global__ void __launch_bounds__(kOrderThreads)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t first = (int64_t)blockIdx.x * per_cta;
     const bool places = (int)blockIdx.x < place_ctas;
+    chain_wait();
     for (int e = threadIdx.x; e < experts; e += kOrderThreads) {
         total[e] = sums ? sums[(size_t)place_ctas * experts + e] : 0;
         before[e] = sums && places ? sums[(size_t)blockIdx.x * experts + e] : 0;
@@ -87,14 +90,17 @@ __global__ void __launch_bounds__(kOrderThreads)
     if (places)
         for (int i = threadIdx.x; i < kOrderWarps * experts; i += kOrderThreads) hist[i] = 0;
     __syncthreads();
-    if (!sums)
-        for (int64_t i = threadIdx.x; i < n; i += kOrderThreads) {
+    if (!sums) {
+        // into `before` or, for this CTA's choices and those behind, into `total`
+        const int bound = (int)n, from = (int)min(first, n);
+#pragma unroll 4
+        for (int i = threadIdx.x; i < bound; i += kOrderThreads) {
             const int e = choice_expert(idx, i, n, experts);
-            if (e >= 0) {
-                atomicAdd(&total[e], 1);
-                if (i < first) atomicAdd(&before[e], 1);
-            }
+            if (e >= 0) atomicAdd(i < from ? &before[e] : &total[e], 1);
         }
+        __syncthreads();
+        for (int e = threadIdx.x; e < experts; e += kOrderThreads) total[e] += before[e];
+    }
     // A warp's choices are consecutive: counted first, so that each warp knows what lies before it.
     const int per_warp = per_cta / kOrderWarps;
     const int64_t mine = first + (int64_t)warp * per_warp;
@@ -192,11 +198,11 @@ int order_launch(const int32_t* idx, int64_t tokens, int topk, int experts, int3
     int* sums = n <= kOneLaunch ? nullptr : static_cast<int*>(work);
     cudaError_t e;
     if (sums) {
-        order_count_kernel<<<place, kOrderThreads, 0, s>>>(idx, n, experts, per, sums);
-        if ((e = cudaGetLastError()) != cudaSuccess) return set_cuda_error(e, "order count kernel launch");
+        e = launch_chained(order_count_kernel, dim3(place), kOrderThreads, 0, s, 1, idx, n, experts, per, sums);
+        if (e != cudaSuccess) return set_cuda_error(e, "order count kernel launch");
         count_launch();
-        order_sum_kernel<<<(experts + 7) / 8, 256, 0, s>>>(sums, place, experts);
-        if ((e = cudaGetLastError()) != cudaSuccess) return set_cuda_error(e, "order sum kernel launch");
+        e = launch_chained(order_sum_kernel, dim3((experts + 7) / 8), 256, 0, s, 1, sums, place, experts);
+        if (e != cudaSuccess) return set_cuda_error(e, "order sum kernel launch");
         count_launch();
     }
     // CTAs beyond those that place choices only help to mark unused rows
@@ -204,9 +210,9 @@ int order_launch(const int32_t* idx, int64_t tokens, int topk, int experts, int3
     const int64_t most = fill < 8 ? (fill > 0 ? fill : 1) : 8;
     const int grid = place > most ? place : (int)most;
     const size_t smem = sizeof(int) * ((size_t)(kOrderWarps + 3) * experts + 1);
-    order_place_kernel<<<grid, kOrderThreads, smem, s>>>(idx, n, topk, experts, per, place, sums, slot, row_of, rows,
-                                                         offsets, counts);
-    if ((e = cudaGetLastError()) != cudaSuccess) return set_cuda_error(e, "order kernel launch");
+    e = launch_chained(order_place_kernel, dim3(grid), kOrderThreads, smem, s, 1, idx, n, topk, experts, per, place, sums, slot,
+                       row_of, rows, offsets, counts);
+    if (e != cudaSuccess) return set_cuda_error(e, "order kernel launch");
     count_launch();
     return 0;
 }
@@ -254,6 +260,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     combine_kernel(const Ty* __restrict__ y, int64_t rows, int64_t cols, const int32_t* __restrict__ slot,
                    const float* __restrict__ weights, int64_t tokens, int topk, To* __restrict__ out) {
     constexpr int kW = VEC ? 8 : 1;
+    chain_wait();
     const int64_t spans = (cols + kCombineThreads * kW - 1) / (kCombineThreads * kW);
     for (int64_t job = blockIdx.x; job < tokens * spans; job += gridDim.x) {
         const int64_t t = job / spans;
@@ -287,6 +294,7 @@ __global__ void __launch_bounds__(kCombineThreads)
                             int topk, Ty* __restrict__ dy, float* __restrict__ dweights) {
     constexpr int kW = VEC ? 8 : 1;
     __shared__ float part[kCombineThreads / 32];
+    chain_wait();
     for (int64_t job = blockIdx.x; job < tokens * topk; job += gridDim.x) {
         const int64_t t = job / topk;
         const int r = slot[job];
@@ -347,11 +355,8 @@ static int combine_go(const void* y, int64_t rows, int64_t cols, const int32_t* 
     if (grid == 0) return -3;
     const Ty* yy = static_cast<const Ty*>(y);
     To* oo = static_cast<To*>(out);
-    if (vec)
-        combine_kernel<Ty, To, true><<<grid, kCombineThreads, 0, s>>>(yy, rows, cols, slot, weights, tokens, topk, oo);
-    else
-        combine_kernel<Ty, To, false><<<grid, kCombineThreads, 0, s>>>(yy, rows, cols, slot, weights, tokens, topk, oo);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_chained(vec ? combine_kernel<Ty, To, true> : combine_kernel<Ty, To, false>, dim3(grid),
+                                         kCombineThreads, 0, s, 1, yy, rows, cols, slot, weights, tokens, topk, oo);
     if (e != cudaSuccess) return set_cuda_error(e, "combine kernel launch");
     count_launch();
     return 0;
@@ -376,13 +381,9 @@ static int combine_back_go(const void* dout, const void* y, int64_t rows, int64_
     const Td* dd = static_cast<const Td*>(dout);
     const Ty* yy = static_cast<const Ty*>(y);
     Ty* oo = static_cast<Ty*>(dy);
-    if (vec)
-        combine_backward_kernel<Td, Ty, true>
-            <<<grid, kCombineThreads, 0, s>>>(dd, yy, rows, cols, slot, weights, tokens, topk, oo, dweights);
-    else
-        combine_backward_kernel<Td, Ty, false>
-            <<<grid, kCombineThreads, 0, s>>>(dd, yy, rows, cols, slot, weights, tokens, topk, oo, dweights);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_chained(vec ? combine_backward_kernel<Td, Ty, true> : combine_backward_kernel<Td, Ty, false>, dim3(grid),
+                       kCombineThreads, 0, s, 1, dd, yy, rows, cols, slot, weights, tokens, topk, oo, dweights);
     if (e != cudaSuccess) return set_cuda_error(e, "combine backward kernel launch");
     count_launch();
     return 0;

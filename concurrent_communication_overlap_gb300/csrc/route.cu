@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     const int at_lane = lane & (L - 1);
     const int E = a.experts, k = a.topk, e0 = at_lane * NI;
     const bool soft = a.score == 0;
+    chain_wait();
     float bias[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) bias[i] = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.0f;
@@ -324,6 +325,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     const int at_lane = lane & (L - 1);
     const int E = a.experts, k = a.topk;
     const bool soft = a.score == 0;
+    chain_wait();
     const int64_t step = (int64_t)gridDim.x * kRouteWarps * kRows;
     for (int64_t row0 = ((int64_t)blockIdx.x * kRouteWarps + warp) * kRows; row0 < tokens; row0 += step) {
         const int64_t row = row0 + lane / L;
@@ -400,8 +402,7 @@ static int route_grid(int64_t tokens, int lanes) {
     return (int)(need < most ? need : most);
 }
 
-static int route_done(const char* what) {
-    cudaError_t e = cudaGetLastError();
+static int route_done(cudaError_t e, const char* what) {
     if (e != cudaSuccess) return set_cuda_error(e, what);
     count_launch();
     return 0;
@@ -443,11 +444,13 @@ static int route_go(const RouteForm& f, cudaStream_t s, const T* x, int64_t ld, 
     const int grid = route_grid(tokens, L);
     if (grid == 0) return -3;
     const int vec = a.experts == L * NI && ((uintptr_t)x & 15u) == 0 && (ld * (int64_t)sizeof(T)) % 16 == 0;
-    const dim3 b(kRouteWarps * 32);
-    if (f.groups == 0) route_kernel<T, NI, L, 0><<<grid, b, 0, s>>>(x, ld, tokens, vec, a, idx, w);
-    else if (f.groups == 1) route_kernel<T, NI, L, 1><<<grid, b, 0, s>>>(x, ld, tokens, vec, a, idx, w);
-    else if constexpr (L == 32) route_kernel<T, NI, L, 2><<<grid, b, 0, s>>>(x, ld, tokens, vec, a, idx, w);
-    return route_done("route kernel launch");
+    const auto go = [&](auto kernel) {
+        return route_done(launch_chained(kernel, dim3(grid), kRouteWarps * 32, 0, s, 1, x, ld, tokens, vec, a, idx, w),
+                          "route kernel launch");
+    };
+    if constexpr (L == 32)
+        if (f.groups == 2) return go(route_kernel<T, NI, L, 2>);
+    return f.groups == 0 ? go(route_kernel<T, NI, L, 0>) : go(route_kernel<T, NI, L, 1>);
 }
 
 template <typename T, int NI, int L>
@@ -455,8 +458,9 @@ static int route_back_go(cudaStream_t s, const T* x, int64_t ld, int64_t tokens,
                          const float* dw, T* dx, int64_t dld) {
     const int grid = route_grid(tokens, L);
     if (grid == 0) return -3;
-    route_backward_kernel<T, NI, L><<<grid, kRouteWarps * 32, 0, s>>>(x, ld, tokens, a, idx, dw, dx, dld);
-    return route_done("route backward kernel launch");
+    return route_done(launch_chained(route_backward_kernel<T, NI, L>, dim3(grid), kRouteWarps * 32, 0, s, 1, x, ld, tokens, a,
+                                     idx, dw, dx, dld),
+                      "route backward kernel launch");
 }
 
 // f.lanes and f.per_lane as template arguments NI_ and L_ of CALL.
