@@ -178,7 +178,7 @@ __device__ __forceinline__ void expert_tiles(const Fp4GemmArgs& g, int* prefix, 
 // turn them through 2 KB of shared memory each, and write whole 64-byte pieces
 // of rows.
 constexpr int kPN = 192;  // columns of one accumulator
-constexpr int kPThreads = 384;
+constexpr int kPThreads = 352;  // producer, MMA, scales, and the epilogue's eight warps
 constexpr int kPEpiWarps = 8;
 
 template <bool NV, int MSUB, int NSUB, typename TC>
@@ -270,51 +270,55 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t* v) {
                  : "r"(addr)
                  : "memory");
 }
-// 16 fp32 values of this lane's row to 64 bytes (fp32) or 32 values to 64 bytes
-// (bf16) of shared memory, then the warp's 32 rows to C, a quarter warp a row.
-// Chunk j of row r lies at chunk j ^ ((r >> 1) & 3): no bank conflicts either way.
-template <typename TC>
-__device__ __forceinline__ void store_rows(uint32_t blk, int lane, const uint32_t* v, TC* C, int64_t row0, int rows,
-                                           int col0, int N) {
-    constexpr int kPer = 16 / sizeof(TC);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        st_shared_v4(blk + (uint32_t)lane * 64u + (uint32_t)((j ^ ((lane >> 1) & 3)) << 4), v[4 * j], v[4 * j + 1],
-                     v[4 * j + 2], v[4 * j + 3]);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + (lane >> 2), j = lane & 3;
-        uint32_t u[4];
-        ld_shared_v4(blk + (uint32_t)r * 64u + (uint32_t)((j ^ ((r >> 1) & 3)) << 4), u);
-        const int col = col0 + j * kPer;
-        if (r < rows && col < N)
-            *reinterpret_cast<uint4*>(C + (row0 + r) * (int64_t)N + col) = make_uint4(u[0], u[1], u[2], u[3]);
+// 64 bytes of each of the warp's 32 rows (16 fp32 or 32 bf16 values a lane, its
+// row's) to C by way of shared memory, so that neighbouring lanes write neighbouring
+// bytes, W at a time: 16 where rows of C are whole 16-byte units, else 4 or 2 (a lane
+// writing its own row instead took 1485 us for 6978 x 23694 x 1942, 241 this way).
+// Columns past N and rows past `rows` are left alone.  The 16-byte chunk j of row r
+// lies at chunk j ^ ((r >> 1) & 3): no bank conflicts at 16 bytes either way.
+template <typename TC, int W>
+__device__ __forceinline__ void write_rows(uint32_t blk, int lane, TC* C, int64_t row0, int rows, int col0, int N) {
+    constexpr int kLanes = 64 / W, kAtOnce = 32 / kLanes;  // lanes a row, rows at once
+    const int in = (lane % kLanes) * W, col = col0 + in / (int)sizeof(TC);
+    if (col >= N) rows = 0;
+    TC* c = C + (row0 + lane / kLanes) * (int64_t)N + col;
+#pragma unroll 4
+    for (int r = lane / kLanes; r < 32; r += kAtOnce, c += (int64_t)kAtOnce * N) {
+        const uint32_t at = blk + (uint32_t)(r * 64 + (((in >> 4) ^ ((r >> 1) & 3)) << 4) + (in & 15));
+        if (r >= rows) break;
+        if constexpr (W == 16) {
+            uint32_t u[4];
+            ld_shared_v4(at, u);
+            *reinterpret_cast<uint4*>(c) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else if constexpr (W == 4) {
+            uint32_t u;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u) : "r"(at) : "memory");
+            *reinterpret_cast<uint32_t*>(c) = u;
+        } else {
+            uint16_t u;
+            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(u) : "r"(at) : "memory");
+            *reinterpret_cast<uint16_t*>(c) = u;
+        }
     }
-    __syncwarp();
 }
 
-// A 32 x 32 piece, already rounded to TC, to C; columns past N and rows past
-// `rows` are left alone.  vec: rows of C are whole 16-byte units.
+// A 32 x 32 piece, already rounded to TC.
 template <typename TC>
-__device__ __forceinline__ void store_piece(const uint32_t* v, uint32_t blk, int lane, bool vec, TC* C, int64_t row0,
+__device__ __forceinline__ void store_piece(const uint32_t* v, uint32_t blk, int lane, int width, TC* C, int64_t row0,
                                             int rows, int col0, int N) {
-    if (vec) {
 #pragma unroll
-        for (int h = 0; h < (int)sizeof(TC) / 2; ++h)
-            store_rows<TC>(blk, lane, v + 16 * h, C, row0, rows, col0 + 16 * h, N);
-    } else if (lane < rows) {
-        TC* crow = C + (row0 + lane) * (int64_t)N;
+    for (int h = 0; h < (int)sizeof(TC) / 2; ++h) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (col0 + j < N) {
-                if constexpr (sizeof(TC) == 2)
-                    crow[col0 + j] = __ushort_as_bfloat16((unsigned short)(v[j / 2] >> (16 * (j & 1))));
-                else
-                    crow[col0 + j] = __uint_as_float(v[j]);
-            }
+        for (int j = 0; j < 4; ++j)
+            st_shared_v4(blk + (uint32_t)lane * 64u + (uint32_t)((j ^ ((lane >> 1) & 3)) << 4), v[16 * h + 4 * j],
+                         v[16 * h + 4 * j + 1], v[16 * h + 4 * j + 2], v[16 * h + 4 * j + 3]);
+        __syncwarp();
+        const int col = col0 + 16 * h;
+        if (width == 16) write_rows<TC, 16>(blk, lane, C, row0, rows, col, N);
+        else if (sizeof(TC) == 4 || width >= 4) write_rows<TC, 4>(blk, lane, C, row0, rows, col, N);
+        else write_rows<TC, 2>(blk, lane, C, row0, rows, col, N);
+        __syncwarp();
     }
-    __syncwarp();
 }
 
 // tmA, tmB: codes; tmSA, tmSB: scales as [row tiles][k tiles * 64] 64-bit words.
@@ -366,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     chain_wait();
-    if (MSUB == 1 && g.offsets && warp == 2) expert_tiles<kRows>(g, prefix, lane);
+    if (MSUB == 1 && g.offsets && warp == 3) expert_tiles<kRows>(g, prefix, lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();  // both CTAs' barriers are ready before either signals the other's
@@ -474,8 +478,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             volatile int no_abort = 0;
             if (!mbar_wait(bar(DRAIN), 0, &no_abort)) report_error(st, -4, kSiteFp4Drain);
         }
-    } else if (warp < 4) {
-        if (warp == 2 && rank == 0) {
+    } else if (warp == 2) {
+        if (rank == 0) {
             // ---------------- scales from shared memory to TMEM, in both CTAs
             const uint32_t lead = elect_lane();
             const uint64_t scale0 = scale_desc(base + Cfg::kABytes + Cfg::kBBytes);
@@ -513,9 +517,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                 }
         }
     } else {
-        const int q = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t blk = staging + (uint32_t)(warp - 4) * 2048u;
-        const bool vec = ((int64_t)g.N * (int)sizeof(TC)) % 16 == 0;
+        const int q = warp & 3, half = (warp - 3) >> 2;
+        const uint32_t blk = staging + (uint32_t)(warp - 3) * 2048u;
+        // bytes that every row of C is aligned to, 16 at most
+        const int row_bytes = g.N * (int)sizeof(TC), width = min(row_bytes & -row_bytes, 16);
         const float ga = g.ga ? *g.ga : 1.0f;
         int local = 0;
         for (int t = first; t < total; t += step, ++local) {
@@ -565,7 +570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i)
-                    store_piece<TC>(&v[i * kWords], blk, lane, vec, static_cast<TC*>(g.C), tile.row0 + r0, rows,
+                    store_piece<TC>(&v[i * kWords], blk, lane, width, static_cast<TC*>(g.C), tile.row0 + r0, rows,
                                     col0 + (b + i) * 32, g.N);
             }
         }
