@@ -82,13 +82,9 @@ __device__ __forceinline__ uint32_t mx_byte(uint32_t u, bool bad) {
     return bad ? 0xffu : (uint32_t)min(max(e, 0), 253);
 }
 
-// Scale byte and codes of 16 columns a thread.  MX: the thread's neighbour (lane ^ 1) holds the block's other half.
+// Codes of 16 values whose block has the largest magnitude amax (NaN if one of them is).
 template <bool NV>
-__device__ __forceinline__ void encode16(float (&v)[16], uint32_t& byte, uint2& codes) {
-    float amax = max_abs_nan(v[0], v[1]);
-#pragma unroll
-    for (int i = 2; i < 16; ++i) amax = max_abs_nan(amax, v[i]);
-    if (!NV) amax = max_abs_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+__device__ __forceinline__ void encode16(float (&v)[16], float amax, uint32_t& byte, uint2& codes) {
     const bool bad = !(amax <= 3.402823466e38f);
     if (!NV) {
         byte = mx_byte(__float_as_uint(amax), bad);
@@ -114,6 +110,14 @@ __device__ __forceinline__ void encode16(float (&v)[16], uint32_t& byte, uint2& 
     codes.x = to_codes(v);
     codes.y = to_codes(v + 8);
     if (NV && byte == 0u) codes.x = codes.y = 0u;
+}
+// The largest magnitude of the block of 16 (NV) or 32 (MX: the other half is with lane ^ 1) values.
+template <bool NV>
+__device__ __forceinline__ float block_max(const float (&v)[16]) {
+    float amax = max_abs_nan(v[0], v[1]);
+#pragma unroll
+    for (int i = 2; i < 16; ++i) amax = max_abs_nan(amax, v[i]);
+    return NV ? amax : max_abs_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
 }
 
 // ---- bf16 rows to MX codes, two values an instruction
@@ -161,14 +165,17 @@ __device__ __forceinline__ uint32_t eight_codes(const uint32_t* w, uint32_t inv)
     r |= two_codes(bmul2(__byte_perm(w[1], w[3], 0x7632), inv)) << 12;
     return r;
 }
-// Scale byte and codes of 16 columns a thread; its neighbour (lane ^ 1) holds the block's other half.
-__device__ __forceinline__ void encode16_mx_bf16(const uint32_t (&w)[8], uint32_t& byte, uint2& codes) {
+// The largest magnitude of 16 bf16 values, in the low half, and (MX) of the 16 with lane ^ 1; as fp32 bits.
+template <bool NV>
+__device__ __forceinline__ uint32_t block_max_bf16(const uint32_t (&w)[8]) {
     uint32_t m = w[0] & 0x7fff7fffu;
 #pragma unroll
     for (int i = 1; i < 8; ++i) m = bmax2_nan(m, w[i] & 0x7fff7fffu);
-    m = bmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = bmax2_nan(m, m >> 16);
-    const uint32_t u = m << 16;  // the low half as fp32
+    if (!NV) m = bmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return bmax2_nan(m, m >> 16) << 16;
+}
+__device__ __forceinline__ void encode16_mx_bf16(const uint32_t (&w)[8], uint32_t& byte, uint2& codes) {
+    const uint32_t u = block_max_bf16<false>(w);
     byte = mx_byte(u, u >= 0x7f800000u);
     const uint32_t inv = ((254u - min(byte, 253u)) << 7) * 0x00010001u;  // 2^-e in both halves
     codes.x = eight_codes(w, inv);
@@ -232,13 +239,9 @@ struct Raw16 {
     }
 };
 
-template <bool NV>
-__device__ __forceinline__ void encode_scaled(float (&v)[16], float inv_t, uint32_t& byte, uint2& codes) {
-    if (NV) {
+__device__ __forceinline__ void scale16(float (&v)[16], float t) {
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) unpack2(mul2(pack2(v[j], v[j + 1]), pack2(inv_t, inv_t)), v[j], v[j + 1]);
-    }
-    encode16<NV>(v, byte, codes);
+    for (int j = 0; j < 16; j += 2) unpack2(mul2(pack2(v[j], v[j + 1]), pack2(t, t)), v[j], v[j + 1]);
 }
 
 // One CTA: 32 rows of one matrix, 128 columns at a time, `across` CTAs a row tile;
@@ -281,7 +284,16 @@ __global__ void __launch_bounds__(kQThreads)
         } else {
             float v[16];
             now.values(v);
-            encode_scaled<NV>(v, inv_t, byte, codes);
+            float amax;
+            if constexpr (sizeof(T) == 2) {
+                // multiplying by a number and rounding keep the order: the maximum may come first
+                amax = __uint_as_float(block_max_bf16<NV>(now.w)) * fabsf(inv_t);
+                scale16(v, inv_t);
+            } else {
+                if (NV) scale16(v, inv_t);
+                amax = block_max<NV>(v);
+            }
+            encode16<NV>(v, amax, byte, codes);
         }
         put16<NV>(byte, codes, have, q, (int64_t)mat * q.rows + r, tile_row, c, pitch, k_tiles);
         now = ahead;
@@ -320,7 +332,8 @@ __global__ void __launch_bounds__(kQThreads)
         for (int j = 0; j < 16; ++j) v[j] = tile[h * 128 + g * 16 + j][i];
         uint32_t byte;
         uint2 codes;
-        encode_scaled<NV>(v, inv_t, byte, codes);
+        if (NV) scale16(v, inv_t);
+        encode16<NV>(v, block_max<NV>(v), byte, codes);
         put16<NV>(byte, codes, r < q.rows, q, (int64_t)mat * q.rows + r, tile_row, c + h * 128, pitch, k_tiles);
     }
 }

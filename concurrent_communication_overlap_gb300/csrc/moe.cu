@@ -32,6 +32,19 @@ __device__ __forceinline__ int choice_expert(const int32_t* idx, int64_t i, int6
     return (e >= 0 && e < experts) ? e : -1;
 }
 
+// Adds choices [from, to) to counts in shared memory; eight loads at a time, which the
+// adds would otherwise keep apart.
+__device__ __forceinline__ void count_choices(const int32_t* idx, int64_t from, int64_t to, int experts, int* counts) {
+    for (int64_t i0 = from + threadIdx.x; i0 < to; i0 += 8 * kOrderThreads) {
+        int e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = choice_expert(idx, i0 + j * kOrderThreads, to, experts);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (e[j] >= 0) atomicAdd(&counts[e[j]], 1);
+    }
+}
+
 // Counts of choices [first, first + per_cta) of each CTA.
 __global__ void __launch_bounds__(kOrderThreads)
     order_count_kernel(const int32_t* __restrict__ idx, int64_t n, int experts, int per_cta, int* __restrict__ counts) {
@@ -40,10 +53,7 @@ __global__ void __launch_bounds__(kOrderThreads)
     for (int e = threadIdx.x; e < experts; e += kOrderThreads) c[e] = 0;
     __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * per_cta;
-    for (int i = threadIdx.x; i < per_cta; i += kOrderThreads) {
-        const int e = choice_expert(idx, first + i, n, experts);
-        if (e >= 0) atomicAdd(&c[e], 1);
-    }
+    count_choices(idx, first, min(n, first + per_cta), experts, c);
     __syncthreads();
     for (int e = threadIdx.x; e < experts; e += kOrderThreads) counts[(size_t)blockIdx.x * experts + e] = c[e];
 }
@@ -91,13 +101,9 @@ __global__ void __launch_bounds__(kOrderThreads)
         for (int i = threadIdx.x; i < kOrderWarps * experts; i += kOrderThreads) hist[i] = 0;
     __syncthreads();
     if (!sums) {
-        // into `before` or, for this CTA's choices and those behind, into `total`
-        const int bound = (int)n, from = (int)min(first, n);
-#pragma unroll 4
-        for (int i = threadIdx.x; i < bound; i += kOrderThreads) {
-            const int e = choice_expert(idx, i, n, experts);
-            if (e >= 0) atomicAdd(i < from ? &before[e] : &total[e], 1);
-        }
+        // the choices of the CTAs before, then this CTA's and those behind
+        count_choices(idx, 0, min(first, n), experts, before);
+        count_choices(idx, min(first, n), n, experts, total);
         __syncthreads();
         for (int e = threadIdx.x; e < experts; e += kOrderThreads) total[e] += before[e];
     }
@@ -123,11 +129,13 @@ __global__ void __launch_bounds__(kOrderThreads)
     }
     if (lane == 31) warp_sums[warp] = incl;
     if (places && (int)threadIdx.x < experts) {
-        int run = before[threadIdx.x];
+        int c[kOrderWarps], run = before[threadIdx.x];
+#pragma unroll
+        for (int w = 0; w < kOrderWarps; ++w) c[w] = hist[w * experts + threadIdx.x];
+#pragma unroll
         for (int w = 0; w < kOrderWarps; ++w) {
-            const int c = hist[w * experts + threadIdx.x];
             hist[w * experts + threadIdx.x] = run;
-            run += c;
+            run += c[w];
         }
     }
     __syncthreads();

@@ -58,8 +58,9 @@ static int check_fp4(const c3_fp4* m, Fp4* q) {
     if (m->rows < 0 || m->cols < 1 || m->count < 1)
         return set_error(C3_EINVAL, "a 4-bit matrix needs rows >= 0, cols >= 1 and count >= 1");
     if (m->format == C3_FP4_MX && m->tensor_scale) return set_error(C3_EINVAL, "C3_FP4_MX has no tensor_scale");
-    if (m->cols > kMaxRows || m->count > 65535 || (m->rows && m->count > kMaxRows / m->rows))
-        return set_error(C3_EUNSUP, "4-bit matrix above 2^31-1 rows or columns");
+    // (a tile's rows past the last one must still have 32-bit numbers)
+    if (m->cols > kMaxRows || m->count > 65535 || (m->rows && m->count > (kMaxRows - 1023) / m->rows))
+        return set_error(C3_EUNSUP, "4-bit matrix near or above 2^31 rows or columns");
     if (m->rows) {
         if (!m->codes || !m->scales) return set_error(C3_EINVAL, "codes or scales is NULL");
         if (!aligned(m->codes, 16) || !aligned(m->scales, 16))

@@ -459,7 +459,7 @@ int c3_selftest_wait(uint64_t limit_ns, int arrive, c3_stream s);
  * Host-side failure injection, so that a caller's error paths (and this
  * library's own recovery) can be tested without faulting a GPU.  Arms a
  * one-shot failure of the next call, on any thread, that reaches `site`:
- *   C3_FAULT_GEMM_LAUNCH     the GEMM kernel launch
+ *   C3_FAULT_GEMM_LAUNCH     the GEMM kernel launch (c3_gemm's, or a 4-bit product's)
  *   C3_FAULT_SM_COLL_LAUNCH  an SM collective kernel launch (copy or reduce-scatter)
  *   C3_FAULT_MEMCPY          the memcpy path's transfer calls
  *   C3_FAULT_DEVICE_INIT     the per-device initialisation (as if allocating the

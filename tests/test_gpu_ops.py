@@ -315,6 +315,11 @@ SMALL = [
     dict(E=60, k=6, score="softmax"),
     dict(E=64, k=8, score="sigmoid"),
     dict(E=33, k=3, score="softmax", bias=True),
+    dict(E=128, k=16, score="softmax", renorm=True),
+    dict(E=64, k=6, score="sigmoid", G=4, keep=2, best=2, renorm=True, bias=True),
+    dict(E=256, k=8, score="sigmoid", G=8, keep=4, best=2, bias=True, scale=2.5),
+    dict(E=250, k=12, score="softmax", G=2, keep=1),
+    dict(E=100, k=4, score="sigmoid", G=25, keep=3),
 ]
 
 
@@ -322,7 +327,7 @@ SMALL = [
 @pytest.mark.parametrize("T", [8192, 8237])
 @pytest.mark.parametrize("r", SMALL, ids=lambda r: "_".join(f"{k}{v}" for k, v in r.items()))
 def test_route_many_tokens(c3, r, T, ty):
-    """Few experts and many tokens take a form of their own: the same results as for few tokens, and the definition's."""
+    """Many tokens share a warp where few do not (below 4096): the same results, and the definition's."""
     rng = np.random.default_rng(T + r["E"])
     E, k = r["E"], r["k"]
     x = grid_logits(rng, T, E)
@@ -334,18 +339,18 @@ def test_route_many_tokens(c3, r, T, ty):
     bias = rng.integers(-8, 9, E) / 16.0 if r.get("bias") else None
     idx, w, router, wide = run_route(c3, r, x, ty, bias, extra=3)
     few_idx, few_w = torch.empty_like(idx), torch.empty_like(w)
-    for at in range(0, T, 4096):
-        n = min(4096, T - at)
+    for at in range(0, T, 4095):
+        n = min(4095, T - at)
         c3.c3_route(router, wide[at:], E + 3, n, few_idx[at:], few_w[at:])
     dw = cuda(rng.standard_normal((T, k)).astype(np.float32))
     dx, few_dx = Guarded((T, E + 1), TD[ty], 5.0), torch.full((T, E + 1), 5.0, dtype=TD[ty], device="cuda")
     c3.c3_route_backward(router, wide, E + 3, T, idx, dw, dx.t, E + 1)
-    for at in range(0, T, 4096):
-        n = min(4096, T - at)
+    for at in range(0, T, 4095):
+        n = min(4095, T - at)
         c3.c3_route_backward(router, wide[at:], E + 3, n, idx[at:], dw[at:], few_dx[at:], E + 1)
     torch.cuda.synchronize()
     assert dx.intact() and bool((dx.t[:, E:] == 5.0).all())
-    by_logit = r["score"] == "softmax" and bias is None
+    by_logit = r["score"] == "softmax" and bias is None and r.get("best", 1) == 1
     if by_logit or r["score"] == "sigmoid":   # keys that no sum over the row enters
         assert torch.equal(idx, few_idx)
     same = (idx == few_idx).all(1)
@@ -534,8 +539,9 @@ def test_quantise(c3, R, C, fmt, ty, transpose):
             assert np.array_equal(o.t[:, :C].float().cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("ty", [0, 1])
 @pytest.mark.parametrize("fmt", [0, 1])
-def test_quantise_special_values(c3, fmt):
+def test_quantise_special_values(c3, fmt, ty):
     x = np.ones((6, 64), np.float32)
     x[0, 3] = np.nan
     x[1, 40] = np.inf
@@ -544,8 +550,13 @@ def test_quantise_special_values(c3, fmt):
     x[4] = np.finfo(np.float32).max
     x[5, :32] = 0
     x[5, 5] = -0.0
+    x[5, 32:] = np.repeat([6, 5, 2.5, 0.25, 0.75, 1.25, 3.5, -5], 4)
     q, codes, scales = new_fp4(c3, 6, 64, fmt)
-    c3.c3_fp4_quantize(cuda(x), 0, 6, 64, q)
+    if ty:
+        x[4] = 3.3e38
+    t = cuda(x).to(TD[ty])
+    x = t.float().cpu().numpy()
+    c3.c3_fp4_quantize(t, ty, 6, 64, q)
     o = torch.empty(6, 64, device="cuda")
     c3.c3_fp4_dequantize(q, o, 0, 64)
     torch.cuda.synchronize()
@@ -682,6 +693,22 @@ def test_product_carries_nan_blocks(c3, fmt):
     C = C.cpu().numpy()
     assert np.array_equal(np.isnan(C), nan)
     assert np.allclose(C[~nan], K, rtol=0.1)   # ones become 6/6, 4 * .25 or the like
+
+
+def test_an_injected_launch_failure_is_reported_once(c3):
+    rng = np.random.default_rng(3)
+    for M in (16, 300):   # both forms of the product
+        a, va = random_fp4(c3, rng, M, 128, 0)
+        b, vb = random_fp4(c3, rng, 200, 128, 0)
+        C = torch.full((M, 200), 7.0, device="cuda")
+        c3.c3_inject_fault(c3.C3_FAULT_GEMM_LAUNCH)
+        assert c3.c3_fp4_gemm(a, b, C, 0, check=False) == c3.C3_ECUDA
+        assert "injected" in c3.c3_last_error()
+        torch.cuda.synchronize()
+        assert bool((C == 7.0).all())
+        c3.c3_fp4_gemm(a, b, C, 0)
+        c3.c3_status_check()
+        assert close(f64(C), va[0], vb[0], 0, 128)
 
 
 def test_product_gradients_are_products(c3):
