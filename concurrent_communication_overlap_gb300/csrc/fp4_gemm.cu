@@ -4,17 +4,21 @@
 // the same for the experts of a sparse layer, whose rows of A lie one expert
 // after the other.
 //
-// Layout (one CTA per SM, 192 threads), as in the bf16 kernel:
-//   warp 0      producer: per stage 128 rows of A and BN rows of B, 256 columns
-//               of 4 bits each (one 128-byte swizzle row), by TMA, and their
-//               scales, which lie in memory as the tensor cores take them, by
-//               plain bulk copies;
-//   warp 1      TMEM owner and MMA issuer: the stage's scales go from shared
-//               memory to TMEM (tcgen05.cp, 128 rows x 4 scales an instruction,
-//               copied to all four lane quarters), then four MMAs of 64 columns;
-//   warps 2..5  epilogue: accumulator to registers, times the matrices' fp32
-//               scales, rounded once to the output type, to C.
-#include "c3_device.cuh"
+// Two kernels: many rows, two SMs on a tile; few rows, the operands' roles swapped.
+// fp4_plan picks.  Both have the same parts, warp by warp:
+//   producer   per stage 256 columns of 4 bits (one 128-byte swizzle row) of A's and
+//              B's rows and their scales, all by TMA; scales lie in memory as the
+//              tensor cores take them;
+//   MMA        four MMAs of 64 columns a stage and accumulator;
+//   scales     128 rows x 4 scales at a time from shared memory to TMEM, copied to all
+//              four lane quarters.  A warp of its own: copies that the MMA warp itself
+//              issues run between its MMAs instead of beside them, however early they
+//              are issued (8192 x 28672 x 8192: 886 us against 661, which is what it took
+//              without any copies; by way of registers and tcgen05.st: 1012);
+//   epilogue   accumulators to registers, times the matrices' fp32 scales, rounded
+//              once to the output type, to C.
+// Every wait is bounded, as in the bf16 kernel.
+#include "ops_device.cuh"
 #include "c3_internal.h"
 
 #include <cuda_bf16.h>
@@ -177,6 +181,10 @@ __device__ __forceinline__ void expert_tiles(const Fp4GemmArgs& g, int* prefix, 
 // epilogue's eight warps in each CTA read 32 x 32 pieces out of TMEM one ahead,
 // turn them through 2 KB of shared memory each, and write whole 64-byte pieces
 // of rows.
+//
+// 8192 x 28672 x 8192 takes 576 us, 6.7 PFLOP/s.  Copies with a part of the work left
+// out put what bounds it side by side: loads alone 463, MMAs alone about 380, and the
+// copies of scales another 70 beside them.
 constexpr int kPN = 192;  // columns of one accumulator
 constexpr int kPThreads = 352;  // producer, MMA, scales, and the epilogue's eight warps
 constexpr int kPEpiWarps = 8;
@@ -592,10 +600,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 // of a tile is padding that has to be brought in, and a warp stores 32
 // neighbours of one row of C.
 //
-// Two CTAs fit an SM: one's start and end hide behind the other's stream.  Where
+// Two CTAs fit an SM: one's start and end hide behind the other's stream (64
+// experts of 2048 x 4096 with 192 rows: 45 us, 5.8 TB/s of weights).  Where
 // there are fewer tiles than CTAs to fill the machine, a cluster of `split` CTAs
 // takes one tile, each a part of K; their fp32 parts meet in shared memory, each
-// CTA adding up its share of A's rows in the order of the ranks.
+// CTA adding up its share of A's rows in the order of the ranks.  13 x 8200 x 8072
+// takes 12.9 us in a chain of calls, where its bytes need 5.5; the rest is set-up, the
+// first loads' latency and the cluster's two meetings.
 constexpr int kRThreads = 256;
 
 template <bool NV, int NT>

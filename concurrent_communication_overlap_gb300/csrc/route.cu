@@ -9,7 +9,11 @@
 // Few lanes a token, because the exchange between lanes, which is the same for
 // one token as for four, is most of the work: 32768 x 60, 6 chosen, takes 354
 // instructions a token with 32 lanes and 192 with 8 (11 us against 15).
-#include "c3_device.cuh"
+//
+// Instructions are what bounds it, not bytes: 65536 x 256 with groups takes 66 us,
+// 765 instructions a token, a third of them the 256 sigmoids, where its bytes need
+// 10.5; 32768 x 60 takes 11 us forward and 9 backward, where they need 1 and 1.
+#include "ops_device.cuh"
 #include "c3_internal.h"
 
 #include <cuda_bf16.h>
