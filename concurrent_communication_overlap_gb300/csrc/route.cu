@@ -10,8 +10,8 @@
 // one token as for four, is most of the work: 32768 x 60, 6 chosen, takes 354
 // instructions a token with 32 lanes and 192 with 8 (11 us against 15).
 //
-// Instructions are what bounds it, not bytes: 65536 x 256 with groups takes 66 us,
-// 765 instructions a token, a third of them the 256 sigmoids, where its bytes need
+// Instructions are what bounds it, not bytes: 65536 x 256 with groups takes 59 us,
+// 717 instructions a token, a third of them the 256 sigmoids, where its bytes need
 // 10.5; 32768 x 60 takes 11 us forward and 9 backward, where they need 1 and 1.
 #include "ops_device.cuh"
 #include "c3_internal.h"
@@ -228,11 +228,14 @@ __device__ __forceinline__ float choice_weight(const T* xr, int mine, const Rout
 // NI experts a lane, L NI >= E.  GROUPS: 0 none, 1 whole runs of lanes, 2 any (L =
 // 32).  vec: rows are whole and 16-byte aligned.  topk <= L.
 template <typename T, int NI, int L, int GROUPS>
-__global__ void __launch_bounds__(kRouteWarps * 32)
+__global__ void __launch_bounds__(kRouteWarps * 32, NI == 16 ? 4 : 1)  // 64 registers: 62 us for 65536 x 256, 66 with 80
     route_kernel(const T* __restrict__ logits, int64_t ld, int64_t tokens, int vec, RouteArgs a,
                  int32_t* __restrict__ idx, float* __restrict__ weights) {
-    __shared__ uint32_t group_keys[GROUPS == 2 ? kRouteWarps : 1][GROUPS == 2 ? 1024 : 1];
     constexpr int kRows = 32 / L;  // tokens of a warp
+    constexpr bool kInMemory = NI >= 8;
+    // a warp's scratch: the groups' keys first, then the sorted lines
+    constexpr int kScratch = GROUPS == 2 ? 1024 : kInMemory ? NI * 32 : 1;
+    __shared__ uint32_t scratch[kRouteWarps][kScratch];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int at_lane = lane & (L - 1);
     const int E = a.experts, k = a.topk, e0 = at_lane * NI;
@@ -274,27 +277,46 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
             key[i] = x[i] > -INFINITY && v > -INFINITY ? order_key(v) : 0u;
         }
         if constexpr (GROUPS == 1) groups_by_lanes<NI, L>(key, E / a.groups, a.group_best, a.topk_groups, lane);
-        if constexpr (GROUPS == 2) groups_by_memory<NI>(key, group_keys[warp], E, a.groups, a.group_best, a.topk_groups, lane);
+        if constexpr (GROUPS == 2) groups_by_memory<NI>(key, scratch[warp], E, a.groups, a.group_best, a.topk_groups, lane);
         // The choice: every lane sorts its keys, and the best of the lanes' heads is
         // taken k times.  Lane j keeps the j-th: its key and the lane it came from.
         uint32_t line[NI];
 #pragma unroll
         for (int i = 0; i < NI; ++i) line[i] = key[i];
         sort_down<NI>(line);
+        // A line of eight or more waits in shared memory, which costs a load a choice instead
+        // of shifting it through registers.
         uint32_t my_key = 0u;
         int my_lane = 0;
+        uint32_t head = line[0];
+        const uint32_t* behind = nullptr;
+        if constexpr (kInMemory) {
+#pragma unroll
+            for (int i = 1; i < NI; ++i) scratch[warp][(i - 1) * 32 + lane] = line[i];
+            scratch[warp][(NI - 1) * 32 + lane] = 0u;
+            behind = &scratch[warp][lane];
+        }
         for (int j = 0; j < k; ++j) {
-            const uint32_t most = lanes_max<L>(line[0]);
-            const int from = __ffs(lanes_ballot<L>(line[0] == most, lane)) - 1;
+            const uint32_t most = lanes_max<L>(head);
+            const int from = __ffs(lanes_ballot<L>(head == most, lane)) - 1;
             if (at_lane == j) {
                 my_key = most;
                 my_lane = from;
             }
-            const bool take = at_lane == from;
+            const bool take = at_lane == from && most != 0u;
+            if constexpr (kInMemory) {
+                if (take) {
+                    head = *behind;
+                    behind += 32;
+                }
+            } else {
 #pragma unroll
-            for (int i = 0; i + 1 < NI; ++i) line[i] = take ? line[i + 1] : line[i];
-            line[NI - 1] = take ? 0u : line[NI - 1];
+                for (int i = 0; i + 1 < NI; ++i) line[i] = take ? line[i + 1] : line[i];
+                line[NI - 1] = take ? 0u : line[NI - 1];
+                head = line[0];
+            }
         }
+        if constexpr (GROUPS == 2) __syncwarp();  // the scratch is the groups' again
         // Which of that lane's experts it was: the first with the key, or the one after as
         // many as earlier choices took of the same key there.  Those are the choices just
         // before: equal keys go by lane, then by register.

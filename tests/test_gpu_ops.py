@@ -129,6 +129,8 @@ ROUTERS = [
     dict(E=512, k=10, score="sigmoid", bias=True),
     dict(E=1000, k=32, score="softmax"),
     dict(E=1024, k=8, score="sigmoid", G=2, keep=1, best=2, renorm=True),
+    dict(E=1000, k=6, score="sigmoid", G=50, keep=7, best=2, bias=True),
+    dict(E=402, k=5, score="softmax", G=201, keep=100),
 ]
 
 
