@@ -621,8 +621,10 @@ struct Fp4RowsCfg {
     static constexpr int kSmem = kStages * (int)kStage + kExtra;
     static constexpr int kAccBufs = NT == 128 ? 1 : 2;
     static constexpr int kSetCols = 8;
-    static constexpr int kSets = 128 / (kKT * kSetCols) > 4 ? 4 : 128 / (kKT * kSetCols);
-    static_assert(kStage % 1024 == 0 && kStages >= 3, "few-rows configuration");
+    // Stages whose scales TMEM holds: no more than the ring's, since a set's last use is
+    // told by that stage's empty barrier, which must not have come round twice.
+    static constexpr int kSets = kStages < 4 ? kStages : 4;
+    static_assert(kStage % 1024 == 0 && kStages >= 3 && kSets * kKT * kSetCols <= 128, "few-rows configuration");
     static_assert(kStages * kStage >= NT * 512, "the parts meet in the ring");
 };
 

@@ -651,7 +651,10 @@ def close(got, a, b, out, K):
 @pytest.mark.parametrize("M,N,K,budget", [
     (1, 1, 1, 0), (1, 128, 64, 0), (7, 5, 33, 0), (128, 128, 256, 0), (129, 127, 257, 0), (16, 1000, 520, 0),
     (300, 200, 1000, 0), (512, 640, 768, 3), (255, 513, 96, 1), (200, 264, 4104, 0), (64, 4096, 2048, 0),
-    (1000, 1032, 130, 0), (13, 384, 8072, 0), (2100, 520, 320, 0), (500, 1600, 2000, 0)])
+    (1000, 1032, 130, 0), (13, 384, 8072, 0), (2100, 520, 320, 0), (500, 1600, 2000, 0),
+    # few rows, long K, more tiles than would be split: every ring goes round several times
+    (128, 20000, 2304, 0), (64, 20000, 2304, 0), (20, 20000, 2304, 0), (100, 300, 9000, 2), (50, 300, 9000, 1),
+    (1100, 400, 9000, 4)])
 def test_product(c3, M, N, K, budget, fmt, out):
     rng = np.random.default_rng(M + N + K)
     a, va = random_fp4(c3, rng, M, K, fmt, 0.75 if fmt else None)
@@ -738,7 +741,9 @@ def test_product_gradients_are_products(c3):
 @pytest.mark.parametrize("E,N,K,counts,budget", [
     (1, 128, 256, [5], 0), (4, 130, 200, [0, 3, 0, 129], 0), (7, 256, 520, [1, 128, 127, 0, 300, 2, 0], 0),
     (3, 1000, 64, [64, 64, 64], 5), (5, 72, 1030, [0, 0, 0, 0, 1], 0), (2, 512, 300, [0, 0], 0),
-    (64, 384, 128, [i % 5 for i in range(64)], 0), (3, 640, 2048, [700, 1, 513], 0)])
+    (64, 384, 128, [i % 5 for i in range(64)], 0), (3, 640, 2048, [700, 1, 513], 0),
+    (40, 1024, 2304, [1 + i % 70 for i in range(40)], 0), (6, 260, 5000, [3, 0, 130, 65, 1, 2], 2),
+    (3, 500, 5000, [400, 300, 513], 6)])
 def test_experts_products(c3, E, N, K, counts, budget, fmt, out):
     rng = np.random.default_rng(E + N + K)
     offsets = np.concatenate([[0], np.cumsum([(c + 127) // 128 * 128 for c in counts])]).astype(np.int32)
