@@ -605,7 +605,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 // there are fewer tiles than CTAs to fill the machine, a cluster of `split` CTAs
 // takes one tile, each a part of K; their fp32 parts meet in shared memory, each
 // CTA adding up its share of A's rows in the order of the ranks.  13 x 8200 x 8072
-// takes 12.9 us in a chain of calls, where its bytes need 5.5; the rest is set-up, the
+// takes 11.7 us in a chain of calls, where its bytes need 5.5; the rest is set-up, the
 // first loads' latency and the cluster's two meetings.
 constexpr int kRThreads = 256;
 
@@ -844,7 +844,10 @@ __global__ void __launch_bounds__(kRThreads, 2)
         // The parts of a tile: share s of A's rows (NT / split of them) is added up by
         // rank s, from the parts that every rank writes into its ring, which is idle:
         // all MMAs and loads of the cluster are done at the first barrier.
-        const int share = NT / split;
+        // Four of A's rows make a piece: 16 bytes a lane, lane after lane, so that a warp
+        // sends 512 bytes in one run (a lane's pieces together, 64 bytes apart from the next
+        // lane's, took 22 us for 100 x 4096 x 4096 over 8 CTAs instead of 13).
+        const int share = NT / split, shift = __ffs(share) - 1;  // powers of two, 4 at least
         const bool live = first < total;
         const int q = warp & 3;
         bool go = true;
@@ -857,17 +860,18 @@ __global__ void __launch_bounds__(kRThreads, 2)
         if (warp >= 4 && live && go) {
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16);
-            const uint32_t mine = base + (uint32_t)(rank * share * 128 + q * 32 + lane) * 4u;
+            const uint32_t mine = base + (uint32_t)(rank * (share / 4) * 128 + q * 32 + lane) * 16u;
 #pragma unroll 1
             for (int j0 = 0; j0 < NT; j0 += 32) {
                 uint32_t r[32];
                 tmem_ld32(taddr + (uint32_t)j0, r);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int to = (j0 + j) / share, at = (j0 + j) - to * share;
-                    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(peer_addr(mine + (uint32_t)at * 512u, (uint32_t)to)),
-                                 "r"(r[j])
+                for (int j = 0; j < 32; j += 4) {
+                    const int to = (j0 + j) >> shift, piece = ((j0 + j) & (share - 1)) >> 2;
+                    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     peer_addr(mine + (uint32_t)piece * 2048u, (uint32_t)to)),
+                                 "r"(r[j]), "r"(r[j + 1]), "r"(r[j + 2]), "r"(r[j + 3])
                                  : "memory");
                 }
             }
@@ -878,13 +882,22 @@ __global__ void __launch_bounds__(kRThreads, 2)
             const Fp4Tile tile = fp4_tile<NT>(g, prefix, first);
             const float alpha = (g.ga ? *g.ga : 1.0f) * (g.gb ? g.gb[tile.expert] : 1.0f);
             const int n = tile.nb * 128 + q * 32 + lane;
-            const float* part = reinterpret_cast<const float*>(gbase) + q * 32 + lane;
-            for (int at = 0; at < share; ++at) {
-                const int j = (int)rank * share + at;
-                if (j >= tile.rows || n >= g.N) break;
-                float sum = 0.0f;
-                for (int s = 0; s < split; ++s) sum += part[(s * share + at) * 128];
-                static_cast<TC*>(g.C)[(tile.row0 + j) * (int64_t)g.N + n] = (TC)(alpha * sum);
+            const float4* part = reinterpret_cast<const float4*>(gbase) + q * 32 + lane;
+            const int mine = min(share, tile.rows - (int)rank * share);
+            TC* c = static_cast<TC*>(g.C) + (tile.row0 + (int)rank * share) * (int64_t)g.N + n;
+#pragma unroll 2
+            for (int at = 0; at < mine; at += 4) {
+                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    if (s < split) {
+                        const float4 v = part[(s * (share / 4) + (at >> 2)) * 128];
+                        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                    }
+                const float out[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n < g.N && at + i < mine) c[(int64_t)(at + i) * g.N] = (TC)(alpha * out[i]);
             }
         }
     }
@@ -1018,8 +1031,12 @@ static Fp4Plan fp4_plan(int64_t M, int64_t N, int64_t K, int experts, bool group
     const int64_t busy = grouped ? (experts < up(M, kTileRows) ? experts : up(M, kTileRows)) * n : tiles;
     // A budget below the whole machine is kept to the letter: one CTA for each SM of it.
     const int64_t slots = cap < sms ? cap : 2 * (int64_t)cap;
+    // The parts' meeting grows with their number and with the rows: up to 8 for 32 rows (32 x
+    // 1024 x 8192: 6.6 us with 8, 7.4 with 4, 11.5 with 1), 4 above (100 x 4096 x 4096: 13.3,
+    // 11.9 and 11.7; 128 x 8192 x 8192: 15.7 with 4, 20.6 with 1).
+    const int most_parts = p.rows == 32 ? 8 : 4;
     p.split = 1;
-    while (p.split < 8 && busy * p.split * 2 <= slots && kb >= 4 * p.split && !(grouped && cap < sms)) p.split *= 2;
+    while (p.split < most_parts && busy * p.split * 2 <= slots && kb >= 4 * p.split && !(grouped && cap < sms)) p.split *= 2;
     p.ctas = p.split > 1 ? (int)(tiles * p.split) : (int)(grouped || slots < tiles ? slots : tiles);
     return p;
 }
