@@ -229,122 +229,161 @@ int order_launch(const int32_t* idx, int64_t tokens, int topk, int experts, int3
 
 // ---------------------------------------------------------------- combine
 
-// Eight consecutive values as fp32, whatever the type.
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+// W consecutive values as fp32, whatever the type: 16 bytes at most at once.
+template <int W>
+__device__ __forceinline__ void load_w(const float* p, float (&v)[W]) {
+    if constexpr (W == 8) {
+        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else if constexpr (W == 2) {
+        const float2 a = *reinterpret_cast<const float2*>(p);
+        v[0] = a.x, v[1] = a.y;
+    } else {
+        v[0] = *p;
     }
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-    uint32_t u[4];
+template <int W>
+__device__ __forceinline__ void load_w(const __nv_bfloat16* p, float (&v)[W]) {
+    if constexpr (W == 1) {
+        v[0] = __bfloat162float(*p);
+    } else {
+        uint32_t u[W / 2];
+        if constexpr (W == 8) {
+            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w;
+        } else {
+            u[0] = *reinterpret_cast<const uint32_t*>(p);
+        }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int i = 0; i < W / 2; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+template <int W>
+__device__ __forceinline__ void store_w(float* p, const float (&v)[W]) {
+    if constexpr (W == 8) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else if constexpr (W == 2) {
+        *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    } else {
+        *p = v[0];
+    }
+}
+template <int W>
+__device__ __forceinline__ void store_w(__nv_bfloat16* p, const float (&v)[W]) {
+    if constexpr (W == 1) {
+        *p = __float2bfloat16_rn(v[0]);
+    } else {
+        uint32_t u[W / 2];
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if constexpr (W == 8)
+            *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+        else
+            *reinterpret_cast<uint32_t*>(p) = u[0];
+    }
+}
 
 constexpr int kCombineThreads = 256;
+constexpr int kCombineWarps = kCombineThreads / 32;
+constexpr int kSpan = 256;  // columns a warp takes at once: 8 a lane, W by W
 
-// out[t] = sum_j w[t][j] y[slot[t][j]], in fp32, j ascending.  A CTA takes one
-// token and a span of columns, so that each row is read in whole runs wherever it
-// lies; VEC: rows are 16-byte aligned, 8 columns a thread.  Bytes bound it: 8192
-// tokens of 8 rows of 4096 bf16 take 100 us, 6.0 TB/s.
-template <typename Ty, typename To, bool VEC>
+// out[t] = sum_j w[t][j] y[slot[t][j]], in fp32, j ascending.  A warp takes one
+// token and kSpan columns, so that each row is read in whole runs wherever it lies,
+// and few or odd columns leave no CTA half empty; lane j fetches the j-th slot and
+// weight for all.  Bytes bound it: 8192 tokens of 8 rows of 4096 bf16 take 102 us,
+// 5.9 TB/s; 8192 of 4 rows of 2171, one value at a time, 63 us where the bytes need 26.
+template <typename Ty, typename To, int W>
 __global__ void __launch_bounds__(kCombineThreads)
     combine_kernel(const Ty* __restrict__ y, int64_t rows, int64_t cols, const int32_t* __restrict__ slot,
                    const float* __restrict__ weights, int64_t tokens, int topk, To* __restrict__ out) {
-    constexpr int kW = VEC ? 8 : 1;
+    const int lane = threadIdx.x & 31;
+    constexpr int U = kSpan / (32 * W);
+    const int64_t spans = (cols + kSpan - 1) / kSpan, jobs = tokens * spans;
     chain_wait();
-    const int64_t spans = (cols + kCombineThreads * kW - 1) / (kCombineThreads * kW);
-    for (int64_t job = blockIdx.x; job < tokens * spans; job += gridDim.x) {
+    for (int64_t job = (int64_t)blockIdx.x * kCombineWarps + (threadIdx.x >> 5); job < jobs;
+         job += (int64_t)gridDim.x * kCombineWarps) {
         const int64_t t = job / spans;
-        const int64_t c = ((job - t * spans) * kCombineThreads + threadIdx.x) * kW;
-        if (c >= cols) continue;
-        float acc[kW] = {};
+        const int64_t c0 = (job - t * spans) * kSpan + lane * W;
+        int r = lane < topk ? slot[t * topk + lane] : -1;
+        if (r >= rows) r = -1;
+        const float w = lane < topk && weights ? weights[t * topk + lane] : 1.0f;
+        float acc[U][W] = {};
+#pragma unroll (W == 8 ? 4 : 2)
         for (int j = 0; j < topk; ++j) {
-            const int r = __ldg(slot + t * topk + j);
-            if (r < 0 || r >= rows) continue;
-            const float w = weights ? __ldg(weights + t * topk + j) : 1.0f;
-            float v[kW];
-            if constexpr (VEC)
-                load8(y + (int64_t)r * cols + c, v);
-            else
-                v[0] = load1(y + (int64_t)r * cols + c);
+            const int rj = __shfl_sync(kAll, r, j);
+            const float wj = __shfl_sync(kAll, w, j);
+            if (rj < 0) continue;
+            const Ty* yr = y + (int64_t)rj * cols;
+            float v[U][W];
 #pragma unroll
-            for (int i = 0; i < kW; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+            for (int u = 0; u < U; ++u)
+                if (c0 + 32 * W * u < cols) load_w<W>(yr + c0 + 32 * W * u, v[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + 32 * W * u < cols) {
+#pragma unroll
+                    for (int i = 0; i < W; ++i) acc[u][i] = fmaf(wj, v[u][i], acc[u][i]);
+                }
         }
-        if constexpr (VEC)
-            store8(out + t * cols + c, acc);
-        else
-            store1(out + t * cols + c, acc[0]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + 32 * W * u < cols) store_w<W>(out + t * cols + c0 + 32 * W * u, acc[u]);
     }
 }
 
-// dy[slot] = w dout[t] and dw = <dout[t], y[slot]>: one CTA a choice, which reads
-// its row of y and of dout once for both.  The same 8192 tokens take 203 us, 5.6 TB/s.
-template <typename Td, typename Ty, bool VEC>
+// dy[slot] = w dout[t] and dw = <dout[t], y[slot]>: one warp a choice, which reads
+// its row of y and of dout once for both.  The same 8192 tokens take 171 us, 6.7 TB/s.
+template <typename Td, typename Ty, int W>
 __global__ void __launch_bounds__(kCombineThreads)
     combine_backward_kernel(const Td* __restrict__ dout, const Ty* __restrict__ y, int64_t rows, int64_t cols,
                             const int32_t* __restrict__ slot, const float* __restrict__ weights, int64_t tokens,
                             int topk, Ty* __restrict__ dy, float* __restrict__ dweights) {
-    constexpr int kW = VEC ? 8 : 1;
-    __shared__ float part[kCombineThreads / 32];
+    constexpr int U = kSpan / (32 * W);
+    const int lane = threadIdx.x & 31;
     chain_wait();
-    for (int64_t job = blockIdx.x; job < tokens * topk; job += gridDim.x) {
-        const int64_t t = job / topk;
+    for (int64_t job = (int64_t)blockIdx.x * kCombineWarps + (threadIdx.x >> 5); job < tokens * topk;
+         job += (int64_t)gridDim.x * kCombineWarps) {
         const int r = slot[job];
         float dot = 0.0f;
         if (r >= 0 && r < rows) {
             const float w = weights ? weights[job] : 1.0f;
-            for (int64_t c = (int64_t)threadIdx.x * kW; c < cols; c += kCombineThreads * kW) {
-                float d[kW], v[kW];
-                if constexpr (VEC) {
-                    load8(dout + t * cols + c, d);
-                    if (dweights) load8(y + (int64_t)r * cols + c, v);
-                } else {
-                    d[0] = load1(dout + t * cols + c);
-                    if (dweights) v[0] = load1(y + (int64_t)r * cols + c);
+            const Td* dr = dout + job / topk * cols;
+            const int64_t at = (int64_t)r * cols;
+#pragma unroll (W == 8 ? 4 : 2)
+            for (int64_t c0 = lane * W; c0 < cols; c0 += kSpan) {
+                float d[U][W], v[U][W];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t c = c0 + 32 * W * u;
+                    if (U > 1 && c >= cols) continue;
+                    load_w<W>(dr + c, d[u]);
+                    if (dweights) load_w<W>(y + at + c, v[u]);
                 }
 #pragma unroll
-                for (int i = 0; i < kW; ++i) {
-                    if (dweights) dot = fmaf(d[i], v[i], dot);
-                    d[i] *= w;
+                for (int u = 0; u < U; ++u) {
+                    const int64_t c = c0 + 32 * W * u;
+                    if (U > 1 && c >= cols) continue;
+                    if (dweights) {
+#pragma unroll
+                        for (int i = 0; i < W; ++i) dot = fmaf(d[u][i], v[u][i], dot);
+                    }
+#pragma unroll
+                    for (int i = 0; i < W; ++i) d[u][i] *= w;
+                    store_w<W>(dy + at + c, d[u]);
                 }
-                if constexpr (VEC)
-                    store8(dy + (int64_t)r * cols + c, d);
-                else
-                    store1(dy + (int64_t)r * cols + c, d[0]);
             }
         }
         if (dweights) {
 #pragma unroll
             for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
-            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                float sum = 0.0f;
-                for (int i = 0; i < kCombineThreads / 32; ++i) sum += part[i];
-                dweights[job] = sum;
-            }
-            __syncthreads();
+            if (lane == 0) dweights[job] = dot;
         }
     }
 }
@@ -352,24 +391,31 @@ __global__ void __launch_bounds__(kCombineThreads)
 static int combine_grid(int64_t jobs) {
     DeviceState* ds = device_state();
     if (!ds) return 0;
-    const int64_t most = (int64_t)ds->sm_count * 64;
-    return (int)(jobs < most ? jobs : most);
+    const int64_t need = (jobs + kCombineWarps - 1) / kCombineWarps, most = (int64_t)ds->sm_count * 32;
+    return (int)(need < most ? need : most);
 }
 
-static bool rows_vec(const void* p, int64_t cols, int bf16) {
-    return ((uintptr_t)p & 15u) == 0 && cols % 8 == 0 && (cols * (bf16 ? 2 : 4)) % 16 == 0;
+// Values at once: 8 where rows are whole 16-byte units of both types, else 2 or 1.
+static int rows_width(const void* p, int64_t cols, int bf16) {
+    const size_t sz = bf16 ? 2 : 4;
+    if ((uintptr_t)p % 16 == 0 && cols % 8 == 0) return 8;
+    return (uintptr_t)p % (2 * sz) == 0 && cols % 2 == 0 ? 2 : 1;
+}
+
+// One of three instances by width.
+template <typename K>
+static K by_width(int w, K k8, K k2, K k1) {
+    return w == 8 ? k8 : w == 2 ? k2 : k1;
 }
 
 template <typename Ty, typename To>
 static int combine_go(const void* y, int64_t rows, int64_t cols, const int32_t* slot, const float* weights,
-                      int64_t tokens, int topk, void* out, bool vec, cudaStream_t s) {
-    const int64_t per = kCombineThreads * (vec ? 8 : 1);
-    const int grid = combine_grid(tokens * ((cols + per - 1) / per));
+                      int64_t tokens, int topk, void* out, int width, cudaStream_t s) {
+    const int grid = combine_grid(tokens * ((cols + kSpan - 1) / kSpan));
     if (grid == 0) return -3;
-    const Ty* yy = static_cast<const Ty*>(y);
-    To* oo = static_cast<To*>(out);
-    const cudaError_t e = launch_chained(vec ? combine_kernel<Ty, To, true> : combine_kernel<Ty, To, false>, dim3(grid),
-                                         kCombineThreads, 0, s, 1, yy, rows, cols, slot, weights, tokens, topk, oo);
+    const auto kernel = by_width(width, combine_kernel<Ty, To, 8>, combine_kernel<Ty, To, 2>, combine_kernel<Ty, To, 1>);
+    const cudaError_t e = launch_chained(kernel, dim3(grid), kCombineThreads, 0, s, 1, static_cast<const Ty*>(y), rows, cols,
+                                         slot, weights, tokens, topk, static_cast<To*>(out));
     if (e != cudaSuccess) return set_cuda_error(e, "combine kernel launch");
     count_launch();
     return 0;
@@ -377,26 +423,25 @@ static int combine_go(const void* y, int64_t rows, int64_t cols, const int32_t* 
 
 int combine_launch(const void* y, int y_bf16, int64_t rows, int64_t cols, const int32_t* slot, const float* weights,
                    int64_t tokens, int topk, void* out, int out_bf16, cudaStream_t s) {
-    const bool vec = rows_vec(y, cols, y_bf16) && rows_vec(out, cols, out_bf16);
+    const int w = rows_width(y, cols, y_bf16), wo = rows_width(out, cols, out_bf16), width = w < wo ? w : wo;
     if (y_bf16)
-        return out_bf16 ? combine_go<__nv_bfloat16, __nv_bfloat16>(y, rows, cols, slot, weights, tokens, topk, out, vec, s)
-                        : combine_go<__nv_bfloat16, float>(y, rows, cols, slot, weights, tokens, topk, out, vec, s);
-    return out_bf16 ? combine_go<float, __nv_bfloat16>(y, rows, cols, slot, weights, tokens, topk, out, vec, s)
-                    : combine_go<float, float>(y, rows, cols, slot, weights, tokens, topk, out, vec, s);
+        return out_bf16 ? combine_go<__nv_bfloat16, __nv_bfloat16>(y, rows, cols, slot, weights, tokens, topk, out, width, s)
+                        : combine_go<__nv_bfloat16, float>(y, rows, cols, slot, weights, tokens, topk, out, width, s);
+    return out_bf16 ? combine_go<float, __nv_bfloat16>(y, rows, cols, slot, weights, tokens, topk, out, width, s)
+                    : combine_go<float, float>(y, rows, cols, slot, weights, tokens, topk, out, width, s);
 }
 
 template <typename Td, typename Ty>
 static int combine_back_go(const void* dout, const void* y, int64_t rows, int64_t cols, const int32_t* slot,
-                           const float* weights, int64_t tokens, int topk, void* dy, float* dweights, bool vec,
+                           const float* weights, int64_t tokens, int topk, void* dy, float* dweights, int width,
                            cudaStream_t s) {
     const int grid = combine_grid(tokens * topk);
     if (grid == 0) return -3;
-    const Td* dd = static_cast<const Td*>(dout);
-    const Ty* yy = static_cast<const Ty*>(y);
-    Ty* oo = static_cast<Ty*>(dy);
-    const cudaError_t e =
-        launch_chained(vec ? combine_backward_kernel<Td, Ty, true> : combine_backward_kernel<Td, Ty, false>, dim3(grid),
-                       kCombineThreads, 0, s, 1, dd, yy, rows, cols, slot, weights, tokens, topk, oo, dweights);
+    const auto kernel = by_width(width, combine_backward_kernel<Td, Ty, 8>, combine_backward_kernel<Td, Ty, 2>,
+                                 combine_backward_kernel<Td, Ty, 1>);
+    const cudaError_t e = launch_chained(kernel, dim3(grid), kCombineThreads, 0, s, 1, static_cast<const Td*>(dout),
+                                         static_cast<const Ty*>(y), rows, cols, slot, weights, tokens, topk,
+                                         static_cast<Ty*>(dy), dweights);
     if (e != cudaSuccess) return set_cuda_error(e, "combine backward kernel launch");
     count_launch();
     return 0;
@@ -405,12 +450,15 @@ static int combine_back_go(const void* dout, const void* y, int64_t rows, int64_
 int combine_backward_launch(const void* dout, int dout_bf16, const void* y, int y_bf16, int64_t rows, int64_t cols,
                             const int32_t* slot, const float* weights, int64_t tokens, int topk, void* dy,
                             float* dweights, cudaStream_t s) {
-    const bool vec = rows_vec(dout, cols, dout_bf16) && rows_vec(dy, cols, y_bf16) && (!dweights || rows_vec(y, cols, y_bf16));
+    int w = rows_width(dout, cols, dout_bf16);
+    const int wd = rows_width(dy, cols, y_bf16), wy = dweights ? rows_width(y, cols, y_bf16) : 8;
+    w = w < wd ? w : wd;
+    w = w < wy ? w : wy;
     if (dout_bf16)
-        return y_bf16 ? combine_back_go<__nv_bfloat16, __nv_bfloat16>(dout, y, rows, cols, slot, weights, tokens, topk, dy, dweights, vec, s)
-                      : combine_back_go<__nv_bfloat16, float>(dout, y, rows, cols, slot, weights, tokens, topk, dy, dweights, vec, s);
-    return y_bf16 ? combine_back_go<float, __nv_bfloat16>(dout, y, rows, cols, slot, weights, tokens, topk, dy, dweights, vec, s)
-                  : combine_back_go<float, float>(dout, y, rows, cols, slot, weights, tokens, topk, dy, dweights, vec, s);
+        return y_bf16 ? combine_back_go<__nv_bfloat16, __nv_bfloat16>(dout, y, rows, cols, slot, weights, tokens, topk, dy, dweights, w, s)
+                      : combine_back_go<__nv_bfloat16, float>(dout, y, rows, cols, slot, weights, tokens, topk, dy, dweights, w, s);
+    return y_bf16 ? combine_back_go<float, __nv_bfloat16>(dout, y, rows, cols, slot, weights, tokens, topk, dy, dweights, w, s)
+                  : combine_back_go<float, float>(dout, y, rows, cols, slot, weights, tokens, topk, dy, dweights, w, s);
 }
 
 }  // namespace c3
