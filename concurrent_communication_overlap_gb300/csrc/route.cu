@@ -10,7 +10,7 @@
 // one token as for four, is most of the work: 32768 x 60, 6 chosen, takes 354
 // instructions a token with 32 lanes and 192 with 8 (11 us against 15).
 //
-// Instructions are what bounds it, not bytes: 65536 x 256 with groups takes 59 us,
+// Instructions are what bounds it, not bytes: 65536 x 256 with groups takes 57 us,
 // 717 instructions a token, a third of them the 256 sigmoids, where its bytes need
 // 10.5; 32768 x 60 takes 11 us forward and 9 backward, where they need 1 and 1.
 #include "ops_device.cuh"
@@ -68,41 +68,72 @@ __device__ __forceinline__ unsigned lanes_ballot(bool v, int lane) {
 }
 __device__ __forceinline__ float sigmoid_f(float x) { return __frcp_rn(1.0f + expf(-x)); }
 
-// N consecutive logits of a row from expert e0 on; -inf past the last.
-template <int N>
-__device__ __forceinline__ void load_row(const float* xr, int e0, int E, bool vec, float (&x)[N]) {
-    if (vec) {
-        if constexpr (N % 4 == 0) {
-#pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(xr + e0 + i);
-                x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-            }
-            return;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = e0 + i < E ? load_f(xr + e0 + i) : -INFINITY;
+// Values of a vector load of N consecutive ones.
+template <typename T, int N>
+__host__ __device__ constexpr int vector_of() {
+    return N % 4 ? 1 : sizeof(T) == 2 && N % 8 == 0 ? 8 : 4;
 }
-template <int N>
-__device__ __forceinline__ void load_row(const __nv_bfloat16* xr, int e0, int E, bool vec, float (&x)[N]) {
-    if (vec) {
-        if constexpr (N % 8 == 0) {
+
+// N consecutive logits of a row from expert e0 on; -inf past the last.  vec: rows
+// start on 16 bytes and are whole vectors.
+template <int N, typename T>
+__device__ __forceinline__ void load_row(const T* xr, int e0, int E, bool vec, float (&x)[N]) {
+    constexpr int V = vector_of<T, N>();
+    if (V > 1 && vec) {
 #pragma unroll
-            for (int i = 0; i < N; i += 8) {
-                const uint4 v = *reinterpret_cast<const uint4*>(xr + e0 + i);
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < N; i += V) {
+            if constexpr (sizeof(T) == 4 && V > 1) {
+                float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                if (e0 + i < E) v = *reinterpret_cast<const float4*>(xr + e0 + i);
+                x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+            } else if constexpr (V > 1) {
+                uint32_t u[V / 2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < V / 2; ++j) u[j] = 0xff80ff80u;  // -inf, twice
+                if (e0 + i < E) {
+                    if constexpr (V == 8) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(xr + e0 + i);
+                        u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2*>(xr + e0 + i);
+                        u[0] = v.x, u[1] = v.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
                     x[i + 2 * j] = __uint_as_float(u[j] << 16);
                     x[i + 2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
                 }
             }
-            return;
         }
+        return;
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = e0 + i < E ? load_f(xr + e0 + i) : -INFINITY;
+}
+
+// The same by way of shared memory, for rows that no vector load fits: neighbouring
+// lanes read neighbouring values.  `stage` is the warp's, 32 N words; a line of it
+// (8 chunks of 16 bytes) has its chunks in an order of its own, so that lanes that
+// read N words each meet in no bank (12 words do not meet as they are).  16000 tokens of 371 experts,
+// 16 a lane: 30.6 us, with loads N apart 34.4.
+template <int N, int L, typename T>
+__device__ __forceinline__ void load_staged(const T* xr, int E, float none, uint32_t* stage, int lane, float (&x)[N]) {
+    const int at_lane = lane & (L - 1), base = (lane / L) * L * N;
+    const auto place = [](int w) { return N & (N - 1) ? w : w ^ ((w >> 3) & 28); };
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int e = at_lane + L * i;
+        stage[place(base + e)] = __float_as_uint(e < E ? load_f(xr + e) : none);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(stage + place(base + at_lane * N + i));
+        x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+    }
+    __syncwarp();
 }
 
 // Groups that are whole runs of 2^j of the token's lanes: score and rank them
@@ -191,21 +222,28 @@ __device__ __forceinline__ void groups_by_memory(uint32_t (&key)[NI], uint32_t* 
     __syncwarp();
 }
 
-// Descending order of N keys, by a bitonic network.
+// Descending order of N keys, by a bitonic network of a power of two: what it has
+// above N is 0, which the compiler sees through.
 template <int N>
-__device__ __forceinline__ void sort_down(uint32_t (&k)[N]) {
+__device__ __forceinline__ void sort_down(uint32_t (&keys)[N]) {
+    constexpr int P = N <= 1 ? 1 : N <= 2 ? 2 : N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : 32;
+    uint32_t k[P];
 #pragma unroll
-    for (int size = 2; size <= N; size <<= 1)
+    for (int i = 0; i < P; ++i) k[i] = i < N ? keys[i < N ? i : 0] : 0u;
+#pragma unroll
+    for (int size = 2; size <= P; size <<= 1)
 #pragma unroll
         for (int d = size >> 1; d; d >>= 1)
 #pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int i = 0; i < P; ++i)
                 if ((i & d) == 0) {
                     const uint32_t a = k[i], b = k[i | d];
-                    const bool down = (i & size) == 0 || size == N;
+                    const bool down = (i & size) == 0 || size == P;
                     k[i] = down ? max(a, b) : min(a, b);
                     k[i | d] = down ? min(a, b) : max(a, b);
                 }
+#pragma unroll
+    for (int i = 0; i < N; ++i) keys[i] = k[i];
 }
 
 // The weight of this lane's choice (expert `mine`, or -1), unscaled.
@@ -226,31 +264,43 @@ __device__ __forceinline__ float choice_weight(const T* xr, int mine, const Rout
 }
 
 // NI experts a lane, L NI >= E.  GROUPS: 0 none, 1 whole runs of lanes, 2 any (L =
-// 32).  vec: rows are whole and 16-byte aligned.  topk <= L.
+// 32).  vec: as load_row's.  topk <= L.
+// Registers: 65536 x 256 took 62 us with 64 and 66 with 80; 16000 x 1000 takes 76 with
+// 128, 81 with 80 and 127 with 218.
 template <typename T, int NI, int L, int GROUPS>
-__global__ void __launch_bounds__(kRouteWarps * 32, NI == 16 ? 4 : 1)  // 64 registers: 62 us for 65536 x 256, 66 with 80
+__global__ void __launch_bounds__(kRouteWarps * 32, NI == 12 || NI == 16 ? 4 : NI == 32 ? 2 : 1)
     route_kernel(const T* __restrict__ logits, int64_t ld, int64_t tokens, int vec, RouteArgs a,
                  int32_t* __restrict__ idx, float* __restrict__ weights) {
     constexpr int kRows = 32 / L;  // tokens of a warp
     constexpr bool kInMemory = NI >= 8;
+    // 8 lanes of 8 share the lines that they load: staged, 32768 x 60 took 2 us more
+    constexpr bool kStaged = NI >= 12 || (NI == 8 && L == 32);
     // a warp's scratch: the groups' keys first, then the sorted lines
     constexpr int kScratch = GROUPS == 2 ? 1024 : kInMemory ? NI * 32 : 1;
-    __shared__ uint32_t scratch[kRouteWarps][kScratch];
+    __shared__ __align__(16) uint32_t scratch[kRouteWarps][kScratch];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int at_lane = lane & (L - 1);
     const int E = a.experts, k = a.topk, e0 = at_lane * NI;
     const bool soft = a.score == 0;
     chain_wait();
-    float bias[NI];
+    float bias[NI] = {};
+    if constexpr (kStaged) {
+        if (a.bias) load_staged<NI, L>(a.bias, E, 0.0f, scratch[warp], lane, bias);
+    } else if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) bias[i] = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.0f;
+        for (int i = 0; i < NI; ++i) bias[i] = e0 + i < E ? a.bias[e0 + i] : 0.0f;
+    }
     const int64_t step = (int64_t)gridDim.x * kRouteWarps * kRows;
     for (int64_t row0 = ((int64_t)blockIdx.x * kRouteWarps + warp) * kRows; row0 < tokens; row0 += step) {
         const int64_t row = row0 + lane / L;
         const bool live = row < tokens;
         const T* xr = logits + (live ? row : row0) * ld;  // a lane without a token repeats another's
         float x[NI];
-        load_row<NI>(xr, e0, E, vec, x);
+        if (kStaged && !vec) {
+            if constexpr (kStaged) load_staged<NI, L>(xr, E, -INFINITY, scratch[warp], lane, x);
+        } else {
+            load_row<NI>(xr, e0, E, vec, x);
+        }
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < NI; ++i) bad |= isnan(x[i]);
@@ -316,7 +366,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NI == 16 ? 4 : 1)  // 64 reg
                 head = line[0];
             }
         }
-        if constexpr (GROUPS == 2) __syncwarp();  // the scratch is the groups' again
+        if constexpr (GROUPS == 2) __syncwarp();  // the scratch is another's again
         // Which of that lane's experts it was: the first with the key, or the one after as
         // many as earlier choices took of the same key there.  Those are the choices just
         // before: equal keys go by lane, then by register.
@@ -445,7 +495,9 @@ struct RouteForm {
     int lanes, per_lane, groups;
 };
 
-static int pow2_up(int n) {
+// Powers of two, and 12: 16 would sort and score a quarter more (16000 x 371: 23.4 us against 30.6).
+static int registers_for(int n) {
+    if (n > 8 && n <= 12) return 12;
     int p = 1;
     while (p < n) p *= 2;
     return p;
@@ -455,7 +507,7 @@ static RouteForm route_form(const RouteArgs& a, int64_t tokens) {
     RouteForm f;
     for (int lanes = tokens < kFewTokens ? 32 : 8; lanes <= 32; lanes *= 2) {
         f.lanes = lanes;
-        f.per_lane = pow2_up((a.experts + lanes - 1) / lanes);
+        f.per_lane = registers_for((a.experts + lanes - 1) / lanes);
         const int gs = a.experts / a.groups, run = gs / f.per_lane;
         const bool runs = a.experts == lanes * f.per_lane && gs % f.per_lane == 0 && (run & (run - 1)) == 0;
         f.groups = a.groups == 1 ? 0 : runs ? 1 : 2;
@@ -469,7 +521,7 @@ static int route_go(const RouteForm& f, cudaStream_t s, const T* x, int64_t ld, 
                     int32_t* idx, float* w) {
     const int grid = route_grid(tokens, L);
     if (grid == 0) return -3;
-    const int vec = a.experts == L * NI && ((uintptr_t)x & 15u) == 0 && (ld * (int64_t)sizeof(T)) % 16 == 0;
+    const int vec = a.experts % vector_of<T, NI>() == 0 && ((uintptr_t)x & 15u) == 0 && (ld * (int64_t)sizeof(T)) % 16 == 0;
     const auto go = [&](auto kernel) {
         return route_done(launch_chained(kernel, dim3(grid), kRouteWarps * 32, 0, s, 1, x, ld, tokens, vec, a, idx, w),
                           "route kernel launch");
@@ -497,6 +549,7 @@ static int route_back_go(cudaStream_t s, const T* x, int64_t ld, int64_t tokens,
             case 2: return CALL(2, 8);                                   \
             case 4: return CALL(4, 8);                                   \
             case 8: return CALL(8, 8);                                   \
+            case 12: return CALL(12, 8);                                 \
             default: return CALL(16, 8);                                 \
         }                                                                \
         if (f.lanes == 16) switch (f.per_lane) {                         \
@@ -504,6 +557,7 @@ static int route_back_go(cudaStream_t s, const T* x, int64_t ld, int64_t tokens,
             case 2: return CALL(2, 16);                                  \
             case 4: return CALL(4, 16);                                  \
             case 8: return CALL(8, 16);                                  \
+            case 12: return CALL(12, 16);                                \
             default: return CALL(16, 16);                                \
         }                                                                \
         switch (f.per_lane) {                                            \
@@ -511,6 +565,7 @@ static int route_back_go(cudaStream_t s, const T* x, int64_t ld, int64_t tokens,
             case 2: return CALL(2, 32);                                  \
             case 4: return CALL(4, 32);                                  \
             case 8: return CALL(8, 32);                                  \
+            case 12: return CALL(12, 32);                                \
             case 16: return CALL(16, 32);                                \
             default: return CALL(32, 32);                                \
         }                                                                \

@@ -387,6 +387,53 @@ def test_route_many_tokens(c3, r, T, ty):
     assert bool(((a - b).abs() <= 2 * 256 * U * 4 * r.get("scale", 1.0) * (20 if r.get("renorm") else 1) + 2 * H * b.abs()).all())
 
 
+# Twelve experts a lane of 32, 16 and 8 lanes (the last two with many tokens), whole and
+# ragged, rows of whole vectors and not.
+TWELVE = [
+    dict(E=384, k=8, score="sigmoid", G=8, keep=4, best=2, renorm=True, bias=True),
+    dict(E=384, k=8, score="softmax", G=6, keep=2),
+    dict(E=371, k=8, score="sigmoid", renorm=True, bias=True),
+    dict(E=372, k=9, score="softmax"),
+    dict(E=360, k=4, score="softmax", renorm=True),
+    dict(E=192, k=8, score="sigmoid", G=4, keep=2, best=2, bias=True),
+    dict(E=189, k=12, score="softmax"),
+    dict(E=180, k=16, score="sigmoid", renorm=True),
+    dict(E=96, k=8, score="sigmoid", G=4, keep=2, best=2, bias=True),
+    dict(E=95, k=3, score="softmax"),
+    dict(E=88, k=8, score="sigmoid", renorm=True, bias=True),
+]
+
+
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("T,extra", [(1, 0), (77, 5), (33, 8)])
+@pytest.mark.parametrize("r", TWELVE, ids=lambda r: "_".join(f"{k}{v}" for k, v in r.items()))
+def test_route_twelve_a_lane(c3, r, T, extra, ty):
+    test_route(c3, r, T, extra, ty)
+
+
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("extra", [0, 3, 8])
+@pytest.mark.parametrize("r", TWELVE, ids=lambda r: "_".join(f"{k}{v}" for k, v in r.items()))
+def test_route_twelve_many_tokens(c3, r, extra, ty):
+    T, E, k = 4101, r["E"], r["k"]
+    rng = np.random.default_rng(E + extra)
+    x = grid_logits(rng, T, E)
+    x[rng.random((T, E)) < 0.05] = -np.inf
+    bias = rng.integers(-8, 9, E) / 16.0 if r.get("bias") else None
+    idx, w, router, wide = run_route(c3, r, x, ty, bias, extra)
+    some = rng.choice(T, 200, replace=False)
+    few_idx, few_w, _, _ = run_route(c3, r, x[some], ty, bias, extra)  # a whole warp a token
+    same = (idx[some] == few_idx).all(1)
+    if r["score"] == "sigmoid" or bias is None:  # the keys do not depend on the number of lanes
+        assert same.all()
+    a, b = f64(w)[some], f64(few_w)
+    assert (np.abs(a - b)[same.cpu().numpy()] <= 128 * U * np.abs(b)[same.cpu().numpy()]).all()
+    ref_idx, ref_w = route_oracle(x[some], E, k, r["score"], bias, **oracle_args(r))
+    hit = (few_idx.cpu().numpy() == ref_idx).all(1)
+    assert hit.mean() > 0.9
+    assert (np.abs(a - ref_w) <= 128 * U * np.abs(ref_w))[hit].all()
+
+
 # ----------------------------------------------------------------------------- order
 
 def order_oracle(idx, E, rows):
