@@ -214,14 +214,39 @@ template <typename T>
 struct Raw16 {
     static constexpr int kWords = 4 * sizeof(T);
     uint32_t w[kWords];
-    __device__ __forceinline__ void load(const T* p, int64_t most, bool vec) {
-        if (vec && most >= 16) {
+    // VEC: every row starts on 16 bytes.  Else the aligned 16-byte pieces around the
+    // columns are loaded and shifted into place, if they lie in [lo, hi): 1518 x 16361
+    // bf16 takes 16 us that way, 19 a value at a time.
+    template <bool VEC>
+    __device__ __forceinline__ void load(const T* p, int64_t most, const T* lo, const T* hi) {
+        if (VEC && most >= 16) {
 #pragma unroll
             for (int i = 0; i < kWords / 4; ++i) {
                 const uint4 a = reinterpret_cast<const uint4*>(p)[i];
                 w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
             }
-        } else if constexpr (sizeof(T) == 2) {
+            return;
+        }
+        if constexpr (!VEC) {
+            const uintptr_t from = (uintptr_t)p & ~(uintptr_t)15;
+            const unsigned off = (unsigned)(uintptr_t)p & 15u;
+            if (most >= 16 && from >= (uintptr_t)lo && from + 4 * (kWords + 4) <= (uintptr_t)hi) {
+                uint32_t u[kWords + 4];
+#pragma unroll
+                for (int i = 0; i <= kWords / 4; ++i) {
+                    const uint4 a = reinterpret_cast<const uint4*>(from)[i];
+                    u[4 * i] = a.x, u[4 * i + 1] = a.y, u[4 * i + 2] = a.z, u[4 * i + 3] = a.w;
+                }
+#pragma unroll
+                for (int i = 0; i < kWords + 2; ++i) u[i] = off & 8u ? u[i + 2] : u[i];
+#pragma unroll
+                for (int i = 0; i < kWords + 1; ++i) u[i] = off & 4u ? u[i + 1] : u[i];
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) w[i] = off & 2u ? __byte_perm(u[i], u[i + 1], 0x5432) : u[i];
+                return;
+            }
+        }
+        if constexpr (sizeof(T) == 2) {
             const uint16_t* s = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -247,11 +272,11 @@ __device__ __forceinline__ void scale16(float (&v)[16], float t) {
 // One CTA: 32 rows of one matrix, 128 columns at a time, `across` CTAs a row tile;
 // a thread's next 16 columns are on their way while these are encoded.  Eight
 // threads a row: a row's scales of a tile are one word, and codes leave 64 bytes at
-// a time.  8192 x 8192 bf16 to MX takes 34 us, 5.0 TB/s; 32768 gathered rows of 4096
-// bf16 to NV 67 us, bound by instructions (187 for 16 columns).
-template <typename T, bool NV>
+// a time.  8192 x 8192 bf16 to MX takes 32 us, 5.3 TB/s; 32768 gathered rows of 4096
+// bf16 to NV 61 us, bound by instructions (187 for 16 columns).
+template <typename T, bool NV, bool VEC>
 __global__ void __launch_bounds__(kQThreads)
-    fp4_quantize_kernel(const T* __restrict__ x, int64_t x_rows, int64_t ld, int vec, const int32_t* __restrict__ row_of,
+    fp4_quantize_kernel(const T* __restrict__ x, int64_t x_rows, int64_t ld, const int32_t* __restrict__ row_of,
                         Fp4 q, int64_t pitch, int64_t k_tiles, int64_t scale_bytes, int64_t x_stride, unsigned spans,
                         unsigned across) {
     const int i = threadIdx.x >> 3, g = threadIdx.x & 7;
@@ -271,15 +296,17 @@ __global__ void __launch_bounds__(kQThreads)
     const float inv_t = NV && q.tensor_scale ? __fdiv_rn(1.0f, q.tensor_scale[mat]) : 1.0f;
     uint8_t* tile_row = q.scales + (int64_t)mat * scale_bytes + (r / kTileRows) * k_tiles * 512 + (r % 32) * 16 +
                         (r % kTileRows) / 32 * 4;
-    const T* xr = x + (int64_t)mat * x_stride + src * ld;
+    const T* lo = x + (int64_t)mat * x_stride;
+    const T* hi = lo + (x_rows - 1) * ld + q.cols;
+    const T* xr = lo + src * ld;
     unsigned u = blockIdx.x - rt * across;
     int64_t c = (int64_t)u * 128 + g * 16;
     Raw16<T> now;
-    now.load(xr + c, have ? q.cols - c : 0, vec);
+    now.template load<VEC>(xr + c, have ? q.cols - c : 0, lo, hi);
     for (; u < spans; u += across) {
         const int64_t next = c + (int64_t)across * 128;
         Raw16<T> ahead;
-        ahead.load(xr + next, have && u + across < spans ? q.cols - next : 0, vec);
+        ahead.template load<VEC>(xr + next, have && u + across < spans ? q.cols - next : 0, lo, hi);
         uint32_t byte;
         uint2 codes;
         if constexpr (!NV && sizeof(T) == 2) {
@@ -486,21 +513,33 @@ int fp4_quantize_launch(const void* x, int bf16, int64_t x_rows, int64_t ld, int
         else C3_GO(float, false);
 #undef C3_GO
     } else {
-        // Eight spans of 128 columns a CTA, so that loads run ahead; a single CTA a span
-        // where rows are few.  Gathered rows are mostly absent when each expert has a
-        // handful, and a CTA that finds none of its 32 leaves.
+        // Up to eight spans of 128 columns a CTA, so that loads run ahead, but six CTAs an
+        // SM first, which is one wave: 4096 x 4096 bf16 to MX takes 8.8 us, with one span a
+        // CTA 12.3, with sixteen an SM's share 12.3 and with two 13.1.  Gathered rows are
+        // mostly absent when each expert has a handful, and a CTA that finds none of its 32
+        // leaves: eight (the 64 experts' product of 192 of 8320 rows of 4096, with its order and
+        // quantisation, takes 52 us, 55 with four or six and 54 to 57 with sixteen).
         const unsigned spans = (unsigned)((cols + 127) / 128);
         const int64_t tiles = (q.rows + kQRows - 1) / kQRows * q.count;
-        const unsigned across = tiles >= 256 || row_of ? (spans + 7) / 8 : spans;
+        DeviceState* ds = device_state();
+        if (!ds) return -3;
+        const int64_t share = tiles * spans / ((int64_t)ds->sm_count * (row_of ? 8 : 6));
+        const unsigned each = (unsigned)(share < 1 ? 1 : share < 8 ? share : 8), across = (spans + each - 1) / each;
         if ((rc = fp4_grid(q, across, &grid))) return rc;
-        const int vec = vec_ok(x, ld, bf16) && (q.count == 1 || (stride * (bf16 ? 2 : 4)) % 16 == 0);
-#define C3_GO(T_, NV_)                                                                                           \
-    e = launch_chained(fp4_quantize_kernel<T_, NV_>, grid, kQThreads, 0, s, 1, static_cast<const T_*>(x), x_rows,    \
-                       ld, vec, row_of, q, q.pitch(), q.k_tiles(), q.scale_bytes(), stride, spans, across)
-        if (bf16 && q.nv) C3_GO(__nv_bfloat16, true);
-        else if (bf16) C3_GO(__nv_bfloat16, false);
-        else if (q.nv) C3_GO(float, true);
-        else C3_GO(float, false);
+        const bool vec = vec_ok(x, ld, bf16) && (q.count == 1 || (stride * (bf16 ? 2 : 4)) % 16 == 0);
+#define C3_GO(T_, NV_, VEC_)                                                                                   \
+    e = launch_chained(fp4_quantize_kernel<T_, NV_, VEC_>, grid, kQThreads, 0, s, 1, static_cast<const T_*>(x),  \
+                       x_rows, ld, row_of, q, q.pitch(), q.k_tiles(), q.scale_bytes(), stride, spans, across)
+#define C3_PICK(T_)                                  \
+    do {                                             \
+        if (q.nv && vec) C3_GO(T_, true, true);      \
+        else if (q.nv) C3_GO(T_, true, false);       \
+        else if (vec) C3_GO(T_, false, true);        \
+        else C3_GO(T_, false, false);                \
+    } while (0)
+        if (bf16) C3_PICK(__nv_bfloat16);
+        else C3_PICK(float);
+#undef C3_PICK
 #undef C3_GO
     }
     if (e != cudaSuccess) return set_cuda_error(e, "4-bit quantise kernel launch");

@@ -590,6 +590,32 @@ def test_quantise(c3, R, C, fmt, ty, transpose):
 
 @pytest.mark.parametrize("ty", [0, 1])
 @pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("R,C", [(1, 5), (1, 16), (2, 47), (33, 128), (70, 333), (300, 1040)])
+def test_quantise_rows_of_any_alignment(c3, R, C, gather, fmt, ty):
+    """Rows that start anywhere, NaNs around them: the codes and scales of the same rows aligned."""
+    rng = np.random.default_rng(R * 3 + C)
+    g = 0.125 if fmt else None
+    x = values(rng, R, C, ty)[0]
+    wide = torch.full((R, C + 8 + -C % 8), float("nan"), dtype=TD[ty], device="cuda")
+    wide[:, :C] = x
+    row_of = torch.randint(-1, R, (R,), dtype=torch.int32, device="cuda") if gather else None
+    for shift in range(8):
+        for ld in range(C, C + 5):
+            results = []
+            flat = torch.full((shift + R * ld,), float("nan"), dtype=TD[ty], device="cuda")
+            odd = flat[shift:].view(R, ld)
+            odd[:, :C] = x
+            for src, pitch in ((wide, wide.shape[1]), (odd, ld)):
+                q, codes, scales = new_fp4(c3, R, C, fmt, g)
+                c3.c3_fp4_quantize(src, ty, R, C, q, ld=pitch, row_of=row_of)
+                torch.cuda.synchronize()
+                results.append((codes.t.clone(), scales.t.clone()))
+            assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1]), (shift, ld)
+
+
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("fmt", [0, 1])
 def test_quantise_special_values(c3, fmt, ty):
     x = np.ones((6, 64), np.float32)
     x[0, 3] = np.nan
