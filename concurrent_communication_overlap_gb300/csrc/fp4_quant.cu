@@ -519,6 +519,8 @@ int fp4_quantize_launch(const void* x, int bf16, int64_t x_rows, int64_t ld, int
         // mostly absent when each expert has a handful, and a CTA that finds none of its 32
         // leaves: eight (192 of 8320 rows of 4096: 6.9 us, with six 7.8, with sixteen 6.2; 4096 of
         // 12224: 10.9 with six and eight, 11.8 with sixteen).
+        const unsigned spans = (unsigned)((cols + 127) / 128);
+        const int64_t tiles = (q.rows + kQRows - 1) / kQRows * q.count;
         DeviceState* ds = device_state();
         if (!ds) return -3;
         const int64_t share = tiles * spans / ((int64_t)ds->sm_count * (row_of ? 8 : 6));
