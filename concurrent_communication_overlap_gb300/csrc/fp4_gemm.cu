@@ -603,7 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 // Two CTAs fit an SM: one's start and end hide behind the other's stream (64
 // experts of 2048 x 4096 with 192 rows: 45 us, 5.8 TB/s of weights).  Where
 // there are fewer tiles than CTAs to fill the machine, a cluster of `split` CTAs
-// takes one tile, each a part of K; their fp32 parts meet in shared memory, each
+// takes a tile at a time, each a part of K; their fp32 parts meet in shared memory, each
 // CTA adding up its share of A's rows in the order of the ranks.  13 x 8200 x 8072
 // takes 11.7 us in a chain of calls, where its bytes need 5.5; the rest is set-up, the
 // first loads' latency and the cluster's two meetings.
@@ -685,222 +685,232 @@ __global__ void __launch_bounds__(kRThreads, 2)
     const int total = NT == 64 && g.offsets ? prefix[g.experts] * g.num_n : g.num_m * g.num_n;
     const uint32_t rank = split > 1 ? cluster_rank() : 0u;
     const int first = split > 1 ? blockIdx.x / split : blockIdx.x;
-    const int step = split > 1 ? total : gridDim.x;  // a cluster takes one tile
+    const int step = gridDim.x / split;
     const int kb0 = (int)((int64_t)g.num_kb * (int)rank / split), kb1 = (int)((int64_t)g.num_kb * ((int)rank + 1) / split);
 
-    if (warp == 0) {
-        if (lane == 0) {
-            // weights that one tile alone reads do not stay in L2
-            const uint64_t pol_w = g.num_m > 1 ? policy_evict_normal() : policy_evict_first(), pol_t = policy_evict_last();
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int t = first; ok && t < total; t += step) {
-                const Fp4Tile tile = fp4_tile<NT>(g, prefix, t);
-                const int trow = (int)tile.row0, wrow = tile.expert * g.N + tile.nb * 128;
-                const int swrow = tile.expert * g.b_row_tiles + tile.nb;
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(bar(S + stage), phase ^ 1u, abort_flag)) {
-                        report_error(st, -4, kSiteFp4Producer);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sb = base + (uint32_t)stage * Cfg::kStage;
-                    const uint32_t sf = sb + Cfg::kWBytes + Cfg::kTBytes;
-                    mbar_arrive_expect_tx(bar(stage), Cfg::kStage);
-                    tma_load_2d(sb, &tmB, bar(stage), kb * 128, wrow, pol_w);
-                    tma_load_2d(sb + Cfg::kWBytes, &tmA, bar(stage), kb * 128, trow, pol_t);
-                    tma_load_2d(sf, &tmSB, bar(stage), kb * KT * 64, swrow, pol_w);
-                    tma_load_2d(sf + Cfg::kSf, &tmSA, bar(stage), kb * KT * 64, trow / 128, pol_t);
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
+    // The roles' places in the ring; a warp has one role.  A cluster does one tile after
+    // the other, a CTA by itself all of its tiles in one go.
+    int stage = 0, set = 0, old_stage = 0, done = 0;
+    uint32_t phase = 0, old_phase = 0, turn = 0;
+    bool ok = true;
+    for (int t0 = first;; t0 += step, turn ^= 1u) {
+        const int end = split > 1 ? min(t0 + 1, total) : total;
+        if (warp == 0) {
+            if (lane == 0) {
+                // weights that one tile alone reads do not stay in L2
+                const uint64_t pol_w = g.num_m > 1 ? policy_evict_normal() : policy_evict_first(), pol_t = policy_evict_last();
+                for (int t = t0; ok && t < end; t += step) {
+                    const Fp4Tile tile = fp4_tile<NT>(g, prefix, t);
+                    const int trow = (int)tile.row0, wrow = tile.expert * g.N + tile.nb * 128;
+                    const int swrow = tile.expert * g.b_row_tiles + tile.nb;
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!mbar_wait(bar(S + stage), phase ^ 1u, abort_flag)) {
+                            report_error(st, -4, kSiteFp4Producer);
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t sb = base + (uint32_t)stage * Cfg::kStage;
+                        const uint32_t sf = sb + Cfg::kWBytes + Cfg::kTBytes;
+                        mbar_arrive_expect_tx(bar(stage), Cfg::kStage);
+                        tma_load_2d(sb, &tmB, bar(stage), kb * 128, wrow, pol_w);
+                        tma_load_2d(sb + Cfg::kWBytes, &tmA, bar(stage), kb * 128, trow, pol_t);
+                        tma_load_2d(sf, &tmSB, bar(stage), kb * KT * 64, swrow, pol_w);
+                        tma_load_2d(sf + Cfg::kSf, &tmSA, bar(stage), kb * KT * 64, trow / 128, pol_t);
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
                 }
             }
-            // Every load must have landed before the CTA ends.
-            volatile int no_abort = 0;
-            for (int i = 0; i < S; ++i)
-                if (!mbar_wait(bar(i), (i < stage) ? phase : (phase ^ 1u), &no_abort))
-                    report_error(st, -4, kSiteFp4Drain);
-        }
-    } else if (warp == 1) {
-        const uint32_t lead = elect_lane();
-        const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(NT >> 3) << 17) | (NV ? 0u : 1u << 23) | (1u << 27);
-        const uint64_t code0 = code_desc(base);
-        int stage = 0, local = 0, set = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int t = first; ok && t < total; t += step, ++local) {
-            const uint32_t shift = (uint32_t)(fp4_tile<NT>(g, prefix, t).row0 % 128) / 32;  // 0 or 2
-            const int buf = local % NB;
-            if (!mbar_wait(bar(TEMPTY + buf), ((uint32_t)(local / NB) & 1u) ^ 1u, abort_flag)) {
-                report_error(st, -4, kSiteFp4Mma);
-                break;
-            }
-            tc_fence_after();
-            const uint32_t d = tmem + (uint32_t)(buf * NT);
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(bar(SREADY + stage), phase, abort_flag)) {
+        } else if (warp == 1) {
+            const uint32_t lead = elect_lane();
+            const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(NT >> 3) << 17) | (NV ? 0u : 1u << 23) | (1u << 27);
+            const uint64_t code0 = code_desc(base);
+            int local = 0;
+            for (int t = t0; ok && t < end; t += step, ++local) {
+                const uint32_t shift = (uint32_t)(fp4_tile<NT>(g, prefix, t).row0 % 128) / 32;  // 0 or 2
+                const int buf = local % NB;
+                if (!mbar_wait(bar(TEMPTY + buf), ((uint32_t)(local / NB) & 1u) ^ 1u, abort_flag)) {
                     report_error(st, -4, kSiteFp4Mma);
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t wd = code0 + (uint64_t)((uint32_t)stage * (Cfg::kStage >> 4));
-                const uint64_t td = wd + (Cfg::kWBytes >> 4);
-                const int steps = min(4, (g.K - kb * kFK + 63) / 64);
-                const uint32_t tsf0 = tmem + 128u + (uint32_t)(set * KT * Cfg::kSetCols);
+                const uint32_t d = tmem + (uint32_t)(buf * NT);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(bar(SREADY + stage), phase, abort_flag)) {
+                        report_error(st, -4, kSiteFp4Mma);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t wd = code0 + (uint64_t)((uint32_t)stage * (Cfg::kStage >> 4));
+                    const uint64_t td = wd + (Cfg::kWBytes >> 4);
+                    const int steps = min(4, (g.K - kb * kFK + 63) / 64);
+                    const uint32_t tsf0 = tmem + 128u + (uint32_t)(set * KT * Cfg::kSetCols);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t tsf = tsf0 + (uint32_t)((NV ? k : k >> 1) * Cfg::kSetCols);
-                    const uint32_t id = NV ? 0u : (uint32_t)(k & 1) * 2u;
-                    mma_fp4<1, NV>(k < steps ? lead : 0u, d, wd + (uint64_t)(2 * k), td + (uint64_t)(2 * k),
-                                   idesc | (id << 4) | (id << 29), tsf, tsf + 4u + shift, k > 0 ? 1u : (uint32_t)(kb > kb0));
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t tsf = tsf0 + (uint32_t)((NV ? k : k >> 1) * Cfg::kSetCols);
+                        const uint32_t id = NV ? 0u : (uint32_t)(k & 1) * 2u;
+                        mma_fp4<1, NV>(k < steps ? lead : 0u, d, wd + (uint64_t)(2 * k), td + (uint64_t)(2 * k),
+                                       idesc | (id << 4) | (id << 29), tsf, tsf + 4u + shift, k > 0 ? 1u : (uint32_t)(kb > kb0));
+                    }
+                    commit_local<1>(lead, bar(S + stage));
+                    set = set + 1 == Cfg::kSets ? 0 : set + 1;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
-                commit_local<1>(lead, bar(S + stage));
-                set = set + 1 == Cfg::kSets ? 0 : set + 1;
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+                if (ok) commit_local<1>(lead, bar(TFULL + buf));
             }
-            if (ok) commit_local<1>(lead, bar(TFULL + buf));
-        }
-        // no MMA may still run when TMEM is freed
-        commit_local<1>(lead, bar(DRAIN));
-        volatile int no_abort = 0;
-        if (!mbar_wait(bar(DRAIN), 0, &no_abort)) report_error(st, -4, kSiteFp4Drain);
-    } else if (warp == 2) {
-        // ---------------- scales from shared memory to TMEM (see the pair kernel)
-        const uint32_t lead = elect_lane();
-        const uint64_t scale0 = scale_desc(base + Cfg::kWBytes + Cfg::kTBytes);
-        int stage = 0, set = 0, old_stage = 0;
-        uint32_t phase = 0, old_phase = 0;
-        int done = 0;
-        bool ok = true;
-        for (int t = first; ok && t < total; t += step)
-            for (int kb = kb0; kb < kb1; ++kb) {
-                ok = mbar_wait(bar(stage), phase, abort_flag);
-                if (ok && done >= Cfg::kSets) ok = mbar_wait(bar(S + old_stage), old_phase, abort_flag);
-                if (!ok) {
-                    report_error(st, -4, kSiteFp4Scales);
+        } else if (warp == 2) {
+            // ---------------- scales from shared memory to TMEM (see the pair kernel)
+            const uint32_t lead = elect_lane();
+            const uint64_t scale0 = scale_desc(base + Cfg::kWBytes + Cfg::kTBytes);
+            for (int t = t0; ok && t < end; t += step)
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = mbar_wait(bar(stage), phase, abort_flag);
+                    if (ok && done >= Cfg::kSets) ok = mbar_wait(bar(S + old_stage), old_phase, abort_flag);
+                    if (!ok) {
+                        report_error(st, -4, kSiteFp4Scales);
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t from = scale0 + (uint64_t)((uint32_t)stage * (Cfg::kStage >> 4));
+                    const uint32_t to = tmem + 128u + (uint32_t)(set * KT * Cfg::kSetCols);
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            copy_scales<1>(lead, to + (uint32_t)(kt * Cfg::kSetCols + i * 4),
+                                           from + (uint64_t)((i * KT + kt) * (512 >> 4)));
+                    commit_local<1>(lead, bar(SREADY + stage));
+                    if (++done > Cfg::kSets && ++old_stage == S) {
+                        old_stage = 0;
+                        old_phase ^= 1u;
+                    }
+                    set = set + 1 == Cfg::kSets ? 0 : set + 1;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+        } else if (warp >= 4 && split == 1) {
+            const int q = warp & 3;
+            const float ga = g.ga ? *g.ga : 1.0f;
+            int local = 0;
+            for (int t = t0; t < end; t += step, ++local) {
+                const Fp4Tile tile = fp4_tile<NT>(g, prefix, t);
+                const int buf = local % NB;
+                const bool go = mbar_wait(bar(TFULL + buf), (uint32_t)(local / NB) & 1u, abort_flag);
+                if (!__all_sync(0xffffffffu, go)) {
+                    report_error(st, -4, kSiteFp4Epilogue);
                     break;
                 }
                 tc_fence_after();
-                const uint64_t from = scale0 + (uint64_t)((uint32_t)stage * (Cfg::kStage >> 4));
-                const uint32_t to = tmem + 128u + (uint32_t)(set * KT * Cfg::kSetCols);
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        copy_scales<1>(lead, to + (uint32_t)(kt * Cfg::kSetCols + i * 4),
-                                       from + (uint64_t)((i * KT + kt) * (512 >> 4)));
-                commit_local<1>(lead, bar(SREADY + stage));
-                if (++done > Cfg::kSets && ++old_stage == S) {
-                    old_stage = 0;
-                    old_phase ^= 1u;
-                }
-                set = set + 1 == Cfg::kSets ? 0 : set + 1;
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-    } else if (warp >= 4 && split == 1) {
-        const int q = warp & 3;
-        const float ga = g.ga ? *g.ga : 1.0f;
-        int local = 0;
-        for (int t = first; t < total; t += step, ++local) {
-            const Fp4Tile tile = fp4_tile<NT>(g, prefix, t);
-            const int buf = local % NB;
-            const bool go = mbar_wait(bar(TFULL + buf), (uint32_t)(local / NB) & 1u, abort_flag);
-            if (!__all_sync(0xffffffffu, go)) {
-                report_error(st, -4, kSiteFp4Epilogue);
-                break;
-            }
-            tc_fence_after();
-            const float alpha = ga * (g.gb ? g.gb[tile.expert] : 1.0f);
-            const int n = tile.nb * 128 + q * 32 + lane;
-            TC* c = static_cast<TC*>(g.C) + tile.row0 * (int64_t)g.N + n;
-            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * NT);
+                const float alpha = ga * (g.gb ? g.gb[tile.expert] : 1.0f);
+                const int n = tile.nb * 128 + q * 32 + lane;
+                TC* c = static_cast<TC*>(g.C) + tile.row0 * (int64_t)g.N + n;
+                const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * NT);
 #pragma unroll 1
-            for (int j0 = 0; j0 < NT && j0 < tile.rows; j0 += 32) {
-                uint32_t r[32];
-                tmem_ld32(taddr + (uint32_t)j0, r);
-                tmem_ld_wait();
+                for (int j0 = 0; j0 < NT && j0 < tile.rows; j0 += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(taddr + (uint32_t)j0, r);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (j0 + j < tile.rows && n < g.N) c[(int64_t)(j0 + j) * g.N] = (TC)(alpha * __uint_as_float(r[j]));
+                    for (int j = 0; j < 32; ++j)
+                        if (j0 + j < tile.rows && n < g.N) c[(int64_t)(j0 + j) * g.N] = (TC)(alpha * __uint_as_float(r[j]));
+                    __syncwarp();
+                }
+                tc_fence_before();
                 __syncwarp();
+                if (lane == 0) mbar_arrive(bar(TEMPTY + buf));
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(TEMPTY + buf));
         }
+        __syncwarp();
+        if (split > 1) {
+            // The parts of a tile: share s of A's rows (NT / split of them) is added up by
+            // rank s, from the parts that every rank writes into its ring, which is idle:
+            // all MMAs and loads of the cluster are done at the first barrier.
+            // Four of A's rows make a piece: 16 bytes a lane, lane after lane, so that a warp
+            // sends 512 bytes in one run (a lane's pieces together, 64 bytes apart from the next
+            // lane's, took 22 us for 100 x 4096 x 4096 over 8 CTAs instead of 13).
+            const int share = NT / split, shift = __ffs(share) - 1;  // powers of two, 4 at least
+            const bool live = t0 < total;
+            const int q = warp & 3;
+            bool go = true;
+            if (warp >= 4 && live) {
+                go = mbar_wait(bar(TFULL), turn, abort_flag);
+                go = __all_sync(0xffffffffu, go);
+                if (!go) report_error(st, -4, kSiteFp4Epilogue);
+            }
+            cluster_sync_all();
+            if (warp >= 4 && live && go) {
+                tc_fence_after();
+                const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16);
+                const uint32_t mine = base + (uint32_t)(rank * (share / 4) * 128 + q * 32 + lane) * 16u;
+#pragma unroll 1
+                for (int j0 = 0; j0 < NT; j0 += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(taddr + (uint32_t)j0, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const int to = (j0 + j) >> shift, piece = ((j0 + j) & (share - 1)) >> 2;
+                        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         peer_addr(mine + (uint32_t)piece * 2048u, (uint32_t)to)),
+                                     "r"(r[j]), "r"(r[j + 1]), "r"(r[j + 2]), "r"(r[j + 3])
+                                     : "memory");
+                    }
+                }
+                tc_fence_before();
+            }
+            cluster_sync_all();
+            if (warp >= 4 && live && go) {
+                const Fp4Tile tile = fp4_tile<NT>(g, prefix, t0);
+                const float alpha = (g.ga ? *g.ga : 1.0f) * (g.gb ? g.gb[tile.expert] : 1.0f);
+                const int n = tile.nb * 128 + q * 32 + lane;
+                const float4* part = reinterpret_cast<const float4*>(gbase) + q * 32 + lane;
+                const int mine = min(share, tile.rows - (int)rank * share);
+                TC* c = static_cast<TC*>(g.C) + (tile.row0 + (int)rank * share) * (int64_t)g.N + n;
+#pragma unroll 2
+                for (int at = 0; at < mine; at += 4) {
+                    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        if (s < split) {
+                            const float4 v = part[(s * (share / 4) + (at >> 2)) * 128];
+                            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                        }
+                    const float out[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n < g.N && at + i < mine) c[(int64_t)(at + i) * g.N] = (TC)(alpha * out[i]);
+                }
+            }
+        }
+        if (split == 1 || t0 + step >= total) break;
+        // the next tile's loads (the other proxy) follow these reads of the parts, its MMAs those of TMEM
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
+    if (warp == 0 && lane == 0) {
+        // Every load must have landed before the CTA ends.
+        volatile int no_abort = 0;
+        for (int i = 0; i < S; ++i)
+            if (!mbar_wait(bar(i), (i < stage) ? phase : (phase ^ 1u), &no_abort))
+                report_error(st, -4, kSiteFp4Drain);
+    } else if (warp == 1) {
+        // no MMA may still run when TMEM is freed
+        commit_local<1>(elect_lane(), bar(DRAIN));
+        volatile int no_abort = 0;
+        if (!mbar_wait(bar(DRAIN), 0, &no_abort)) report_error(st, -4, kSiteFp4Drain);
     }
     __syncwarp();
-    if (split > 1) {
-        // The parts of a tile: share s of A's rows (NT / split of them) is added up by
-        // rank s, from the parts that every rank writes into its ring, which is idle:
-        // all MMAs and loads of the cluster are done at the first barrier.
-        // Four of A's rows make a piece: 16 bytes a lane, lane after lane, so that a warp
-        // sends 512 bytes in one run (a lane's pieces together, 64 bytes apart from the next
-        // lane's, took 22 us for 100 x 4096 x 4096 over 8 CTAs instead of 13).
-        const int share = NT / split, shift = __ffs(share) - 1;  // powers of two, 4 at least
-        const bool live = first < total;
-        const int q = warp & 3;
-        bool go = true;
-        if (warp >= 4 && live) {
-            go = mbar_wait(bar(TFULL), 0u, abort_flag);
-            go = __all_sync(0xffffffffu, go);
-            if (!go) report_error(st, -4, kSiteFp4Epilogue);
-        }
-        cluster_sync_all();
-        if (warp >= 4 && live && go) {
-            tc_fence_after();
-            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16);
-            const uint32_t mine = base + (uint32_t)(rank * (share / 4) * 128 + q * 32 + lane) * 16u;
-#pragma unroll 1
-            for (int j0 = 0; j0 < NT; j0 += 32) {
-                uint32_t r[32];
-                tmem_ld32(taddr + (uint32_t)j0, r);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const int to = (j0 + j) >> shift, piece = ((j0 + j) & (share - 1)) >> 2;
-                    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     peer_addr(mine + (uint32_t)piece * 2048u, (uint32_t)to)),
-                                 "r"(r[j]), "r"(r[j + 1]), "r"(r[j + 2]), "r"(r[j + 3])
-                                 : "memory");
-                }
-            }
-            tc_fence_before();
-        }
-        cluster_sync_all();
-        if (warp >= 4 && live && go) {
-            const Fp4Tile tile = fp4_tile<NT>(g, prefix, first);
-            const float alpha = (g.ga ? *g.ga : 1.0f) * (g.gb ? g.gb[tile.expert] : 1.0f);
-            const int n = tile.nb * 128 + q * 32 + lane;
-            const float4* part = reinterpret_cast<const float4*>(gbase) + q * 32 + lane;
-            const int mine = min(share, tile.rows - (int)rank * share);
-            TC* c = static_cast<TC*>(g.C) + (tile.row0 + (int)rank * share) * (int64_t)g.N + n;
-#pragma unroll 2
-            for (int at = 0; at < mine; at += 4) {
-                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    if (s < split) {
-                        const float4 v = part[(s * (share / 4) + (at >> 2)) * 128];
-                        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-                    }
-                const float out[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (n < g.N && at + i < mine) c[(int64_t)(at + i) * g.N] = (TC)(alpha * out[i]);
-            }
-        }
-    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -1037,7 +1047,9 @@ static Fp4Plan fp4_plan(int64_t M, int64_t N, int64_t K, int experts, bool group
     const int most_parts = p.rows == 32 ? 8 : 4;
     p.split = 1;
     while (p.split < most_parts && busy * p.split * 2 <= slots && kb >= 4 * p.split && !(grouped && cap < sms)) p.split *= 2;
-    p.ctas = p.split > 1 ? (int)(tiles * p.split) : (int)(grouped || slots < tiles ? slots : tiles);
+    // One wave: of the tiles that the buffer has room for, the counts leave few (26 tokens to
+    // 6 of 6 experts of 1440 x 2688, 72 of 168 tiles: a cluster for each takes 3 us more).
+    p.ctas = (int)((tiles * p.split < slots ? tiles * p.split : slots) / p.split) * p.split;
     return p;
 }
 

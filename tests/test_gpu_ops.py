@@ -836,6 +836,16 @@ def test_experts_products(c3, E, N, K, counts, budget, fmt, out):
     assert (got[~mine] == 77.0).all()
 
 
+@pytest.mark.parametrize("out", [0, 1])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("E,N,K,counts,budget", [
+    (64, 100, 2048, [1] * 20 + [5100] + [2] * 43, 0), (40, 250, 1100, [4900] + [0, 1, 64] * 13, 0),
+    (6, 1440, 2690, [26] * 6, 0)])
+def test_experts_products_more_tiles_than_clusters(c3, E, N, K, counts, budget, fmt, out):
+    """K split over clusters that each do several tiles: an expert has far more rows than the rest."""
+    test_experts_products(c3, E, N, K, counts, budget, fmt, out)
+
+
 def test_experts_products_skip_bad_ranges(c3):
     rng = np.random.default_rng(4)
     E, N, K, R = 5, 128, 128, 512
