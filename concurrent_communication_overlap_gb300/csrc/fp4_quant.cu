@@ -16,6 +16,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 namespace c3 {
 
 constexpr int kQRows = 32;                 // rows of a CTA's tile: one row group of a scale tile
@@ -189,9 +191,6 @@ __device__ __forceinline__ void encode16_mx_bf16(const uint32_t (&w)[8], uint32_
     codes.y = to_codes(v);
 }
 
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-
 // The codes and the scale byte of columns c .. c + 15 of row r to their places; every lane of the warp takes part.
 template <bool NV>
 __device__ __forceinline__ void put16(uint32_t byte, uint2 codes, bool have, const Fp4& q, int64_t mat_row, uint8_t* tile_row,
@@ -269,6 +268,26 @@ __device__ __forceinline__ void scale16(float (&v)[16], float t) {
     for (int j = 0; j < 16; j += 2) unpack2(mul2(pack2(v[j], v[j + 1]), pack2(t, t)), v[j], v[j + 1]);
 }
 
+template <typename T, bool NV>
+__device__ __forceinline__ void encode_raw(const Raw16<T>& x, float inv_t, uint32_t& byte, uint2& codes) {
+    if constexpr (!NV && sizeof(T) == 2) {
+        encode16_mx_bf16(x.w, byte, codes);
+    } else {
+        float v[16];
+        x.values(v);
+        float amax;
+        if constexpr (sizeof(T) == 2) {
+            // multiplying by a number and rounding keep the order: the maximum may come first
+            amax = __uint_as_float(block_max_bf16<NV>(x.w)) * fabsf(inv_t);
+            scale16(v, inv_t);
+        } else {
+            if (NV) scale16(v, inv_t);
+            amax = block_max<NV>(v);
+        }
+        encode16<NV>(v, amax, byte, codes);
+    }
+}
+
 // One CTA: 32 rows of one matrix, 128 columns at a time, `across` CTAs a row tile;
 // a thread's next 16 columns are on their way while these are encoded.  Eight
 // threads a row: a row's scales of a tile are one word, and codes leave 64 bytes at
@@ -309,63 +328,97 @@ __global__ void __launch_bounds__(kQThreads)
         ahead.template load<VEC>(xr + next, have && u + across < spans ? q.cols - next : 0, lo, hi);
         uint32_t byte;
         uint2 codes;
-        if constexpr (!NV && sizeof(T) == 2) {
-            encode16_mx_bf16(now.w, byte, codes);
-        } else {
-            float v[16];
-            now.values(v);
-            float amax;
-            if constexpr (sizeof(T) == 2) {
-                // multiplying by a number and rounding keep the order: the maximum may come first
-                amax = __uint_as_float(block_max_bf16<NV>(now.w)) * fabsf(inv_t);
-                scale16(v, inv_t);
-            } else {
-                if (NV) scale16(v, inv_t);
-                amax = block_max<NV>(v);
-            }
-            encode16<NV>(v, amax, byte, codes);
-        }
+        encode_raw<T, NV>(now, inv_t, byte, codes);
         put16<NV>(byte, codes, have, q, (int64_t)mat * q.rows + r, tile_row, c, pitch, k_tiles);
         now = ahead;
         c = next;
     }
 }
 
-// The transpose of what lies in memory: 32 rows x 256 columns, turned in shared
-// memory, whose rows are the matrix's columns, 32 values and one of padding each
-// (2050 x 4100 fp32 to NV: 16 us).
-template <typename T, bool NV>
-__global__ void __launch_bounds__(kQThreads)
+// The transpose of what lies in memory: 64 rows x 128 columns, turned in shared
+// memory, which holds the values of two neighbouring rows as one word, column after
+// column.  A lane loads two values of a column at once where PAIRS (else one after
+// the other) and encodes 16 columns of two rows.  The columns' skew of 4 (bf16) or 2
+// (fp32) words for each 16 lets the lanes of a warp, 4 pairs of rows x 8 lots of 16
+// columns, meet in no bank.  All of a thread's loads are on their way before the first
+// is stored: 8192 x 8192 bf16 to NV takes 44 us, where a load waited for the store before
+// it 133, and with a value at a time, each in a word of its own, 83; fp32 to MX 49 us
+// (bytes 45); 2050 x 4100 fp32 to NV 7.7 us.  Four CTAs an SM: three take 48 and 53 us for
+// the large ones, five, whose registers spill, 43 and 60.
+constexpr int kTRows = 64;
+constexpr int kTCols = 128;
+
+template <typename T, bool NV, bool PAIRS>
+__global__ void __launch_bounds__(kQThreads, 4)
     fp4_quantize_turned_kernel(const T* __restrict__ x, int64_t ld, Fp4 q, int64_t pitch, int64_t k_tiles,
-                               int64_t scale_bytes, int64_t x_stride, unsigned col_tiles) {
-    __shared__ float tile[kQCols][kQRows + 1];
-    const int i = threadIdx.x >> 3, g = threadIdx.x & 7;
-    const unsigned rt = blockIdx.x / col_tiles;
-    const int64_t c0 = (int64_t)(blockIdx.x - rt * col_tiles) * kQCols, c = c0 + g * 16;
-    const int64_t r = (int64_t)rt * kQRows + i;
+                               int64_t scale_bytes, int64_t x_stride, unsigned row_tiles) {
+    using Two = typename std::conditional<sizeof(T) == 2, uint32_t, uint2>::type;
+    constexpr int kSkew = sizeof(T) == 2 ? 4 : 2, kPairs = kTRows / 2, kWarps = kQThreads / 32;
+    __shared__ Two tile[kTCols * kPairs + kTCols / 16 * kSkew];
+    const int i = threadIdx.x >> 3, g = threadIdx.x & 7, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // neighbouring CTAs read neighbours in memory
+    const unsigned ct = blockIdx.x / row_tiles, rt = blockIdx.x - ct * row_tiles;
+    const int64_t c0 = (int64_t)ct * kTCols;
     const int mat = blockIdx.y;
-    const int rr = threadIdx.x & 31;
-    const int64_t row = (int64_t)rt * kQRows + rr;
-    const T* from = x + (int64_t)mat * x_stride + c0 * ld + row;
-    const int most = (int)min((int64_t)kQCols, q.cols - c0);
+    const int64_t row = (int64_t)rt * kTRows + 2 * lane;  // the lane loads it and the next
+    const int most = (int)min((int64_t)kTCols, q.cols - c0);
+    const int rows = (int)max((int64_t)0, min((int64_t)2, q.rows - row));
+    const T* from = x + (int64_t)mat * x_stride + (c0 + warp) * ld + row;
     chain_wait();
-#pragma unroll 16
-    for (int cc = threadIdx.x >> 5; cc < kQCols; cc += kQThreads / 32)
-        tile[cc][rr] = (cc < most && row < q.rows) ? load1(from + cc * ld) : 0.0f;
-    __syncthreads();
     const float inv_t = NV && q.tensor_scale ? __fdiv_rn(1.0f, q.tensor_scale[mat]) : 1.0f;
-    uint8_t* tile_row = q.scales + (int64_t)mat * scale_bytes + (r / kTileRows) * k_tiles * 512 + (r % 32) * 16 +
-                        (r % kTileRows) / 32 * 4;
+    using Bits = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
+    Two v[kTCols / kWarps];  // all on their way before the first is stored
+#pragma unroll
+    for (int n = 0; n < kTCols / kWarps; ++n, from += kWarps * ld) {
+        const int have = warp + n * kWarps < most ? rows : 0;
+        const Bits* p = reinterpret_cast<const Bits*>(from);
+        if constexpr (PAIRS) {
+            v[n] = Two{};
+            if (have == 2) v[n] = *reinterpret_cast<const Two*>(p);
+        } else {
+            Bits lo = 0, hi = 0;
+            if (have > 0) lo = p[0];
+            if (have > 1) hi = p[1];
+            if constexpr (sizeof(T) == 2)
+                v[n] = lo | (uint32_t)hi << 16;
+            else
+                v[n] = make_uint2(lo, hi);
+        }
+    }
+    if (PAIRS && rows == 1) {  // an odd number of rows
+        from -= kTCols * ld;
+#pragma unroll 1
+        for (int n = 0; n < kTCols / kWarps; ++n, from += kWarps * ld) {
+            if (warp + n * kWarps >= most) break;
+            const Bits last = *reinterpret_cast<const Bits*>(from);
+            tile[(warp + n * kWarps) * kPairs + n / 2 * kSkew + lane] = Two{last};
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < kTCols / kWarps; ++n)
+        if (!(PAIRS && rows == 1 && warp + n * kWarps < most))
+            tile[(warp + n * kWarps) * kPairs + n / 2 * kSkew + lane] = v[n];
+    __syncthreads();
+    Two u[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) u[j] = tile[(g * 16 + j) * kPairs + g * kSkew + i];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        float v[16];
+        Raw16<T> raw;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = tile[h * 128 + g * 16 + j][i];
+        for (int j = 0; j < Raw16<T>::kWords; ++j) {
+            if constexpr (sizeof(T) == 2)
+                raw.w[j] = __byte_perm(u[2 * j], u[2 * j + 1], h ? 0x7632 : 0x5410);
+            else
+                raw.w[j] = h ? u[j].y : u[j].x;
+        }
         uint32_t byte;
         uint2 codes;
-        if (NV) scale16(v, inv_t);
-        encode16<NV>(v, block_max<NV>(v), byte, codes);
-        put16<NV>(byte, codes, r < q.rows, q, (int64_t)mat * q.rows + r, tile_row, c + h * 128, pitch, k_tiles);
+        encode_raw<T, NV>(raw, inv_t, byte, codes);
+        const int64_t r = (int64_t)rt * kTRows + 2 * i + h;
+        uint8_t* tile_row = q.scales + (int64_t)mat * scale_bytes + (r / kTileRows) * k_tiles * 512 + (r % 32) * 16 +
+                            (r % kTileRows) / 32 * 4;
+        put16<NV>(byte, codes, r < q.rows, q, (int64_t)mat * q.rows + r, tile_row, c0 + g * 16, pitch, k_tiles);
     }
 }
 
@@ -481,9 +534,9 @@ __global__ void __launch_bounds__(kQThreads)
 
 // ---------------------------------------------------------------- host side
 
-// `per_row` CTAs for each 32 rows of each matrix.
-static int fp4_grid(const Fp4& q, int64_t per_row, dim3* grid) {
-    const int64_t n = (q.rows + kQRows - 1) / kQRows * per_row;
+// `per_tile` CTAs for each `rows` rows of each matrix.
+static int fp4_grid(const Fp4& q, int rows, int64_t per_tile, dim3* grid) {
+    const int64_t n = (q.rows + rows - 1) / rows * per_tile;
     if (n > 0x7fffffff || q.count > 65535) return set_error(-5, "4-bit matrix has too many tiles for one launch");
     *grid = dim3((unsigned)n, (unsigned)q.count);
     return 0;
@@ -502,15 +555,23 @@ int fp4_quantize_launch(const void* x, int bf16, int64_t x_rows, int64_t ld, int
     int rc;
     cudaError_t e;
     if (transpose) {
-        const unsigned col_tiles = (unsigned)((cols + kQCols - 1) / kQCols);
-        if ((rc = fp4_grid(q, col_tiles, &grid))) return rc;
-#define C3_GO(T_, NV_)                                                                                       \
-    e = launch_chained(fp4_quantize_turned_kernel<T_, NV_>, grid, kQThreads, 0, s, 1, static_cast<const T_*>(x), \
-                       ld, q, q.pitch(), q.k_tiles(), q.scale_bytes(), stride, col_tiles)
-        if (bf16 && q.nv) C3_GO(__nv_bfloat16, true);
-        else if (bf16) C3_GO(__nv_bfloat16, false);
-        else if (q.nv) C3_GO(float, true);
-        else C3_GO(float, false);
+        const unsigned col_tiles = (unsigned)((cols + kTCols - 1) / kTCols);
+        if ((rc = fp4_grid(q, kTRows, col_tiles, &grid))) return rc;
+        const unsigned row_tiles = (unsigned)((q.rows + kTRows - 1) / kTRows);
+        const bool pairs = (uintptr_t)x % (bf16 ? 4 : 8) == 0 && ld % 2 == 0;
+#define C3_GO(T_, NV_, PAIRS_)                                                                                  \
+    e = launch_chained(fp4_quantize_turned_kernel<T_, NV_, PAIRS_>, grid, kQThreads, 0, s, 1,                     \
+                       static_cast<const T_*>(x), ld, q, q.pitch(), q.k_tiles(), q.scale_bytes(), stride, row_tiles)
+#define C3_PICK(T_)                                    \
+    do {                                               \
+        if (q.nv && pairs) C3_GO(T_, true, true);      \
+        else if (q.nv) C3_GO(T_, true, false);         \
+        else if (pairs) C3_GO(T_, false, true);        \
+        else C3_GO(T_, false, false);                  \
+    } while (0)
+        if (bf16) C3_PICK(__nv_bfloat16);
+        else C3_PICK(float);
+#undef C3_PICK
 #undef C3_GO
     } else {
         // Up to eight spans of 128 columns a CTA, so that loads run ahead, but six CTAs an
@@ -525,7 +586,7 @@ int fp4_quantize_launch(const void* x, int bf16, int64_t x_rows, int64_t ld, int
         if (!ds) return -3;
         const int64_t share = tiles * spans / ((int64_t)ds->sm_count * (row_of ? 8 : 6));
         const unsigned each = (unsigned)(share < 1 ? 1 : share < 8 ? share : 8), across = (spans + each - 1) / each;
-        if ((rc = fp4_grid(q, across, &grid))) return rc;
+        if ((rc = fp4_grid(q, kQRows, across, &grid))) return rc;
         const bool vec = vec_ok(x, ld, bf16) && (q.count == 1 || (stride * (bf16 ? 2 : 4)) % 16 == 0);
 #define C3_GO(T_, NV_, VEC_)                                                                                   \
     e = launch_chained(fp4_quantize_kernel<T_, NV_, VEC_>, grid, kQThreads, 0, s, 1, static_cast<const T_*>(x),  \
@@ -550,7 +611,7 @@ int fp4_quantize_launch(const void* x, int bf16, int64_t x_rows, int64_t ld, int
 int fp4_dequantize_launch(const Fp4& q, void* x, int bf16, int64_t ld, cudaStream_t s) {
     dim3 grid;
     const unsigned col_tiles = (unsigned)((q.cols + kQCols - 1) / kQCols);
-    int rc = fp4_grid(q, col_tiles, &grid);
+    int rc = fp4_grid(q, kQRows, col_tiles, &grid);
     if (rc) return rc;
     const bool vec = vec_ok(x, ld, bf16);
     cudaError_t e;

@@ -616,6 +616,29 @@ def test_quantise_rows_of_any_alignment(c3, R, C, gather, fmt, ty):
 
 @pytest.mark.parametrize("ty", [0, 1])
 @pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("R", [1, 2, 63, 65, 130, 257])
+@pytest.mark.parametrize("C", [5, 128, 300])
+def test_quantise_transposed_is_the_transpose_quantised(c3, R, C, fmt, ty):
+    """Rows in pairs and singly, an odd last one, NaNs beside the columns."""
+    rng = np.random.default_rng(R + 1000 * C)
+    g = 0.3 if fmt else None
+    x = values(rng, R, C, ty)[0]
+    for count in (1, 2):
+        want, codes, scales = new_fp4(c3, R, C, fmt, [g] * count if fmt else None, count=count)
+        c3.c3_fp4_quantize(torch.stack([x] * count), ty, R, C, want)
+        for ld, shift in ((R, 0), (R + 1, 0), (R + 2, 1), (R + 3, 2)):
+            flat = torch.full((shift + count * C * ld,), float("nan"), dtype=TD[ty], device="cuda")
+            view = flat[shift:].view(count, C, ld)
+            view[:, :, :R] = x.t()
+            q, c2, s2 = new_fp4(c3, R, C, fmt, [g] * count if fmt else None, count=count)
+            c3.c3_fp4_quantize(view, ty, C, R, q, ld=ld, transpose=True)
+            torch.cuda.synchronize()
+            assert c2.intact() and s2.intact()
+            assert torch.equal(c2.t, codes.t) and torch.equal(s2.t, scales.t), (ld, shift, count)
+
+
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("fmt", [0, 1])
 def test_quantise_special_values(c3, fmt, ty):
     x = np.ones((6, 64), np.float32)
     x[0, 3] = np.nan
