@@ -95,9 +95,16 @@ __device__ __forceinline__ void encode16(float (&v)[16], float amax, uint32_t& b
 #pragma unroll
         for (int i = 0; i < 16; i += 2) unpack2(mul2(pack2(v[i], v[i + 1]), i2), v[i], v[i + 1]);
     } else {
-        byte = to_e4m3(__fdiv_rn(amax, 6.0f));
+        // amax / 6 and 1 / s, correctly rounded, by one correction each (Markstein, IBM J. Res.
+        // Dev. 34, 1990): of a product with the rounded 1 / 6 (a quotient so small that the
+        // remainder underflows is scale 0 either way), and of the reciprocal instruction's result,
+        // which is off by an ulp at most (s has four bits, so its significand is not all ones).
+        const float sixth = 1.0f / 6.0f, quot = amax * sixth;
+        byte = to_e4m3(fmaf(fmaf(-6.0f, quot, amax), sixth, quot));
         const float s = from_e4m3(byte);
-        const float inv = byte ? __frcp_rn(s) : 0.0f;
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+        inv = byte ? fmaf(inv, fmaf(-s, inv, 1.0f), inv) : 0.0f;
         const uint64_t i2 = pack2(inv, inv), s2 = pack2(-s, -s);
         // v / s, correctly rounded, from the rounded reciprocal and one correction by the
         // remainder (Markstein, IBM J. Res. Dev. 34, 1990); what is so small that the
@@ -292,7 +299,7 @@ __device__ __forceinline__ void encode_raw(const Raw16<T>& x, float inv_t, uint3
 // a thread's next 16 columns are on their way while these are encoded.  Eight
 // threads a row: a row's scales of a tile are one word, and codes leave 64 bytes at
 // a time.  8192 x 8192 bf16 to MX takes 32 us, 5.3 TB/s; 32768 gathered rows of 4096
-// bf16 to NV 61 us, bound by instructions (187 for 16 columns).
+// bf16 to NV 54 us, bound by instructions.
 template <typename T, bool NV, bool VEC>
 __global__ void __launch_bounds__(kQThreads)
     fp4_quantize_kernel(const T* __restrict__ x, int64_t x_rows, int64_t ld, const int32_t* __restrict__ row_of,
@@ -341,9 +348,9 @@ __global__ void __launch_bounds__(kQThreads)
 // the other) and encodes 16 columns of two rows.  The columns' skew of 4 (bf16) or 2
 // (fp32) words for each 16 lets the lanes of a warp, 4 pairs of rows x 8 lots of 16
 // columns, meet in no bank.  All of a thread's loads are on their way before the first
-// is stored: 8192 x 8192 bf16 to NV takes 44 us, where a load waited for the store before
+// is stored: 8192 x 8192 bf16 to NV takes 43 us, where a load waited for the store before
 // it 133, and with a value at a time, each in a word of its own, 83; fp32 to MX 49 us
-// (bytes 45); 2050 x 4100 fp32 to NV 7.7 us.  Four CTAs an SM: three take 48 and 53 us for
+// (bytes 45); 2050 x 4100 fp32 to NV 7.4 us.  Four CTAs an SM: three take 48 and 53 us for
 // the large ones, five, whose registers spill, 43 and 60.
 constexpr int kTRows = 64;
 constexpr int kTCols = 128;

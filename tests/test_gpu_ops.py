@@ -637,6 +637,36 @@ def test_quantise_transposed_is_the_transpose_quantised(c3, R, C, fmt, ty):
             assert torch.equal(c2.t, codes.t) and torch.equal(s2.t, scales.t), (ld, shift, count)
 
 
+def test_quantise_every_nv_scale(c3):
+    """Each e4m3 scale with each tie between codes and its neighbours in fp32; and maxima around the scales' own ties."""
+    bits = np.arange(1, 127)
+    s = np.where(bits < 8, bits * 2.0 ** -9, (8 + bits % 8) * 2.0 ** (bits // 8 - 10)).astype(np.float32)
+    ties = np.float32([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, 6])
+    x = []
+    for way in (0, -np.inf, np.inf):
+        t = s[:, None] * ties[None]
+        x.append(t if way == 0 else np.nextafter(t, np.float32(way)))
+        x[-1][:, -1] = 6 * s
+    # 16 columns: eight ties and their negatives, without the maximum's
+    blocks = np.concatenate([np.concatenate([b, -b], 1) for b in x])
+    mid = np.float32(6) * (s[1:] + s[:-1]) / 2
+    peaks = np.concatenate([mid, np.nextafter(mid, np.float32(np.inf)), np.nextafter(mid, np.float32(0)),
+                            np.float32([1e-45, 1e-38, 6 * 2.0 ** -11, 6 * 2.0 ** -10, 5.9 * 2.0 ** -10, 3e38, 2688, 2800])])
+    more = np.zeros((len(peaks), 16), np.float32)
+    more[:, 3] = peaks
+    more[:, 5] = -peaks / 2
+    x = np.concatenate([blocks, more]).astype(np.float32)
+    R, C = x.shape
+    for transpose in (False, True):
+        q, codes, scales = new_fp4(c3, R, C, 1)
+        src = cuda(np.ascontiguousarray(x.T) if transpose else x)
+        c3.c3_fp4_quantize(src, 0, src.shape[0], src.shape[1], q, transpose=transpose)
+        torch.cuda.synchronize()
+        ref_codes, ref_bytes, _, _ = quantise_oracle(x, 1)
+        assert np.array_equal(read_tiles(scales.t[0].cpu().numpy(), R, 1)[0], ref_bytes)
+        assert np.array_equal(codes.t[0].cpu().numpy(), ref_codes)
+
+
 @pytest.mark.parametrize("ty", [0, 1])
 @pytest.mark.parametrize("fmt", [0, 1])
 def test_quantise_special_values(c3, fmt, ty):
