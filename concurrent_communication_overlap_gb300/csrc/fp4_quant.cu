@@ -299,7 +299,7 @@ __device__ __forceinline__ void encode_raw(const Raw16<T>& x, float inv_t, uint3
 // a thread's next 16 columns are on their way while these are encoded.  Eight
 // threads a row: a row's scales of a tile are one word, and codes leave 64 bytes at
 // a time.  8192 x 8192 bf16 to MX takes 32 us, 5.3 TB/s; 32768 gathered rows of 4096
-// bf16 to NV 54 us, bound by instructions.
+// bf16 to NV 54 us, bound by the conversion instruction.
 template <typename T, bool NV, bool VEC>
 __global__ void __launch_bounds__(kQThreads)
     fp4_quantize_kernel(const T* __restrict__ x, int64_t x_rows, int64_t ld, const int32_t* __restrict__ row_of,
