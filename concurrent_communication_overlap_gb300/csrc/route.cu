@@ -2,7 +2,8 @@
 // their weights, and the gradient of the weights with respect to the logits.
 //
 // L lanes a token (8, 16 or 32, so a warp takes 4, 2 or 1).  Lane l of them
-// holds the logits of NI consecutive experts, l NI and up, in registers.  The
+// holds the logits of NI consecutive experts, l NI and up (in groups, those of a run
+// of lanes being a group), in registers.  The
 // choice compares 32-bit integers that order as the float keys do; of equal keys
 // the lowest lane, and in it the lowest register, is the lowest expert.
 //
@@ -11,7 +12,7 @@
 // instructions a token with 32 lanes and 192 with 8 (11 us against 15).
 //
 // Instructions are what bounds it, not bytes: 65536 x 256 with groups takes 57 us,
-// 717 instructions a token, a third of them the 256 sigmoids, where its bytes need
+// about 720 instructions a token, a third of them the 256 sigmoids, where its bytes need
 // 10.5; 32768 x 60 takes 11 us forward and 9 backward, where they need 1 and 1.
 #include "ops_device.cuh"
 #include "c3_internal.h"
@@ -74,42 +75,48 @@ __host__ __device__ constexpr int vector_of() {
     return N % 4 ? 1 : sizeof(T) == 2 && N % 8 == 0 ? 8 : 4;
 }
 
-// N consecutive logits of a row from expert e0 on; -inf past the last.  vec: rows
-// start on 16 bytes and are whole vectors.
+// N consecutive logits of a row from expert e0 on; -inf from expert `end` on.  vec:
+// rows start on 16 bytes and lanes end at whole vectors.
 template <int N, typename T>
-__device__ __forceinline__ void load_row(const T* xr, int e0, int E, bool vec, float (&x)[N]) {
+__device__ __forceinline__ void load_row(const T* xr, int e0, int end, bool vec, float (&x)[N]) {
     constexpr int V = vector_of<T, N>();
-    if (V > 1 && vec) {
+    if (V == 1 || !vec) {
 #pragma unroll
-        for (int i = 0; i < N; i += V) {
-            if constexpr (sizeof(T) == 4 && V > 1) {
-                float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                if (e0 + i < E) v = *reinterpret_cast<const float4*>(xr + e0 + i);
-                x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-            } else if constexpr (V > 1) {
-                uint32_t u[V / 2];
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) u[j] = 0xff80ff80u;  // -inf, twice
-                if (e0 + i < E) {
-                    if constexpr (V == 8) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(xr + e0 + i);
-                        u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2*>(xr + e0 + i);
-                        u[0] = v.x, u[1] = v.y;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) {
-                    x[i + 2 * j] = __uint_as_float(u[j] << 16);
-                    x[i + 2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-                }
-            }
-        }
+        for (int i = 0; i < N; ++i) x[i] = e0 + i < end ? load_f(xr + e0 + i) : -INFINITY;
         return;
     }
+    const auto vector = [&](int i) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(xr + e0 + i);
+            x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+        } else {
+            uint32_t u[V / 2 + 1];
+            if constexpr (V == 8) {
+                const uint4 v = *reinterpret_cast<const uint4*>(xr + e0 + i);
+                u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(xr + e0 + i);
+                u[0] = v.x, u[1] = v.y;
+            }
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = e0 + i < E ? load_f(xr + e0 + i) : -INFINITY;
+            for (int j = 0; j < V / 2; ++j) {
+                x[i + 2 * j] = __uint_as_float(u[j] << 16);
+                x[i + 2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+            }
+        }
+    };
+    if constexpr (V > 1) {
+        if (e0 + N <= end) {
+#pragma unroll
+            for (int i = 0; i < N; i += V) vector(i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < N; i += V)
+                if (e0 + i < end) vector(i);
+        }
+    }
 }
 
 // The same by way of shared memory, for rows that no vector load fits: neighbouring
@@ -136,17 +143,37 @@ __device__ __forceinline__ void load_staged(const T* xr, int E, float none, uint
     __syncwarp();
 }
 
-// Groups that are whole runs of 2^j of the token's lanes: score and rank them
-// with shuffles.  Sets the keys of groups outside the best `keep` to 0.
+// The same for lanes whose first experts e0 are not N apart: value by value, each 32
+// skewed by one word, which keeps lanes 12 or 16 experts apart in banks of their own.
+template <int N, int L, typename T>
+__device__ __forceinline__ void load_staged(const T* xr, int E, int e0, int end, float none, uint32_t* stage, int lane,
+                                            float (&x)[N]) {
+    const int at_lane = lane & (L - 1), base = (lane / L) * (L * N / 32 * 33);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int e = at_lane + L * i;
+        if (e < E) stage[base + e + (e >> 5)] = __float_as_uint(load_f(xr + e));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int e = e0 + i;
+        x[i] = e < end ? __uint_as_float(stage[base + e + (e >> 5)]) : none;
+    }
+    __syncwarp();
+}
+
+// Groups that are whole runs of `lanes`, a power of two, of the token's lanes: score and
+// rank them with shuffles.  Sets the keys of groups outside the best `keep` to 0.
 template <int NI, int L>
-__device__ __forceinline__ void groups_by_lanes(uint32_t (&key)[NI], int gs, int best_of, int keep, int lane) {
+__device__ __forceinline__ void groups_by_lanes(uint32_t (&key)[NI], int lanes, int best_of, int keep, int lane) {
     uint32_t b1 = 0u, b2 = 0u;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         b2 = max(b2, min(b1, key[i]));
         b1 = max(b1, key[i]);
     }
-    const int lanes = gs / NI;
     for (int o = 1; o < lanes; o <<= 1) {
         const uint32_t c1 = __shfl_xor_sync(kFull, b1, o), c2 = __shfl_xor_sync(kFull, b2, o);
         b2 = max(max(b2, c2), min(b1, c1));
@@ -263,8 +290,8 @@ __device__ __forceinline__ float choice_weight(const T* xr, int mine, const Rout
     return s > 0.0f ? w / s : 0.0f;
 }
 
-// NI experts a lane, L NI >= E.  GROUPS: 0 none, 1 whole runs of lanes, 2 any (L =
-// 32).  vec: as load_row's.  topk <= L.
+// NI experts a lane, L NI >= E.  GROUPS: 0 none, 1 a run of L / groups lanes each (groups
+// a power of two), 2 any (L = 32).  vec: as load_row's.  topk <= L.
 // Registers: 65536 x 256 took 62 us with 64 and 66 with 80; 16000 x 1000 takes 76 with
 // 128, 81 with 80 and 127 with 218.
 template <typename T, int NI, int L, int GROUPS>
@@ -276,19 +303,29 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NI == 12 || NI == 16 ? 4 : N
     // 8 lanes of 8 share the lines that they load: staged, 32768 x 60 took 2 us more
     constexpr bool kStaged = NI >= 12 || (NI == 8 && L == 32);
     // a warp's scratch: the groups' keys first, then the sorted lines
-    constexpr int kScratch = GROUPS == 2 ? 1024 : kInMemory ? NI * 32 : 1;
+    constexpr int kScratch = GROUPS == 2 ? 1024 : kInMemory ? NI * (GROUPS == 1 ? 33 : 32) : 1;
     __shared__ __align__(16) uint32_t scratch[kRouteWarps][kScratch];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int at_lane = lane & (L - 1);
-    const int E = a.experts, k = a.topk, e0 = at_lane * NI;
+    const int E = a.experts, k = a.topk;
+    // This lane's experts, [e0, end): a run of L / groups lanes has a group's, else each lane the next NI.
+    const int run = GROUPS == 1 ? L / a.groups : 1, shift = GROUPS == 1 ? __ffs(run) - 1 : 0;
+    const int size = GROUPS == 1 ? E / a.groups : 0;
+    const auto first_of = [&](int l) { return GROUPS == 1 ? (l >> shift) * size + (l & (run - 1)) * NI : l * NI; };
+    const int e0 = first_of(at_lane), end = GROUPS == 1 ? (at_lane >> shift) * size + size : E;
     const bool soft = a.score == 0;
     chain_wait();
     float bias[NI] = {};
     if constexpr (kStaged) {
-        if (a.bias) load_staged<NI, L>(a.bias, E, 0.0f, scratch[warp], lane, bias);
+        if (a.bias) {
+            if constexpr (GROUPS == 1)
+                load_staged<NI, L>(a.bias, E, e0, end, 0.0f, scratch[warp], lane, bias);
+            else
+                load_staged<NI, L>(a.bias, E, 0.0f, scratch[warp], lane, bias);
+        }
     } else if (a.bias) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) bias[i] = e0 + i < E ? a.bias[e0 + i] : 0.0f;
+        for (int i = 0; i < NI; ++i) bias[i] = e0 + i < end ? a.bias[e0 + i] : 0.0f;
     }
     const int64_t step = (int64_t)gridDim.x * kRouteWarps * kRows;
     for (int64_t row0 = ((int64_t)blockIdx.x * kRouteWarps + warp) * kRows; row0 < tokens; row0 += step) {
@@ -297,9 +334,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NI == 12 || NI == 16 ? 4 : N
         const T* xr = logits + (live ? row : row0) * ld;  // a lane without a token repeats another's
         float x[NI];
         if (kStaged && !vec) {
-            if constexpr (kStaged) load_staged<NI, L>(xr, E, -INFINITY, scratch[warp], lane, x);
+            if constexpr (kStaged && GROUPS == 1)
+                load_staged<NI, L>(xr, E, e0, end, -INFINITY, scratch[warp], lane, x);
+            else if constexpr (kStaged)
+                load_staged<NI, L>(xr, E, -INFINITY, scratch[warp], lane, x);
         } else {
-            load_row<NI>(xr, e0, E, vec, x);
+            load_row<NI>(xr, e0, end, vec, x);
         }
         bool bad = false;
 #pragma unroll
@@ -326,7 +366,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NI == 12 || NI == 16 ? 4 : N
                 v = expf(v - top) / total + bias[i];
             key[i] = x[i] > -INFINITY && v > -INFINITY ? order_key(v) : 0u;
         }
-        if constexpr (GROUPS == 1) groups_by_lanes<NI, L>(key, E / a.groups, a.group_best, a.topk_groups, lane);
+        if constexpr (GROUPS == 1) groups_by_lanes<NI, L>(key, run, a.group_best, a.topk_groups, lane);
         if constexpr (GROUPS == 2) groups_by_memory<NI>(key, scratch[warp], E, a.groups, a.group_best, a.topk_groups, lane);
         // The choice: every lane sorts its keys, and the best of the lanes' heads is
         // taken k times.  Lane j keeps the j-th: its key and the lane it came from.
@@ -373,11 +413,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NI == 12 || NI == 16 ? 4 : N
         const uint32_t key_up = __shfl_up_sync(kFull, my_key, 1, L);
         const int lane_up = __shfl_up_sync(kFull, my_lane, 1, L);
         const unsigned starts = lanes_ballot<L>(at_lane == 0 || key_up != my_key || lane_up != my_lane, lane);
+        const int from0 = first_of(my_lane);
         int skip = __clz(starts << (31 - at_lane)), mine = -1;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const uint32_t there = __shfl_sync(kFull, key[i], my_lane, L);
-            if (there == my_key && mine < 0 && skip-- == 0) mine = my_lane * NI + i;
+            if (there == my_key && mine < 0 && skip-- == 0) mine = from0 + i;
         }
         if (my_key == 0u) mine = -1;
         float w = choice_weight<T, L>(xr, mine, a, top, total) * a.scale;
@@ -490,7 +531,9 @@ constexpr int64_t kFewTokens = 4096;
 // lanes 256; more registers a lane would cost more in sorting and shifting them
 // than the exchange saves.  Few tokens do not fill the machine: a whole warp is
 // then the shortest way (8 x 256 with groups: 6.1 us a call against 7.8 with 16
-// lanes; 8192 x 60: 6.8 against 6.4 with 8).  Groups other than whole runs of lanes take a whole warp.
+// lanes; 8192 x 60: 6.8 against 6.4 with 8).  Groups that are a power of two in number have
+// a run of lanes each, whatever their size (16000 x 160 in 8 groups: 14 us; by way of memory,
+// as other numbers of groups, which take a whole warp, 41).
 struct RouteForm {
     int lanes, per_lane, groups;
 };
@@ -507,10 +550,10 @@ static RouteForm route_form(const RouteArgs& a, int64_t tokens) {
     RouteForm f;
     for (int lanes = tokens < kFewTokens ? 32 : 8; lanes <= 32; lanes *= 2) {
         f.lanes = lanes;
-        f.per_lane = registers_for((a.experts + lanes - 1) / lanes);
-        const int gs = a.experts / a.groups, run = gs / f.per_lane;
-        const bool runs = a.experts == lanes * f.per_lane && gs % f.per_lane == 0 && (run & (run - 1)) == 0;
-        f.groups = a.groups == 1 ? 0 : runs ? 1 : 2;
+        const int run = (a.groups & (a.groups - 1)) == 0 ? lanes / a.groups : 0;  // lanes a group
+        f.groups = a.groups == 1 ? 0 : run ? 1 : 2;
+        const int share = f.groups == 1 ? run : lanes, held = f.groups == 1 ? a.experts / a.groups : a.experts;
+        f.per_lane = registers_for((held + share - 1) / share);
         if (a.topk <= lanes && f.per_lane <= 16 && f.groups != 2) return f;
     }
     return f;  // 32 lanes
@@ -521,7 +564,8 @@ static int route_go(const RouteForm& f, cudaStream_t s, const T* x, int64_t ld, 
                     int32_t* idx, float* w) {
     const int grid = route_grid(tokens, L);
     if (grid == 0) return -3;
-    const int vec = a.experts % vector_of<T, NI>() == 0 && ((uintptr_t)x & 15u) == 0 && (ld * (int64_t)sizeof(T)) % 16 == 0;
+    const int whole = f.groups == 1 ? a.experts / a.groups : a.experts;
+    const int vec = whole % vector_of<T, NI>() == 0 && ((uintptr_t)x & 15u) == 0 && (ld * (int64_t)sizeof(T)) % 16 == 0;
     const auto go = [&](auto kernel) {
         return route_done(launch_chained(kernel, dim3(grid), kRouteWarps * 32, 0, s, 1, x, ld, tokens, vec, a, idx, w),
                           "route kernel launch");

@@ -434,6 +434,33 @@ def test_route_twelve_many_tokens(c3, r, extra, ty):
     assert (np.abs(a - ref_w) <= 128 * U * np.abs(ref_w))[hit].all()
 
 
+# Groups that are a power of two in number and no power of two in size: a run of lanes each, the last not full.
+RAGGED_GROUPS = [
+    dict(E=160, k=6, score="sigmoid", G=8, keep=3, best=2, renorm=True, bias=True),
+    dict(E=488, k=4, score="sigmoid", G=4, keep=1, best=2, bias=True),
+    dict(E=200, k=8, score="softmax", G=4, keep=2),
+    dict(E=24, k=3, score="sigmoid", G=8, keep=2, best=2, bias=True),
+    dict(E=34, k=6, score="softmax", G=2, keep=1),
+    dict(E=96, k=5, score="sigmoid", G=32, keep=7, best=2, bias=True),
+    dict(E=1000, k=8, score="sigmoid", G=8, keep=3, best=2, renorm=True, bias=True),
+    dict(E=104, k=8, score="softmax", G=8, keep=3, renorm=True),
+]
+
+
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("T,extra", [(1, 0), (77, 5), (33, 8)])
+@pytest.mark.parametrize("r", RAGGED_GROUPS, ids=lambda r: "_".join(f"{k}{v}" for k, v in r.items()))
+def test_route_ragged_groups(c3, r, T, extra, ty):
+    test_route(c3, r, T, extra, ty)
+
+
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("extra", [0, 3, 8])
+@pytest.mark.parametrize("r", RAGGED_GROUPS, ids=lambda r: "_".join(f"{k}{v}" for k, v in r.items()))
+def test_route_ragged_groups_many_tokens(c3, r, extra, ty):
+    test_route_twelve_many_tokens(c3, r, extra, ty)
+
+
 # ----------------------------------------------------------------------------- order
 
 def order_oracle(idx, E, rows):
