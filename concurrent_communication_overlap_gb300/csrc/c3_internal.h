@@ -196,11 +196,12 @@ void ce_release_graphs(int device);
 // The arguments have been checked (ops_api.cpp); each call is one or two
 // kernels on `s` and returns 0 or a negative c3_status.
 
-// A router (c3_router).  by_score: keys are the softmax scores themselves and
-// not the logits, which order alike without a bias or sums over groups.
+// A router (c3_router).  by_score: keys are the scores plus the bias and not the
+// logits, which order as the scores do where there is no bias.  pairs: groups are
+// ranked by the sum of two scores.
 struct RouteArgs {
     const float* bias;
-    int experts, topk, groups, topk_groups, group_best, score, renorm, by_score;
+    int experts, topk, groups, topk_groups, group_best, score, renorm, by_score, pairs;
     float scale;
 };
 int route_launch(const void* logits, int bf16, int64_t ld, int64_t tokens, const RouteArgs& a, int32_t* idx,

@@ -40,7 +40,8 @@ static int check_router(const c3_router* r, RouteArgs* a) {
     a->group_best = r->group_best;
     a->score = r->score;
     a->renorm = r->renorm;
-    a->by_score = r->score == C3_SCORE_SOFTMAX && (r->bias || (r->groups > 1 && r->group_best == 2));
+    a->by_score = r->bias != nullptr;
+    a->pairs = r->groups > 1 && r->group_best == 2;
     a->scale = r->scale;
     return C3_OK;
 }

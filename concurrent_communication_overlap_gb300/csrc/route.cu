@@ -5,7 +5,9 @@
 // holds the logits of NI consecutive experts, l NI and up (in groups, those of a run
 // of lanes being a group), in registers.  The
 // choice compares 32-bit integers that order as the float keys do; of equal keys
-// the lowest lane, and in it the lowest register, is the lowest expert.
+// the lowest lane, and in it the lowest register, is the lowest expert.  Without a
+// bias the keys are the logits: the scores order as they do, but fp32 scores of
+// different logits can be equal (every sigmoid above 17 is 1).
 //
 // Few lanes a token, because the exchange between lanes, which is the same for
 // one token as for four, is most of the work: 32768 x 60, 6 chosen, takes 354
@@ -165,9 +167,11 @@ __device__ __forceinline__ void load_staged(const T* xr, int E, int e0, int end,
 }
 
 // Groups that are whole runs of `lanes`, a power of two, of the token's lanes: score and
-// rank them with shuffles.  Sets the keys of groups outside the best `keep` to 0.
-template <int NI, int L>
-__device__ __forceinline__ void groups_by_lanes(uint32_t (&key)[NI], int lanes, int best_of, int keep, int lane) {
+// rank them with shuffles, by their best key or the sum of the scores of the best two.
+// Sets the keys of groups outside the best `keep` to 0.
+template <int NI, int L, typename Score>
+__device__ __forceinline__ void groups_by_lanes(uint32_t (&key)[NI], int lanes, int best_of, int keep, int lane,
+                                                const Score& score_of) {
     uint32_t b1 = 0u, b2 = 0u;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -179,7 +183,8 @@ __device__ __forceinline__ void groups_by_lanes(uint32_t (&key)[NI], int lanes, 
         b2 = max(max(b2, c2), min(b1, c1));
         b1 = max(b1, c1);
     }
-    const uint32_t score = (best_of == 2 && b2) ? order_key(order_value(b1) + order_value(b2)) : b1;
+    uint32_t score = b1;
+    if (best_of == 2 && b1) score = order_key(score_of(b1) + (b2 ? score_of(b2) : 0.0f));
     const int mine = (lane & (L - 1)) / lanes, groups = L / lanes;
     int rank = 0;
     for (int g = 0; g < groups; ++g) {
@@ -192,15 +197,21 @@ __device__ __forceinline__ void groups_by_lanes(uint32_t (&key)[NI], int lanes, 
     }
 }
 
-// Groups of any size, by way of shared memory (1024 words a warp): lane g + 32 j
-// takes group g + 32 j, each lane reading from a place of its own on.
-template <int NI>
+// Groups of any size, by way of shared memory (1024 words a warp: the keys, or where keys
+// are logits and two scores are summed (sum_scores) the scores): lane g + 32 j takes group
+// g + 32 j, each lane reading from a place of its own on.
+template <int NI, typename Score>
 __device__ __forceinline__ void groups_by_memory(uint32_t (&key)[NI], uint32_t* gk, int E, int G, int best_of, int keep,
-                                                 int lane) {
+                                                 int lane, bool sum_scores, const Score& score_of) {
     const int gs = E / G;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
         if (lane * NI + i < E) gk[lane * NI + i] = key[i];
+    if (sum_scores) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (lane * NI + i < E && key[i]) gk[lane * NI + i] = order_key(score_of(key[i]));
+    }
     __syncwarp();
     uint32_t score[NI];
 #pragma unroll
@@ -346,7 +357,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NI == 12 || NI == 16 ? 4 : N
         for (int i = 0; i < NI; ++i) bad |= isnan(x[i]);
         bad = lanes_ballot<L>(bad, lane) != 0u;
         float top = 0.0f, total = 1.0f;
-        if (soft && (a.by_score || !a.renorm)) {
+        if (soft && (a.by_score || a.pairs || !a.renorm)) {
             top = x[0];
 #pragma unroll
             for (int i = 1; i < NI; ++i) top = fmaxf(top, x[i]);
@@ -357,17 +368,25 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NI == 12 || NI == 16 ? 4 : N
             total = lanes_sum<L>(total);
         }
         uint32_t key[NI];
+        const auto set_key = [&](int i, float v) { key[i] = x[i] > -INFINITY && v > -INFINITY ? order_key(v) : 0u; };
+        if (!a.by_score) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            float v = x[i];
-            if (!soft)
-                v = sigmoid_f(v) + bias[i];
-            else if (a.by_score)
-                v = expf(v - top) / total + bias[i];
-            key[i] = x[i] > -INFINITY && v > -INFINITY ? order_key(v) : 0u;
+            for (int i = 0; i < NI; ++i) set_key(i, x[i]);
+        } else if (soft) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) set_key(i, expf(x[i] - top) / total + bias[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) set_key(i, sigmoid_f(x[i]) + bias[i]);
         }
-        if constexpr (GROUPS == 1) groups_by_lanes<NI, L>(key, run, a.group_best, a.topk_groups, lane);
-        if constexpr (GROUPS == 2) groups_by_memory<NI>(key, scratch[warp], E, a.groups, a.group_best, a.topk_groups, lane);
+        const auto score_of = [&](uint32_t key) {
+            const float v = order_value(key);
+            return a.by_score ? v : soft ? expf(v - top) / total : sigmoid_f(v);
+        };
+        if constexpr (GROUPS == 1) groups_by_lanes<NI, L>(key, run, a.group_best, a.topk_groups, lane, score_of);
+        if constexpr (GROUPS == 2)
+            groups_by_memory<NI>(key, scratch[warp], E, a.groups, a.group_best, a.topk_groups, lane,
+                                 a.pairs && !a.by_score, score_of);
         // The choice: every lane sorts its keys, and the best of the lanes' heads is
         // taken k times.  Lane j keeps the j-th: its key and the lane it came from.
         uint32_t line[NI];

@@ -572,10 +572,10 @@ typedef enum { C3_SCORE_SOFTMAX = 0, C3_SCORE_SIGMOID = 1 } c3_score;
 /* A router: how logits become a choice of experts and weights.
  *   score s_e: softmax over the experts whose logit is above -inf, or
  *     1 / (1 + exp(-x_e)).
- *   key: s_e + bias_e (bias may be NULL).  With softmax, no bias and
- *     group_best 1 the logits are compared themselves: they order as the
- *     scores do.  An expert with a logit or a key of -inf or NaN is not
- *     eligible.
+ *   key: s_e + bias_e, in fp32.  Without a bias (NULL) the logits are compared
+ *     themselves: they order as the scores do, and where fp32 scores are equal
+ *     (sigmoids of 18 and 25) still tell the better expert.  An expert with a
+ *     logit or a key of -inf or NaN is not eligible.
  *   groups: consecutive experts / groups experts form a group; its score is
  *     the sum of its best group_best eligible keys (one, where it has only
  *     one).  Experts outside the best topk_groups groups are not eligible.
