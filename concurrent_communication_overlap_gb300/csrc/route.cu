@@ -508,13 +508,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
                 const float dot = lanes_sum<L>(q * g);
                 d = q * (g - dot);
             } else {
-                const float s = mine >= 0 ? sigmoid_f(xm) : 0.0f;
+                // 1 - s cancels where s is near 1: there it is exp(-x) s.  And s / S comes first:
+                // (g - sg / S) / S may overflow.
+                const float e = expf(-xm), s = mine >= 0 ? __frcp_rn(1.0f + e) : 0.0f;
+                const float c = e < 1.0f ? e * s : 1.0f - s;
                 if (a.renorm) {
                     const float S = lanes_sum<L>(s);
                     const float sg = lanes_sum<L>(s * g);
-                    d = S > 0.0f ? (g - sg / S) / S * s * (1.0f - s) : 0.0f;
+                    d = S > 0.0f ? s / S * (g - sg / S) * c : 0.0f;
                 } else {
-                    d = g * s * (1.0f - s);
+                    d = g * s * c;
                 }
             }
 #pragma unroll

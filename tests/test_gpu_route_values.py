@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_ops import f64, run_route  # noqa: E402
+from test_gpu_ops import TD, Guarded, cuda, f64, run_route  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 U, H = 2.0 ** -24, 2.0 ** -8
@@ -62,3 +62,41 @@ def test_sigmoid_orders_as_its_logits(c3, r, T, base):
     assert np.array_equal(idx.cpu().numpy(), want)
     ref = 1 / (1 + np.exp(-np.take_along_axis(x, want, 1)))
     assert (np.abs(f64(w) - ref) <= 128 * U * ref + TINY).all()
+
+
+# ----------------------------------------------------------------------------- gradients far from 0
+
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T", [24, 4200])
+@pytest.mark.parametrize("lo,hi", [(8, 20), (-20, -8), (-88.6, -85), (-88.6, 30), (30, 80)])
+def test_sigmoid_gradient_keeps_its_digits(c3, lo, hi, T, renorm, ty):
+    """c g s (1 - s), and with renorm c q (g - sum q g) (1 - s) with q = s / S: scores and complements near 0 have their
+    digits too.  s and 1 - s are each three operations and an exponential (2 ulp): 8 u; S sums 8 terms: 16 u; so a term is
+    within 64 u of itself, the terms being |g| and, with renorm, |g| + sum q |g|.  Below 2^-126 numbers are 2^-149 apart
+    (bf16 2^-133): a factor that small is off by half that, 2^-150 / 3e-39 = 4 u of itself at -88.6, and so may a result
+    be (three times that, for the factors it came from)."""
+    E, k, scale = 40, 8, 2.5
+    rng = np.random.default_rng(T)
+    x = f64(cuda(rng.uniform(lo, hi, (T, E)).astype(np.float32)).to(TD[ty]))
+    r = dict(E=E, k=k, score="sigmoid", renorm=renorm, scale=scale)
+    idx, _, router, wide = run_route(c3, r, x, ty)
+    dw = rng.standard_normal((T, k)).astype(np.float32) * 3
+    dx = Guarded((T, E), TD[ty], 5.0)
+    c3.c3_route_backward(router, wide, E, T, idx, cuda(dw), dx.t, E)
+    torch.cuda.synchronize()
+    assert dx.intact()
+    idx = idx.cpu().numpy()
+    z = np.take_along_axis(x, idx, 1)
+    s, c, g = 1 / (1 + np.exp(-z)), 1 / (1 + np.exp(z)), scale * dw.astype(np.float64)
+    if renorm:
+        q = s / s.sum(1, keepdims=True)
+        d, mag = q * (g - (q * g).sum(1, keepdims=True)) * c, q * (np.abs(g) + (q * np.abs(g)).sum(1, keepdims=True)) * c
+    else:
+        d = mag = g * s * c
+    ref, tol = np.zeros((T, E)), np.zeros((T, E))
+    np.put_along_axis(ref, idx, d, 1)
+    np.put_along_axis(tol, idx, 64 * U * np.abs(mag) + 3 * (2.0 ** -133 if ty else 2.0 ** -149), 1)
+    if ty:
+        tol = tol + H * np.abs(ref)
+    assert (np.abs(f64(dx.t) - ref) <= tol).all()
