@@ -352,9 +352,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NI == 12 || NI == 16 ? 4 : N
         } else {
             load_row<NI>(xr, e0, end, vec, x);
         }
+        // weights are NaN where a logit is NaN, or +inf with the softmax
         bool bad = false;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) bad |= isnan(x[i]);
+        for (int i = 0; i < NI; ++i) bad |= soft ? !(x[i] < INFINITY) : isnan(x[i]);
         bad = lanes_ballot<L>(bad, lane) != 0u;
         float top = 0.0f, total = 1.0f;
         if (soft && (a.by_score || a.pairs || !a.renorm)) {
@@ -369,9 +370,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NI == 12 || NI == 16 ? 4 : N
         }
         uint32_t key[NI];
         const auto set_key = [&](int i, float v) { key[i] = x[i] > -INFINITY && v > -INFINITY ? order_key(v) : 0u; };
-        if (!a.by_score) {
+        const bool no_score = soft && !(top < INFINITY);  // +inf in the row: the scores are NaN
+        if (!a.by_score || no_score) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) set_key(i, x[i]);
+            for (int i = 0; i < NI; ++i) set_key(i, x[i] + bias[i]);
         } else if (soft) {
 #pragma unroll
             for (int i = 0; i < NI; ++i) set_key(i, expf(x[i] - top) / total + bias[i]);
@@ -381,7 +383,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NI == 12 || NI == 16 ? 4 : N
         }
         const auto score_of = [&](uint32_t key) {
             const float v = order_value(key);
-            return a.by_score ? v : soft ? expf(v - top) / total : sigmoid_f(v);
+            if (a.by_score || no_score) return v;
+            return soft ? expf(v - top) / total : sigmoid_f(v);
         };
         if constexpr (GROUPS == 1) groups_by_lanes<NI, L>(key, run, a.group_best, a.topk_groups, lane, score_of);
         if constexpr (GROUPS == 2)

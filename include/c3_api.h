@@ -586,7 +586,8 @@ typedef enum { C3_SCORE_SOFTMAX = 0, C3_SCORE_SIGMOID = 1 } c3_score;
  *     for the softmax as a softmax over the chosen logits, which never
  *     divides by zero; for the sigmoid 0 where the sum is 0.
  * A NaN logit makes all weights of its token NaN, and so does +inf with the
- * softmax. */
+ * softmax, whose keys are then the logits plus the bias: the token's choice is
+ * made either way, and only places without an expert have weight 0. */
 typedef struct {
     const float *bias;  /* device, [experts], or NULL */
     int experts;        /* 1..1024 */

@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_ops import TD, Guarded, cuda, f64, run_route  # noqa: E402
+from test_gpu_ops import TD, Guarded, cuda, f64, grid_logits, route_oracle, run_route  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 U, H = 2.0 ** -24, 2.0 ** -8
@@ -100,3 +100,71 @@ def test_sigmoid_gradient_keeps_its_digits(c3, lo, hi, T, renorm, ty):
     if ty:
         tol = tol + H * np.abs(ref)
     assert (np.abs(f64(dx.t) - ref) <= tol).all()
+
+
+# ----------------------------------------------------------------------------- infinities
+
+@pytest.mark.parametrize("T", [6, 4101])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("r", [dict(E=16, k=4), dict(E=16, k=4, bias=True), dict(E=16, k=4, G=4, keep=2, best=2),
+                               dict(E=24, k=5, G=4, keep=2, bias=True), dict(E=100, k=3, G=25, keep=4, best=2),
+                               dict(E=100, k=3, G=25, keep=4, best=2, bias=True), dict(E=400, k=9, bias=True)], ids=name)
+def test_softmax_of_plus_infinity(c3, r, renorm, T):
+    """A choice as by the logits (plus the bias), weights of NaN: the token is neither dropped nor quietly given weights."""
+    r = dict(r, score="softmax", renorm=renorm)
+    E, k, G, keep, best = r["E"], r["k"], r.get("G", 1), r.get("keep", 1), r.get("best", 1)
+    rng = np.random.default_rng(E)
+    x = grid_logits(rng, T, E)
+    x[0, E // 2] = np.inf
+    x[1, 1] = x[1, E - 2] = np.inf
+    x[2, 0] = np.inf
+    x[2, 3:9] = -np.inf
+    x[T - 1] = np.inf
+    bias = rng.integers(-8, 9, E) / 16.0 if r.get("bias") else np.zeros(E)
+    if r.get("bias"):
+        bias[2] = -np.inf
+    idx, w, router, wide = run_route(c3, r, x, 0, bias if r.get("bias") else None)
+    idx, w = idx.cpu().numpy(), f64(w)
+    for t in (0, 1, 2, T - 1):
+        with np.errstate(invalid="ignore"):
+            key = x[t] + bias
+        key = np.where(np.isnan(key), -np.inf, key)     # +inf under a bias of -inf: not eligible
+        if G > 1:
+            per = np.sort(key.reshape(G, -1), 1)[:, ::-1][:, :best]
+            score = np.where(per[:, 0] > -np.inf, np.where(per > -np.inf, per, 0).sum(1), -np.inf)
+            kept = np.argsort(-score, kind="stable")[:keep]
+            key = np.where(np.isin(np.arange(E) // (E // G), kept), key, -np.inf)
+        want = np.argsort(-key, kind="stable")[:k]
+        want = np.where(key[want] > -np.inf, want, -1)
+        assert np.array_equal(idx[t], want), t
+        assert np.isnan(w[t][want >= 0]).all() and (w[t][want < 0] == 0).all()
+    assert np.isfinite(w[3:T - 1]).all()
+    dx = torch.empty(T, E, device="cuda")
+    c3.c3_route_backward(router, wide, E, T, cuda(idx), cuda(rng.standard_normal((T, k)).astype(np.float32)), dx, E)
+    torch.cuda.synchronize()
+    dx = f64(dx)
+    assert np.isfinite(dx[3:T - 1]).all()
+    for t in (0, 1, 2, T - 1):
+        chosen = idx[t][idx[t] >= 0]
+        if renorm and not np.isinf(x[t, chosen]).any():
+            continue    # the infinity was masked by its bias: the chosen logits are finite
+        assert np.isnan(dx[t, chosen]).all(), t
+
+
+@pytest.mark.parametrize("T", [6, 4101])
+def test_sigmoid_of_infinities(c3, T):
+    """1 and 0 like any other score: +inf is the best expert, -inf none."""
+    E, k = 16, 4
+    x = grid_logits(np.random.default_rng(1), T, E)
+    x[0, 5] = x[0, 9] = np.inf
+    x[1, 2:] = -np.inf
+    x[2] = np.inf
+    r = dict(E=E, k=k, score="sigmoid")
+    idx, w, router, wide = run_route(c3, r, x, 0)
+    ref_idx, ref_w = route_oracle(x[:6], E, k, "sigmoid")
+    assert np.array_equal(idx.cpu().numpy()[:6], ref_idx)
+    assert (np.abs(f64(w)[:6] - ref_w) <= 128 * U * ref_w).all()
+    dx = torch.empty(T, E, device="cuda")
+    c3.c3_route_backward(router, wide, E, T, idx, torch.ones(T, k, device="cuda"), dx, E)
+    torch.cuda.synchronize()
+    assert bool((dx[2] == 0).all()) and bool((dx[0, [5, 9]] == 0).all()) and bool(torch.isfinite(dx).all())
