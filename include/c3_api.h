@@ -616,7 +616,10 @@ int c3_route(const c3_router *r, const void *logits, int64_t ld, int64_t tokens,
  *   dlogits[t][e] = sum_j dweights[t][j] d weights[t][j] / d logits[t][e],
  * in the logits' type, row distance dld, every entry written (zeros where the
  * weights do not depend on an expert).  Entries of idx outside 0..experts-1
- * count as none.
+ * count as none.  A token whose weights are NaN: the softmax without renorm
+ * reads its whole row, and a NaN or +inf there makes all of dlogits[t] NaN;
+ * the other forms read the chosen logits alone, so dlogits[t] is NaN at the
+ * chosen experts where one of these is +inf (softmax) or dweights[t] is NaN.
  */
 int c3_route_backward(const c3_router *r, const void *logits, int64_t ld, int64_t tokens,
                       const int32_t *idx, const float *dweights, void *dlogits, int64_t dld,

@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_ops import TD, Guarded, cuda, f64, grid_logits, route_oracle, run_route  # noqa: E402
+from test_gpu_ops import TD, Guarded, cuda, f64, grid_logits, route_grad_oracle, route_oracle, run_route  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 U, H = 2.0 ** -24, 2.0 ** -8
@@ -168,3 +168,35 @@ def test_sigmoid_of_infinities(c3, T):
     c3.c3_route_backward(router, wide, E, T, idx, torch.ones(T, k, device="cuda"), dx, E)
     torch.cuda.synchronize()
     assert bool((dx[2] == 0).all()) and bool((dx[0, [5, 9]] == 0).all()) and bool(torch.isfinite(dx).all())
+
+
+# ----------------------------------------------------------------------------- NaN rows
+
+@pytest.mark.parametrize("T", [3, 4101])
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+def test_gradient_of_a_nan_row(c3, score, renorm, T):
+    """Softmax without renorm: NaN for the whole row, which every logit enters.  Else the gradient is that of the chosen
+    logits (the NaN is not one of them), and NaN where dweights is."""
+    E, k = 24, 4
+    rng = np.random.default_rng(2)
+    x = grid_logits(rng, T, E)
+    x[1, 7] = np.nan
+    x[2, 7] = np.nan
+    r = dict(E=E, k=k, score=score, renorm=renorm)
+    idx, w, router, wide = run_route(c3, r, x, 0)
+    assert bool(torch.isnan(w[1:3]).all()) and bool(torch.isfinite(w[0]).all())
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    dw[2] = np.nan
+    dx = torch.empty(T, E, device="cuda")
+    c3.c3_route_backward(router, wide, E, T, idx, cuda(dw), dx, E)
+    torch.cuda.synchronize()
+    idx, dx = idx.cpu().numpy(), f64(dx)
+    assert np.isfinite(dx[0]).all()
+    assert np.isnan(dx[2, idx[2]]).all()
+    if score == "softmax" and not renorm:
+        assert np.isnan(dx[1:3]).all()
+        return
+    ref = route_grad_oracle(x[1:2], idx[1:2], dw[1:2].astype(np.float64), r)[0]
+    assert (np.abs(dx[1] - ref) <= 256 * U * 4).all()
+    rest = np.setdiff1d(np.arange(E), idx[2])
+    assert (dx[2, rest] == 0).all()
