@@ -6,7 +6,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_ops import TD, Guarded, cuda, f64, grid_logits, route_grad_oracle, route_oracle, run_route  # noqa: E402
+from test_gpu_ops import (RAGGED_GROUPS, ROUTERS, TD, TWELVE, Guarded, cuda, f64, grid_logits,  # noqa: E402
+                          route_grad_oracle, route_oracle, run_route)
 
 pytestmark = pytest.mark.gpu
 U, H = 2.0 ** -24, 2.0 ** -8
@@ -200,3 +201,65 @@ def test_gradient_of_a_nan_row(c3, score, renorm, T):
     assert (np.abs(dx[1] - ref) <= 256 * U * 4).all()
     rest = np.setdiff1d(np.arange(E), idx[2])
     assert (dx[2, rest] == 0).all()
+
+
+# ----------------------------------------------------------------------------- every choice by itself
+
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("T", [77, 4101])
+@pytest.mark.parametrize("r", ROUTERS + TWELVE + RAGGED_GROUPS, ids=name)
+def test_every_choice_is_one_of_the_best(c3, r, T, ty):
+    """Different experts, of groups that may stay, in descending order, none better left out, equal ones by number; and
+    the weights of exactly these.  Keys and group scores are fp32 sums of at most two scores and a bias: a softmax score
+    is 128 u off itself at most, a sigmoid less, a sum adds a u of a number of at most 4: 256 u in all."""
+    E, k, G, keep, best = r["E"], r["k"], r.get("G", 1), r.get("keep", 1), r.get("best", 1)
+    rng = np.random.default_rng(T * 100 + E)
+    x = grid_logits(rng, T, E)
+    x[rng.random((T, E)) < 0.03] = -np.inf
+    bias = rng.integers(-8, 9, E) / 16.0 if r.get("bias") else None
+    idx, w, _, _ = run_route(c3, r, x, ty, bias, extra=T % 3)
+    idx, w = idx.cpu().numpy(), f64(w)
+    some = np.arange(T) if T < 100 else rng.choice(T, 150, replace=False)
+    room = 256 * U
+    for t in some:
+        ok = x[t] > -np.inf
+        if not ok.any():
+            assert (idx[t] == -1).all() and (w[t] == 0).all()
+            continue
+        if r["score"] == "softmax":
+            s = np.exp(np.where(ok, x[t], -np.inf) - x[t][ok].max())
+            s = s / s.sum()
+        else:
+            s = np.where(ok, 1 / (1 + np.exp(-x[t])), 0)
+        key = np.where(ok, s + (0 if bias is None else bias), -np.inf)
+        low = 0 if bias is None and best == 1 else room    # logits themselves: no rounding
+        group = np.arange(E) // (E // G)
+        top = np.sort(key.reshape(G, -1), 1)[:, ::-1][:, :best]
+        score = np.where(top[:, 0] > -np.inf, np.where(top > -np.inf, top, 0).sum(1), -np.inf)
+        cut = np.sort(score)[::-1][keep - 1]
+        may = (score >= cut - low) & (score > -np.inf)
+        if not low:
+            may &= np.isin(np.arange(G), np.argsort(-score, kind="stable")[:keep])
+        must = may if may.sum() <= keep else may & (score > cut + low)
+        n = (idx[t] >= 0).sum()
+        mine = idx[t][:n]
+        assert (idx[t][n:] == -1).all() and (w[t][n:] == 0).all()
+        assert len(set(mine)) == n and ok[mine].all() and may[group[mine]].all(), t
+        assert len(set(group[mine])) <= keep
+        if n < k:   # fewer than k only where the groups that stay have no more
+            assert n >= (ok & must[group]).sum(), t
+        if n:
+            assert (np.diff(key[mine]) <= low).all(), t
+            left = np.setdiff1d(np.nonzero(ok & must[group])[0], mine)
+            if n == k and len(left):
+                assert key[left].max() <= key[mine].min() + low, t
+            # equal logits and biases have equal keys, whatever the rounding: the lower number goes first
+            same = (x[t][mine][:, None] == x[t][left][None])
+            if bias is not None:
+                same &= bias[mine][:, None] == bias[left][None]
+            assert not (same & (mine[:, None] > left[None]) & (group[mine][:, None] == group[left][None])).any(), t
+            chosen = s[mine]
+            if r.get("renorm"):
+                chosen = chosen / chosen.sum()
+            ref = r.get("scale", 1.0) * chosen
+            assert (np.abs(w[t][:n] - ref) <= 128 * U * ref).all(), t
