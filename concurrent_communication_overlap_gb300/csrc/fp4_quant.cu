@@ -282,14 +282,14 @@ __device__ __forceinline__ void encode_raw(const Raw16<T>& x, float inv_t, uint3
     } else {
         float v[16];
         x.values(v);
+        // multiplying by a number and rounding keep the order: the maximum may come first.  A block
+        // of zeros has scale 0 whatever the matrix's, 1 / 0 for a matrix of zeros by its own maximum.
         float amax;
-        if constexpr (sizeof(T) == 2) {
-            // multiplying by a number and rounding keep the order: the maximum may come first
-            amax = __uint_as_float(block_max_bf16<NV>(x.w)) * fabsf(inv_t);
+        if constexpr (sizeof(T) == 2) amax = __uint_as_float(block_max_bf16<NV>(x.w));
+        else amax = block_max<NV>(v);
+        if (NV) {
             scale16(v, inv_t);
-        } else {
-            if (NV) scale16(v, inv_t);
-            amax = block_max<NV>(v);
+            amax = amax == 0.0f ? 0.0f : amax * fabsf(inv_t);
         }
         encode16<NV>(v, amax, byte, codes);
     }

@@ -682,8 +682,9 @@ size_t c3_fp4_scale_bytes(int64_t rows, int64_t cols, int format);
  *   Scales: MX the smallest power of two with max|x| <= 6 * scale (no element
  *   saturates); NV e4m3(max|y| / 6), to nearest even and at most 448, of
  *   y = x * (1 / tensor_scale).  Codes: to the nearest value of x / scale, ties
- *   to the even code.  A block of zeros has scale 0 (byte 0); a block with a
- *   NaN or an infinity has a NaN scale and stands for NaNs.
+ *   to the even code.  A block of zeros has scale byte 0 and stays one, also where
+ *   1 / tensor_scale is infinite (max|x| / 2688 of a matrix of zeros is 0); a
+ *   block with a NaN or an infinity in x or y has a NaN scale and stands for NaNs.
  *   transpose  0, or 1 to quantise the transpose of x: q has x_cols rows and
  *              x_rows columns, and the blocks run along x's columns (the
  *              operands of a product's gradients)
