@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "fp4_plan.h"
+
 namespace c3 {
 
 // One CTA's residency: the SM it ran on and its %globaltimer window.
@@ -209,7 +211,6 @@ int route_launch(const void* logits, int bf16, int64_t ld, int64_t tokens, const
 int route_backward_launch(const void* logits, int bf16, int64_t ld, int64_t tokens, const RouteArgs& a,
                           const int32_t* idx, const float* dweights, void* dlogits, int64_t dld, cudaStream_t s);
 
-constexpr int kTileRows = 128;  // rows of a scale tile; an expert's rows start at a multiple of it
 int64_t order_rows(int64_t tokens, int topk, int experts);
 size_t order_bytes(int64_t tokens, int topk, int experts);
 int order_launch(const int32_t* idx, int64_t tokens, int topk, int experts, int32_t* slot, int32_t* row_of,

@@ -5,7 +5,7 @@
 // after the other.
 //
 // Two kernels: many rows, two SMs on a tile; few rows, the operands' roles swapped.
-// fp4_plan picks.  Both have the same parts, warp by warp:
+// fp4_plan (fp4_plan.h) picks.  Both have the same parts, warp by warp:
 //   producer   per stage 256 columns of 4 bits (one 128-byte swizzle row) of A's and
 //              B's rows and their scales, all by TMA; scales lie in memory as the
 //              tensor cores take them;
@@ -28,7 +28,6 @@
 namespace c3 {
 
 constexpr int kFM = 128;             // rows of A in a tile
-constexpr int kFK = 256;             // columns of a stage: 128 bytes of codes
 constexpr int kFGroupM = 16;
 constexpr int kFSmemLimit = 232448;  // 227 KiB
 constexpr int kFHalfSmem = 115712;   // two CTAs on an SM: half of 228 KiB less 1 KiB each
@@ -185,7 +184,6 @@ __device__ __forceinline__ void expert_tiles(const Fp4GemmArgs& g, int* prefix, 
 // 8192 x 28672 x 8192 takes 576 us, 6.7 PFLOP/s.  Copies with a part of the work left
 // out put what bounds it side by side: loads alone 463, MMAs alone about 380, and the
 // copies of scales another 70 beside them.
-constexpr int kPN = 192;  // columns of one accumulator
 constexpr int kPThreads = 352;  // producer, MMA, scales, and the epilogue's eight warps
 constexpr int kPEpiWarps = 8;
 
@@ -992,65 +990,6 @@ int fp4_gemm_init_device() {
     if (e == cudaSuccess) e = fp4_attr<true, __nv_bfloat16>();
     if (e != cudaSuccess) return set_cuda_error(e, "cudaFuncSetAttribute(4-bit gemm)");
     return 0;
-}
-
-// How a product runs: rows and columns of a tile (512 x 192, 256 x 384 or 256 x 192
-// on two SMs; 128, 64 or 32 x 128 with the roles swapped), and over how many CTAs a
-// tile's K is split.
-struct Fp4Plan {
-    int rows, cols, split, ctas;
-};
-
-static Fp4Plan fp4_plan(int64_t M, int64_t N, int64_t K, int experts, bool grouped, int cap, int sms) {
-    Fp4Plan p{};
-    const int64_t kb = (K + kFK - 1) / kFK;
-    auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    // Rows an expert has on average: the buffer's, less the padding that it has room for (c3_moe_rows).
-    const int64_t pad = (int64_t)(kTileRows - 1) * experts;
-    const int64_t per = !grouped ? M : M > pad ? (M - pad) / experts : 0;
-    if (cap >= 2 && per > 128) {
-        // Cycles of the busiest pair, from 8192 x 28672 x 8192 in each form (637, 579 and
-        // 569 us): a stage of 256 columns of K takes 620 with one accumulator and 1080 with
-        // two, whose read-out, 1500, nothing hides, nor the store of the last (256 x 28672 x
-        // 8192: 32.8 us in two waves of 192 columns, 34.6 in one of 384).
-        const int64_t pairs = cap / 2;
-        int64_t best = 0;
-        for (int form = 0; form < 3; ++form) {
-            const int rows = form == 1 ? 512 : 256, cols = form == 2 ? 2 * kPN : kPN;
-            if (grouped && form == 1) continue;  // an expert's last tile would be mostly empty
-            // of an expert's rows, half a tile on average is past its count
-            const int64_t tiles = grouped ? experts * up(per + rows / 2, rows) : up(M, rows);
-            const int64_t cost = up(tiles * up(N, cols), pairs) * (form ? kb * 1080 + 1500 : kb * 620 + 300) + (form ? 6000 : 1200);
-            if (best == 0 || cost < best) {
-                best = cost;
-                p.rows = rows;
-                p.cols = cols;
-            }
-        }
-        p.split = 1;
-        const int64_t tiles = (up(M, p.rows) + (grouped ? experts : 0)) * up(N, p.cols);
-        p.ctas = 2 * (int)(tiles < pairs ? tiles : pairs);
-        return p;
-    }
-    p.rows = grouped ? 64 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
-    p.cols = 128;
-    const int64_t n = up(N, 128);
-    // An expert with any row has whole scale tiles to itself, so busy experts are at
-    // most M / 128 and tiles of 64 rows at most M / 64.
-    const int64_t tiles = up(M, p.rows) * n;
-    const int64_t busy = grouped ? (experts < up(M, kTileRows) ? experts : up(M, kTileRows)) * n : tiles;
-    // A budget below the whole machine is kept to the letter: one CTA for each SM of it.
-    const int64_t slots = cap < sms ? cap : 2 * (int64_t)cap;
-    // The parts' meeting grows with their number and with the rows: up to 8 for 32 rows (32 x
-    // 1024 x 8192: 6.6 us with 8, 7.4 with 4, 11.5 with 1), 4 above (100 x 4096 x 4096: 13.3,
-    // 11.9 and 11.7; 128 x 8192 x 8192: 15.7 with 4, 20.6 with 1).
-    const int most_parts = p.rows == 32 ? 8 : 4;
-    p.split = 1;
-    while (p.split < most_parts && busy * p.split * 2 <= slots && kb >= 4 * p.split && !(grouped && cap < sms)) p.split *= 2;
-    // One wave: of the tiles that the buffer has room for, the counts leave few (26 tokens to
-    // 6 of 6 experts of 1440 x 2688, 72 of 168 tiles: a cluster for each takes 3 us more).
-    p.ctas = (int)((tiles * p.split < slots ? tiles * p.split : slots) / p.split) * p.split;
-    return p;
 }
 
 template <bool NV, int MSUB, int NSUB, typename TC>
