@@ -576,15 +576,20 @@ typedef enum { C3_SCORE_SOFTMAX = 0, C3_SCORE_SIGMOID = 1 } c3_score;
  *     themselves: they order as the scores do, and where fp32 scores are equal
  *     (sigmoids of 18 and 25) still tell the better expert.  An expert with a
  *     logit or a key of -inf or NaN is not eligible.
- *   groups: consecutive experts / groups experts form a group; its score is
- *     the sum of its best group_best eligible keys (one, where it has only
- *     one).  Experts outside the best topk_groups groups are not eligible.
+ *   groups: consecutive experts / groups experts form a group; it is ranked by
+ *     its best key, or with group_best 2 by the sum of s_e + bias_e of its best
+ *     two eligible experts (of one, where it has only one).  Experts outside the best topk_groups groups are not eligible.
+ *   Keys with a bias, and sums of two scores, that differ by less than their
+ *     fp32 rounding may go either way; those of the softmax, whose sum runs in
+ *     another order for 4096 tokens and more, also from one number of tokens
+ *     to another.  The same call gives the same choice.
  *   The topk best keys are chosen, in descending order; equal keys, and equal
  *     groups, go to the lowest number.  A token with fewer eligible experts
  *     has idx -1 and weight 0 in the places that are left.
  *   weight: scale * s_e; with renorm scale * s_e / (sum of the chosen s),
  *     for the softmax as a softmax over the chosen logits, which never
- *     divides by zero; for the sigmoid 0 where the sum is 0.
+ *     divides by zero; for the sigmoid 0 where the sum is 0 (an fp32 sigmoid
+ *     is, below -88.7).
  * A NaN logit makes all weights of its token NaN, and so does +inf with the
  * softmax, whose keys are then the logits plus the bias: the token's choice is
  * made either way, and only places without an expert have weight 0. */
@@ -703,6 +708,11 @@ int c3_fp4_dequantize(const c3_fp4 *q, void *x, int x_type, int64_t ld, c3_strea
  * C[m][n] = sum_k a[m][k] * b[n][k] of two 4-bit matrices of one format and
  * equal cols (count 1), accumulated in fp32 on the tensor cores, rounded once
  * to c_type (C: a->rows x b->rows, 16-byte aligned).  sm_budget as for c3_gemm.
+ * The tensor cores' additions cut off what does not fit instead of rounding it:
+ * the fp32 sum is off by at most (cols / 64 + 64) * 2^-23 of sum |a b|, most of
+ * it towards zero.  Sums that fit 24 bits are exact, as those of MX matrices of
+ * like scales are; NV matrices of positive values were off by 20 * 2^-24 at 8192
+ * columns and 322 * 2^-24 at 65536.
  * The gradients of a product are products of the same kind: of the output's
  * gradient with the transposed operand, quantised along the other axis.
  */
@@ -714,7 +724,11 @@ int c3_fp4_gemm(const c3_fp4 *a, const c3_fp4 *b, void *C, int c_type, int sm_bu
  *   C[r][n] = sum_k x[r][k] * w[e][n][k]
  * with w->count experts (1..1024), whose rows do not overlap.  Rows of C that
  * no expert has are left as they were.  An expert whose offset is no multiple of 128, or whose rows do
- * not lie within x, is skipped.
+ * not lie within x, is skipped.  x->rows should be about c3_moe_rows of the call's tokens: the form
+ * of the product goes by it.
+ * The gradient with respect to x is the same product with the transposed w.  That with respect to w
+ * is not one of these: its sums run over each expert's rows, whose number only the device knows
+ * while a 4-bit matrix has its columns on the host.
  */
 int c3_fp4_gemm_experts(const c3_fp4 *x, const c3_fp4 *w, const int32_t *offsets,
                         const int32_t *counts, void *C, int c_type, int sm_budget, c3_stream s);

@@ -1,10 +1,10 @@
-"""4-bit matrices whose fp32 scale is what their own maximum gives, zeros among them."""
+"""4-bit matrices of zeros under any fp32 scale, and products whose sums are long and of one sign."""
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_ops import TD, cuda, f64, new_fp4, quantise_oracle, read_tiles  # noqa: E402
+from test_gpu_ops import TD, cuda, f64, new_fp4, quantise_oracle, random_fp4, read_tiles  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +79,21 @@ def test_a_matrix_of_zeros_with_its_own_scale(c3, M, N):
     c3.c3_fp4_gemm(a, b, C, 0)
     c3.c3_status_check()
     assert bool((C == 0).all())
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("M,N,K", [(20, 130, 20000), (300, 200, 20000), (64, 128, 65536)])
+def test_long_sums_of_one_sign(c3, M, N, K, fmt):
+    """fp32 outputs where every addition can lose something on the same side: the header's bound, (K / 64 + 64) 2^-23 of
+    sum |a b|, and one rounding of the output's own."""
+    rng = np.random.default_rng(K + M)
+    a, va = random_fp4(c3, rng, M, K, fmt)
+    b, vb = random_fp4(c3, rng, N, K, fmt)
+    for q in (a, b):
+        q._keep[0].bitwise_and_(0x77)   # no signs
+    va, vb = np.abs(va[0]), np.abs(vb[0])
+    C = torch.empty(M, N, device="cuda")
+    c3.c3_fp4_gemm(a, b, C, 0)
+    c3.c3_status_check()
+    ref = va @ vb.T
+    assert (np.abs(f64(C) - ref) <= ((K / 64 + 64) * 2.0 ** -23 + 2.0 ** -24) * ref).all()
