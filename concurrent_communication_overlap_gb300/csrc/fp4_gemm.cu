@@ -181,9 +181,12 @@ __device__ __forceinline__ void expert_tiles(const Fp4GemmArgs& g, int* prefix, 
 // turn them through 2 KB of shared memory each, and write whole 64-byte pieces
 // of rows.
 //
-// 8192 x 28672 x 8192 takes 576 us, 6.7 PFLOP/s.  Copies with a part of the work left
-// out put what bounds it side by side: loads alone 463, MMAs alone about 380, and the
-// copies of scales another 70 beside them.
+// 8192 x 28672 x 8192 MX takes 576 to 592 us, 6.5 to 6.7 PFLOP/s.  Copies with a part of the
+// work left out put what bounds it side by side: loads alone 463, MMAs alone about 380, and
+// the copies of scales another 70 beside them.  NV, with twice the scales, takes 8 to 15%
+// more, 4096 x 7680 x 8192 101 us (MX) and 104.
+//
+// The bf16 epilogues of two accumulators spill 20 to 28 bytes a thread, once a tile.
 constexpr int kPThreads = 352;  // producer, MMA, scales, and the epilogue's eight warps
 constexpr int kPEpiWarps = 8;
 
@@ -603,7 +606,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 // there are fewer tiles than CTAs to fill the machine, a cluster of `split` CTAs
 // takes a tile at a time, each a part of K; their fp32 parts meet in shared memory, each
 // CTA adding up its share of A's rows in the order of the ranks.  13 x 8200 x 8072
-// takes 11.7 us in a chain of calls, where its bytes need 5.5; the rest is set-up, the
+// takes 12.3 us in a chain of calls, where its bytes need 5.5; the rest is set-up, the
 // first loads' latency and the cluster's two meetings.
 constexpr int kRThreads = 256;
 

@@ -21,9 +21,16 @@ inline Fp4Plan fp4_plan(int64_t M, int64_t N, int64_t K, int experts, bool group
     Fp4Plan p{};
     const int64_t kb = (K + kFK - 1) / kFK;
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    // Rows an expert has on average: the buffer's, less the padding that it has room for (c3_moe_rows).
+    // Rows an expert has on average: the buffer's, less the padding that it has room for
+    // (c3_moe_rows).  The counts are on the device: a buffer with far more room than a call's
+    // tokens need is planned for as if it were full.
     const int64_t pad = (int64_t)(kTileRows - 1) * experts;
     const int64_t per = !grouped ? M : M > pad ? (M - pad) / experts : 0;
+    // Above 128 rows the form for few rows reads the weights once for every 128 of them (us by
+    // pairs and by few-row tiles, MX): 160 x 28672 x 8192 30.4 and 44.1, 256 x 28672 x 8192 31.1
+    // and 47.0, 256 x 4096 x 4096 10.4 and 13.2.  Up to 64 rows it is the better one, 25.9 against
+    // 29.2 and 8.6 against 9.9; of 65 to 128 only where N is large (128 x 28672 x 8192 29.6 against
+    // 30.2, but 128 x 4096 x 4096 12.1 against 10.4 and 128 x 8192 x 2048 12.1 against 8.4).
     if (cap >= 2 && per > 128) {
         // Cycles of the busiest pair, from 8192 x 28672 x 8192 in each form (637, 579 and
         // 569 us): a stage of 256 columns of K takes 620 with one accumulator and 1080 with

@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(256) order_sum_kernel(int* __restrict__ counts
     if (lane == 0) counts[(size_t)ctas * experts + e] = run;
 }
 
-// sums: order_sum_kernel's, or NULL where every CTA counts for itself.
+// sums: order_sum_kernel's, or NULL where every CTA counts for itself.  1024 threads have 64
+// registers each, of which the 32 warps' counts take half: 24 bytes spill.
 __global__ void __launch_bounds__(kOrderThreads)
     order_place_kernel(const int32_t* __restrict__ idx, int64_t n, int topk, int experts, int per_cta, int place_ctas,
                        const int* __restrict__ sums, int32_t* __restrict__ slot, int32_t* __restrict__ row_of,

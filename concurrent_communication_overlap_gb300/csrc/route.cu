@@ -13,9 +13,12 @@
 // one token as for four, is most of the work: 32768 x 60, 6 chosen, takes 354
 // instructions a token with 32 lanes and 192 with 8 (11 us against 15).
 //
-// Instructions are what bounds it, not bytes: 65536 x 256 with groups takes 57 us,
-// about 720 instructions a token, a third of them the 256 sigmoids, where its bytes need
-// 10.5; 32768 x 60 takes 11 us forward and 9 backward, where they need 1 and 1.
+// Not bytes bound it.  65536 x 256, sigmoids, bias and groups, takes 55 us, its bytes
+// need 10.5: 742 instructions a token fill 71% of the issue slots (without a bias or
+// groups 432, 64%, 37 us); for the rest a CTA's 8 warps, 4 CTAs an SM, wait for one
+// another's shuffles and shared memory, for fixed latencies and for the ALU, 61% busy.
+// 32768 x 60, softmax: 7.6 us for 182 instructions a token, 65%; its gradient 5.0, most
+// of it waiting for loads (an index, the logit that it names, then the row): 50%.
 #include "ops_device.cuh"
 #include "c3_internal.h"
 
@@ -23,7 +26,7 @@
 
 namespace c3 {
 
-constexpr int kRouteWarps = 8;  // tokens per CTA and pass
+constexpr int kRouteWarps = 8;  // of a CTA, each with 32 / L tokens a pass
 constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ float load_f(const float* p) { return __ldg(p); }
@@ -303,8 +306,9 @@ __device__ __forceinline__ float choice_weight(const T* xr, int mine, const Rout
 
 // NI experts a lane, L NI >= E.  GROUPS: 0 none, 1 a run of L / groups lanes each (groups
 // a power of two), 2 any (L = 32).  vec: as load_row's.  topk <= L.
-// Registers: 65536 x 256 took 62 us with 64 and 66 with 80; 16000 x 1000 takes 76 with
-// 128, 81 with 80 and 127 with 218.
+// Registers: 65536 x 256 takes 55 us with 64 and 60 with 80; 16000 x 1000 takes 72 with
+// 128, 77 with 80 and 119 with 218.  Groups by way of memory spill 56 bytes with NI = 16
+// and 16 with NI = 32, the others none.
 template <typename T, int NI, int L, int GROUPS>
 __global__ void __launch_bounds__(kRouteWarps * 32, NI == 12 || NI == 16 ? 4 : NI == 32 ? 2 : 1)
     route_kernel(const T* __restrict__ logits, int64_t ld, int64_t tokens, int vec, RouteArgs a,
@@ -555,15 +559,17 @@ constexpr int64_t kFewTokens = 4096;
 // Lanes a token and experts a lane.  8 lanes hold 128 experts in 16 registers, 16
 // lanes 256; more registers a lane would cost more in sorting and shifting them
 // than the exchange saves.  Few tokens do not fill the machine: a whole warp is
-// then the shortest way (8 x 256 with groups: 6.1 us a call against 7.8 with 16
-// lanes; 8192 x 60: 6.8 against 6.4 with 8).  Groups that are a power of two in number have
+// then the shortest way (softmax, fp32, us with a whole warp and with fewer lanes: 2048 x 256
+// 3.6 and 6.6, 4096 x 256 5.3 and 7.5, 8192 x 256 7.9 and 8.0, 16384 x 256 12.9 and 11.8;
+// 8192 x 128 5.1 and 7.1, 16384 x 128 8.3 and 7.8; 8192 x 60 4.4 and 4.5, 16384 x 60 6.7 and
+// 4.9: kFewTokens could be two to three times what it is).  Groups that are a power of two in number have
 // a run of lanes each, whatever their size (16000 x 160 in 8 groups: 14 us; by way of memory,
 // as other numbers of groups, which take a whole warp, 41).
 struct RouteForm {
     int lanes, per_lane, groups;
 };
 
-// Powers of two, and 12: 16 would sort and score a quarter more (16000 x 371: 23.4 us against 30.6).
+// Powers of two, and 12: 16 would sort and score a quarter more (16000 x 371 with a bias: 23.4 us against 30.6).
 static int registers_for(int n) {
     if (n > 8 && n <= 12) return 12;
     int p = 1;
