@@ -142,6 +142,7 @@ __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4GemmArgs& g, const int* pre
 // A, or do not start at a whole scale tile, has none: nothing out of range is touched.
 template <int ROWS>
 __device__ __forceinline__ void expert_tiles(const Fp4GemmArgs& g, int* prefix, int lane) {
+    const int64_t limit = (int64_t)g.num_m + g.experts;
     int run = 0;
     for (int e0 = 0; e0 < g.experts; e0 += 32) {
         const int e = e0 + lane;
@@ -156,8 +157,8 @@ __device__ __forceinline__ void expert_tiles(const Fp4GemmArgs& g, int* prefix, 
             const int v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
-        if (e < g.experts) prefix[e + 1] = run + incl;
-        run += __shfl_sync(0xffffffffu, incl, 31);
+        if (e < g.experts) prefix[e + 1] = tiles_up_to(run, incl, limit);
+        run = tiles_up_to(run, __shfl_sync(0xffffffffu, incl, 31), limit);
     }
     if (lane == 0) prefix[0] = 0;
 }

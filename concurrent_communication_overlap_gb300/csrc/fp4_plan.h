@@ -10,6 +10,19 @@ constexpr int kTileRows = 128;  // rows of a scale tile; an expert's rows start 
 constexpr int kFK = 256;        // columns of a stage: 128 bytes of codes
 constexpr int kPN = 192;        // columns of one accumulator of the form for many rows
 
+#ifdef __CUDACC__
+#define C3_BOTH __host__ __device__
+#else
+#define C3_BOTH
+#endif
+
+// Row tiles of the experts up to one: `before` and `more`, at most `limit`.  Experts whose rows
+// do not overlap have no more than a matrix's tiles and one for each, which the host has found
+// to be few enough for 32 bits; counts from the device that say otherwise stop there.
+C3_BOTH inline int tiles_up_to(int64_t before, int64_t more, int64_t limit) {
+    return (int)(before + more < limit ? before + more : limit);
+}
+
 // How a product runs: rows and columns of a tile (512 x 192, 256 x 384 or 256 x 192
 // on two SMs; 128, 64 or 32 x 128 with the roles swapped), and over how many CTAs a
 // tile's K is split.

@@ -91,3 +91,33 @@ def test_forms_of_the_measured_products(plan):
     assert plan(13, 8200, 8072)[:3] == (32, 128, 4)
     assert plan(8192 * 4 + 127 * 32, 4096, 4096, 32, True)[:2] == (256, 384)
     assert plan(192 + 127 * 64, 2048, 4096, 64, True)[:2] == (64, 128)
+
+
+def test_overlapping_experts_stay_in_32_bits(tmp_path):
+    """Counts that claim the whole matrix for each of 1024 experts: the running sum of row tiles, as the kernels form it,
+    times the column tiles would pass 2^31 (1024 x 31250 x 224); held at the limit it is monotone and in range."""
+    src = tmp_path / "tiles.cpp"
+    src.write_text(r'''
+#include <cstdio>
+#include "fp4_plan.h"
+int main() {
+  const long long M = 2000000, rows = 64, experts = 1024, num_n = 224, num_m = (M + rows - 1) / rows;
+  const long long limit = num_m + experts;
+  int run = 0, prefix[1025] = {0};
+  for (int e0 = 0; e0 < experts; e0 += 32) {
+    int incl = 0;
+    for (int l = 0; l < 32; ++l) {
+      incl += (int)num_m;
+      prefix[e0 + l + 1] = c3::tiles_up_to(run, incl, limit);
+    }
+    run = c3::tiles_up_to(run, incl, limit);
+  }
+  for (int e = 0; e < experts; ++e)
+    if (prefix[e + 1] < prefix[e] || prefix[e + 1] > limit) return 1;
+  if (prefix[1] != num_m || prefix[experts] != limit) return 2;
+  return (long long)prefix[experts] * num_n > 0x7fffffffLL ? 3 : 0;
+}
+''')
+    exe = tmp_path / "tiles"
+    subprocess.run(["g++", "-std=c++17", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
