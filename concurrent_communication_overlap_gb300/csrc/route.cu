@@ -3,15 +3,14 @@
 //
 // L lanes a token (8, 16 or 32, so a warp takes 4, 2 or 1).  Lane l of them
 // holds the logits of NI consecutive experts, l NI and up (in groups, those of a run
-// of lanes being a group), in registers.  The
-// choice compares 32-bit integers that order as the float keys do; of equal keys
+// of lanes being a group), in registers.  The choice compares 32-bit integers that order as the float keys do; of equal keys
 // the lowest lane, and in it the lowest register, is the lowest expert.  Without a
 // bias the keys are the logits: the scores order as they do, but fp32 scores of
 // different logits can be equal (every sigmoid above 17 is 1).
 //
 // Few lanes a token, because the exchange between lanes, which is the same for
-// one token as for four, is most of the work: 32768 x 60, 6 chosen, takes 354
-// instructions a token with 32 lanes and 192 with 8 (11 us against 15).
+// one token as for four, is most of the work: 32768 x 60, 6 chosen, took 354
+// instructions a token with 32 lanes and 192 with 8 (16384 x 60: 6.7 us and 4.9).
 //
 // Not bytes bound it.  65536 x 256, sigmoids, bias and groups, takes 55 us, its bytes
 // need 10.5: 742 instructions a token fill 71% of the issue slots (without a bias or
@@ -562,9 +561,9 @@ constexpr int64_t kFewTokens = 4096;
 // then the shortest way (softmax, fp32, us with a whole warp and with fewer lanes: 2048 x 256
 // 3.6 and 6.6, 4096 x 256 5.3 and 7.5, 8192 x 256 7.9 and 8.0, 16384 x 256 12.9 and 11.8;
 // 8192 x 128 5.1 and 7.1, 16384 x 128 8.3 and 7.8; 8192 x 60 4.4 and 4.5, 16384 x 60 6.7 and
-// 4.9: kFewTokens could be two to three times what it is).  Groups that are a power of two in number have
-// a run of lanes each, whatever their size (16000 x 160 in 8 groups: 14 us; by way of memory,
-// as other numbers of groups, which take a whole warp, 41).
+// 4.9: kFewTokens could be two to three times what it is).  Groups that are a power of two
+// in number have a run of lanes each, whatever their size (16000 x 160 in 8 groups: 14 us; by
+// way of memory, as other numbers of groups, which take a whole warp, 41).
 struct RouteForm {
     int lanes, per_lane, groups;
 };
