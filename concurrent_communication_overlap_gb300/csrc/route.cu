@@ -3,10 +3,11 @@
 //
 // L lanes a token (8, 16 or 32, so a warp takes 4, 2 or 1).  Lane l of them
 // holds the logits of NI consecutive experts, l NI and up (in groups, those of a run
-// of lanes being a group), in registers.  The choice compares 32-bit integers that order as the float keys do; of equal keys
-// the lowest lane, and in it the lowest register, is the lowest expert.  Without a
-// bias the keys are the logits: the scores order as they do, but fp32 scores of
-// different logits can be equal (every sigmoid above 17 is 1).
+// of lanes being a group), in registers.  The choice compares 32-bit integers that
+// order as the float keys do; of equal keys the lowest lane, and in it the lowest
+// register, is the lowest expert.  Without a bias the keys are the logits: the scores
+// order as they do, but fp32 scores of different logits can be equal (every sigmoid
+// above 17 is 1).
 //
 // Few lanes a token, because the exchange between lanes, which is the same for
 // one token as for four, is most of the work: 32768 x 60, 6 chosen, took 354
