@@ -55,15 +55,6 @@ __device__ __forceinline__ uint64_t code_desc(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-// One lane of a converged warp.  The warps that issue tensor-core work stay
-// together and predicate the instruction alone: their addresses and descriptors
-// then live in uniform registers (one lane branching off to issue took 640
-// cycles for a stage of four MMAs, 400 this way).
-__device__ __forceinline__ uint32_t elect_lane() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r;
-}
 // GROUP: CTAs that share the tile (1 or 2).
 template <int GROUP, bool NV>
 __device__ __forceinline__ void mma_fp4(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
@@ -90,17 +81,6 @@ __device__ __forceinline__ void copy_scales(uint32_t lead, uint32_t taddr, uint6
     else C3_CP("1");
 #undef C3_CP
 }
-// Arrive on this CTA's `bar` once all that the thread issued has completed.
-template <int GROUP>
-__device__ __forceinline__ void commit_local(uint32_t lead, uint32_t bar) {
-#define C3_COMMIT(G_)                                                                                \
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q tcgen05.commit.cta_group::" G_   \
-                 ".mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead) : "memory")
-    if constexpr (GROUP == 2) C3_COMMIT("2");
-    else C3_COMMIT("1");
-#undef C3_COMMIT
-}
-
 // One output tile: its expert, rows and columns.
 struct Fp4Tile {
     int expert;       // matrix of B
@@ -216,70 +196,6 @@ struct Fp4PairCfg {
     static_assert(kStages >= kSets && 2 * kPN + kSets * kKT * kSetCols <= 512, "pair configuration");
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t leader_addr(uint32_t local) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(local));
-    return r;
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A wait whose phase another CTA of the cluster may complete.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (*abort) return false;
-            if (globaltimer() - t0 > kWaitLimitNs) {
-                *abort = 1;
-                return false;
-            }
-        }
-    }
-}
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y,
-                                                 uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
-        : "memory");
-}
-__device__ __forceinline__ void commit_pair(uint32_t lead, uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
-        "h"((uint16_t)3), "r"(lead)
-        : "memory");
-}
-
-__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t* v) {
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                 : "r"(addr)
-                 : "memory");
-}
 // 64 bytes of each of the warp's 32 rows (16 fp32 or 32 bf16 values a lane, its
 // row's) to C by way of shared memory, so that neighbouring lanes write neighbouring
 // bytes, W at a time: 16 where rows of C are whole 16-byte units, else 4 or 2 (a lane
@@ -629,12 +545,6 @@ struct Fp4RowsCfg {
     static_assert(kStage % 1024 == 0 && kStages >= 3 && kSets * kKT * kSetCols <= 128, "few-rows configuration");
     static_assert(kStages * kStage >= NT * 512, "the parts meet in the ring");
 };
-
-__device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
-    return r;
-}
 
 template <bool NV, int NT, typename TC>
 __global__ void __launch_bounds__(kRThreads, 2)

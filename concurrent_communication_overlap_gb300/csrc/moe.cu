@@ -230,67 +230,6 @@ int order_launch(const int32_t* idx, int64_t tokens, int topk, int experts, int3
 
 // ---------------------------------------------------------------- combine
 
-// W consecutive values as fp32, whatever the type: 16 bytes at most at once.
-template <int W>
-__device__ __forceinline__ void load_w(const float* p, float (&v)[W]) {
-    if constexpr (W == 8) {
-        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else if constexpr (W == 2) {
-        const float2 a = *reinterpret_cast<const float2*>(p);
-        v[0] = a.x, v[1] = a.y;
-    } else {
-        v[0] = *p;
-    }
-}
-template <int W>
-__device__ __forceinline__ void load_w(const __nv_bfloat16* p, float (&v)[W]) {
-    if constexpr (W == 1) {
-        v[0] = __bfloat162float(*p);
-    } else {
-        uint32_t u[W / 2];
-        if constexpr (W == 8) {
-            const uint4 a = *reinterpret_cast<const uint4*>(p);
-            u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w;
-        } else {
-            u[0] = *reinterpret_cast<const uint32_t*>(p);
-        }
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
-    }
-}
-template <int W>
-__device__ __forceinline__ void store_w(float* p, const float (&v)[W]) {
-    if constexpr (W == 8) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else if constexpr (W == 2) {
-        *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
-    } else {
-        *p = v[0];
-    }
-}
-template <int W>
-__device__ __forceinline__ void store_w(__nv_bfloat16* p, const float (&v)[W]) {
-    if constexpr (W == 1) {
-        *p = __float2bfloat16_rn(v[0]);
-    } else {
-        uint32_t u[W / 2];
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        if constexpr (W == 8)
-            *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-        else
-            *reinterpret_cast<uint32_t*>(p) = u[0];
-    }
-}
-
 constexpr int kCombineThreads = 256;
 constexpr int kCombineWarps = kCombineThreads / 32;
 constexpr int kSpan = 256;  // columns a warp takes at once: 8 a lane, W by W

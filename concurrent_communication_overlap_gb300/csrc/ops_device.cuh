@@ -1,8 +1,10 @@
-// ops_device.cuh -- what the routing and 4-bit kernels share beyond the device
-// helpers of the GEMM: chained launches and the codes of their waits.
+// ops_device.cuh -- what the operators' kernels share beyond the device helpers of the GEMM: chained
+// launches, the codes of their waits, values by vectors, and two SMs on one tile.
 #pragma once
 
 #include "c3_device.cuh"
+
+#include <cuda_bf16.h>
 
 namespace c3 {
 
@@ -47,6 +49,161 @@ inline cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, unsigned
     cudaError_t e = cudaLaunchKernelEx(&c, kernel, static_cast<Params>(args)...);
     if (e != cudaSuccess) cudaGetLastError();
     return e;
+}
+
+// ---------------------------------------------------------------- values by vectors
+
+// W consecutive values as fp32, whatever the type: 16 bytes at most at once.
+template <int W>
+__device__ __forceinline__ void load_w(const float* p, float (&v)[W]) {
+    if constexpr (W == 8) {
+        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else if constexpr (W == 2) {
+        const float2 a = *reinterpret_cast<const float2*>(p);
+        v[0] = a.x, v[1] = a.y;
+    } else {
+        v[0] = *p;
+    }
+}
+template <int W>
+__device__ __forceinline__ void load_w(const __nv_bfloat16* p, float (&v)[W]) {
+    if constexpr (W == 1) {
+        v[0] = __bfloat162float(*p);
+    } else {
+        uint32_t u[W / 2];
+        if constexpr (W == 8) {
+            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w;
+        } else {
+            u[0] = *reinterpret_cast<const uint32_t*>(p);
+        }
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+}
+template <int W>
+__device__ __forceinline__ void store_w(float* p, const float (&v)[W]) {
+    if constexpr (W == 8) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else if constexpr (W == 2) {
+        *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    } else {
+        *p = v[0];
+    }
+}
+template <int W>
+__device__ __forceinline__ void store_w(__nv_bfloat16* p, const float (&v)[W]) {
+    if constexpr (W == 1) {
+        *p = __float2bfloat16_rn(v[0]);
+    } else {
+        uint32_t u[W / 2];
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if constexpr (W == 8)
+            *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+        else
+            *reinterpret_cast<uint32_t*>(p) = u[0];
+    }
+}
+
+// ---------------------------------------------------------------- clusters, and two SMs on one tile
+
+// One lane of a converged warp.  The warps that issue tensor-core work stay
+// together and predicate the instruction alone: their addresses and descriptors
+// then live in uniform registers (one lane branching off to issue took 640
+// cycles for a stage of four MMAs, 400 this way).
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+// Arrive on this CTA's `bar` once all that the thread issued has completed.
+template <int GROUP>
+__device__ __forceinline__ void commit_local(uint32_t lead, uint32_t bar) {
+#define C3_COMMIT(G_)                                                                                \
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q tcgen05.commit.cta_group::" G_   \
+                 ".mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead) : "memory")
+    if constexpr (GROUP == 2) C3_COMMIT("2");
+    else C3_COMMIT("1");
+#undef C3_COMMIT
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t leader_addr(uint32_t local) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(local));
+    return r;
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A wait whose phase another CTA of the cluster may complete.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort) return false;
+            if (globaltimer() - t0 > kWaitLimitNs) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y,
+                                                 uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"((uint16_t)3), "r"(lead)
+        : "memory");
+}
+
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t* v) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
 }
 
 }  // namespace c3
