@@ -149,12 +149,19 @@ def _load():
         "c3_moe_combine": [_vp, _int, _i64, _i64, _vp, _vp, _i64, _int, _vp, _int, _vp],
         "c3_moe_combine_backward": [_vp, _int, _vp, _int, _i64, _i64, _vp, _vp, _i64, _int, _vp, _vp, _vp],
     }
+    sig |= {
+        "c3_embed": [_vp, _int, _i64, _i64, _i64, _i64, _vp, _i64, ctypes.c_float, _vp, _int, _i64, _vp],
+        "c3_embed_backward_bytes": [_i64, _i64, _i64],
+        "c3_embed_backward": [_vp, _int, _i64, _vp, _i64, _i64, ctypes.c_float, _int, _vp, _int, _i64, _i64, _i64, _vp, _sz,
+                              _vp],
+    }
     for name, args in sig.items():
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = _int
     lib.c3_moe_rows.restype = _i64
     lib.c3_moe_order_bytes.restype = _sz
+    lib.c3_embed_backward_bytes.restype = _sz
     lib.c3_fp4_code_bytes.restype = _sz
     lib.c3_fp4_scale_bytes.restype = _sz
     lib.c3_kernel_launches.argtypes = []
@@ -171,7 +178,8 @@ EXPORTED = ("c3_get_device_info", "c3_strerror", "c3_last_error", "c3_status_che
             "c3_rp_predict", "c3_rp_predict_elastic", "c3_cta_windows",
             "c3_route", "c3_route_backward", "c3_moe_rows", "c3_moe_order_bytes", "c3_moe_order",
             "c3_fp4_code_bytes", "c3_fp4_scale_bytes", "c3_fp4_quantize", "c3_fp4_dequantize", "c3_fp4_gemm",
-            "c3_fp4_gemm_experts", "c3_moe_combine", "c3_moe_combine_backward")
+            "c3_fp4_gemm_experts", "c3_moe_combine", "c3_moe_combine_backward",
+            "c3_embed", "c3_embed_backward_bytes", "c3_embed_backward")
 
 
 def lib():
@@ -458,3 +466,30 @@ def c3_moe_combine_backward(dout, dout_type, y, y_type, rows, cols, slot, weight
     rc = _lib.c3_moe_combine_backward(_ptr(dout), dout_type, _ptr(y), y_type, rows, cols, _ptr(slot), _ptr(weights),
                                       tokens, topk, _ptr(dy), _ptr(dweights), _stream(stream))
     return _done(rc, "c3_moe_combine_backward", check)
+
+
+def _work_bytes(work, nbytes):
+    """Bytes of a workspace: a tensor's own, or those given with an address."""
+    if nbytes is not None:
+        return nbytes
+    return 0 if work is None else work.numel() * work.element_size()
+
+
+def c3_embed(table, type, rows, cols, ids, tokens, out, out_type, scale=1.0, first=0, ld=None, out_ld=None, stream=None,
+             check=True):
+    rc = _lib.c3_embed(_ptr(table), type, rows, cols, cols if ld is None else ld, first, _ptr(ids), tokens, scale, _ptr(out),
+                       out_type, cols if out_ld is None else out_ld, _stream(stream))
+    return _done(rc, "c3_embed", check)
+
+
+def c3_embed_backward_bytes(tokens, rows, cols):
+    return int(_lib.c3_embed_backward_bytes(int(tokens), int(rows), int(cols)))
+
+
+def c3_embed_backward(dout, dout_type, ids, tokens, dtable, type, rows, cols, work, scale=1.0, first=0, accumulate=False,
+                      dout_ld=None, ld=None, work_bytes=None, stream=None, check=True):
+    """work: a tensor (its size is taken from it) or an address with work_bytes."""
+    rc = _lib.c3_embed_backward(_ptr(dout), dout_type, cols if dout_ld is None else dout_ld, _ptr(ids), tokens, first, scale,
+                                int(accumulate), _ptr(dtable), type, rows, cols, cols if ld is None else ld, _ptr(work),
+                                _work_bytes(work, work_bytes), _stream(stream))
+    return _done(rc, "c3_embed_backward", check)

@@ -243,6 +243,21 @@ int fp4_gemm_launch(const Fp4& a, const Fp4& b, const int32_t* offsets, const in
 int fp4_gemm_init_device();
 int order_init_device();
 
+// ---------------------------------------------------------------- embeddings and orthogonalisation
+
+// A table of rows x cols at distance ld, the ids of its rows from `first` on, and the tokens' rows
+// (the lookup's output, the gradient's input) at distance out_ld.
+struct EmbedArgs {
+    int64_t rows, cols, ld, first, tokens, out_ld;
+    float scale;
+};
+int embed_launch(const void* table, int bf16, const EmbedArgs& a, const int32_t* ids, void* out, int out_bf16,
+                 cudaStream_t s);
+size_t embed_backward_bytes(int64_t tokens, int64_t rows, int64_t cols);
+int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, const int32_t* ids, int accumulate,
+                          void* table, int bf16, void* work, cudaStream_t s);
+int embed_init_device();
+
 int status_reset_launch(DevStatus* st, cudaStream_t s);
 int selftest_wait_launch(DevStatus* st, unsigned long long limit_ns, int arrive, cudaStream_t s);
 int zero_fill_launch(void* buf, size_t bytes, cudaStream_t s);

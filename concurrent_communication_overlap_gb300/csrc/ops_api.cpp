@@ -1,5 +1,6 @@
-// ops_api.cpp -- the C ABI of the routing and 4-bit operators: argument checks,
-// then one launcher each (route.cu, moe.cu, fp4_quant.cu, fp4_gemm.cu).
+// ops_api.cpp -- the C ABI of the routing and 4-bit operators, the embeddings and the
+// orthogonalisation: argument checks, then one launcher each (route.cu, moe.cu,
+// fp4_quant.cu, fp4_gemm.cu, embed.cu, ortho.cu).
 #include "../../include/c3_api.h"
 #include "c3_internal.h"
 
@@ -275,6 +276,53 @@ int c3_moe_combine_backward(const void* dout, int dout_type, const void* y, int 
         return set_error(C3_EALIGN, "a pointer is not aligned to its element");
     return combine_backward_launch(dout, dout_type == C3_BF16, y, y_type == C3_BF16, rows, cols, slot, weights, tokens,
                                    topk, dy, dweights, static_cast<cudaStream_t>(s));
+}
+
+static int check_embed(int64_t rows, int64_t cols, int64_t ld, int type, int64_t first, int64_t tokens, int64_t out_ld,
+                       int out_type, float scale, EmbedArgs* a) {
+    if (rows < 0 || cols < 0 || tokens < 0 || first < 0) return set_error(C3_EINVAL, "negative rows, cols, tokens or first");
+    if (rows > kMaxRows || cols > kMaxRows || tokens > kMaxRows || first > kMaxRows)
+        return set_error(C3_EUNSUP, "rows, columns, tokens or ids above 2^31-1");
+    if (ld < cols || out_ld < cols) return set_error(C3_EINVAL, "a row distance is below cols");
+    if (!is_type(type) || !is_type(out_type)) return set_error(C3_EINVAL, "unknown type");
+    if (!std::isfinite(scale)) return set_error(C3_EINVAL, "scale must be finite");
+    *a = EmbedArgs{rows, cols, ld, first, tokens, out_ld, scale};
+    return C3_OK;
+}
+
+int c3_embed(const void* table, int type, int64_t rows, int64_t cols, int64_t ld, int64_t first, const int32_t* ids,
+             int64_t tokens, float scale, void* out, int out_type, int64_t out_ld, c3_stream s) {
+    EmbedArgs a;
+    int rc = check_embed(rows, cols, ld, type, first, tokens, out_ld, out_type, scale, &a);
+    if (rc) return rc;
+    if (tokens == 0 || cols == 0) return C3_OK;
+    if ((!table && rows) || !ids || !out) return set_error(C3_EINVAL, "table, ids or out is NULL");
+    if (!aligned(table, type_bytes(type)) || !aligned(out, type_bytes(out_type)) || !aligned(ids, 4))
+        return set_error(C3_EALIGN, "a pointer is not aligned to its element");
+    return embed_launch(table, type == C3_BF16, a, ids, out, out_type == C3_BF16, static_cast<cudaStream_t>(s));
+}
+
+size_t c3_embed_backward_bytes(int64_t tokens, int64_t rows, int64_t cols) {
+    if (tokens < 0 || rows < 0 || cols < 0 || tokens > kMaxRows || rows > kMaxRows || cols > kMaxRows) return 0;
+    return embed_backward_bytes(tokens, rows, cols);
+}
+
+int c3_embed_backward(const void* dout, int dout_type, int64_t dout_ld, const int32_t* ids, int64_t tokens, int64_t first,
+                      float scale, int accumulate, void* dtable, int type, int64_t rows, int64_t cols, int64_t ld, void* work,
+                      size_t work_bytes, c3_stream s) {
+    EmbedArgs a;
+    int rc = check_embed(rows, cols, ld, type, first, tokens, dout_ld, dout_type, scale, &a);
+    if (rc) return rc;
+    if (accumulate != 0 && accumulate != 1) return set_error(C3_EINVAL, "accumulate must be 0 or 1");
+    if (rows == 0 || cols == 0 || (tokens == 0 && accumulate)) return C3_OK;
+    if ((tokens && (!dout || !ids)) || !dtable || !work) return set_error(C3_EINVAL, "dout, ids, dtable or work is NULL");
+    if (!aligned(dout, type_bytes(dout_type)) || !aligned(dtable, type_bytes(type)) || !aligned(ids, 4))
+        return set_error(C3_EALIGN, "a pointer is not aligned to its element");
+    if (!aligned(work, 16)) return set_error(C3_EALIGN, "work must be 16-byte aligned");
+    if (work_bytes < embed_backward_bytes(tokens, rows, cols))
+        return set_error(C3_EINVAL, "work is smaller than c3_embed_backward_bytes");
+    return embed_backward_launch(dout, dout_type == C3_BF16, a, ids, accumulate, dtable, type == C3_BF16, work,
+                                 static_cast<cudaStream_t>(s));
 }
 
 }  // extern "C"

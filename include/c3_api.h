@@ -753,6 +753,45 @@ int c3_moe_combine_backward(const void *dout, int dout_type, const void *y, int 
                             int64_t cols, const int32_t *slot, const float *weights, int64_t tokens,
                             int topk, void *dy, float *dweights, c3_stream s);
 
+/* ------------------------------------------------------------------------
+ * The two ends of a training step: the lookup of embeddings and the gradient
+ * of their table, of which a rank may hold a shard (the lookups of all shards
+ * add up to the whole, as c3_allreduce does it; gradients are its payload),
+ * and the orthogonalisation of an update, which needs the whole matrix
+ * (c3_allgather).  The conventions of the operators above hold.  A workspace
+ * is scratch of one call at a time: calls that may overlap on the GPU, and
+ * graphs that may run side by side, need one each.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Lookup:  out[t] = scale * table[ids[t] - first], in fp32, rounded once.
+ *   table  [rows][cols] of `type` (row distance ld): the rows of ids first ..
+ *          first + rows - 1, a shard or a whole vocabulary
+ *   ids    int32 [tokens], device; a token whose id has no row here (another
+ *          shard's, or padding such as -1) gets zeros
+ *   out    [tokens][cols] of out_type, row distance out_ld; must not overlap table
+ */
+int c3_embed(const void *table, int type, int64_t rows, int64_t cols, int64_t ld, int64_t first, const int32_t *ids,
+             int64_t tokens, float scale, void *out, int out_type, int64_t out_ld, c3_stream s);
+
+/*
+ * Its gradient with respect to the table:
+ *   dtable[v] = scale * sum over t with ids[t] == first + v of dout[t],
+ * and with accumulate = 1 that is added to what dtable[v] holds, and rows that
+ * no token names are left as they were (accumulate = 0: zeros).  The tokens are
+ * sorted by row, the sums run in fp32 in an order that does not depend on
+ * timing, and each row is rounded once, after the addition.
+ *   dout    [tokens][cols] of dout_type, row distance dout_ld
+ *   dtable  [rows][cols] of `type`, row distance ld; overlaps neither dout nor ids
+ *   work    at least c3_embed_backward_bytes(tokens, rows, cols) bytes, device,
+ *           16-byte aligned, scratch
+ * c3_embed_backward_bytes is host only: 0 for bad arguments.
+ */
+size_t c3_embed_backward_bytes(int64_t tokens, int64_t rows, int64_t cols);
+int c3_embed_backward(const void *dout, int dout_type, int64_t dout_ld, const int32_t *ids, int64_t tokens, int64_t first,
+                      float scale, int accumulate, void *dtable, int type, int64_t rows, int64_t cols, int64_t ld,
+                      void *work, size_t work_bytes, c3_stream s);
+
 #ifdef __cplusplus
 }
 #endif
