@@ -155,6 +155,11 @@ def _load():
         "c3_embed_backward": [_vp, _int, _i64, _vp, _i64, _i64, ctypes.c_float, _int, _vp, _int, _i64, _i64, _i64, _vp, _sz,
                               _vp],
     }
+    sig |= {
+        "c3_orthogonalize_bytes": [_i64, _i64, _int],
+        "c3_orthogonalize": [_vp, _int, _i64, _i64, _i64, _int, _vp, _int, ctypes.c_float, ctypes.c_float, _vp, _i64, _vp,
+                             _sz, _int, _vp],
+    }
     for name, args in sig.items():
         f = getattr(lib, name)
         f.argtypes = args
@@ -162,6 +167,7 @@ def _load():
     lib.c3_moe_rows.restype = _i64
     lib.c3_moe_order_bytes.restype = _sz
     lib.c3_embed_backward_bytes.restype = _sz
+    lib.c3_orthogonalize_bytes.restype = _sz
     lib.c3_fp4_code_bytes.restype = _sz
     lib.c3_fp4_scale_bytes.restype = _sz
     lib.c3_kernel_launches.argtypes = []
@@ -179,7 +185,8 @@ EXPORTED = ("c3_get_device_info", "c3_strerror", "c3_last_error", "c3_status_che
             "c3_route", "c3_route_backward", "c3_moe_rows", "c3_moe_order_bytes", "c3_moe_order",
             "c3_fp4_code_bytes", "c3_fp4_scale_bytes", "c3_fp4_quantize", "c3_fp4_dequantize", "c3_fp4_gemm",
             "c3_fp4_gemm_experts", "c3_moe_combine", "c3_moe_combine_backward",
-            "c3_embed", "c3_embed_backward_bytes", "c3_embed_backward")
+            "c3_embed", "c3_embed_backward_bytes", "c3_embed_backward",
+            "c3_orthogonalize_bytes", "c3_orthogonalize")
 
 
 def lib():
@@ -493,3 +500,17 @@ def c3_embed_backward(dout, dout_type, ids, tokens, dtable, type, rows, cols, wo
                                 int(accumulate), _ptr(dtable), type, rows, cols, cols if ld is None else ld, _ptr(work),
                                 _work_bytes(work, work_bytes), _stream(stream))
     return _done(rc, "c3_embed_backward", check)
+
+
+def c3_orthogonalize_bytes(rows, cols, count=1):
+    return int(_lib.c3_orthogonalize_bytes(int(rows), int(cols), int(count)))
+
+
+def c3_orthogonalize(x, type, rows, cols, out, work, coeffs, scale=1.0, eps=1e-7, count=1, ld=None, out_ld=None, sm_budget=0,
+                     work_bytes=None, stream=None, check=True):
+    """coeffs: a list of (a, b, c), one a step.  work: a tensor (its size is taken from it) or an address with work_bytes."""
+    flat = None if coeffs is None else (ctypes.c_float * (3 * len(coeffs)))(*[v for abc in coeffs for v in abc])
+    rc = _lib.c3_orthogonalize(_ptr(x), type, rows, cols, cols if ld is None else ld, count, flat,
+                               0 if coeffs is None else len(coeffs), eps, scale, _ptr(out), cols if out_ld is None else out_ld,
+                               _ptr(work), _work_bytes(work, work_bytes), sm_budget, _stream(stream))
+    return _done(rc, "c3_orthogonalize", check)

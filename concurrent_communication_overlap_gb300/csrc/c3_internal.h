@@ -257,6 +257,10 @@ size_t embed_backward_bytes(int64_t tokens, int64_t rows, int64_t cols);
 int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, const int32_t* ids, int accumulate,
                           void* table, int bf16, void* work, cudaStream_t s);
 int embed_init_device();
+size_t ortho_bytes(int64_t rows, int64_t cols, int count);
+int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld, int count, const float (*coeffs)[3],
+                 int steps, double eps, float scale, void* out, int64_t out_ld, void* work, int sm_budget, cudaStream_t s);
+int ortho_init_device();
 
 int status_reset_launch(DevStatus* st, cudaStream_t s);
 int selftest_wait_launch(DevStatus* st, unsigned long long limit_ns, int arrive, cudaStream_t s);

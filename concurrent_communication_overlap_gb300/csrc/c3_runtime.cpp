@@ -99,6 +99,8 @@ static int init_device(DeviceState& ds, int dev) {
     if (rc) return rc;
     rc = embed_init_device();
     if (rc) return rc;
+    rc = ortho_init_device();
+    if (rc) return rc;
     ds.ready = true;
     return 0;
 }

@@ -23,8 +23,6 @@
 
 #include <cuda_bf16.h>
 
-#include <mutex>
-
 namespace c3 {
 
 constexpr int kFM = 128;             // rows of A in a tile
@@ -195,57 +193,6 @@ struct Fp4PairCfg {
     static constexpr int kSets = NV ? 2 : 4;          // stages whose scales TMEM holds
     static_assert(kStages >= kSets && 2 * kPN + kSets * kKT * kSetCols <= 512, "pair configuration");
 };
-
-// 64 bytes of each of the warp's 32 rows (16 fp32 or 32 bf16 values a lane, its
-// row's) to C by way of shared memory, so that neighbouring lanes write neighbouring
-// bytes, W at a time: 16 where rows of C are whole 16-byte units, else 4 or 2 (a lane
-// writing its own row instead took 1485 us for 6978 x 23694 x 1942, 241 this way).
-// Columns past N and rows past `rows` are left alone.  The 16-byte chunk j of row r
-// lies at chunk j ^ ((r >> 1) & 3): no bank conflicts at 16 bytes either way.
-template <typename TC, int W>
-__device__ __forceinline__ void write_rows(uint32_t blk, int lane, TC* C, int64_t row0, int rows, int col0, int N) {
-    constexpr int kLanes = 64 / W, kAtOnce = 32 / kLanes;  // lanes a row, rows at once
-    const int in = (lane % kLanes) * W, col = col0 + in / (int)sizeof(TC);
-    if (col >= N) rows = 0;
-    TC* c = C + (row0 + lane / kLanes) * (int64_t)N + col;
-#pragma unroll 4
-    for (int r = lane / kLanes; r < 32; r += kAtOnce, c += (int64_t)kAtOnce * N) {
-        const uint32_t at = blk + (uint32_t)(r * 64 + (((in >> 4) ^ ((r >> 1) & 3)) << 4) + (in & 15));
-        if (r >= rows) break;
-        if constexpr (W == 16) {
-            uint32_t u[4];
-            ld_shared_v4(at, u);
-            *reinterpret_cast<uint4*>(c) = make_uint4(u[0], u[1], u[2], u[3]);
-        } else if constexpr (W == 4) {
-            uint32_t u;
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u) : "r"(at) : "memory");
-            *reinterpret_cast<uint32_t*>(c) = u;
-        } else {
-            uint16_t u;
-            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(u) : "r"(at) : "memory");
-            *reinterpret_cast<uint16_t*>(c) = u;
-        }
-    }
-}
-
-// A 32 x 32 piece, already rounded to TC.
-template <typename TC>
-__device__ __forceinline__ void store_piece(const uint32_t* v, uint32_t blk, int lane, int width, TC* C, int64_t row0,
-                                            int rows, int col0, int N) {
-#pragma unroll
-    for (int h = 0; h < (int)sizeof(TC) / 2; ++h) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            st_shared_v4(blk + (uint32_t)lane * 64u + (uint32_t)((j ^ ((lane >> 1) & 3)) << 4), v[16 * h + 4 * j],
-                         v[16 * h + 4 * j + 1], v[16 * h + 4 * j + 2], v[16 * h + 4 * j + 3]);
-        __syncwarp();
-        const int col = col0 + 16 * h;
-        if (width == 16) write_rows<TC, 16>(blk, lane, C, row0, rows, col, N);
-        else if (sizeof(TC) == 4 || width >= 4) write_rows<TC, 4>(blk, lane, C, row0, rows, col, N);
-        else write_rows<TC, 2>(blk, lane, C, row0, rows, col, N);
-        __syncwarp();
-    }
-}
 
 // tmA, tmB: codes; tmSA, tmSB: scales as [row tiles][k tiles * 64] 64-bit words.
 template <bool NV, int MSUB, int NSUB, typename TC>
@@ -497,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i)
                     store_piece<TC>(&v[i * kWords], blk, lane, width, static_cast<TC*>(g.C), tile.row0 + r0, rows,
-                                    col0 + (b + i) * 32, g.N);
+                                    col0 + (b + i) * 32, g.N, g.N);
             }
         }
     }
@@ -833,27 +780,10 @@ __global__ void __launch_bounds__(kRThreads, 2)
 
 // ---------------------------------------------------------------- host side
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn fp4_encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
 // The codes of all `count` matrices as one byte matrix: box 128 bytes x box_rows.
 // Bytes past the last column read as zeros.
 static int code_map(CUtensorMap* map, const Fp4& q, int box_rows) {
-    EncodeTiledFn fn = fp4_encode_fn();
+    EncodeTiledFn fn = tensor_map_encode();
     if (!fn) return set_error(-3, "cuTensorMapEncodeTiled entry point unavailable");
     cuuint64_t dims[2] = {(cuuint64_t)((q.cols + 1) / 2), (cuuint64_t)q.rows * (cuuint64_t)q.count};
     cuuint64_t strides[1] = {(cuuint64_t)q.pitch()};
@@ -868,7 +798,7 @@ static int code_map(CUtensorMap* map, const Fp4& q, int box_rows) {
 
 // The scales of all matrices as rows of 64-bit words, one row tile a row; what lies past the last k tile reads as zeros.
 static int scale_map(CUtensorMap* map, const Fp4& q, int box_rows) {
-    EncodeTiledFn fn = fp4_encode_fn();
+    EncodeTiledFn fn = tensor_map_encode();
     if (!fn) return set_error(-3, "cuTensorMapEncodeTiled entry point unavailable");
     cuuint64_t dims[2] = {(cuuint64_t)q.k_tiles() * 64, (cuuint64_t)q.row_tiles() * (cuuint64_t)q.count};
     cuuint64_t strides[1] = {(cuuint64_t)q.k_tiles() * 512};

@@ -3,6 +3,7 @@
 // fp4_quant.cu, fp4_gemm.cu, embed.cu, ortho.cu).
 #include "../../include/c3_api.h"
 #include "c3_internal.h"
+#include "ortho_plan.h"
 
 #include <cmath>
 
@@ -11,6 +12,7 @@ namespace c3 {
 constexpr int64_t kMaxRows = 0x7FFFFFFF;  // row numbers are 32-bit
 constexpr int kMaxTopk = 32;              // a warp's lanes
 constexpr int kMaxExperts = 1024;
+constexpr int64_t kMaxOrtho = 1 << 24;
 
 static_assert(C3_TILE_ROWS == kTileRows, "tile rows");
 
@@ -323,6 +325,43 @@ int c3_embed_backward(const void* dout, int dout_type, int64_t dout_ld, const in
         return set_error(C3_EINVAL, "work is smaller than c3_embed_backward_bytes");
     return embed_backward_launch(dout, dout_type == C3_BF16, a, ids, accumulate, dtable, type == C3_BF16, work,
                                  static_cast<cudaStream_t>(s));
+}
+
+static int check_ortho(int64_t rows, int64_t cols, int count) {
+    if (rows < 0 || cols < 0 || count < 0) return set_error(C3_EINVAL, "negative rows, cols or count");
+    // (sizes of workspaces, 2 bytes an element, stay within 64 bits)
+    if (rows > kMaxOrtho || cols > kMaxOrtho || count > 65535) return set_error(C3_EUNSUP, "above 2^24 rows or columns, or 65535 matrices");
+    return C3_OK;
+}
+
+size_t c3_orthogonalize_bytes(int64_t rows, int64_t cols, int count) {
+    if (check_ortho(rows, cols, count)) return 0;
+    return ortho_bytes(rows, cols, count);
+}
+
+int c3_orthogonalize(const void* x, int type, int64_t rows, int64_t cols, int64_t ld, int count, const float* coeffs,
+                     int steps, float eps, float scale, void* out, int64_t out_ld, void* work, size_t work_bytes,
+                     int sm_budget, c3_stream s) {
+    int rc = check_ortho(rows, cols, count);
+    if (rc) return rc;
+    if (!is_type(type)) return set_error(C3_EINVAL, "unknown type");
+    if (ld < cols || out_ld < cols) return set_error(C3_EINVAL, "a row distance is below cols");
+    if (steps < 1 || steps > kOrthoSteps) return set_error(C3_EINVAL, "steps must be 1..32");
+    if (!coeffs) return set_error(C3_EINVAL, "coeffs is NULL");
+    for (int i = 0; i < 3 * steps; ++i)
+        if (!std::isfinite(coeffs[i])) return set_error(C3_EINVAL, "coeffs must be finite");
+    if (!std::isfinite(eps) || eps < 0 || !std::isfinite(scale)) return set_error(C3_EINVAL, "eps must be finite and not negative, scale finite");
+    if (sm_budget < 0 || sm_budget == 1) return set_error(C3_EINVAL, "sm_budget must be 0 or at least 2");
+    OrthoStep steps_of[kOrthoSteps];
+    const float(*triples)[3] = reinterpret_cast<const float(*)[3]>(coeffs);
+    if (!ortho_steps(triples, steps, steps_of)) return set_error(C3_EINVAL, "coeffs let the iterates grow past 2^20");
+    if (rows == 0 || cols == 0 || count == 0) return C3_OK;
+    if (!x || !out || !work) return set_error(C3_EINVAL, "x, out or work is NULL");
+    if (!aligned(x, type_bytes(type)) || !aligned(out, 2)) return set_error(C3_EALIGN, "a pointer is not aligned to its element");
+    if (!aligned(work, 256)) return set_error(C3_EALIGN, "work must be 256-byte aligned");
+    if (work_bytes < ortho_bytes(rows, cols, count)) return set_error(C3_EINVAL, "work is smaller than c3_orthogonalize_bytes");
+    return ortho_launch(x, type == C3_BF16, rows, cols, ld, count, triples, steps, eps, scale, out, out_ld, work, sm_budget,
+                        static_cast<cudaStream_t>(s));
 }
 
 }  // extern "C"

@@ -1,0 +1,678 @@
+// ortho.cu -- orthogonalises an update by Newton-Schulz products:
+//   X = U / (|U|_F + eps);   X <- (a I + b X X^T + c (X X^T)^2) X, some times;   out = scale X
+// (the transposed products where U is tall, so that the square matrices have the short side).
+//
+// Iterates are fp16 times powers of two (ortho_plan.h): the tensor cores' bf16 rate with 11 bits
+// instead of 8.  Five steps end 1.2e-3 off (2-norm, relative, a random
+// 1024 x 1024), below a bf16 output's own rounding (1.7e-3); eight times that, as bf16 would have it, is above.  The polynomial is one matrix, its multiple of I included: a X and (b A + c A^2) X,
+// which nearly cancel, are never rounded apart.
+//
+// The norm and the conversion are two passes over U; a step is three products by one kernel:
+//   A = X X^T and P = a I + b A + c A A   symmetric: tiles on and above the diagonal alone, each
+//                                         written twice;
+//   X <- P X.
+// Operands lie in memory as they are, along K or across it; the tensor cores take either.
+#include "ops_device.cuh"
+#include "c3_internal.h"
+#include "ortho_plan.h"
+
+#include <cuda_fp16.h>
+
+namespace c3 {
+
+constexpr unsigned kAll = 0xffffffffu;
+
+// ---------------------------------------------------------------- norm and conversion
+
+constexpr int kOrthoThreads = 1024;
+constexpr int kOrthoWarps = kOrthoThreads / 32;
+constexpr int kOrthoSpan = 256;
+
+// Squares of values are summed three times, times 2^-140, 1 and 2^140: whatever the magnitudes, one of
+// the sums neither overflows nor loses what matters.
+constexpr float kTiny = 8.470329472543003e-22f, kHuge = 1.1805916207174113e21f;  // 2^-70, 2^70
+
+struct OrthoIn {
+    const void* x;
+    int64_t rows, cols, ld;
+    int count, parts;
+    double eps;
+    int power;  // 2^power: X's first scale
+    double* sums;
+    float* scale;
+    __half* out;
+    int64_t pitch;
+};
+
+template <typename T, int W>
+__global__ void __launch_bounds__(kOrthoThreads) ortho_norm_kernel(OrthoIn g) {
+    __shared__ double part[3][kOrthoWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t spans = (g.cols + kOrthoSpan - 1) / kOrthoSpan, jobs = g.rows * spans;
+    constexpr int U = kOrthoSpan / (32 * W);
+    chain_wait();
+    for (int64_t i = blockIdx.x; i < (int64_t)g.count * g.parts; i += gridDim.x) {
+        const int64_t m = i / g.parts, p = i - m * g.parts;
+        const T* x = static_cast<const T*>(g.x) + m * g.rows * g.ld;
+        float low = 0.0f, mid = 0.0f, high = 0.0f;
+#pragma unroll 4
+        for (int64_t job = p * kOrthoWarps + warp; job < jobs; job += (int64_t)g.parts * kOrthoWarps) {
+            const int64_t r = job / spans, c0 = (job - r * spans) * kOrthoSpan + lane * W;
+            float v[U][W] = {};
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + 32 * W * u < g.cols) load_w<W>(x + r * g.ld + c0 + 32 * W * u, v[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+                    const float l = v[u][k] * kTiny, h = v[u][k] * kHuge;
+                    low = fmaf(l, l, low);
+                    mid = fmaf(v[u][k], v[u][k], mid);
+                    high = fmaf(h, h, high);
+                }
+        }
+        double s[3] = {low, mid, high};
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(kAll, s[k], o);
+            if (lane == 0) part[k][warp] = s[k];
+        }
+        __syncthreads();
+        if (warp < 3) {
+            double t = part[warp][lane];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(kAll, t, o);
+            if (lane == 0) g.sums[(m * g.parts + p) * 3 + warp] = t;
+        }
+        __syncthreads();
+    }
+}
+
+// X = U 2^-e in fp16, where 2^e is the power of two above |U| + eps: exact for bf16.  What is left of the
+// division, 2^e / (|U| + eps) in (1, 2], goes to scale[m] and into the first step's products.  A NaN or an
+// infinity makes the whole matrix NaN.
+template <typename T, int W>
+__global__ void __launch_bounds__(kOrthoThreads) ortho_convert_kernel(OrthoIn g) {
+    __shared__ double part[3][kOrthoWarps];
+    __shared__ float factors[2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t spans = (g.pitch + kOrthoSpan - 1) / kOrthoSpan, jobs = g.rows * spans;
+    constexpr int U = kOrthoSpan / (32 * W);
+    chain_wait();
+    for (int64_t i = blockIdx.x; i < (int64_t)g.count * g.parts; i += gridDim.x) {
+        const int64_t m = i / g.parts, p = i - m * g.parts;
+        double s[3] = {};
+        for (int j = threadIdx.x; j < g.parts; j += kOrthoThreads)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) s[k] += g.sums[(m * g.parts + j) * 3 + k];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(kAll, s[k], o);
+            if (lane == 0) part[k][warp] = s[k];
+        }
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                s[k] = part[k][lane];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(kAll, s[k], o);
+            }
+            if (lane == 0) {
+                const double one = 2.0 * 1180591620717411303424.0 * 590295810358705651712.0;  // 2^140
+                double sum = s[1];
+                if (!(sum < 1e36)) sum = s[0] * one;
+                else if (sum < 1e-18) sum = s[2] / one;
+                const double r = sqrt(sum) + g.eps;
+                int e = 0;
+                const double f = frexp(r, &e);
+                const bool fine = isfinite(r);
+                // two factors: one alone may leave fp32's range
+                const int half = fine ? (g.power - e) / 2 : 0;
+                factors[0] = fine ? (r > 0 ? (float)ldexp(1.0, half) : 0.0f) : __int_as_float(0x7fc00000);
+                factors[1] = fine ? (float)ldexp(1.0, g.power - e - half) : 0.0f;
+                if (p == 0) g.scale[m] = fine && r > 0 ? (float)(1.0 / f) : 1.0f;
+            }
+        }
+        __syncthreads();
+        const float f0 = factors[0], f1 = factors[1];
+        const T* x = static_cast<const T*>(g.x) + m * g.rows * g.ld;
+        __half* out = g.out + m * g.rows * g.pitch;
+#pragma unroll 2
+        for (int64_t job = p * kOrthoWarps + warp; job < jobs; job += (int64_t)g.parts * kOrthoWarps) {
+            const int64_t r = job / spans, c0 = (job - r * spans) * kOrthoSpan + lane * W;
+            float v[U][W] = {};
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + 32 * W * u < g.cols) load_w<W>(x + r * g.ld + c0 + 32 * W * u, v[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t c = c0 + 32 * W * u;
+                if (c >= g.pitch) continue;
+                __half* to = out + r * g.pitch + c;
+                if constexpr (W == 1) {
+                    *to = __float2half_rn(v[u][0] * f0 * f1);
+                } else {
+                    uint32_t h[W / 2];
+#pragma unroll
+                    for (int k = 0; k < W / 2; ++k) {
+                        const __half2 t = __floats2half2_rn(v[u][2 * k] * f0 * f1, v[u][2 * k + 1] * f0 * f1);
+                        h[k] = *reinterpret_cast<const uint32_t*>(&t);
+                    }
+                    if constexpr (W == 8) *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+                    else *reinterpret_cast<uint32_t*>(to) = h[0];
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- products
+//
+// A cluster of two CTAs shares a tile of 256 x NT (tcgen05.mma, cta_group::2): each brings in half of
+// A's rows and half of B's and holds the accumulators of its own 128 rows, two sets of them, so that
+// the read-out of a tile hides behind the next.  ACROSS_A, ACROSS_B: the operand lies with its rows
+// (the output's rows or columns) along memory and K across it.
+constexpr int kGThreads = 320;  // producer, MMA, and the epilogue's eight warps
+constexpr int kGEpiWarps = 8;
+constexpr int kGK = 64;         // K of a stage: 128 bytes
+constexpr int kGSmemLimit = 232448;
+constexpr int kGGroupM = 16;
+
+enum OrthoWaitSite : int {
+    kSiteOrthoProducer = 16,
+    kSiteOrthoMma = 17,
+    kSiteOrthoEpilogue = 18,
+    kSiteOrthoDrain = 19,
+};
+
+// out = alpha A B^T (times scale[m] `times` times) + beta mat + diag I, rounded to fp16 or bf16.
+struct OrthoProduct {
+    void* out;
+    const __half* mat;   // NULL, or fp16 at the output's place (fp16 outputs)
+    const float* scale;
+    int64_t ld, stride;  // of out, and from one matrix to the next
+    int64_t store_cols;  // columns that may be written
+    int M, N, num_kb, count;
+    int bf16, times;
+    int width;           // bytes that rows of out are aligned to
+    float alpha, beta, diag;
+    OrthoTiles tiles;    // symmetric: tiles above the diagonal
+    int64_t per_matrix;  // tiles of one matrix
+};
+
+template <int NT>
+struct OrthoCfg {
+    static constexpr uint32_t kABytes = 128 * 128;
+    static constexpr uint32_t kBBytes = NT / 2 * 128;
+    static constexpr uint32_t kStage = kABytes + kBBytes;
+    static constexpr uint32_t kStaging = kGEpiWarps * 2048;
+    static constexpr int kExtra = 1024 + 512 + (int)kStaging;
+    static constexpr int kFit = (kGSmemLimit - kExtra) / (int)kStage;
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
+    static constexpr int kSmem = kStages * (int)kStage + kExtra;
+};
+
+__device__ __forceinline__ uint64_t along_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+           ((uint64_t)2 << 61);
+}
+// Rows along memory: 64 of them and one K a 128-byte line, 8 K a swizzle atom of 1024 bytes, 64 K a box
+// of 8 KB; leading offset from one box to the next 64 rows, stride offset from atom to atom.
+__device__ __forceinline__ uint64_t across_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ void mma_pair(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate),
+        "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, int32_t z,
+                                                 uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+        : "memory");
+}
+
+struct OrthoTile {
+    int m, row, col;  // matrix, first row and column
+};
+
+template <int NT>
+__device__ __forceinline__ OrthoTile ortho_tile(const OrthoProduct& g, int64_t t) {
+    OrthoTile r;
+    r.m = (int)(t / g.per_matrix);
+    int64_t in = t - r.m * g.per_matrix;
+    if (g.tiles.skip) {
+        int i = 0;
+        while (i + 1 < g.tiles.rows && g.tiles.before(i + 1) <= in) ++i;
+        r.row = i * 256;
+        r.col = (int)(in - g.tiles.before(i) + (int64_t)g.tiles.skip * i) * NT;
+        return r;
+    }
+    const int64_t per = (int64_t)kGGroupM * g.tiles.cols;
+    const int grp = (int)(in / per), first = grp * kGGroupM;
+    const int gm = min(g.tiles.rows - first, kGGroupM);
+    const int at = (int)(in - grp * per);
+    r.row = (first + at % gm) * 256;
+    r.col = at / gm * NT;
+    return r;
+}
+
+template <int NT, bool ACROSS_A, bool ACROSS_B>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
+    ortho_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, OrthoProduct g,
+                         DevStatus* st) {
+    using Cfg = OrthoCfg<NT>;
+    constexpr int S = Cfg::kStages;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const uint32_t staging = base + S * Cfg::kStage;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(gbase + S * Cfg::kStage + Cfg::kStaging);
+    // stage full [0, S), empty [S, 2S), accumulator full 2S.., empty 2S+2.., drain 2S+4
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    auto bar = [&](int i) { return smem_addr(&bars[i]); };
+    const int TFULL = 2 * S, TEMPTY = 2 * S + 2, DRAIN = 2 * S + 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < S; ++i) {
+            mbar_init(bar(i), 1);
+            mbar_init(bar(S + i), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar(TFULL + b), 1);
+            mbar_init(bar(TEMPTY + b), 2 * kGEpiWarps);
+        }
+        mbar_init(bar(DRAIN), 1);
+        fence_barrier_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    chain_wait();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers are ready before either signals the other's
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int64_t total = g.per_matrix * g.count, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol_a = policy_evict_last(), pol_b = policy_evict_normal();
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int64_t t = first; ok && t < total; t += step) {
+                const OrthoTile tile = ortho_tile<NT>(g, t);
+                const int arow = tile.row + (int)rank * 128, brow = tile.col + (int)rank * (NT / 2);
+                for (int kb = 0; kb < g.num_kb; ++kb) {
+                    if (!mbar_wait_cluster(bar(S + stage), phase ^ 1u, abort_flag)) {
+                        report_error(st, -4, kSiteOrthoProducer);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = base + (uint32_t)stage * Cfg::kStage, sb = sa + Cfg::kABytes;
+                    const uint32_t full = leader_addr(bar(stage));
+                    if (rank == 0) mbar_arrive_expect_tx(bar(stage), 2 * Cfg::kStage);
+                    if constexpr (ACROSS_A) {
+                        tma_load_3d_pair(sa, &tmA, full, arow, kb * kGK, tile.m, pol_a);
+                        tma_load_3d_pair(sa + 8192, &tmA, full, arow + 64, kb * kGK, tile.m, pol_a);
+                    } else {
+                        tma_load_3d_pair(sa, &tmA, full, kb * kGK, arow, tile.m, pol_a);
+                    }
+                    if constexpr (ACROSS_B) {
+#pragma unroll
+                        for (int j = 0; j < NT / 128; ++j)
+                            tma_load_3d_pair(sb + j * 8192, &tmB, full, brow + j * 64, kb * kGK, tile.m, pol_b);
+                    } else {
+                        tma_load_3d_pair(sb, &tmB, full, kb * kGK, brow, tile.m, pol_b);
+                    }
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // The pair's loads have all landed once every stage that was filled has been freed (its
+            // MMAs follow its loads): wait for that before the CTA may end.  After a wait gave up,
+            // the leader's full barriers tell it instead.
+            volatile int no_abort = 0;
+            for (int i = 0; (ok || rank == 0) && i < S; ++i)
+                if (!mbar_wait_cluster(bar(ok ? S + i : i), (i < stage) ? phase : (phase ^ 1u), &no_abort))
+                    report_error(st, -4, kSiteOrthoDrain);
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const uint32_t lead = elect_lane();
+            // D fp32, A and B fp16, which lie along K or across it, N >> 3, M >> 4
+            const uint32_t idesc = (1u << 4) | ((ACROSS_A ? 1u : 0u) << 15) | ((ACROSS_B ? 1u : 0u) << 16) |
+                                   ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+            const uint64_t a0 = ACROSS_A ? across_desc(base) : along_desc(base);
+            const uint64_t b0 = ACROSS_B ? across_desc(base + Cfg::kABytes) : along_desc(base + Cfg::kABytes);
+            // 16 of K: 32 bytes along a line, or two atoms
+            constexpr uint32_t ka = ACROSS_A ? 2048 >> 4 : 2, kb16 = ACROSS_B ? 2048 >> 4 : 2;
+            int stage = 0, local = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int64_t t = first; ok && t < total; t += step, ++local) {
+                const int buf = local & 1;
+                if (!mbar_wait_cluster(bar(TEMPTY + buf), ((uint32_t)(local >> 1) & 1u) ^ 1u, abort_flag)) {
+                    report_error(st, -4, kSiteOrthoMma);
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(buf * NT);
+                for (int kb = 0; kb < g.num_kb; ++kb) {
+                    if (!mbar_wait_cluster(bar(stage), phase, abort_flag)) {
+                        report_error(st, -4, kSiteOrthoMma);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = a0 + (uint64_t)((uint32_t)stage * (Cfg::kStage >> 4));
+                    const uint64_t bd = b0 + (uint64_t)((uint32_t)stage * (Cfg::kStage >> 4));
+#pragma unroll
+                    for (int k = 0; k < kGK / 16; ++k)
+                        mma_pair(lead, d, ad + (uint64_t)(k * ka), bd + (uint64_t)(k * kb16), idesc, k > 0 ? 1u : (uint32_t)(kb > 0));
+                    commit_pair(lead, bar(S + stage));
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) commit_pair(lead, bar(TFULL + buf));
+            }
+            // no MMA may still run when TMEM is freed
+            commit_local<2>(lead, bar(DRAIN));
+            volatile int no_abort = 0;
+            if (!mbar_wait(bar(DRAIN), 0, &no_abort)) report_error(st, -4, kSiteOrthoDrain);
+        }
+    } else {
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t blk = staging + (uint32_t)(warp - 2) * 2048u;
+        constexpr int kPieces = NT / 64;  // of 32 columns: half of the tile's
+        int local = 0;
+        for (int64_t t = first; t < total; t += step, ++local) {
+            const OrthoTile tile = ortho_tile<NT>(g, t);
+            const int buf = local & 1;
+            const bool ready = mbar_wait_cluster(bar(TFULL + buf), (uint32_t)(local >> 1) & 1u, abort_flag);
+            if (!__all_sync(kAll, ready)) {
+                report_error(st, -4, kSiteOrthoEpilogue);
+                break;
+            }
+            tc_fence_after();
+            const int row0 = tile.row + (int)rank * 128 + q * 32, col0 = tile.col + half * (NT / 2);
+            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * NT + half * (NT / 2));
+            float alpha = g.alpha;
+            for (int i = 0; i < g.times; ++i) alpha *= g.scale[tile.m];
+            uint16_t* out = static_cast<uint16_t*>(g.out) + tile.m * g.stride;
+            const int64_t place = tile.m * g.stride + (int64_t)(row0 + lane) * g.ld;
+            // Read out and rounded first: the accumulator is free again before anything is stored.
+            uint32_t v[kPieces][16];
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                const int c0 = col0 + p * 32;
+                uint32_t r[32];
+                tmem_ld32(taddr + (uint32_t)(p * 32), r);
+                uint4 old[4];
+                if (g.mat) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        old[j] = row0 + lane < g.M && c0 + 8 * j < g.store_cols
+                                     ? *reinterpret_cast<const uint4*>(g.mat + place + c0 + 8 * j)
+                                     : make_uint4(0, 0, 0, 0);
+                }
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float x = alpha * __uint_as_float(r[2 * j]), y = alpha * __uint_as_float(r[2 * j + 1]);
+                    if (g.mat) {
+                        const uint32_t w = j % 4 == 0 ? old[j / 4].x : j % 4 == 1 ? old[j / 4].y : j % 4 == 2 ? old[j / 4].z : old[j / 4].w;
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                        x = fmaf(g.beta, f.x, x);
+                        y = fmaf(g.beta, f.y, y);
+                        if (row0 + lane == c0 + 2 * j) x += g.diag;
+                        if (row0 + lane == c0 + 2 * j + 1) y += g.diag;
+                    }
+                    if (g.bf16) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+                        v[p][j] = *reinterpret_cast<const uint32_t*>(&h);
+                    } else {
+                        const __half2 h = __floats2half2_rn(x, y);
+                        v[p][j] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(leader_addr(bar(TEMPTY + buf)));
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                const int c0 = col0 + p * 32;
+                if (g.tiles.skip && c0 < row0) continue;  // below the diagonal: another piece's mirror image
+                store_piece<uint16_t>(v[p], blk, lane, g.width, out, row0, g.M - row0, c0, (int)g.store_cols, g.ld);
+                if (g.tiles.skip && c0 > row0 && row0 + lane < g.M) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        uint16_t* to = out + (int64_t)(c0 + 2 * j) * g.ld + row0 + lane;
+                        if (c0 + 2 * j < g.N) to[0] = (uint16_t)v[p][j];
+                        if (c0 + 2 * j + 1 < g.N) to[g.ld] = (uint16_t)(v[p][j] >> 16);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // nothing of this CTA's is signalled or read by the other any more
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+template <typename F>
+static int each_product(F f) {
+    int rc = f(ortho_product_kernel<256, false, false>, OrthoCfg<256>::kSmem);
+    if (!rc) rc = f(ortho_product_kernel<256, true, true>, OrthoCfg<256>::kSmem);
+    if (!rc) rc = f(ortho_product_kernel<256, false, true>, OrthoCfg<256>::kSmem);
+    if (!rc) rc = f(ortho_product_kernel<128, false, false>, OrthoCfg<128>::kSmem);
+    if (!rc) rc = f(ortho_product_kernel<128, true, true>, OrthoCfg<128>::kSmem);
+    if (!rc) rc = f(ortho_product_kernel<128, false, true>, OrthoCfg<128>::kSmem);
+    return rc;
+}
+
+int ortho_init_device() {
+    return each_product([](auto kernel, int smem) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return e == cudaSuccess ? 0 : set_cuda_error(e, "cudaFuncSetAttribute(orthogonalisation)");
+    });
+}
+
+// fp16 matrices [count][rows][pitch], in boxes of 64 columns x box_rows.  What lies past a matrix reads as zeros.
+static int ortho_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t pitch, int count, int box_rows) {
+    EncodeTiledFn fn = tensor_map_encode();
+    if (!fn) return set_error(-3, "cuTensorMapEncodeTiled entry point unavailable");
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
+    cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)(rows * pitch) * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? 0 : set_error(-3, "cuTensorMapEncodeTiled (orthogonalisation) failed");
+}
+
+size_t ortho_bytes(int64_t rows, int64_t cols, int count) { return ortho_work(rows, cols, count).bytes; }
+
+template <typename T>
+static cudaError_t ortho_in(int w, unsigned grid, cudaStream_t s, const OrthoIn& in) {
+    auto go = [&](auto norm, auto convert) {
+        cudaError_t e = launch_chained(norm, dim3(grid), kOrthoThreads, 0, s, 1, in);
+        if (e != cudaSuccess) return e;
+        count_launch();
+        return launch_chained(convert, dim3(grid), kOrthoThreads, 0, s, 1, in);
+    };
+    return w == 8   ? go(ortho_norm_kernel<T, 8>, ortho_convert_kernel<T, 8>)
+           : w == 2 ? go(ortho_norm_kernel<T, 2>, ortho_convert_kernel<T, 2>)
+                    : go(ortho_norm_kernel<T, 1>, ortho_convert_kernel<T, 1>);
+}
+
+int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld, int count, const float (*coeffs)[3], int steps,
+                 double eps, float scale, void* out, int64_t out_ld, void* work, int sm_budget, cudaStream_t s) {
+    DeviceState* ds = device_state();
+    if (!ds) return -3;
+    if (take_fault(kFaultGemmLaunch)) return set_error(-3, "injected failure: GEMM launch");
+    OrthoStep step[kOrthoSteps];
+    if (!ortho_steps(coeffs, steps, step)) return set_error(-1, "coeffs let the iterates grow without bound");
+    const int cap = (sm_budget <= 0 || sm_budget > ds->sm_count) ? ds->sm_count : sm_budget;
+    const OrthoWork w = ortho_work(rows, cols, count);
+    uint8_t* base = static_cast<uint8_t*>(work);
+    const int64_t m = w.short_side;
+    const bool tall = rows > cols;
+
+    OrthoIn in;
+    in.x = x;
+    in.rows = rows;
+    in.cols = cols;
+    in.ld = ld;
+    in.count = count;
+    in.eps = eps;
+    in.power = step[0].x;
+    in.sums = reinterpret_cast<double*>(base + w.sums);
+    in.scale = reinterpret_cast<float*>(base + w.scale);
+    in.out = reinterpret_cast<__half*>(base + w.x0);
+    in.pitch = w.xpitch;
+    // a part has at least 32 rows' worth of work for its warps, and every SM has a part
+    const int64_t jobs = rows * ((cols + kOrthoSpan - 1) / kOrthoSpan), most = (jobs + kOrthoWarps - 1) / kOrthoWarps;
+    const int64_t want = (2 * (int64_t)cap + count - 1) / count;
+    in.parts = (int)(most < want ? most : want);
+    if (in.parts > kOrthoParts) in.parts = kOrthoParts;
+    const int64_t all = (int64_t)in.parts * count, fit = sm_budget > 0 && cap < ds->sm_count ? cap : 2 * (int64_t)cap;
+    const int size = bf16 ? 2 : 4;
+    const int64_t unit8 = 8 * size < 16 ? 8 * size : 16;
+    auto fits = [&](int64_t bytes) { return (uintptr_t)x % bytes == 0 && ld * size % bytes == 0; };
+    const int wide = cols % 8 == 0 && fits(unit8) ? 8 : cols % 2 == 0 && fits(2 * size) ? 2 : 1;
+    const unsigned grid = (unsigned)(all < fit ? all : fit);
+    cudaError_t e = bf16 ? ortho_in<__nv_bfloat16>(wide, grid, s, in) : ortho_in<float>(wide, grid, s, in);
+    if (e != cudaSuccess) return set_cuda_error(e, "orthogonalisation: norm kernel launch");
+    count_launch();
+
+    const int64_t num_r = (rows + 255) / 256;
+    // Narrower tiles where wider ones would leave SMs idle.
+    const bool narrow = num_r * ((cols + 255) / 256) * count < cap / 2;
+    const int nt = narrow ? 128 : 256;
+    auto blocks = [](int64_t n, int by) { return (int)((n + by - 1) / by); };
+    auto product = [&](bool across_a, bool across_b, const CUtensorMap& a, const CUtensorMap& b, OrthoProduct& g) -> int {
+        g.per_matrix = g.tiles.skip ? g.tiles.total() : (int64_t)g.tiles.rows * g.tiles.cols;
+        const int64_t tiles = g.per_matrix * count, pairs = cap / 2;
+        const dim3 ctas((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+        auto go = [&](auto kernel, int smem) { return launch_chained(kernel, ctas, kGThreads, smem, s, 1, a, b, g, ds->status); };
+        cudaError_t err;
+        if (narrow) {
+            const int sm = OrthoCfg<128>::kSmem;
+            err = across_a ? go(ortho_product_kernel<128, true, true>, sm)
+                           : across_b ? go(ortho_product_kernel<128, false, true>, sm) : go(ortho_product_kernel<128, false, false>, sm);
+        } else {
+            const int sm = OrthoCfg<256>::kSmem;
+            err = across_a ? go(ortho_product_kernel<256, true, true>, sm)
+                           : across_b ? go(ortho_product_kernel<256, false, true>, sm) : go(ortho_product_kernel<256, false, false>, sm);
+        }
+        if (err != cudaSuccess) return set_cuda_error(err, "orthogonalisation: product kernel launch");
+        count_launch();
+        return 0;
+    };
+    __half* X[2] = {reinterpret_cast<__half*>(base + w.x0), reinterpret_cast<__half*>(base + w.x1)};
+    __half* G = reinterpret_cast<__half*>(base + w.g);
+    __half* P = reinterpret_cast<__half*>(base + w.p);
+    // In boxes of 128 and of 64 rows: A along K; B along K in boxes of nt / 2; either across K in boxes of 64.
+    CUtensorMap x128[2], x64[2], g128, g64, p128, p64;
+    int rc = 0;
+    for (int i = 0; i < 2 && !rc; ++i) {
+        rc = ortho_map(&x128[i], X[i], rows, cols, w.xpitch, count, 128);
+        if (!rc) rc = ortho_map(&x64[i], X[i], rows, cols, w.xpitch, count, 64);
+    }
+    if (!rc) rc = ortho_map(&g128, G, m, m, w.gpitch, count, 128);
+    if (!rc) rc = ortho_map(&g64, G, m, m, w.gpitch, count, 64);
+    if (!rc) rc = ortho_map(&p128, P, m, m, w.gpitch, count, 128);
+    if (!rc) rc = ortho_map(&p64, P, m, m, w.gpitch, count, 64);
+    if (rc) return rc;
+
+    for (int i = 0; i < steps; ++i) {
+        const OrthoStep& t = step[i];
+        const int now = i & 1;
+        auto two = [](int p) { return (float)std::ldexp(1.0, p); };
+        OrthoProduct g{};
+        g.scale = in.scale;
+        g.count = count;
+        // A = X X^T (X^T X): the stored 2^x X give 2^2x of it
+        g.out = G;
+        g.ld = g.store_cols = w.gpitch;
+        g.stride = m * w.gpitch;
+        g.M = g.N = (int)m;
+        g.num_kb = blocks(tall ? rows : cols, kGK);
+        g.width = 16;
+        g.times = i == 0 ? 2 : 0;
+        g.alpha = two(t.g - 2 * t.x);
+        g.tiles = OrthoTiles{blocks(m, 256), blocks(m, nt), 256 / nt};
+        rc = tall ? product(true, true, x64[now], x64[now], g) : product(false, false, x128[now], narrow ? x64[now] : x128[now], g);
+        if (rc) return rc;
+        // P = a I + b A + c A A
+        g.out = P;
+        g.mat = G;
+        g.num_kb = blocks(m, kGK);
+        g.times = 0;
+        g.alpha = t.c * two(t.p - 2 * t.g);
+        g.beta = t.b * two(t.p - t.g);
+        g.diag = t.a * two(t.p);
+        if ((rc = product(false, false, g128, narrow ? g64 : g128, g))) return rc;
+        // X <- P X (X P)
+        const bool last = i + 1 == steps;
+        g.mat = nullptr;
+        g.M = (int)rows;
+        g.N = (int)cols;
+        g.times = i == 0 ? 1 : 0;
+        g.alpha = last ? scale * two(-t.p - t.x) : two(t.next - t.p - t.x);
+        g.bf16 = last;
+        g.tiles = OrthoTiles{(int)num_r, blocks(cols, nt), 0};
+        if (last) {
+            g.out = out;
+            g.ld = out_ld;
+            g.stride = rows * out_ld;
+            g.store_cols = cols;
+            const uintptr_t bits = (uintptr_t)out | (uintptr_t)(2 * out_ld) | (uintptr_t)(2 * cols);
+            g.width = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+        } else {
+            g.out = X[now ^ 1];
+            g.ld = g.store_cols = w.xpitch;
+            g.stride = rows * w.xpitch;
+        }
+        rc = tall ? product(false, false, x128[now], narrow ? p64 : p128, g) : product(false, true, p128, x64[now], g);
+        if (rc) return rc;
+    }
+    return 0;
+}
+
+}  // namespace c3

@@ -1,0 +1,113 @@
+// ortho_plan.h -- how an orthogonalisation is laid out and scaled (ortho.cu has the
+// kernels).  Host arithmetic alone, so that it can be checked without a GPU.
+#pragma once
+
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+
+namespace c3 {
+
+constexpr int kOrthoSteps = 32;        // polynomials at most
+constexpr int kOrthoTop = 13;          // stored values stay below 2^13 times their bound: 8 times below fp16's largest
+constexpr double kOrthoMost = 1 << 20; // the largest singular value that an iterate may reach
+
+// One step: X <- (a + b X X^T + c X X^T X X^T) X.  Matrices are held in fp16 times powers of two,
+// 2^x, 2^g and 2^p for X, X X^T and the polynomial, so that the largest entry they can have stays
+// well below fp16's range and small ones keep their digits; next: the power for the X that the step makes.
+struct OrthoStep {
+    float a, b, c;
+    int x, g, p, next;
+};
+
+// The power of two that takes `bound` below 2^kOrthoTop.
+inline int ortho_power(double bound) {
+    int e = 0;
+    std::frexp(bound > 1.0 / kOrthoMost ? bound : 1.0 / kOrthoMost, &e);
+    return kOrthoTop - e;
+}
+
+// Entries of a matrix are at most its largest singular value.  Those of X are at most 1 after the
+// division by the norm, and a step takes s to s |a + b s^2 + c s^4|: bounds of it, and of the
+// polynomial, over 0..s.  False where the iterates may grow past kOrthoMost.
+inline bool ortho_steps(const float (*coeffs)[3], int steps, OrthoStep* out) {
+    double top = 1.0;
+    for (int i = 0; i < steps; ++i) {
+        const double a = coeffs[i][0], b = coeffs[i][1], c = coeffs[i][2], q = top * top;
+        auto poly = [&](double t) { return std::fabs(a + b * t + c * t * t); };
+        auto image = [&](double t) { return std::sqrt(t) * poly(t); };
+        double pmax = std::fmax(poly(0), poly(q)), smax = image(q);
+        if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < q) pmax = std::fmax(pmax, poly(-b / (2 * c)));
+        // a + 3 b t + 5 c t^2 = 0, t = s^2
+        const double disc = 9 * b * b - 20 * a * c;
+        double roots[2] = {-1, -1};
+        if (c != 0 && disc >= 0) {
+            roots[0] = (-3 * b + std::sqrt(disc)) / (10 * c);
+            roots[1] = (-3 * b - std::sqrt(disc)) / (10 * c);
+        } else if (c == 0 && b != 0) {
+            roots[0] = -a / (3 * b);
+        }
+        for (double t : roots)
+            if (t > 0 && t < q) smax = std::fmax(smax, image(t));
+        OrthoStep& s = out[i];
+        s.a = coeffs[i][0], s.b = coeffs[i][1], s.c = coeffs[i][2];
+        s.x = ortho_power(top);
+        s.g = ortho_power(q);
+        s.p = ortho_power(pmax);
+        // values rounded to 11 bits are up to 2^-11 off what the bound was found for, four times over
+        // values rounded to 11 bits are up to 2^-11 off, four times over, what the bound was found for
+        top = 1.002 * smax;
+        if (!(top <= kOrthoMost) || !(pmax <= kOrthoMost)) return false;
+        s.next = ortho_power(top);
+    }
+    return true;
+}
+
+// Upper triangle of a symmetric product, diagonal included, in tiles of 256 x cols: row block i has
+// the columns' blocks from i * 256 / cols on.
+struct OrthoTiles {
+    int rows, cols;  // blocks
+    int skip;        // 256 / width of a column block; 0: every tile
+#ifdef __CUDACC__
+    __host__ __device__
+#endif
+    int64_t before(int i) const { return (int64_t)i * cols - (int64_t)skip * i * (i - 1) / 2; }
+    int64_t total() const {
+        int64_t t = 0;
+        for (int i = 0; i < rows; ++i) t += cols - (int64_t)skip * i > 0 ? cols - (int64_t)skip * i : 0;
+        return t;
+    }
+};
+
+// The workspace: where each part begins, in bytes; pitches in elements.
+struct OrthoWork {
+    int64_t xpitch, gpitch, short_side;
+    size_t scale, sums, x0, x1, g, p, bytes;
+};
+
+constexpr int kOrthoParts = 512;  // partial sums of a matrix's norm at most
+
+inline OrthoWork ortho_work(int64_t rows, int64_t cols, int count) {
+    OrthoWork w;
+    w.short_side = rows < cols ? rows : cols;
+    w.xpitch = (cols + 7) / 8 * 8;
+    w.gpitch = (w.short_side + 7) / 8 * 8;
+    size_t at = 0;
+    auto part = [&](size_t bytes) {
+        const size_t from = at;
+        at += (bytes + 255) / 256 * 256;
+        return from;
+    };
+    w.scale = part((size_t)count * sizeof(float));
+    w.sums = part((size_t)count * kOrthoParts * 3 * sizeof(double));
+    const size_t x = (size_t)count * (size_t)rows * (size_t)w.xpitch * 2;
+    const size_t g = (size_t)count * (size_t)w.short_side * (size_t)w.gpitch * 2;
+    w.x0 = part(x);
+    w.x1 = part(x);
+    w.g = part(g);
+    w.p = part(g);
+    w.bytes = at;
+    return w;
+}
+
+}  // namespace c3

@@ -1,0 +1,241 @@
+"""The orthogonalisation on the GPU, against the same recurrence in 64 bits.
+
+Tolerances (h = 2^-8 and f = 2^-11, half a step of bf16 and fp16 relative to the value).  One step, entry by entry:
+A = X X^T is off by f |A| and, summed in fp32 over K, by K 2^-23 |X| |X|^T at most; P by |b| dA + |c| (dA |A| + |A| dA)
+and f |P| and its own sums' m 2^-23 |c| |A| |A|; the result by dP |X| + |P| dX and K 2^-23 |P| |X|, where dX is f |X|
+for fp32 inputs and 0 for bf16, and by h of itself.  Several steps, in the 2-norm: three roundings a step of f at most
+each, independent of one another, each carried on by a factor of at most 3.4445, the quintic's steepest slope on the
+singular values that it leaves: 3.4445 f sqrt(3 steps), and h for the output."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_ops import Guarded, c3, f64  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+H, F, U = 2.0 ** -8, 2.0 ** -11, 2.0 ** -24
+TD = {0: torch.float32, 1: torch.bfloat16}
+QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def oracle(u, coeffs, eps=1e-7):
+    """The recurrence on one matrix (float64 tensor), with the coefficients as fp32 holds them."""
+    x = u.T if u.shape[0] > u.shape[1] else u
+    x = x / (torch.linalg.vector_norm(x) + float(np.float32(eps)))
+    for a, b, c in np.asarray(coeffs, np.float32).astype(np.float64):
+        g = x @ x.T
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return x.T if u.shape[0] > u.shape[1] else x
+
+
+def one_step_bound(u, coeffs, exact_input):
+    """Bound of the error of one step, entry by entry, before the output's own rounding."""
+    x = u.T if u.shape[0] > u.shape[1] else u
+    x = (x / torch.linalg.vector_norm(x)).abs()
+    a, b, c = map(abs, coeffs)
+    m, n = x.shape
+    dx = x * (0 if exact_input else F) + 2.0 ** -38  # (and what fp16's smallest steps leave, times 2^-13)
+    g = x @ x.T
+    dg = F * g + n * 2 * U * g + dx @ x.T + x @ dx.T + 2.0 ** -37
+    p = a * torch.eye(m, dtype=x.dtype, device=x.device) + b * g + c * (g @ g)
+    dp = b * dg + c * (dg @ g + g @ dg) + F * p + m * 2 * U * c * (g @ g) + 2.0 ** -34
+    d = dp @ x + p @ dx + m * 2 * U * (p @ x)
+    return d.T if u.shape[0] > u.shape[1] else d
+
+
+def momentum(rng, count, m, n, rank=3, strong=3.0):
+    x = rng.standard_normal((count, m, n))
+    r = min(rank, m, n)
+    return x + strong * rng.standard_normal((count, m, r)) @ rng.standard_normal((count, r, n))
+
+
+def run(c3, x, ty, count, rows, cols, coeffs, ld=None, out_ld=None, out=None, work=None, **kw):  # noqa: F811
+    out_ld = cols if out_ld is None else out_ld
+    if out is None:
+        out = torch.full((count, rows, out_ld), 7.0, dtype=torch.bfloat16, device="cuda")
+    if work is None:
+        work = torch.full((c3.c3_orthogonalize_bytes(rows, cols, count),), 0xC3, dtype=torch.uint8, device="cuda")
+    c3.c3_orthogonalize(x, ty, rows, cols, out, work, coeffs, count=count, ld=ld, out_ld=out_ld, **kw)
+    return out
+
+
+SHAPES = [(1, 1), (1, 9), (9, 1), (2, 2), (8, 8), (7, 100), (100, 7), (64, 64), (127, 129), (128, 256), (129, 127),
+          (255, 300), (256, 256), (300, 255), (257, 1000), (520, 257), (600, 640), (1000, 1000)]
+
+
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_one_step(c3, ty, rows, cols):  # noqa: F811
+    rng = np.random.default_rng(rows * 3 + cols)
+    x = torch.from_numpy(momentum(rng, 1, rows, cols)).cuda().to(TD[ty])
+    scale = float(np.float32(1.3))
+    for coeffs in (QUINTIC, (1.5, -0.5, 0.0), (0.0, 2.0, 0.0), (0.0, 0.0, -3.0), (1.0, 0.0, 0.0)):
+        out = run(c3, x, ty, 1, rows, cols, [coeffs], scale=scale)
+        u = x[0].double()
+        ref = scale * oracle(u, [coeffs])
+        tol = scale * one_step_bound(u, coeffs, ty == 1) + H * ref.abs() + 1e-30
+        assert ((out[0].double() - ref).abs() <= tol * (1 + 1e-6)).all(), coeffs
+    c3.c3_status_check()
+
+
+def relative(out, ref):
+    return float(torch.linalg.vector_norm(out.double() - ref) / torch.linalg.vector_norm(ref))
+
+
+@pytest.mark.parametrize("ty,count,rows,cols,pad,out_pad,steps", [
+    (1, 1, 64, 64, 0, 0, 5), (0, 1, 200, 300, 0, 0, 5), (1, 3, 300, 200, 0, 0, 5), (0, 2, 129, 515, 3, 5, 5),
+    (1, 2, 515, 129, 8, 8, 6), (1, 5, 96, 1000, 4, 2, 3), (0, 1, 1000, 1000, 0, 0, 2), (1, 1, 1531, 700, 1, 1, 5),
+    (0, 7, 40, 33, 0, 7, 5), (1, 1, 2304, 2200, 0, 0, 4), (1, 40, 256, 264, 0, 0, 5), (0, 1, 700, 5001, 0, 0, 5),
+    (1, 1, 5000, 520, 0, 0, 5)])
+def test_several_steps(c3, ty, count, rows, cols, pad, out_pad, steps):  # noqa: F811
+    rng = np.random.default_rng(rows + cols)
+    ld, out_ld = cols + pad, cols + out_pad
+    g = Guarded((count, rows, ld), TD[ty])
+    g.t.copy_(torch.from_numpy(momentum(rng, count, rows, ld)))
+    keep = g.t.clone()
+    out = Guarded((count, rows, out_ld), torch.bfloat16, 7.0)
+    work = Guarded((c3.c3_orthogonalize_bytes(rows, cols, count),), torch.uint8, 0xC3)
+    run(c3, g.t, ty, count, rows, cols, [QUINTIC] * steps, ld=ld, out_ld=out_ld, out=out.t, work=work.t)
+    c3.c3_status_check()
+    for i in range(count):
+        ref = oracle(g.t[i, :, :cols].double(), [QUINTIC] * steps)
+        assert relative(out.t[i, :, :cols], ref) <= 3.4445 * F * (3 * steps) ** 0.5 + H
+    assert (out.t[:, :, cols:] == 7).all() and torch.equal(g.t, keep)
+    assert out.intact() and work.intact() and g.intact()
+    again = run(c3, g.t, ty, count, rows, cols, [QUINTIC] * steps, ld=ld, out_ld=out_ld)
+    assert torch.equal(again[:, :, :cols], out.t[:, :, :cols])
+
+
+def test_error_before_the_output_is_rounded(c3):  # noqa: F811
+    """Roundings spread evenly over their steps are off by f / sqrt(3) in the square mean, so what they add up to is
+    below 3.4445 f sqrt(3 steps / 3), 3.8e-3 for five steps.  Independent errors add up in squares, so the
+    output's own rounding, found on the oracle, is taken off that way."""
+    rng = np.random.default_rng(0)
+    for rows, cols in ((1024, 1024), (512, 2048), (3000, 700)):
+        x = torch.from_numpy(momentum(rng, 1, rows, cols, rank=8, strong=1.0)).cuda().to(torch.bfloat16)
+        out = run(c3, x, 1, 1, rows, cols, [QUINTIC] * 5)[0].double()
+        ref = oracle(x[0].double(), [QUINTIC] * 5)
+        own, both = relative(ref.to(torch.bfloat16).double(), ref), relative(out, ref)
+        print(rows, cols, own, both)
+        assert both ** 2 - own ** 2 <= (3.4445 * F) ** 2 * 5, (rows, cols, own, both)
+
+
+def test_singular_values_near_one(c3):  # noqa: F811
+    rng = np.random.default_rng(4)
+    q, _ = np.linalg.qr(rng.standard_normal((300, 200)))
+    x = torch.from_numpy(q).cuda().float().unsqueeze(0) * 17
+    out = run(c3, x, 0, 1, 300, 200, [(1.5, -0.5, 0.0)] * 12 )
+    # all singular values alike, 1 / sqrt(200) after the norm: the cubic takes them to 1 within twelve steps
+    assert relative(out[0], torch.from_numpy(q).cuda()) <= 3.4445 * F * 6 + H
+
+
+def test_magnitudes(c3):  # noqa: F811
+    """The norm takes any magnitude out, as far as eps lets it."""
+    rng = np.random.default_rng(8)
+    x = momentum(rng, 1, 70, 90)
+    ref = None
+    for power in (0, 60, -60, 115, -120):
+        u = torch.from_numpy(x * 2.0 ** power).cuda().float()
+        out = run(c3, u, 0, 1, 70, 90, [QUINTIC] * 5, eps=0.0)
+        ref = out if ref is None else ref
+        assert torch.equal(out, ref), power  # powers of two: the same bits
+    # eps of the norm's size halves what the first step starts from
+    u = torch.from_numpy(x).cuda().float()
+    norm = float(torch.linalg.vector_norm(u.double()))
+    out = run(c3, u, 0, 1, 70, 90, [QUINTIC] * 2, eps=norm)
+    assert relative(out[0], oracle(u[0].double(), [QUINTIC] * 2, eps=norm)) <= 3.4445 * F * 6 ** 0.5 + H
+    # values whose squares fp32 cannot hold, beside ordinary ones
+    u[0, 0, 0] = 3e38
+    out = run(c3, u, 0, 1, 70, 90, [QUINTIC] * 5)
+    ref = oracle(u[0].double(), [QUINTIC] * 5)
+    assert relative(out[0], ref) <= 3.4445 * F * 15 ** 0.5 + H
+    # subnormal numbers
+    u = torch.full((1, 3, 5), 1e-42, device="cuda")
+    out = run(c3, u, 0, 1, 3, 5, [QUINTIC] * 5, eps=0.0)
+    assert relative(out[0], oracle(u[0].double(), [QUINTIC] * 5, eps=0.0)) <= 3.4445 * F * 15 ** 0.5 + H
+
+
+def test_zeros_and_what_is_not_finite(c3):  # noqa: F811
+    rng = np.random.default_rng(6)
+    for rows, cols in ((40, 70), (270, 140)):
+        x = torch.from_numpy(momentum(rng, 6, rows, cols)).cuda().to(torch.bfloat16)
+        clean = run(c3, x, 1, 6, rows, cols, [QUINTIC] * 5)
+        x[1], x[2, rows - 1, cols - 1], x[4, 0, 3] = 0, float("nan"), -float("inf")
+        out = run(c3, x, 1, 6, rows, cols, [QUINTIC] * 5)
+        assert (out[1] == 0).all() and out[2].isnan().all() and out[4].isnan().all()
+        for i in (0, 3, 5):
+            assert torch.equal(out[i], clean[i])
+        out = run(c3, x[1:2], 1, 1, rows, cols, [QUINTIC] * 5, eps=0.0)
+        assert (out == 0).all()
+        x[3, 5:] = 0  # of low rank, rows of zeros
+        out = run(c3, x, 1, 6, rows, cols, [QUINTIC] * 5)
+        assert (out[3, 5:] == 0).all()
+        assert relative(out[3], oracle(x[3].double(), [QUINTIC] * 5)) <= 3.4445 * F * 15 ** 0.5 + H
+
+
+def test_in_place_on_a_stream_and_in_a_graph(c3):  # noqa: F811
+    rng = np.random.default_rng(2)
+    rows, cols = 390, 520
+    xs = [torch.from_numpy(momentum(rng, 2, rows, cols)).cuda().to(torch.bfloat16) for _ in range(3)]
+    want = [run(c3, x, 1, 2, rows, cols, [QUINTIC] * 5) for x in xs]
+    size = c3.c3_orthogonalize_bytes(rows, cols, 2)
+    work, other = (torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2))
+    x, side, graph = xs[0].clone(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        c3.c3_orthogonalize(x, 1, rows, cols, x, work, [QUINTIC] * 5, count=2, stream=torch.cuda.current_stream())
+    for k in (1, 2, 0):
+        x.copy_(xs[k])
+        y = xs[(k + 1) % 3].clone()
+        torch.cuda.synchronize()
+        graph.replay()
+        c3.c3_orthogonalize(y, 1, rows, cols, y, other, [QUINTIC] * 5, count=2, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(x, want[k]) and torch.equal(y, want[(k + 1) % 3])
+    c3.c3_status_check()
+
+
+@pytest.mark.parametrize("budget", [2, 3, 16, 150, 1000])
+def test_budgets_change_nothing(c3, budget):  # noqa: F811
+    rng = np.random.default_rng(11)
+    x = torch.from_numpy(momentum(rng, 2, 700, 900)).cuda().to(torch.bfloat16)
+    u = x.double()
+    out = run(c3, x, 1, 2, 700, 900, [QUINTIC] * 5, sm_budget=budget)
+    for i in range(2):
+        assert relative(out[i], oracle(u[i], [QUINTIC] * 5)) <= 3.4445 * F * 15 ** 0.5 + H
+    c3.c3_status_check()
+
+
+def test_past_32_bits(c3):  # noqa: F811
+    """A stack of matrices whose elements pass 2^31, one step each."""
+    count, rows, cols = 17, 8192, 16384  # 2.28 G elements
+    x = torch.zeros(count, rows, cols, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    for i in (0, 15, 16):
+        x[i, :300, -200:] = torch.randn(300, 200, generator=gen, device="cuda").to(torch.bfloat16)
+        x[i, -100:, :50] = torch.randn(100, 50, generator=gen, device="cuda").to(torch.bfloat16)
+    out = run(c3, x, 1, count, rows, cols, [QUINTIC])
+    c3.c3_status_check()
+    for i in (0, 15, 16):
+        # two blocks that share no rows or columns: each is a product of its own, with the whole matrix's norm
+        norm = torch.linalg.vector_norm(x[i].double()) + 1e-7
+        for r, c in ((slice(0, 300), slice(cols - 200, cols)), (slice(rows - 100, rows), slice(0, 50))):
+            u = x[i, r, c].double() / norm
+            a, b, q = np.asarray(QUINTIC, np.float32).astype(np.float64)
+            ref = a * u + b * (u @ (u.T @ u)) + q * (u @ (u.T @ u) @ (u.T @ u))
+            assert relative(out[i, r, c], ref) <= 3.4445 * F * 3 ** 0.5 + H
+        assert (out[i, 300:-100] == 0).all() and (out[i, :300, :-200] == 0).all() and (out[i, -100:, 50:] == 0).all()
+    for i in range(1, 15):
+        assert not out[i].any()
+
+
+def test_an_injected_launch_failure_is_reported(c3):  # noqa: F811
+    x = torch.ones(1, 8, 8, dtype=torch.bfloat16, device="cuda")
+    c3.c3_inject_fault(c3.C3_FAULT_GEMM_LAUNCH)
+    with pytest.raises(c3.C3Error) as e:
+        run(c3, x, 1, 1, 8, 8, [QUINTIC])
+    assert e.value.status == c3.C3_ECUDA and "injected" in str(e.value)
+    run(c3, x, 1, 1, 8, 8, [QUINTIC])
+    c3.c3_status_check()
