@@ -38,15 +38,21 @@ struct OrthoIn {
     int count, parts;
     double eps;
     int power;  // 2^power: X's first scale
-    double* sums;
+    float* sums;
     float* scale;
     __half* out;
     int64_t pitch;
 };
 
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
 template <typename T, int W>
 __global__ void __launch_bounds__(kOrthoThreads) ortho_norm_kernel(OrthoIn g) {
-    __shared__ double part[3][kOrthoWarps];
+    __shared__ float part[3][kOrthoWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t spans = (g.cols + kOrthoSpan - 1) / kOrthoSpan, jobs = g.rows * spans;
     constexpr int U = kOrthoSpan / (32 * W);
@@ -72,18 +78,15 @@ __global__ void __launch_bounds__(kOrthoThreads) ortho_norm_kernel(OrthoIn g) {
                     high = fmaf(h, h, high);
                 }
         }
-        double s[3] = {low, mid, high};
+        float s[3] = {low, mid, high};
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(kAll, s[k], o);
+            s[k] = warp_sum(s[k]);
             if (lane == 0) part[k][warp] = s[k];
         }
         __syncthreads();
         if (warp < 3) {
-            double t = part[warp][lane];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(kAll, t, o);
+            const float t = warp_sum(part[warp][lane]);
             if (lane == 0) g.sums[(m * g.parts + p) * 3 + warp] = t;
         }
         __syncthreads();
@@ -95,7 +98,6 @@ __global__ void __launch_bounds__(kOrthoThreads) ortho_norm_kernel(OrthoIn g) {
 // infinity makes the whole matrix NaN.
 template <typename T, int W>
 __global__ void __launch_bounds__(kOrthoThreads) ortho_convert_kernel(OrthoIn g) {
-    __shared__ double part[3][kOrthoWarps];
     __shared__ float factors[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t spans = (g.pitch + kOrthoSpan - 1) / kOrthoSpan, jobs = g.rows * spans;
@@ -103,24 +105,14 @@ __global__ void __launch_bounds__(kOrthoThreads) ortho_convert_kernel(OrthoIn g)
     chain_wait();
     for (int64_t i = blockIdx.x; i < (int64_t)g.count * g.parts; i += gridDim.x) {
         const int64_t m = i / g.parts, p = i - m * g.parts;
-        double s[3] = {};
-        for (int j = threadIdx.x; j < g.parts; j += kOrthoThreads)
-#pragma unroll
-            for (int k = 0; k < 3; ++k) s[k] += g.sums[(m * g.parts + j) * 3 + k];
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(kAll, s[k], o);
-            if (lane == 0) part[k][warp] = s[k];
-        }
-        __syncthreads();
         if (warp == 0) {
+            float s[3] = {};
+#pragma unroll 4
+            for (int j = lane; j < g.parts; j += 32)
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                s[k] = part[k][lane];
+                for (int k = 0; k < 3; ++k) s[k] += g.sums[(m * g.parts + j) * 3 + k];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(kAll, s[k], o);
-            }
+            for (int k = 0; k < 3; ++k) s[k] = warp_sum(s[k]);
             if (lane == 0) {
                 const double one = 2.0 * 1180591620717411303424.0 * 590295810358705651712.0;  // 2^140
                 double sum = s[1];
@@ -308,11 +300,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    chain_wait();
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();  // both CTAs' barriers are ready before either signals the other's
     tc_fence_after();
+    chain_wait();
     const uint32_t tmem = *tmem_slot;
     const int64_t total = g.per_matrix * g.count, first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
@@ -561,7 +553,7 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
     in.count = count;
     in.eps = eps;
     in.power = step[0].x;
-    in.sums = reinterpret_cast<double*>(base + w.sums);
+    in.sums = reinterpret_cast<float*>(base + w.sums);
     in.scale = reinterpret_cast<float*>(base + w.scale);
     in.out = reinterpret_cast<__half*>(base + w.x0);
     in.pitch = w.xpitch;

@@ -28,7 +28,7 @@ def test_workspace_sizes(c3):
     for m, n, k in ((1, 1, 1), (5, 9, 3), (300, 77, 2), (4096, 4096, 1)):
         s = min(m, n)
         need = k * (2 * m * -(-n // 8) * 16 + 2 * s * -(-s // 8) * 16)
-        assert need <= size(m, n, k) <= need + k * 512 * 24 + 4 * k + 2048, (m, n, k)
+        assert need <= size(m, n, k) <= need + k * 512 * 12 + 4 * k + 2048, (m, n, k)
 
 
 def test_refusals(c3):
