@@ -13,101 +13,94 @@ constexpr int kEmbedThreads = 256;
 constexpr int kEmbedWarps = kEmbedThreads / 32;
 constexpr int kSpan = 256;  // columns a warp takes of a row at once, 8 a lane
 
-// ---------------------------------------------------------------- rows wherever they begin
+// ---------------------------------------------------------------- a warp's part of a row
 //
-// A lane's 8 values of a row are 16 or 32 bytes.  Where every row begins at a multiple of 16 bytes
-// and has whole vectors (SHIFT false) they are loaded and stored as they are.  Elsewhere a row's
-// aligned 16-byte units are: loads take the units that hold a lane's values, one more than they
-// fill, and shift them into place; stores shift the values on by what the row is off, the lane
-// before lending its last ones, and write whole units but for the row's ends.  A unit is touched
-// only where it holds a value of the row.
+// A warp holds kSpan consecutive values of a row, 8 a lane: W neighbours of them, and again 32 W
+// further on, so that every load and store of the warp is one run of W * 32 values.  W is what
+// every row's beginning, and its length, are a multiple of: 16 bytes at most.
 
-template <typename T, bool SHIFT>
-struct Units {
-    static constexpr int kCount = (int)sizeof(T) / 2 + (SHIFT ? 1 : 0);
-    uint4 v[kCount];
-};
+template <int BYTES>
+struct WordOf;
+template <>
+struct WordOf<2> { using type = uint16_t; };
+template <>
+struct WordOf<4> { using type = uint32_t; };
+template <>
+struct WordOf<8> { using type = uint2; };
+template <>
+struct WordOf<16> { using type = uint4; };
 
-// The units of the 8 values from p on, of a row that ends at `end`.
-template <typename T, bool SHIFT>
-__device__ __forceinline__ void load_units(const T* p, const T* end, Units<T, SHIFT>& r) {
-    const uintptr_t at = SHIFT ? (uintptr_t)p & ~(uintptr_t)15 : (uintptr_t)p;
-#pragma unroll
-    for (int i = 0; i < Units<T, SHIFT>::kCount; ++i)
-        r.v[i] = at + 16 * i < (uintptr_t)end ? *reinterpret_cast<const uint4*>(at + 16 * i) : make_uint4(0, 0, 0, 0);
-}
+template <typename T, int W>
+struct Part {
+    using Word = typename WordOf<W * (int)sizeof(T)>::type;
+    Word w[8 / W];
 
-// w moved down by `bytes` (whole values of T).
-template <typename T, int N>
-__device__ __forceinline__ void shift_words(uint32_t (&w)[N], int bytes) {
+    // from p, the place of this lane's first value; n: the row's values from there on.  FULL: all are there.
+    template <bool FULL>
+    __device__ __forceinline__ void load(const T* p, int n) {
 #pragma unroll
-    for (int step = 16; step >= 4; step /= 2)
-        if (bytes & step) {
-#pragma unroll
-            for (int i = 0; i + step / 4 < N; ++i) w[i] = w[i + step / 4];
-        }
-    if (sizeof(T) == 2 && (bytes & 2)) {
-#pragma unroll
-        for (int i = 0; i + 1 < N; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        for (int q = 0; q < 8 / W; ++q)
+            if (FULL || q * 32 * W < n) w[q] = *reinterpret_cast<const Word*>(p + q * 32 * W);
     }
-}
-
-template <typename T, bool SHIFT>
-__device__ __forceinline__ void unit_values(const Units<T, SHIFT>& r, const T* p, float (&v)[8]) {
-    uint32_t w[4 * Units<T, SHIFT>::kCount];
+    __device__ __forceinline__ void values(float (&v)[8]) const {
 #pragma unroll
-    for (int i = 0; i < Units<T, SHIFT>::kCount; ++i) w[4 * i] = r.v[i].x, w[4 * i + 1] = r.v[i].y, w[4 * i + 2] = r.v[i].z, w[4 * i + 3] = r.v[i].w;
-    if constexpr (SHIFT) shift_words<T>(w, (int)((uintptr_t)p & 15));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
-        else v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-    }
-}
-
-// The warp's values of a row, n of them (kSpan at most); p: the place of this lane's first.
-template <typename T, bool SHIFT>
-__device__ __forceinline__ void store_values(T* p, const float (&v)[8], int n, int lane) {
-    constexpr int NW = 2 * (int)sizeof(T), VB = 16 / (int)sizeof(T);
-    uint32_t w[NW + 4];
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-        if constexpr (sizeof(T) == 4) {
-            w[4 + i] = __float_as_uint(v[i]);
-        } else {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[4 + i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-    }
-    if constexpr (!SHIFT) {
-        if (8 * lane >= n) return;
-#pragma unroll
-        for (int j = 0; j < NW / 4; ++j)
-            reinterpret_cast<uint4*>(p)[j] = make_uint4(w[4 + 4 * j], w[5 + 4 * j], w[6 + 4 * j], w[7 + 4 * j]);
-    } else {
-        using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
-        const int off = (int)((uintptr_t)p & 15), k = off / (int)sizeof(T);
-        auto value = [&](const uint32_t* x, int i) { return (Bits)(sizeof(T) == 4 ? x[i] : x[i / 2] >> (16 * (i & 1))); };
-        if (lane == 31) {  // what is left behind the last whole unit
-#pragma unroll
-            for (int i = 8 - VB + 1; i < 8; ++i)
-                if (i >= 8 - k && 248 + i < n) reinterpret_cast<Bits*>(p)[i] = value(w + 4, i);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(kAll, w[NW + i], 1);
-        shift_words<T>(w, 16 - off);
-#pragma unroll
-        for (int j = 0; j < NW / 4; ++j) {
-            const int first = 8 * lane - k + j * VB;
-            Bits* at = reinterpret_cast<Bits*>(p) + (j * VB - k);
-            if (first >= 0 && first + VB <= n) {
-                *reinterpret_cast<uint4*>(at) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        for (int q = 0; q < 8 / W; ++q) {
+            if constexpr (W * sizeof(T) == 2) {
+                v[q] = __uint_as_float((uint32_t)w[q] << 16);
             } else {
+                uint32_t u[4];
+                if constexpr (W * sizeof(T) == 4) u[0] = w[q];
+                else u[0] = w[q].x, u[1] = w[q].y;
+                if constexpr (W * sizeof(T) == 16) u[2] = w[q].z, u[3] = w[q].w;
 #pragma unroll
-                for (int i = 0; i < VB; ++i)
-                    if (first + i >= 0 && first + i < n) at[i] = value(w + 4 * j, i);
+                for (int i = 0; i < W; ++i) {
+                    if constexpr (sizeof(T) == 4) v[q * W + i] = __uint_as_float(u[i]);
+                    else v[q * W + i] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+                }
             }
         }
+    }
+    template <bool FULL>
+    __device__ __forceinline__ static void store(T* p, int n, const float (&v)[8]) {
+#pragma unroll
+        for (int q = 0; q < 8 / W; ++q) {
+            if (!FULL && q * 32 * W >= n) continue;
+            if constexpr (W * sizeof(T) == 2) {
+                p[q * 32] = __float2bfloat16_rn(v[q]);
+            } else {
+                uint32_t u[4];
+#pragma unroll
+                for (int i = 0; i < W * (int)sizeof(T) / 4; ++i) {
+                    if constexpr (sizeof(T) == 4) {
+                        u[i] = __float_as_uint(v[q * W + i]);
+                    } else {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[q * W + 2 * i], v[q * W + 2 * i + 1]);
+                        u[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                }
+                Word x;
+                if constexpr (W * sizeof(T) == 4) x = u[0];
+                else x.x = u[0], x.y = u[1];
+                if constexpr (W * sizeof(T) == 16) x.z = u[2], x.w = u[3];
+                *reinterpret_cast<Word*>(p + q * 32 * W) = x;
+            }
+        }
+    }
+};
+
+// Single bf16 values, stored in pairs: lane l has values 32 i + l, i < 8, of the piece from column c0 on of a row of
+// `cols`, at least one pair of which is aligned to 4 bytes at an even lane.  Lanes of a pair trade half their values.
+__device__ __forceinline__ void store_pairs(__nv_bfloat16* row, int64_t c0, int64_t cols, const float (&v)[8], int lane) {
+    const bool odd = lane & 1;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float got = __shfl_xor_sync(kAll, odd ? v[i] : v[i + 1], 1);
+        const float lo = odd ? got : v[i], hi = odd ? v[i + 1] : got;
+        const int64_t c = c0 + 32 * (i + odd) + (lane & ~1);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        if (c >= 0 && c + 1 < cols) *reinterpret_cast<__nv_bfloat162*>(row + c) = h;
+        else if (c >= 0 && c < cols) row[c] = h.x;
+        else if (c + 1 >= 0 && c + 1 < cols) row[c + 1] = h.y;
     }
 }
 
@@ -115,48 +108,76 @@ __device__ __forceinline__ void store_values(T* p, const float (&v)[8], int n, i
 
 // out[t] = scale * table[ids[t] - first], zeros where that is no row.  A warp takes kAhead pieces
 // of kSpan columns, of one token or of several, whose loads are all in flight before the first is used.
+//
+// Rows of bf16 of odd length: pieces of a row that begins at no multiple of 4 bytes begin one column
+// before, so that pairs of values are aligned where they are stored.
 constexpr int kAhead = 4;
 
-template <typename Tt, typename To, bool SHIFT>
+template <typename Tt, typename To, int W>
 __global__ void __launch_bounds__(kEmbedThreads)
     embed_kernel(const Tt* __restrict__ table, int64_t rows, int64_t cols, int64_t ld, int64_t first,
                  const int32_t* __restrict__ ids, int64_t tokens, float scale, To* __restrict__ out, int64_t out_ld) {
+    constexpr bool kPairs = W == 1 && sizeof(To) == 2;
     const int lane = threadIdx.x & 31;
-    const int64_t spans = (cols + kSpan - 1) / kSpan, jobs = tokens * spans;
+    const int64_t spans = (cols + (kPairs ? 1 : 0) + kSpan - 1) / kSpan, jobs = tokens * spans;
     chain_wait();
     for (int64_t job = ((int64_t)blockIdx.x * kEmbedWarps + (threadIdx.x >> 5)) * kAhead; job < jobs;
          job += (int64_t)gridDim.x * kEmbedWarps * kAhead) {
-        Units<Tt, SHIFT> raw[kAhead];
-        const Tt* from[kAhead];
-        int64_t t[kAhead], c[kAhead];
-        int id[kAhead];
-        t[0] = job / spans;
-        c[0] = job - t[0] * spans;
+        Part<Tt, W> part[kAhead];
+        int t[kAhead], span[kAhead], id[kAhead];
+        bool have[kAhead];
+        t[0] = (int)(job / spans);
+        span[0] = (int)(job - t[0] * spans);
 #pragma unroll
         for (int u = 1; u < kAhead; ++u) {
-            const bool over = c[u - 1] + 1 == spans;
+            const bool over = span[u - 1] + 1 == spans;
             t[u] = t[u - 1] + over;
-            c[u] = over ? 0 : c[u - 1] + 1;
+            span[u] = over ? 0 : span[u - 1] + 1;
         }
+        // the piece's first column
+        auto column = [&](int u) {
+            const int64_t c = (int64_t)span[u] * kSpan;
+            return kPairs && ((uintptr_t)(out + t[u] * out_ld) & 2) ? c - 1 : c;
+        };
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) id[u] = t[u] < tokens ? ids[t[u]] : -1;
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int64_t r = (int64_t)id[u] - first, col = c[u] * kSpan + lane * 8;
-            from[u] = nullptr;
-            if (r < 0 || r >= rows || col >= cols) continue;
-            from[u] = table + r * ld + col;
-            load_units<Tt, SHIFT>(from[u], table + r * ld + cols, raw[u]);
+            const int64_t r = (int64_t)id[u] - first;
+            have[u] = r >= 0 && r < rows;
+            if constexpr (kPairs) {
+                const int64_t at = column(u) + lane;
+                if (have[u]) {
+                    const Tt* from = table + r * ld + at;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (at + 32 * q >= 0 && at + 32 * q < cols)
+                            part[u].w[q] = *reinterpret_cast<const typename Part<Tt, 1>::Word*>(from + 32 * q);
+                }
+            } else {
+                const int64_t left = cols - column(u);
+                const Tt* from = table + r * ld + column(u) + lane * W;
+                if (have[u] && left >= kSpan) part[u].template load<true>(from, 0);
+                else if (have[u]) part[u].template load<false>(from, (int)left - lane * W);
+            }
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (t[u] >= tokens) break;
             float v[8] = {};
-            if (from[u]) unit_values<Tt, SHIFT>(raw[u], from[u], v);
+            if (have[u]) {
+                part[u].values(v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = from[u] ? v[i] * scale : 0.0f;
-            const int64_t left = cols - c[u] * kSpan;
-            store_values<To, SHIFT>(out + t[u] * out_ld + c[u] * kSpan + lane * 8, v, (int)(left < kSpan ? left : kSpan), lane);
+                for (int i = 0; i < 8; ++i) v[i] *= scale;
+            }
+            if constexpr (kPairs) {
+                store_pairs(out + t[u] * out_ld, column(u), cols, v, lane);
+            } else {
+                const int64_t left = cols - column(u);
+                To* to = out + t[u] * out_ld + column(u) + lane * W;
+                if (left >= kSpan) Part<To, W>::template store<true>(to, 0, v);
+                else Part<To, W>::template store<false>(to, (int)left - lane * W, v);
+            }
         }
     }
 }
@@ -172,6 +193,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortBits = 10;  // a digit at most: a thread a bin in the scans
 constexpr int kSortCtas = 8;
+constexpr int kFew = 32;       // tokens of a row that is never cut: a chunk's length at least, a warp's lanes at most
 constexpr int kSortAhead = 8;  // pairs a lane holds: up to 65536 tokens are read once a pass
 
 // What the sort leaves for the sums.
@@ -187,11 +209,11 @@ __device__ __forceinline__ int remote_int(uint32_t addr) {
 }
 
 // pairs: where the sorted (row, token) end up; other: as much scratch.  joins: numbers of the chunks
-// (of `chunk` places) whose last row goes on in the next and has more than `few` tokens.
+// (of `chunk` places) whose last row goes on in the next and has more than kFew tokens.
 // touched: a bit a row of the table, or NULL.
 __global__ void __launch_bounds__(kSortThreads, 1)
     embed_sort_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t first, int64_t rows, int bits, int passes,
-                      int2* pairs, int2* other, int chunk, int few, EmbedOrder* order, int* joins, uint32_t* touched) {
+                      int2* pairs, int2* other, int chunk, EmbedOrder* order, int* joins, uint32_t* touched) {
     extern __shared__ int shared[];
     const int bins = 1 << bits;
     int* total = shared;                       // [bins] this CTA's, read by the others
@@ -233,6 +255,16 @@ __global__ void __launch_bounds__(kSortThreads, 1)
             }
         };
         auto digit = [&](int2 p) { return p.x < 0 ? -1 : (p.x >> shift) & (bins - 1); };
+        // the lanes of the same digit, a vote a bit (four times as fast as a match of all lanes)
+        auto alike = [&](int d) {
+            unsigned same = __ballot_sync(kAll, d >= 0);
+            for (int b = 0; b < bits; ++b) {
+                const unsigned one = __ballot_sync(kAll, (d >> b) & 1);
+                same &= (d >> b) & 1 ? one : ~one;
+            }
+            return same;
+        };
+        unsigned same[kSortAhead];
         for (int d = lane; d < bins; d += 32) mine_hist[d] = 0;
         __syncwarp();
         for (int64_t i0 = mine; i0 < end; i0 += 32 * kSortAhead) {
@@ -241,8 +273,8 @@ __global__ void __launch_bounds__(kSortThreads, 1)
             for (int j = 0; j < kSortAhead; ++j) {
                 if (i0 + 32 * j >= end) break;
                 const int d = digit(held[j]);
-                const unsigned same = __match_any_sync(kAll, d);
-                if (d >= 0 && (same & before_me) == 0) mine_hist[d] += __popc(same);
+                same[j] = alike(d);
+                if (d >= 0 && (same[j] & before_me) == 0) mine_hist[d] += __popc(same[j]);
                 __syncwarp();
             }
         }
@@ -296,10 +328,10 @@ __global__ void __launch_bounds__(kSortThreads, 1)
             for (int j = 0; j < kSortAhead; ++j) {
                 if (i0 + 32 * j >= end) break;
                 const int dig = digit(held[j]);
-                const unsigned same = __match_any_sync(kAll, dig);
-                if (dig >= 0) to[mine_hist[dig] + __popc(same & before_me)] = held[j];
+                if (per > 32 * kSortAhead) same[j] = alike(dig);
+                if (dig >= 0) to[mine_hist[dig] + __popc(same[j] & before_me)] = held[j];
                 __syncwarp();
-                if (dig >= 0 && (same & before_me) == 0) mine_hist[dig] += __popc(same);
+                if (dig >= 0 && (same[j] & before_me) == 0) mine_hist[dig] += __popc(same[j]);
                 __syncwarp();
             }
         }
@@ -310,7 +342,7 @@ __global__ void __launch_bounds__(kSortThreads, 1)
         const int64_t next = (p / chunk + 1) * chunk;
         const int row = __ldcg(&pairs[p].x);
         const int last = p > 0 ? __ldcg(&pairs[p - 1].x) : -1;
-        const int cut = next < valid ? __ldcg(&pairs[next].x) : -1, far = p + few < valid ? __ldcg(&pairs[p + few].x) : -1;
+        const int cut = next < valid ? __ldcg(&pairs[next].x) : -1, far = p + kFew < valid ? __ldcg(&pairs[p + kFew].x) : -1;
         if (last == row) continue;
         if (touched) atomicOr(&touched[row >> 5], 1u << (row & 31));
         if (cut == row && far == row) joins[atomicAdd(&order->joins, 1)] = (int)(p / chunk);
@@ -320,8 +352,7 @@ __global__ void __launch_bounds__(kSortThreads, 1)
 // ---------------------------------------------------------------- sums
 //
 // The sorted places are cut into chunks.  A warp adds up kSpan columns of a chunk's
-// tokens, in order.  A row of at most `few` tokens (a chunk's length, 32 at most) is the
-// business of the chunk that it begins in, wherever it ends; of a longer one that is cut,
+// tokens, in order.  A row of at most kFew tokens is the business of the chunk that it begins in, wherever it ends; of a longer one that is cut,
 // the part behind a cut goes to heads[chunk] and the part before the first to tails[chunk],
 // and embed_join_kernel adds those up, in the order of the chunks.  Rows that no token
 // names are written as zeros beside, by warps of their own.
@@ -333,43 +364,82 @@ struct EmbedSum {
     float* heads;             // [chunks][pitch]
     float* tails;
     int64_t rows, cols, ld, dout_ld, pitch;
-    int chunk, few;
+    int chunk;
     int accumulate;
     float scale;
 };
 
+// Partial sums in fp32: as the lanes hold them, W neighbours in units of 16 bytes at most.
+template <int W>
+struct Parked {
+    static constexpr int V = W < 4 ? W : 4;
+    __device__ __forceinline__ static void store(float* p, int n, const float (&v)[8]) {
+#pragma unroll
+        for (int q = 0; q < 8 / W; ++q) {
+            if (q * 32 * W >= n) continue;
+#pragma unroll
+            for (int i = 0; i < W; i += V) {
+                if constexpr (V == 4) *reinterpret_cast<float4*>(p + q * 32 * W + i) = make_float4(v[q * W + i], v[q * W + i + 1], v[q * W + i + 2], v[q * W + i + 3]);
+                else if constexpr (V == 2) *reinterpret_cast<float2*>(p + q * 32 * W + i) = make_float2(v[q * W + i], v[q * W + i + 1]);
+                else p[q * 32 * W + i] = v[q * W + i];
+            }
+        }
+    }
+    __device__ __forceinline__ static void load(const float* p, int n, float (&v)[8]) {
+#pragma unroll
+        for (int q = 0; q < 8 / W; ++q) {
+            const bool have = q * 32 * W < n;
+#pragma unroll
+            for (int i = 0; i < W; i += V) {
+                if constexpr (V == 4) {
+                    const float4 x = have ? *reinterpret_cast<const float4*>(p + q * 32 * W + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    v[q * W + i] = x.x, v[q * W + i + 1] = x.y, v[q * W + i + 2] = x.z, v[q * W + i + 3] = x.w;
+                } else if constexpr (V == 2) {
+                    const float2 x = have ? *reinterpret_cast<const float2*>(p + q * 32 * W + i) : make_float2(0.0f, 0.0f);
+                    v[q * W + i] = x.x, v[q * W + i + 1] = x.y;
+                } else {
+                    v[q * W + i] = have ? p[q * 32 * W + i] : 0.0f;
+                }
+            }
+        }
+    }
+};
+
 // table[row] (+)= scale * v: the warp's kSpan columns, of which n are there.
-template <typename Tt, bool SHIFT>
+template <typename Tt, int W>
 __device__ __forceinline__ void add_row(const EmbedSum& g, Tt* table, int row, int64_t c0, int n, const float (&v)[8], int lane) {
-    Tt* at = table + (int64_t)row * g.ld + c0 + lane * 8;
+    Tt* at = table + (int64_t)row * g.ld + c0 + lane * W;
     float o[8];
-    if (g.accumulate && 8 * lane < n) {
-        Units<Tt, SHIFT> raw;
-        load_units<Tt, SHIFT>(at, at - lane * 8 + n, raw);
-        unit_values<Tt, SHIFT>(raw, at, o);
+    if (g.accumulate) {
+        Part<Tt, W> old;
+        old.template load<false>(at, n - lane * W);
+        old.values(o);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = g.accumulate ? fmaf(g.scale, v[i], o[i]) : g.scale * v[i];
-    // (neighbours' loads share units with this lane's stores)
-    if (SHIFT) __syncwarp();
-    store_values<Tt, SHIFT>(at, o, n, lane);
+    Part<Tt, W>::template store<false>(at, n - lane * W, o);
 }
 
 // A row of zeros, by a warp.
-template <typename Tt, bool SHIFT>
+template <typename Tt, int W>
 __device__ __forceinline__ void zero_row(Tt* row, int64_t cols, int lane) {
     const float zero[8] = {};
-    for (int64_t c = 0; c < cols; c += kSpan)
-        store_values<Tt, SHIFT>(row + c + lane * 8, zero, (int)(cols - c < kSpan ? cols - c : kSpan), lane);
+    if constexpr (W == 1 && sizeof(Tt) == 2) {
+        for (int64_t c = (uintptr_t)row & 2 ? -1 : 0; c < cols; c += kSpan) store_pairs(row, c, cols, zero, lane);
+    } else {
+        int64_t c = 0;
+        for (; c + kSpan <= cols; c += kSpan) Part<Tt, W>::template store<true>(row + c + lane * W, 0, zero);
+        if (c < cols) Part<Tt, W>::template store<false>(row + c + lane * W, (int)(cols - c) - lane * W, zero);
+    }
 }
 
 // Length of the run of ones from bit 0 on.
 __device__ __forceinline__ int run_of(unsigned bits) { return bits == kAll ? 32 : __ffs(~bits) - 1; }
 
-template <typename Td, typename Tt, bool SHIFT>
-__global__ void __launch_bounds__(kEmbedThreads)
+template <typename Td, typename Tt, int W>
+__global__ void __launch_bounds__(kEmbedThreads, 2)
     embed_sum_kernel(const Td* __restrict__ dout, Tt* __restrict__ table, EmbedSum g) {
-    constexpr int B = SHIFT && sizeof(Td) == 4 ? 4 : 8;  // rows in flight
+    constexpr int B = 8;  // rows in flight
     const int lane = threadIdx.x & 31;
     const int64_t spans = (g.cols + kSpan - 1) / kSpan;
     const int64_t step = (int64_t)gridDim.x * kEmbedWarps;
@@ -389,11 +459,11 @@ __global__ void __launch_bounds__(kEmbedThreads)
         const int before = run_of(__ballot_sync(kAll, b0 == row0)), here = run_of(__ballot_sync(kAll, f0 == row0));
         const int until = run_of(__ballot_sync(kAll, b1 == row1)), after = run_of(__ballot_sync(kAll, f1 == row1));
         bool head = before > 0, goes_on = after > 0;
-        if (head && before + here <= g.few) {  // few: the chunk before has them
+        if (head && before + here <= kFew) {  // few: the chunk before has them
             p0 += here;
             head = false;
         }
-        if (goes_on && until + after <= g.few) {
+        if (goes_on && until + after <= kFew) {
             p1 += after;
             goes_on = false;
         }
@@ -401,25 +471,26 @@ __global__ void __launch_bounds__(kEmbedThreads)
         float acc[8] = {};
         int row = -1;
         auto flush = [&](bool more) {
-            if (head) store_values<float, false>(g.heads + ch * g.pitch + c0 + lane * 8, acc, n, lane);
-            else if (more) store_values<float, false>(g.tails + ch * g.pitch + c0 + lane * 8, acc, n, lane);
-            else add_row<Tt, SHIFT>(g, table, row, c0, n, acc, lane);
+            if (head || more) Parked<W>::store((head ? g.heads : g.tails) + ch * g.pitch + c0 + lane * W, n - lane * W, acc);
+            else add_row<Tt, W>(g, table, row, c0, n, acc, lane);
             head = false;
         };
         for (int64_t q = p0; q < p1; q += 32) {
             const int2 mine = q + lane < p1 ? g.pairs[q + lane] : make_int2(-1, 0);
             const int many = (int)(p1 - q < 32 ? p1 - q : 32);
             for (int j0 = 0; j0 < many; j0 += B) {
-                Units<Td, SHIFT> raw[B];
+                Part<Td, W> held[B];
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
-                    const Td* from = dout + (int64_t)__shfl_sync(kAll, mine.y, (j0 + b) & 31) * g.dout_ld + c0;
-                    if (j0 + b < many && 8 * lane < n) load_units<Td, SHIFT>(from + 8 * lane, from + n, raw[b]);
+                    const int64_t t = __shfl_sync(kAll, mine.y, (j0 + b) & 31);
+                    const Td* from = dout + t * g.dout_ld + c0 + lane * W;
+                    if (j0 + b >= many) continue;
+                    if (n == kSpan) held[b].template load<true>(from, 0);
+                    else held[b].template load<false>(from, n - lane * W);
                 }
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
                     const int r = __shfl_sync(kAll, mine.x, (j0 + b) & 31);
-                    const Td* from = dout + (int64_t)__shfl_sync(kAll, mine.y, (j0 + b) & 31) * g.dout_ld + c0;
                     if (j0 + b >= many) break;
                     if (r != row) {
                         if (row >= 0) flush(false);
@@ -428,7 +499,7 @@ __global__ void __launch_bounds__(kEmbedThreads)
                         for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
                     }
                     float v[8];
-                    unit_values<Td, SHIFT>(raw[b], from, v);
+                    held[b].values(v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) acc[i] += v[i];
                 }
@@ -443,7 +514,7 @@ __global__ void __launch_bounds__(kEmbedThreads)
         const uint32_t bits = g.touched[job >> 3] >> ((job & 7) * 4);
         for (int i = 0; i < 4; ++i) {
             const int64_t r = job * 4 + i;
-            if (r < g.rows && !(bits >> i & 1)) zero_row<Tt, SHIFT>(table + r * g.ld, g.cols, lane);
+            if (r < g.rows && !(bits >> i & 1)) zero_row<Tt, W>(table + r * g.ld, g.cols, lane);
         }
     }
 }
@@ -451,9 +522,9 @@ __global__ void __launch_bounds__(kEmbedThreads)
 // The rows that were cut: tails[c] + heads[c + 1] + ... , a warp a row and kSpan columns; of rows with
 // more than kJoinAlone parts every warp of the CTA adds up consecutive ones, and the warps' sums meet
 // in shared memory, in order.
-constexpr int kJoinAlone = 64;
+constexpr int kJoinAlone = 16;
 
-template <typename Tt, bool SHIFT>
+template <typename Tt, int W>
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(Tt* __restrict__ table, EmbedSum g) {
     __shared__ float part[kEmbedWarps][8][32];
     __shared__ int parts_of[kEmbedWarps];
@@ -464,14 +535,17 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(Tt* __restric
     for (int64_t job0 = (int64_t)blockIdx.x * kEmbedWarps; job0 < jobs; job0 += (int64_t)gridDim.x * kEmbedWarps) {
         // the sum of parts from..to-1 of a job's, this lane's columns
         auto add_up = [&](int64_t ch, int64_t c, int n, int from, int to, float (&acc)[8]) {
-            if (8 * lane >= n) return;
-#pragma unroll 8
-            for (int k = from; k < to; ++k) {
-                const float* src = (k ? g.heads : g.tails) + (ch + k) * g.pitch + c + 8 * lane;
-                float v[8];
-                load_w<8>(src, v);
+            for (int k0 = from; k0 < to; k0 += 4) {
+                float v[4][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] += v[i];
+                for (int j = 0; j < 4; ++j) {
+                    const int k = k0 + j;
+                    Parked<W>::load((k ? g.heads : g.tails) + (ch + k) * g.pitch + c + lane * W, k < to ? n - lane * W : 0, v[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[i] += v[j][i];
             }
         };
         const int64_t job = job0 + warp;
@@ -491,7 +565,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(Tt* __restric
             if (parts <= kJoinAlone) {
                 float acc[8] = {};
                 add_up(ch, c, n, 0, parts, acc);
-                add_row<Tt, SHIFT>(g, table, row, c, n, acc, lane);
+                add_row<Tt, W>(g, table, row, c, n, acc, lane);
             }
         }
         if (lane == 0) parts_of[warp] = parts;
@@ -513,7 +587,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(Tt* __restric
                     acc[i] = 0.0f;
                     for (int x = 0; x < kEmbedWarps; ++x) acc[i] += part[x][i][lane];
                 }
-                add_row<Tt, SHIFT>(g, table, g.pairs[(ch + 1) * g.chunk].x, c, n, acc, lane);
+                add_row<Tt, W>(g, table, g.pairs[(ch + 1) * g.chunk].x, c, n, acc, lane);
             }
             __syncthreads();
         }
@@ -526,7 +600,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(Tt* __restric
 // rows that no id names.
 constexpr int kFewTokens = 256;
 
-template <typename Td, typename Tt, bool SHIFT>
+template <typename Td, typename Tt, int W>
 __global__ void __launch_bounds__(kEmbedThreads)
     embed_few_kernel(const Td* __restrict__ dout, const int32_t* __restrict__ ids, int tokens, int64_t first,
                      Tt* __restrict__ table, EmbedSum g) {
@@ -560,7 +634,7 @@ __global__ void __launch_bounds__(kEmbedThreads)
         for (int j0 = t & ~31; j0 < tokens; j0 += 32) {
             unsigned same = __ballot_sync(kAll, j0 + lane < tokens && keys[(j0 + lane) & (kFewTokens - 1)] == row);
             while (same) {
-                Units<Td, SHIFT> raw[B];
+                Part<Td, W> raw[B];
                 const Td* from[B];
                 unsigned left = same;
 #pragma unroll
@@ -569,20 +643,20 @@ __global__ void __launch_bounds__(kEmbedThreads)
                     if (!left) continue;
                     from[b] = dout + (int64_t)(j0 + __ffs(left) - 1) * g.dout_ld + c0;
                     left &= left - 1;
-                    if (8 * lane < n) load_units<Td, SHIFT>(from[b] + 8 * lane, from[b] + n, raw[b]);
+                    raw[b].template load<false>(from[b] + lane * W, n - lane * W);
                 }
                 same = left;
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
                     if (!from[b]) break;
                     float v[8];
-                    unit_values<Td, SHIFT>(raw[b], from[b], v);
+                    raw[b].values(v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) acc[i] += v[i];
                 }
             }
         }
-        add_row<Tt, SHIFT>(g, table, row, c0, n, acc, lane);
+        add_row<Tt, W>(g, table, row, c0, n, acc, lane);
     }
     if (g.accumulate) return;
     const int64_t groups = (g.rows + 3) / 4;
@@ -593,16 +667,29 @@ __global__ void __launch_bounds__(kEmbedThreads)
         bits = __reduce_or_sync(kAll, bits);
         for (int i = 0; i < 4; ++i) {
             const int64_t r = job * 4 + i;
-            if (r < g.rows && !(bits >> i & 1)) zero_row<Tt, SHIFT>(table + r * g.ld, g.cols, lane);
+            if (r < g.rows && !(bits >> i & 1)) zero_row<Tt, W>(table + r * g.ld, g.cols, lane);
         }
     }
 }
 
 // ---------------------------------------------------------------- host side
 
-// Every row begins at a multiple of 16 bytes and has whole vectors of 8 values.
-static bool whole(const void* p, int64_t ld, int64_t cols, int bf16) {
-    return cols % 8 == 0 && (uintptr_t)p % 16 == 0 && (uintptr_t)ld * (bf16 ? 2 : 4) % 16 == 0;
+// Rows as they lie in memory: base, row distance, type.
+struct Lines {
+    const void* p;
+    int64_t ld;
+    int bf16;
+    bool fits(int w) const {
+        const uintptr_t unit = (uintptr_t)w * (bf16 ? 2 : 4);
+        return unit <= 16 && (uintptr_t)p % unit == 0 && ld % w == 0;
+    }
+};
+// Neighbouring values that a lane loads at once: 16 bytes of the wider type, less where rows do not
+// begin at, or are not whole, units of so many.
+static int width(int64_t cols, const Lines& x, const Lines& y) {
+    int w = 8;
+    while (w > 1 && (cols % w || !x.fits(w) || !y.fits(w))) w /= 2;
+    return w;
 }
 
 int embed_init_device() {
@@ -616,11 +703,20 @@ static unsigned up_to(int64_t jobs, int per_cta, int64_t most) {
     return (unsigned)(ctas < most ? ctas : most);
 }
 
-// f(Ta, Tb, SHIFT) as values of types.
+// f(Ta, Tb, W) as values of types.
 template <typename F>
-static cudaError_t by_types(int a_bf16, int b_bf16, bool shift, F f) {
+static cudaError_t by_types(int a_bf16, int b_bf16, int w, F f) {
     auto second = [&](auto a) {
-        auto third = [&](auto b) { return shift ? f(a, b, std::true_type()) : f(a, b, std::false_type()); };
+        auto third = [&](auto b) {
+            switch (w) {
+                case 8:
+                    if constexpr (sizeof(a) == 2 && sizeof(b) == 2) return f(a, b, std::integral_constant<int, 8>());
+                    [[fallthrough]];
+                case 4: return f(a, b, std::integral_constant<int, 4>());
+                case 2: return f(a, b, std::integral_constant<int, 2>());
+                default: return f(a, b, std::integral_constant<int, 1>());
+            }
+        };
         return b_bf16 ? third(__nv_bfloat16()) : third(float());
     };
     return a_bf16 ? second(__nv_bfloat16()) : second(float());
@@ -630,14 +726,14 @@ int embed_launch(const void* table, int bf16, const EmbedArgs& a, const int32_t*
                  cudaStream_t s) {
     DeviceState* ds = device_state();
     if (!ds) return -3;
-    const bool shift = !(whole(table, a.ld, a.cols, bf16) && whole(out, a.out_ld, a.cols, out_bf16));
-    const int64_t jobs = a.tokens * ((a.cols + kSpan - 1) / kSpan);
+    const int w = width(a.cols, {table, a.ld, bf16}, {out, a.out_ld, out_bf16});
+    const int64_t jobs = a.tokens * ((a.cols + 1 + kSpan - 1) / kSpan);  // (one more column where pairs begin before a row)
     // Few pieces are spread over the warps of more CTAs than they fill: each takes kAhead all the same.
     const unsigned grid = up_to(jobs, kEmbedWarps * kAhead, (int64_t)ds->sm_count * 8);
-    const cudaError_t e = by_types(bf16, out_bf16, shift, [&](auto t, auto o, auto sh) {
+    const cudaError_t e = by_types(bf16, out_bf16, w, [&](auto t, auto o, auto wide_of) {
         using Tt = decltype(t);
         using To = decltype(o);
-        return launch_chained(embed_kernel<Tt, To, decltype(sh)::value>, dim3(grid), kEmbedThreads, 0, s, 1,
+        return launch_chained(embed_kernel<Tt, To, decltype(wide_of)::value>, dim3(grid), kEmbedThreads, 0, s, 1,
                               static_cast<const Tt*>(table), a.rows, a.cols, a.ld, a.first, ids, a.tokens, a.scale,
                               static_cast<To*>(out), a.out_ld);
     });
@@ -656,7 +752,8 @@ struct EmbedWork {
 static EmbedWork embed_work(int64_t tokens, int64_t rows, int64_t cols) {
     EmbedWork w;
     const int64_t spans = (cols + kSpan - 1) / kSpan;
-    w.chunk = 8;
+    w.chunk = kFew;
+    static_assert(kFew == 32, "a warp's votes find a short row's ends");
     while ((tokens + w.chunk - 1) / w.chunk * spans > 16384 && w.chunk < (1 << 20)) w.chunk *= 2;
     w.chunks = (int)((tokens + w.chunk - 1) / w.chunk);
     w.pitch = (cols + 7) / 8 * 8;
@@ -701,18 +798,17 @@ int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, c
     g.dout_ld = a.out_ld;
     g.pitch = w.pitch;
     g.chunk = w.chunk;
-    g.few = w.chunk < 32 ? w.chunk : 32;
     g.accumulate = accumulate;
     g.scale = a.scale;
     const int64_t spans = (a.cols + kSpan - 1) / kSpan, zeros = accumulate ? 0 : (a.rows + 3) / 4;
     const int64_t most = (int64_t)ds->sm_count * 8;
-    const bool shift = !(whole(dout, a.out_ld, a.cols, dout_bf16) && whole(table, a.ld, a.cols, bf16));
+    const int wide = width(a.cols, {dout, a.out_ld, dout_bf16}, {table, a.ld, bf16});
     if (a.tokens <= kFewTokens) {
         const unsigned grid = up_to(a.tokens * spans + zeros, kEmbedWarps, most);
-        const cudaError_t e = by_types(dout_bf16, bf16, shift, [&](auto d, auto t, auto sh) {
+        const cudaError_t e = by_types(dout_bf16, bf16, wide, [&](auto d, auto t, auto wide_of) {
             using Td = decltype(d);
             using Tt = decltype(t);
-            return launch_chained(embed_few_kernel<Td, Tt, decltype(sh)::value>, dim3(grid), kEmbedThreads, 0, s, 1,
+            return launch_chained(embed_few_kernel<Td, Tt, decltype(wide_of)::value>, dim3(grid), kEmbedThreads, 0, s, 1,
                                   static_cast<const Td*>(dout), ids, a.tokens, a.first, static_cast<Tt*>(table), g);
         });
         if (e != cudaSuccess) return set_cuda_error(e, "embedding gradient kernel launch");
@@ -726,20 +822,20 @@ int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, c
     const int ctas = a.tokens <= 4 * kSortThreads ? 1 : kSortCtas;
     cudaError_t e = launch_chained(embed_sort_kernel, dim3(ctas), kSortThreads, sizeof(int) * (kSortWarps + 1) << bits, s,
                                    (unsigned)ctas, ids, a.tokens, a.first, a.rows, bits, passes, pairs,
-                                   reinterpret_cast<int2*>(base + w.other), w.chunk, g.few, order, joins, touched);
+                                   reinterpret_cast<int2*>(base + w.other), w.chunk, order, joins, touched);
     if (e != cudaSuccess) return set_cuda_error(e, "embedding order kernel launch");
     count_launch();
     const unsigned grid = up_to(w.chunks * spans + zeros, kEmbedWarps, most);
     const unsigned join_grid = w.chunks > 1 ? up_to((int64_t)(w.chunks - 1) * spans, kEmbedWarps, most) : 0;
-    e = by_types(dout_bf16, bf16, shift, [&](auto d, auto t, auto sh) {
+    e = by_types(dout_bf16, bf16, wide, [&](auto d, auto t, auto wide_of) {
         using Td = decltype(d);
         using Tt = decltype(t);
-        constexpr bool kShift = decltype(sh)::value;
-        cudaError_t err = launch_chained(embed_sum_kernel<Td, Tt, kShift>, dim3(grid), kEmbedThreads, 0, s, 1,
+        constexpr int W = decltype(wide_of)::value;
+        cudaError_t err = launch_chained(embed_sum_kernel<Td, Tt, W>, dim3(grid), kEmbedThreads, 0, s, 1,
                                          static_cast<const Td*>(dout), static_cast<Tt*>(table), g);
         if (err != cudaSuccess || join_grid == 0) return err;
         count_launch();
-        return launch_chained(embed_join_kernel<Tt, kShift>, dim3(join_grid), kEmbedThreads, 0, s, 1, static_cast<Tt*>(table), g);
+        return launch_chained(embed_join_kernel<Tt, W>, dim3(join_grid), kEmbedThreads, 0, s, 1, static_cast<Tt*>(table), g);
     });
     if (e != cudaSuccess) return set_cuda_error(e, "embedding gradient kernel launch");
     count_launch();
