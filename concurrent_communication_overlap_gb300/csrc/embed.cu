@@ -89,95 +89,128 @@ struct Part {
 };
 
 // Single bf16 values, stored in pairs: lane l has values 32 i + l, i < 8, of the piece from column c0 on of a row of
-// `cols`, at least one pair of which is aligned to 4 bytes at an even lane.  Lanes of a pair trade half their values.
+// `cols`; row + c0 is aligned to 4 bytes.  Lanes of a pair trade half their values.  ZERO: all are 0.
+template <bool ZERO>
 __device__ __forceinline__ void store_pairs(__nv_bfloat16* row, int64_t c0, int64_t cols, const float (&v)[8], int lane) {
     const bool odd = lane & 1;
+    __nv_bfloat162 h[4];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const float got = __shfl_xor_sync(kAll, odd ? v[i] : v[i + 1], 1);
-        const float lo = odd ? got : v[i], hi = odd ? v[i + 1] : got;
-        const int64_t c = c0 + 32 * (i + odd) + (lane & ~1);
-        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-        if (c >= 0 && c + 1 < cols) *reinterpret_cast<__nv_bfloat162*>(row + c) = h;
-        else if (c >= 0 && c < cols) row[c] = h.x;
-        else if (c + 1 >= 0 && c + 1 < cols) row[c + 1] = h.y;
+    for (int i = 0; i < 4; ++i) {
+        if (ZERO) {
+            h[i] = __floats2bfloat162_rn(0.0f, 0.0f);
+        } else {
+            const float got = __shfl_xor_sync(kAll, odd ? v[2 * i] : v[2 * i + 1], 1);
+            h[i] = __floats2bfloat162_rn(odd ? got : v[2 * i], odd ? v[2 * i + 1] : got);
+        }
+    }
+    const int64_t c = c0 + (odd ? 32 : 0) + (lane & ~1);
+    if (c0 >= 0 && c0 + kSpan <= cols) {
+        __nv_bfloat162* at = reinterpret_cast<__nv_bfloat162*>(row + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[32 * i] = h[i];
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t at = c + 64 * i;
+        if (at >= 0 && at + 1 < cols) *reinterpret_cast<__nv_bfloat162*>(row + at) = h[i];
+        else if (at >= 0 && at < cols) row[at] = h[i].x;
+        else if (at + 1 >= 0 && at + 1 < cols) row[at + 1] = h[i].y;
     }
 }
 
 // ---------------------------------------------------------------- lookup
 
-// out[t] = scale * table[ids[t] - first], zeros where that is no row.  A warp takes kAhead pieces
-// of kSpan columns, of one token or of several, whose loads are all in flight before the first is used.
+// out[t] = scale * table[ids[t] - first], zeros where that is no row.  A warp takes up to kAhead
+// pieces of kSpan columns at once, all their loads in flight before the first is used: neighbours of
+// one token's row, or where a row has fewer, of several tokens'.  Rows are done one after the other: a
+// block of columns of all tokens after the other reads frequent rows from memory once, but 65536 x 8192
+// bf16 took 318 us that way and 280 this way, whose runs in memory are whole rows.
 //
 // Rows of bf16 of odd length: pieces of a row that begins at no multiple of 4 bytes begin one column
 // before, so that pairs of values are aligned where they are stored.
 constexpr int kAhead = 4;
 
+struct EmbedLookup {
+    int64_t rows, cols, ld, first, out_ld;
+    int tokens;
+    int spans;         // pieces of a row
+    int block, times;  // pieces of a warp at once: `block` of each of `times` tokens
+    float scale;
+};
+
 template <typename Tt, typename To, int W>
-__global__ void __launch_bounds__(kEmbedThreads)
-    embed_kernel(const Tt* __restrict__ table, int64_t rows, int64_t cols, int64_t ld, int64_t first,
-                 const int32_t* __restrict__ ids, int64_t tokens, float scale, To* __restrict__ out, int64_t out_ld) {
+__global__ void __launch_bounds__(kEmbedThreads, 3)
+    embed_kernel(const Tt* __restrict__ table, const int32_t* __restrict__ ids, To* __restrict__ out, EmbedLookup g) {
     constexpr bool kPairs = W == 1 && sizeof(To) == 2;
     const int lane = threadIdx.x & 31;
-    const int64_t spans = (cols + (kPairs ? 1 : 0) + kSpan - 1) / kSpan, jobs = tokens * spans;
+    const unsigned groups = ((unsigned)g.tokens + g.times - 1) / g.times;  // of tokens
+    const int blocks = (g.spans + g.block - 1) / g.block;
+    const int64_t jobs = (int64_t)groups * blocks, step = (int64_t)gridDim.x * kEmbedWarps;
     chain_wait();
-    for (int64_t job = ((int64_t)blockIdx.x * kEmbedWarps + (threadIdx.x >> 5)) * kAhead; job < jobs;
-         job += (int64_t)gridDim.x * kEmbedWarps * kAhead) {
-        Part<Tt, W> part[kAhead];
-        int t[kAhead], span[kAhead], id[kAhead];
-        bool have[kAhead];
-        t[0] = (int)(job / spans);
-        span[0] = (int)(job - t[0] * spans);
+    int64_t job = (int64_t)blockIdx.x * kEmbedWarps + (threadIdx.x >> 5);
+    const unsigned step_at = (unsigned)(step / blocks);
+    const int step_b = (int)(step - (int64_t)step_at * blocks);
+    unsigned at = (unsigned)(job / blocks);
+    int b = (int)(job - (int64_t)at * blocks);
+    for (; job < jobs; job += step) {
+        int64_t r[kAhead];
 #pragma unroll
-        for (int u = 1; u < kAhead; ++u) {
-            const bool over = span[u - 1] + 1 == spans;
-            t[u] = t[u - 1] + over;
-            span[u] = over ? 0 : span[u - 1] + 1;
+        for (int u = 0; u < kAhead; ++u) {
+            const unsigned t = at * g.times + (g.times > 1 ? u / g.block : 0);
+            r[u] = t < (unsigned)g.tokens ? (int64_t)ids[t] - g.first : -1;
         }
-        // the piece's first column
+        Part<Tt, W> part[kAhead];
+        // piece u: its token and its first column
+        auto token = [&](int u) { return at * g.times + (g.times > 1 ? u / g.block : 0); };
         auto column = [&](int u) {
-            const int64_t c = (int64_t)span[u] * kSpan;
-            return kPairs && ((uintptr_t)(out + t[u] * out_ld) & 2) ? c - 1 : c;
+            const int64_t c = (int64_t)(b * g.block + (g.times > 1 ? u % g.block : u)) * kSpan;
+            return kPairs && ((uintptr_t)(out + token(u) * g.out_ld) & 2) ? c - 1 : c;
+        };
+        auto exists = [&](int u) {
+            return u < g.block * g.times && token(u) < (unsigned)g.tokens && b * g.block + (g.times > 1 ? u % g.block : u) < g.spans;
         };
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) id[u] = t[u] < tokens ? ids[t[u]] : -1;
-#pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int64_t r = (int64_t)id[u] - first;
-            have[u] = r >= 0 && r < rows;
-            if constexpr (kPairs) {
-                const int64_t at = column(u) + lane;
-                if (have[u]) {
-                    const Tt* from = table + r * ld + at;
+            if (!exists(u) || r[u] < 0 || r[u] >= g.rows) continue;
+            const int64_t c0 = column(u);
+            const Tt* from = table + r[u] * g.ld + c0 + lane * W;
+            if (c0 >= 0 && c0 + kSpan <= g.cols) {
+                part[u].template load<true>(from, 0);
+            } else if constexpr (kPairs) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (at + 32 * q >= 0 && at + 32 * q < cols)
-                            part[u].w[q] = *reinterpret_cast<const typename Part<Tt, 1>::Word*>(from + 32 * q);
-                }
+                for (int q = 0; q < 8; ++q)
+                    if (c0 + lane + 32 * q >= 0 && c0 + lane + 32 * q < g.cols)
+                        part[u].w[q] = *reinterpret_cast<const typename Part<Tt, 1>::Word*>(from + 32 * q);
             } else {
-                const int64_t left = cols - column(u);
-                const Tt* from = table + r * ld + column(u) + lane * W;
-                if (have[u] && left >= kSpan) part[u].template load<true>(from, 0);
-                else if (have[u]) part[u].template load<false>(from, (int)left - lane * W);
+                part[u].template load<false>(from, (int)(g.cols - c0) - lane * W);
             }
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            if (t[u] >= tokens) break;
+            if (!exists(u)) continue;
+            const int64_t c0 = column(u);
+            const bool have = r[u] >= 0 && r[u] < g.rows;
+            To* to = out + token(u) * g.out_ld;
             float v[8] = {};
-            if (have[u]) {
+            if (have) {
                 part[u].values(v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= scale;
+                for (int i = 0; i < 8; ++i) v[i] *= g.scale;
             }
             if constexpr (kPairs) {
-                store_pairs(out + t[u] * out_ld, column(u), cols, v, lane);
+                if (have) store_pairs<false>(to, c0, g.cols, v, lane);
+                else store_pairs<true>(to, c0, g.cols, v, lane);
             } else {
-                const int64_t left = cols - column(u);
-                To* to = out + t[u] * out_ld + column(u) + lane * W;
-                if (left >= kSpan) Part<To, W>::template store<true>(to, 0, v);
-                else Part<To, W>::template store<false>(to, (int)left - lane * W, v);
+                if (c0 + kSpan <= g.cols) Part<To, W>::template store<true>(to + c0 + lane * W, 0, v);
+                else Part<To, W>::template store<false>(to + c0 + lane * W, (int)(g.cols - c0) - lane * W, v);
             }
+        }
+        at += step_at;
+        b += step_b;
+        if (b >= blocks) {
+            b -= blocks;
+            ++at;
         }
     }
 }
@@ -194,12 +227,12 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortBits = 10;  // a digit at most: a thread a bin in the scans
 constexpr int kSortCtas = 8;
 constexpr int kFew = 32;       // tokens of a row that is never cut: a chunk's length at least, a warp's lanes at most
-constexpr int kSortAhead = 8;  // pairs a lane holds: up to 65536 tokens are read once a pass
+constexpr int kSortHeld = 256;  // pairs a warp holds in shared memory: up to 65536 tokens are read once a pass
 
 // What the sort leaves for the sums.
 struct EmbedOrder {
     int valid;  // tokens that have a row
-    int joins;  // chunks whose last row goes on in the next and is joined
+    int joins;  // rows that are cut, counted by the sums
 };
 
 __device__ __forceinline__ int remote_int(uint32_t addr) {
@@ -208,25 +241,28 @@ __device__ __forceinline__ int remote_int(uint32_t addr) {
     return v;
 }
 
-// pairs: where the sorted (row, token) end up; other: as much scratch.  joins: numbers of the chunks
-// (of `chunk` places) whose last row goes on in the next and has more than kFew tokens.
-// touched: a bit a row of the table, or NULL.
+// pairs: where the sorted (row, token) end up; other: as much scratch.
+// touched: 1 for a row of the table that a token names, 0 for others; or NULL.
 __global__ void __launch_bounds__(kSortThreads, 1)
     embed_sort_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t first, int64_t rows, int bits, int passes,
-                      int2* pairs, int2* other, int chunk, EmbedOrder* order, int* joins, uint32_t* touched) {
+                      int2* pairs, int2* other, EmbedOrder* order, uint8_t* touched) {
     extern __shared__ int shared[];
     const int bins = 1 << bits;
     int* total = shared;                       // [bins] this CTA's, read by the others
     int* hist = shared + bins;                 // [warps][bins]
+    int2* held = reinterpret_cast<int2*>(hist + kSortWarps * bins);  // [warps][kSortHeld] pairs
+    uint16_t* places = reinterpret_cast<uint16_t*>(held + kSortWarps * kSortHeld);
     __shared__ int warp_sums[kSortWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned before_me = (1u << lane) - 1;
     const int ctas = (int)gridDim.x, rank = (int)blockIdx.x;
     int* mine_hist = hist + warp * bins;
+    int2* mine_held = held + warp * kSortHeld;
+    uint16_t* mine_place = places + warp * kSortHeld;
     chain_wait();
     if (touched)
-        for (int64_t i = (int64_t)rank * kSortThreads + threadIdx.x; i < (rows + 31) / 32; i += (int64_t)ctas * kSortThreads)
-            touched[i] = 0;
+        for (int64_t i = (int64_t)rank * kSortThreads + threadIdx.x; i < (rows + 15) / 16; i += (int64_t)ctas * kSortThreads)
+            reinterpret_cast<uint4*>(touched)[i] = make_uint4(0, 0, 0, 0);
     if (rank == 0 && threadIdx.x == 0) order->joins = 0;
     int valid = 0;
     for (int pass = 0; pass < passes; ++pass) {
@@ -238,44 +274,56 @@ __global__ void __launch_bounds__(kSortThreads, 1)
         const int64_t mine = ((int64_t)rank * kSortWarps + warp) * per;
         const int64_t end = mine + per < count ? mine + per : count;
         const int shift = pass * bits;
-        int2 held[kSortAhead];
+        // kSortHeld pairs from i0 on to shared memory, all loads in flight at once; rows that are none: -1
         auto fetch = [&](int64_t i0) {
+            int2 p[kSortHeld / 32];
 #pragma unroll
-            for (int j = 0; j < kSortAhead; ++j) {
+            for (int j = 0; j < kSortHeld / 32; ++j) {
                 const int64_t i = i0 + 32 * j + lane;
-                held[j] = make_int2(-1, 0);
-                if (i < end) held[j] = pass ? __ldcg(from + i) : make_int2(ids[i], (int)i);
+                p[j] = make_int2(-1, 0);
+                if (i < end) p[j] = pass ? __ldcg(from + i) : make_int2(ids[i], (int)i);
             }
-            if (pass == 0) {
 #pragma unroll
-                for (int j = 0; j < kSortAhead; ++j) {
-                    const int64_t r = (int64_t)held[j].x - first;
-                    held[j].x = i0 + 32 * j + lane < end && r >= 0 && r < rows ? (int)r : -1;
+            for (int j = 0; j < kSortHeld / 32; ++j) {
+                if (pass == 0) {
+                    const int64_t r = (int64_t)p[j].x - first;
+                    p[j].x = i0 + 32 * j + lane < end && r >= 0 && r < rows ? (int)r : -1;
                 }
+                mine_held[32 * j + lane] = p[j];
             }
+            __syncwarp();
+        };
+        // A lane's place among those of its digit that the warp has seen, which `mine_hist` counts.  The lanes
+        // of the same digit are found by a vote a bit.
+        auto place = [&](int d) {
+            unsigned same = __ballot_sync(kAll, d >= 0);
+#pragma unroll
+            for (int b = 0; b < kSortBits; ++b) {
+                const bool bit = (d >> b) & 1;
+                const unsigned one = __ballot_sync(kAll, bit);
+                same &= bit ? one : ~one;
+            }
+            int at = 0;
+            if (d >= 0) at = mine_hist[d];
+            __syncwarp();
+            if (d >= 0 && (same & before_me) == 0) mine_hist[d] = at + __popc(same);
+            __syncwarp();
+            return at + __popc(same & before_me);
         };
         auto digit = [&](int2 p) { return p.x < 0 ? -1 : (p.x >> shift) & (bins - 1); };
-        // the lanes of the same digit, a vote a bit (four times as fast as a match of all lanes)
-        auto alike = [&](int d) {
-            unsigned same = __ballot_sync(kAll, d >= 0);
-            for (int b = 0; b < bits; ++b) {
-                const unsigned one = __ballot_sync(kAll, (d >> b) & 1);
-                same &= (d >> b) & 1 ? one : ~one;
-            }
-            return same;
-        };
-        unsigned same[kSortAhead];
+        auto groups = [&](int64_t i0) { return (int)((end - i0 + 31) / 32 < kSortHeld / 32 ? (end - i0 + 31) / 32 : kSortHeld / 32); };
+        const bool again = per > kSortHeld;
         for (int d = lane; d < bins; d += 32) mine_hist[d] = 0;
         __syncwarp();
-        for (int64_t i0 = mine; i0 < end; i0 += 32 * kSortAhead) {
+        // (Loops are left rolled: the kernel runs each instruction a few times, and fetching them counts.)
+#pragma unroll 1
+        for (int64_t i0 = mine; i0 < end; i0 += kSortHeld) {
             fetch(i0);
-#pragma unroll
-            for (int j = 0; j < kSortAhead; ++j) {
-                if (i0 + 32 * j >= end) break;
-                const int d = digit(held[j]);
-                same[j] = alike(d);
-                if (d >= 0 && (same[j] & before_me) == 0) mine_hist[d] += __popc(same[j]);
-                __syncwarp();
+            const int many = groups(i0);
+#pragma unroll 1
+            for (int j = 0; j < many; ++j) {
+                const int at = place(digit(mine_held[32 * j + lane]));
+                if (!again) mine_place[32 * j + lane] = (uint16_t)at;
             }
         }
         __syncthreads();
@@ -322,31 +370,24 @@ __global__ void __launch_bounds__(kSortThreads, 1)
             }
         }
         __syncthreads();
-        for (int64_t i0 = mine; i0 < end; i0 += 32 * kSortAhead) {
-            if (per > 32 * kSortAhead) fetch(i0);
-#pragma unroll
-            for (int j = 0; j < kSortAhead; ++j) {
-                if (i0 + 32 * j >= end) break;
-                const int dig = digit(held[j]);
-                if (per > 32 * kSortAhead) same[j] = alike(dig);
-                if (dig >= 0) to[mine_hist[dig] + __popc(same[j] & before_me)] = held[j];
-                __syncwarp();
-                if (dig >= 0 && (same[j] & before_me) == 0) mine_hist[dig] += __popc(same[j]);
-                __syncwarp();
+#pragma unroll 1
+        for (int64_t i0 = mine; i0 < end; i0 += kSortHeld) {
+            if (again) fetch(i0);
+            const int many = groups(i0);
+#pragma unroll 1
+            for (int j = 0; j < many; ++j) {
+                const int2 p = mine_held[32 * j + lane];
+                const int dig = digit(p);
+                const int at = again ? place(dig) : dig >= 0 ? mine_hist[dig] + mine_place[32 * j + lane] : 0;
+                if (dig < 0) continue;
+                to[at] = p;
+                if (pass == 0 && touched) touched[p.x] = 1;
             }
+            __syncwarp();
         }
         cluster_sync_all();  // the pairs are where the next pass looks for them, and `total` has been read
     }
     if (rank == 0 && threadIdx.x == 0) order->valid = valid;
-    for (int64_t p = (int64_t)rank * kSortThreads + threadIdx.x; p < valid; p += (int64_t)ctas * kSortThreads) {
-        const int64_t next = (p / chunk + 1) * chunk;
-        const int row = __ldcg(&pairs[p].x);
-        const int last = p > 0 ? __ldcg(&pairs[p - 1].x) : -1;
-        const int cut = next < valid ? __ldcg(&pairs[next].x) : -1, far = p + kFew < valid ? __ldcg(&pairs[p + kFew].x) : -1;
-        if (last == row) continue;
-        if (touched) atomicOr(&touched[row >> 5], 1u << (row & 31));
-        if (cut == row && far == row) joins[atomicAdd(&order->joins, 1)] = (int)(p / chunk);
-    }
 }
 
 // ---------------------------------------------------------------- sums
@@ -358,9 +399,9 @@ __global__ void __launch_bounds__(kSortThreads, 1)
 // names are written as zeros beside, by warps of their own.
 struct EmbedSum {
     const int2* pairs;
-    const EmbedOrder* order;
-    const int* joins;
-    const uint32_t* touched;  // NULL: rows without tokens are left as they are
+    EmbedOrder* order;
+    int* joins;               // the chunks that such rows begin in
+    const uint8_t* touched;  // NULL: rows without tokens are left as they are
     float* heads;             // [chunks][pitch]
     float* tails;
     int64_t rows, cols, ld, dout_ld, pitch;
@@ -425,7 +466,7 @@ template <typename Tt, int W>
 __device__ __forceinline__ void zero_row(Tt* row, int64_t cols, int lane) {
     const float zero[8] = {};
     if constexpr (W == 1 && sizeof(Tt) == 2) {
-        for (int64_t c = (uintptr_t)row & 2 ? -1 : 0; c < cols; c += kSpan) store_pairs(row, c, cols, zero, lane);
+        for (int64_t c = (uintptr_t)row & 2 ? -1 : 0; c < cols; c += kSpan) store_pairs<true>(row, c, cols, zero, lane);
     } else {
         int64_t c = 0;
         for (; c + kSpan <= cols; c += kSpan) Part<Tt, W>::template store<true>(row + c + lane * W, 0, zero);
@@ -436,10 +477,11 @@ __device__ __forceinline__ void zero_row(Tt* row, int64_t cols, int lane) {
 // Length of the run of ones from bit 0 on.
 __device__ __forceinline__ int run_of(unsigned bits) { return bits == kAll ? 32 : __ffs(~bits) - 1; }
 
-template <typename Td, typename Tt, int W>
+template <typename Td, typename Tt, int W, bool ACCUMULATE>
 __global__ void __launch_bounds__(kEmbedThreads, 2)
     embed_sum_kernel(const Td* __restrict__ dout, Tt* __restrict__ table, EmbedSum g) {
-    constexpr int B = 8;  // rows in flight
+    // rows in flight; of a table that is added to, its rows too
+    constexpr int B = ACCUMULATE ? 4 : 8;
     const int lane = threadIdx.x & 31;
     const int64_t spans = (g.cols + kSpan - 1) / kSpan;
     const int64_t step = (int64_t)gridDim.x * kEmbedWarps;
@@ -467,129 +509,108 @@ __global__ void __launch_bounds__(kEmbedThreads, 2)
             p1 += after;
             goes_on = false;
         }
-        if (p0 >= p1) continue;
         float acc[8] = {};
-        int row = -1;
-        auto flush = [&](bool more) {
-            if (head || more) Parked<W>::store((head ? g.heads : g.tails) + ch * g.pitch + c0 + lane * W, n - lane * W, acc);
-            else add_row<Tt, W>(g, table, row, c0, n, acc, lane);
-            head = false;
-        };
         for (int64_t q = p0; q < p1; q += 32) {
             const int2 mine = q + lane < p1 ? g.pairs[q + lane] : make_int2(-1, 0);
             const int many = (int)(p1 - q < 32 ? p1 - q : 32);
+            // tokens that are the last of their row here
+            const unsigned ends = __ballot_sync(kAll, q + lane + 1 >= p1 || g.pairs[q + lane + 1].x != mine.x);
             for (int j0 = 0; j0 < many; j0 += B) {
                 Part<Td, W> held[B];
+                Part<Tt, W> old[ACCUMULATE ? B : 1];
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
-                    const int64_t t = __shfl_sync(kAll, mine.y, (j0 + b) & 31);
-                    const Td* from = dout + t * g.dout_ld + c0 + lane * W;
+                    const int64_t t = __shfl_sync(kAll, mine.y, (j0 + b) & 31), r = __shfl_sync(kAll, mine.x, (j0 + b) & 31);
                     if (j0 + b >= many) continue;
+                    const Td* from = dout + t * g.dout_ld + c0 + lane * W;
                     if (n == kSpan) held[b].template load<true>(from, 0);
                     else held[b].template load<false>(from, n - lane * W);
+                    if (ACCUMULATE && (ends >> (j0 + b) & 1)) old[b].template load<false>(table + r * g.ld + c0 + lane * W, n - lane * W);
                 }
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
-                    const int r = __shfl_sync(kAll, mine.x, (j0 + b) & 31);
+                    const int64_t r = __shfl_sync(kAll, mine.x, (j0 + b) & 31);
                     if (j0 + b >= many) break;
-                    if (r != row) {
-                        if (row >= 0) flush(false);
-                        row = r;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-                    }
                     float v[8];
                     held[b].values(v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) acc[i] += v[i];
+                    if (!(ends >> (j0 + b) & 1)) continue;
+                    const bool tail = goes_on && q + j0 + b + 1 == p1;
+                    if (head || tail) {
+                        if (!head && c0 == 0 && lane == 0) g.joins[atomicAdd(&g.order->joins, 1)] = (int)ch;
+                        Parked<W>::store((head ? g.heads : g.tails) + ch * g.pitch + c0 + lane * W, n - lane * W, acc);
+                    } else {
+                        if (ACCUMULATE) old[b].values(v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = ACCUMULATE ? fmaf(g.scale, acc[i], v[i]) : g.scale * acc[i];
+                        Part<Tt, W>::template store<false>(table + r * g.ld + c0 + lane * W, n - lane * W, v);
+                    }
+                    head = false;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
                 }
             }
         }
-        flush(goes_on);
     }
-    if (g.touched == nullptr) return;
+    if (ACCUMULATE) return;
     // rows without tokens, a warp four of them
     const int64_t groups = (g.rows + 3) / 4;
     for (job -= jobs; job < groups; job += step) {
-        const uint32_t bits = g.touched[job >> 3] >> ((job & 7) * 4);
+        const uint32_t named = reinterpret_cast<const uint32_t*>(g.touched)[job];
         for (int i = 0; i < 4; ++i) {
             const int64_t r = job * 4 + i;
-            if (r < g.rows && !(bits >> i & 1)) zero_row<Tt, W>(table + r * g.ld, g.cols, lane);
+            if (r < g.rows && !(named >> (8 * i) & 1)) zero_row<Tt, W>(table + r * g.ld, g.cols, lane);
         }
     }
 }
 
-// The rows that were cut: tails[c] + heads[c + 1] + ... , a warp a row and kSpan columns; of rows with
-// more than kJoinAlone parts every warp of the CTA adds up consecutive ones, and the warps' sums meet
-// in shared memory, in order.
-constexpr int kJoinAlone = 16;
-
+// The rows that were cut: tails[c] + heads[c + 1] + ... .  A CTA takes a row and kSpan columns; its warps
+// add up consecutive parts, and the warps' sums meet in shared memory, in order.
 template <typename Tt, int W>
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(Tt* __restrict__ table, EmbedSum g) {
     __shared__ float part[kEmbedWarps][8][32];
-    __shared__ int parts_of[kEmbedWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t spans = (g.cols + kSpan - 1) / kSpan;
     chain_wait();
     const int64_t valid = g.order->valid, jobs = g.order->joins * spans;
-    for (int64_t job0 = (int64_t)blockIdx.x * kEmbedWarps; job0 < jobs; job0 += (int64_t)gridDim.x * kEmbedWarps) {
-        // the sum of parts from..to-1 of a job's, this lane's columns
-        auto add_up = [&](int64_t ch, int64_t c, int n, int from, int to, float (&acc)[8]) {
-            for (int k0 = from; k0 < to; k0 += 4) {
-                float v[4][8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = k0 + j;
-                    Parked<W>::load((k ? g.heads : g.tails) + (ch + k) * g.pitch + c + lane * W, k < to ? n - lane * W : 0, v[j]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[i] += v[j][i];
-            }
-        };
-        const int64_t job = job0 + warp;
-        int parts = 0;
-        if (job < jobs) {
-            const int64_t at = job / spans, c = (job - at * spans) * kSpan, ch = g.joins[at];
-            const int n = (int)(g.cols - c < kSpan ? g.cols - c : kSpan);
-            const int row = g.pairs[(ch + 1) * g.chunk].x;
-            for (parts = 1;; parts += 32) {  // how many chunks begin with the row
-                const int64_t p = (ch + parts + lane) * g.chunk;
-                const int more = run_of(__ballot_sync(kAll, p < valid && g.pairs[p < valid ? p : 0].x == row));
-                if (more < 32) {
-                    parts += more;
-                    break;
-                }
-            }
-            if (parts <= kJoinAlone) {
-                float acc[8] = {};
-                add_up(ch, c, n, 0, parts, acc);
-                add_row<Tt, W>(g, table, row, c, n, acc, lane);
+    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+        const int64_t at = job / spans, c = (job - at * spans) * kSpan, ch = g.joins[at];
+        const int n = (int)(g.cols - c < kSpan ? g.cols - c : kSpan);
+        const int row = g.pairs[(ch + 1) * g.chunk].x;
+        int parts = 1;
+        for (;; parts += 32) {  // how many chunks begin with the row
+            const int64_t p = (ch + parts + lane) * g.chunk;
+            const int more = run_of(__ballot_sync(kAll, p < valid && g.pairs[p < valid ? p : 0].x == row));
+            if (more < 32) {
+                parts += more;
+                break;
             }
         }
-        if (lane == 0) parts_of[warp] = parts;
+        const int per = (parts + kEmbedWarps - 1) / kEmbedWarps, to = min(parts, (warp + 1) * per);
+        float acc[8] = {};
+#pragma unroll 1
+        for (int k0 = warp * per; k0 < to; k0 += 4) {
+            float v[4][8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                Parked<W>::load((k0 + j ? g.heads : g.tails) + (ch + k0 + j) * g.pitch + c + lane * W, k0 + j < to ? n - lane * W : 0, v[j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] += v[j][i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[warp][i][lane] = acc[i];
         __syncthreads();
-        for (int w = 0; w < kEmbedWarps; ++w) {
-            const int many = parts_of[w];
-            if (many <= kJoinAlone) continue;
-            const int64_t at = (job0 + w) / spans, c = (job0 + w - at * spans) * kSpan, ch = g.joins[at];
-            const int n = (int)(g.cols - c < kSpan ? g.cols - c : kSpan);
-            const int per = (many + kEmbedWarps - 1) / kEmbedWarps;
-            float acc[8] = {};
-            add_up(ch, c, n, min(many, warp * per), min(many, (warp + 1) * per), acc);
+        if (warp == 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) part[warp][i][lane] = acc[i];
-            __syncthreads();
-            if (warp == 0) {
+            for (int i = 0; i < 8; ++i) {
+                acc[i] = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    acc[i] = 0.0f;
-                    for (int x = 0; x < kEmbedWarps; ++x) acc[i] += part[x][i][lane];
-                }
-                add_row<Tt, W>(g, table, g.pairs[(ch + 1) * g.chunk].x, c, n, acc, lane);
+                for (int x = 0; x < kEmbedWarps; ++x) acc[i] += part[x][i][lane];
             }
-            __syncthreads();
+            add_row<Tt, W>(g, table, row, c, n, acc, lane);
         }
         __syncthreads();
     }
@@ -692,8 +713,12 @@ static int width(int64_t cols, const Lines& x, const Lines& y) {
     return w;
 }
 
+static size_t sort_smem(int bits) {
+    return (sizeof(int) * (kSortWarps + 1) << bits) + (size_t)kSortWarps * kSortHeld * (sizeof(int2) + sizeof(uint16_t));
+}
+
 int embed_init_device() {
-    const int most = (int)sizeof(int) * (kSortWarps + 1) << kSortBits;
+    const int most = (int)sort_smem(kSortBits);
     cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     return e == cudaSuccess ? 0 : set_cuda_error(e, "cudaFuncSetAttribute(embedding order)");
 }
@@ -727,15 +752,25 @@ int embed_launch(const void* table, int bf16, const EmbedArgs& a, const int32_t*
     DeviceState* ds = device_state();
     if (!ds) return -3;
     const int w = width(a.cols, {table, a.ld, bf16}, {out, a.out_ld, out_bf16});
-    const int64_t jobs = a.tokens * ((a.cols + 1 + kSpan - 1) / kSpan);  // (one more column where pairs begin before a row)
-    // Few pieces are spread over the warps of more CTAs than they fill: each takes kAhead all the same.
-    const unsigned grid = up_to(jobs, kEmbedWarps * kAhead, (int64_t)ds->sm_count * 8);
+    EmbedLookup g;
+    g.rows = a.rows;
+    g.cols = a.cols;
+    g.ld = a.ld;
+    g.first = a.first;
+    g.out_ld = a.out_ld;
+    g.scale = a.scale;
+    g.tokens = (int)a.tokens;
+    g.spans = (int)((a.cols + (w == 1 && out_bf16) + kSpan - 1) / kSpan);  // pairs may begin a column before the row
+    const int blocks = (g.spans + kAhead - 1) / kAhead;
+    g.block = (g.spans + blocks - 1) / blocks;
+    g.times = kAhead / g.block;
+    const int64_t jobs = (a.tokens + g.times - 1) / g.times * ((g.spans + g.block - 1) / g.block);
+    const unsigned grid = up_to(jobs, kEmbedWarps, (int64_t)ds->sm_count * 8);
     const cudaError_t e = by_types(bf16, out_bf16, w, [&](auto t, auto o, auto wide_of) {
         using Tt = decltype(t);
         using To = decltype(o);
         return launch_chained(embed_kernel<Tt, To, decltype(wide_of)::value>, dim3(grid), kEmbedThreads, 0, s, 1,
-                              static_cast<const Tt*>(table), a.rows, a.cols, a.ld, a.first, ids, a.tokens, a.scale,
-                              static_cast<To*>(out), a.out_ld);
+                              static_cast<const Tt*>(table), ids, static_cast<To*>(out), g);
     });
     if (e != cudaSuccess) return set_cuda_error(e, "embedding kernel launch");
     count_launch();
@@ -766,7 +801,7 @@ static EmbedWork embed_work(int64_t tokens, int64_t rows, int64_t cols) {
     w.pairs = part((size_t)tokens * sizeof(int2));
     w.other = part((size_t)tokens * sizeof(int2));
     w.joins = part((size_t)w.chunks * sizeof(int));
-    w.touched = part((size_t)(rows + 31) / 32 * sizeof(uint32_t));
+    w.touched = part((size_t)rows);
     w.heads = part((size_t)w.chunks * (size_t)w.pitch * sizeof(float));
     w.tails = part((size_t)w.chunks * (size_t)w.pitch * sizeof(float));
     w.bytes = at;
@@ -784,7 +819,7 @@ int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, c
     int2* pairs = reinterpret_cast<int2*>(base + w.pairs);
     EmbedOrder* order = reinterpret_cast<EmbedOrder*>(base);
     int* joins = reinterpret_cast<int*>(base + w.joins);
-    uint32_t* touched = accumulate ? nullptr : reinterpret_cast<uint32_t*>(base + w.touched);
+    uint8_t* touched = accumulate ? nullptr : base + w.touched;
     EmbedSum g;
     g.pairs = pairs;
     g.order = order;
@@ -820,19 +855,21 @@ int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, c
     const int passes = (bits + kSortBits - 1) / kSortBits;
     bits = (bits + passes - 1) / passes;
     const int ctas = a.tokens <= 4 * kSortThreads ? 1 : kSortCtas;
-    cudaError_t e = launch_chained(embed_sort_kernel, dim3(ctas), kSortThreads, sizeof(int) * (kSortWarps + 1) << bits, s,
+    cudaError_t e = launch_chained(embed_sort_kernel, dim3(ctas), kSortThreads, sort_smem(bits), s,
                                    (unsigned)ctas, ids, a.tokens, a.first, a.rows, bits, passes, pairs,
-                                   reinterpret_cast<int2*>(base + w.other), w.chunk, order, joins, touched);
+                                   reinterpret_cast<int2*>(base + w.other), order, touched);
     if (e != cudaSuccess) return set_cuda_error(e, "embedding order kernel launch");
     count_launch();
     const unsigned grid = up_to(w.chunks * spans + zeros, kEmbedWarps, most);
-    const unsigned join_grid = w.chunks > 1 ? up_to((int64_t)(w.chunks - 1) * spans, kEmbedWarps, most) : 0;
+    const unsigned join_grid = w.chunks > 1 ? up_to((int64_t)(w.chunks - 1) * spans, 1, most) : 0;
     e = by_types(dout_bf16, bf16, wide, [&](auto d, auto t, auto wide_of) {
         using Td = decltype(d);
         using Tt = decltype(t);
         constexpr int W = decltype(wide_of)::value;
-        cudaError_t err = launch_chained(embed_sum_kernel<Td, Tt, W>, dim3(grid), kEmbedThreads, 0, s, 1,
-                                         static_cast<const Td*>(dout), static_cast<Tt*>(table), g);
+        auto sum = [&](auto kernel) {
+            return launch_chained(kernel, dim3(grid), kEmbedThreads, 0, s, 1, static_cast<const Td*>(dout), static_cast<Tt*>(table), g);
+        };
+        const cudaError_t err = accumulate ? sum(embed_sum_kernel<Td, Tt, W, true>) : sum(embed_sum_kernel<Td, Tt, W, false>);
         if (err != cudaSuccess || join_grid == 0) return err;
         count_launch();
         return launch_chained(embed_join_kernel<Tt, W>, dim3(join_grid), kEmbedThreads, 0, s, 1, static_cast<Tt*>(table), g);
