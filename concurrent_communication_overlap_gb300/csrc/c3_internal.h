@@ -105,6 +105,7 @@ struct DeviceState {
     cudaStream_t s_capture = nullptr;  // private stream for capturing copy-engine graphs
     cudaEvent_t ev[8] = {};
     DevStatus* status = nullptr;       // device status block
+    int embed_clusters = 0;            // clusters of the embedding gradient's first kernel that run at once
     unsigned int next_sched = 0;       // round-robin scheduler slot
     unsigned int next_coll_sched = 0;  // round-robin copy work-counter slot
     bool ready = false;
@@ -256,7 +257,7 @@ int embed_launch(const void* table, int bf16, const EmbedArgs& a, const int32_t*
 size_t embed_backward_bytes(int64_t tokens, int64_t rows, int64_t cols);
 int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, const int32_t* ids, int accumulate,
                           void* table, int bf16, void* work, cudaStream_t s);
-int embed_init_device();
+int embed_init_device(int* clusters);  // clusters of 8 CTAs of its sort that run at once
 size_t ortho_bytes(int64_t rows, int64_t cols, int count);
 int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld, int count, const float (*coeffs)[3],
                  int steps, double eps, float scale, void* out, int64_t out_ld, void* work, int sm_budget, cudaStream_t s);

@@ -97,7 +97,7 @@ static int init_device(DeviceState& ds, int dev) {
     if (rc) return rc;
     rc = order_init_device();
     if (rc) return rc;
-    rc = embed_init_device();
+    rc = embed_init_device(&ds.embed_clusters);
     if (rc) return rc;
     rc = ortho_init_device();
     if (rc) return rc;

@@ -121,97 +121,95 @@ __device__ __forceinline__ void store_pairs(__nv_bfloat16* row, int64_t c0, int6
 
 // ---------------------------------------------------------------- lookup
 
-// out[t] = scale * table[ids[t] - first], zeros where that is no row.  A warp takes up to kAhead
-// pieces of kSpan columns at once, all their loads in flight before the first is used: neighbours of
-// one token's row, or where a row has fewer, of several tokens'.  Rows are done one after the other: a
-// block of columns of all tokens after the other reads frequent rows from memory once, but 65536 x 8192
-// bf16 took 318 us that way and 280 this way, whose runs in memory are whole rows.
+// out[t] = scale * table[ids[t] - first], zeros where that is no row.  A warp takes kAhead pieces
+// of kSpan columns, of one token or of several, whose loads are all in flight before the first is used.
 //
 // Rows of bf16 of odd length: pieces of a row that begins at no multiple of 4 bytes begin one column
 // before, so that pairs of values are aligned where they are stored.
-constexpr int kAhead = 4;
-
-struct EmbedLookup {
-    int64_t rows, cols, ld, first, out_ld;
-    int tokens;
-    int spans;         // pieces of a row
-    int block, times;  // pieces of a warp at once: `block` of each of `times` tokens
-    float scale;
-};
+constexpr int kAhead = 2;  // 4 (100 registers): 10007 x 2051 fp32 to bf16 18.4 us, 2: 14.9
 
 template <typename Tt, typename To, int W>
-__global__ void __launch_bounds__(kEmbedThreads, 3)
-    embed_kernel(const Tt* __restrict__ table, const int32_t* __restrict__ ids, To* __restrict__ out, EmbedLookup g) {
+__global__ void __launch_bounds__(kEmbedThreads)
+    embed_kernel(const Tt* __restrict__ table, int64_t rows, int64_t cols, int64_t ld, int64_t first,
+                 const int32_t* __restrict__ ids, int64_t tokens, float scale, To* __restrict__ out, int64_t out_ld) {
     constexpr bool kPairs = W == 1 && sizeof(To) == 2;
     const int lane = threadIdx.x & 31;
-    const unsigned groups = ((unsigned)g.tokens + g.times - 1) / g.times;  // of tokens
-    const int blocks = (g.spans + g.block - 1) / g.block;
-    const int64_t jobs = (int64_t)groups * blocks, step = (int64_t)gridDim.x * kEmbedWarps;
+    const int64_t spans = (cols + (kPairs ? 1 : 0) + kSpan - 1) / kSpan, jobs = tokens * spans;
     chain_wait();
-    int64_t job = (int64_t)blockIdx.x * kEmbedWarps + (threadIdx.x >> 5);
-    const unsigned step_at = (unsigned)(step / blocks);
-    const int step_b = (int)(step - (int64_t)step_at * blocks);
-    unsigned at = (unsigned)(job / blocks);
-    int b = (int)(job - (int64_t)at * blocks);
-    for (; job < jobs; job += step) {
-        int64_t r[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const unsigned t = at * g.times + (g.times > 1 ? u / g.block : 0);
-            r[u] = t < (unsigned)g.tokens ? (int64_t)ids[t] - g.first : -1;
-        }
+    for (int64_t job = ((int64_t)blockIdx.x * kEmbedWarps + (threadIdx.x >> 5)) * kAhead; job < jobs;
+         job += (int64_t)gridDim.x * kEmbedWarps * kAhead) {
         Part<Tt, W> part[kAhead];
-        // piece u: its token and its first column
-        auto token = [&](int u) { return at * g.times + (g.times > 1 ? u / g.block : 0); };
+        int t[kAhead], span[kAhead], id[kAhead];
+        bool have[kAhead];
+        t[0] = (int)(job / spans);
+        span[0] = (int)(job - t[0] * spans);
+#pragma unroll
+        for (int u = 1; u < kAhead; ++u) {
+            const bool over = span[u - 1] + 1 == spans;
+            t[u] = t[u - 1] + over;
+            span[u] = over ? 0 : span[u - 1] + 1;
+        }
+        // the piece's first column
         auto column = [&](int u) {
-            const int64_t c = (int64_t)(b * g.block + (g.times > 1 ? u % g.block : u)) * kSpan;
-            return kPairs && ((uintptr_t)(out + token(u) * g.out_ld) & 2) ? c - 1 : c;
+            const int64_t c = (int64_t)span[u] * kSpan;
+            return kPairs && ((uintptr_t)(out + t[u] * out_ld) & 2) ? c - 1 : c;
         };
-        auto exists = [&](int u) {
-            return u < g.block * g.times && token(u) < (unsigned)g.tokens && b * g.block + (g.times > 1 ? u % g.block : u) < g.spans;
-        };
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) id[u] = t[u] < tokens ? ids[t[u]] : -1;
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            if (!exists(u) || r[u] < 0 || r[u] >= g.rows) continue;
-            const int64_t c0 = column(u);
-            const Tt* from = table + r[u] * g.ld + c0 + lane * W;
-            if (c0 >= 0 && c0 + kSpan <= g.cols) {
-                part[u].template load<true>(from, 0);
-            } else if constexpr (kPairs) {
+            const int64_t r = (int64_t)id[u] - first;
+            have[u] = r >= 0 && r < rows;
+            if constexpr (kPairs) {
+                const int64_t c0 = column(u), at = c0 + lane;
+                const Tt* from = table + r * ld + at;
+                if (have[u] && c0 >= 0 && c0 + kSpan <= cols) {
+                    part[u].template load<true>(from, 0);
+                } else if (have[u]) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (c0 + lane + 32 * q >= 0 && c0 + lane + 32 * q < g.cols)
-                        part[u].w[q] = *reinterpret_cast<const typename Part<Tt, 1>::Word*>(from + 32 * q);
+                    for (int q = 0; q < 8; ++q)
+                        if (at + 32 * q >= 0 && at + 32 * q < cols)
+                            part[u].w[q] = *reinterpret_cast<const typename Part<Tt, 1>::Word*>(from + 32 * q);
+                }
             } else {
-                part[u].template load<false>(from, (int)(g.cols - c0) - lane * W);
+                const int64_t left = cols - column(u);
+                const Tt* from = table + r * ld + column(u) + lane * W;
+                if (have[u] && left >= kSpan) part[u].template load<true>(from, 0);
+                else if (have[u]) part[u].template load<false>(from, (int)left - lane * W);
             }
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            if (!exists(u)) continue;
-            const int64_t c0 = column(u);
-            const bool have = r[u] >= 0 && r[u] < g.rows;
-            To* to = out + token(u) * g.out_ld;
+            if (t[u] >= tokens) break;
             float v[8] = {};
-            if (have) {
+            if (have[u]) {
                 part[u].values(v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= g.scale;
+                for (int i = 0; i < 8; ++i) v[i] *= scale;
             }
             if constexpr (kPairs) {
-                if (have) store_pairs<false>(to, c0, g.cols, v, lane);
-                else store_pairs<true>(to, c0, g.cols, v, lane);
+                if (have[u]) store_pairs<false>(out + t[u] * out_ld, column(u), cols, v, lane);
+                else store_pairs<true>(out + t[u] * out_ld, column(u), cols, v, lane);
             } else {
-                if (c0 + kSpan <= g.cols) Part<To, W>::template store<true>(to + c0 + lane * W, 0, v);
-                else Part<To, W>::template store<false>(to + c0 + lane * W, (int)(g.cols - c0) - lane * W, v);
+                const int64_t left = cols - column(u);
+                To* to = out + t[u] * out_ld + column(u) + lane * W;
+                if (left >= kSpan) Part<To, W>::template store<true>(to, 0, v);
+                else Part<To, W>::template store<false>(to, (int)left - lane * W, v);
             }
         }
-        at += step_at;
-        b += step_b;
-        if (b >= blocks) {
-            b -= blocks;
-            ++at;
-        }
+    }
+}
+
+// A row of zeros, by a warp.
+template <typename Tt, int W>
+__device__ __forceinline__ void zero_row(Tt* row, int64_t cols, int lane) {
+    const float zero[8] = {};
+    if constexpr (W == 1 && sizeof(Tt) == 2) {
+        for (int64_t c = (uintptr_t)row & 2 ? -1 : 0; c < cols; c += kSpan) store_pairs<true>(row, c, cols, zero, lane);
+    } else {
+        int64_t c = 0;
+        for (; c + kSpan <= cols; c += kSpan) Part<Tt, W>::template store<true>(row + c + lane * W, 0, zero);
+        if (c < cols) Part<Tt, W>::template store<false>(row + c + lane * W, (int)(cols - c) - lane * W, zero);
     }
 }
 
@@ -242,10 +240,8 @@ __device__ __forceinline__ int remote_int(uint32_t addr) {
 }
 
 // pairs: where the sorted (row, token) end up; other: as much scratch.
-// touched: 1 for a row of the table that a token names, 0 for others; or NULL.
-__global__ void __launch_bounds__(kSortThreads, 1)
-    embed_sort_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t first, int64_t rows, int bits, int passes,
-                      int2* pairs, int2* other, EmbedOrder* order, uint8_t* touched) {
+__device__ __forceinline__ void sort_by_row(const int32_t* __restrict__ ids, int64_t n, int64_t first, int64_t rows, int bits,
+                                            int passes, int2* pairs, int2* other, EmbedOrder* order) {
     extern __shared__ int shared[];
     const int bins = 1 << bits;
     int* total = shared;                       // [bins] this CTA's, read by the others
@@ -255,14 +251,11 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     __shared__ int warp_sums[kSortWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned before_me = (1u << lane) - 1;
-    const int ctas = (int)gridDim.x, rank = (int)blockIdx.x;
+    constexpr int ctas = kSortCtas;
+    const int rank = (int)cluster_rank();
     int* mine_hist = hist + warp * bins;
     int2* mine_held = held + warp * kSortHeld;
     uint16_t* mine_place = places + warp * kSortHeld;
-    chain_wait();
-    if (touched)
-        for (int64_t i = (int64_t)rank * kSortThreads + threadIdx.x; i < (rows + 15) / 16; i += (int64_t)ctas * kSortThreads)
-            reinterpret_cast<uint4*>(touched)[i] = make_uint4(0, 0, 0, 0);
     if (rank == 0 && threadIdx.x == 0) order->joins = 0;
     int valid = 0;
     for (int pass = 0; pass < passes; ++pass) {
@@ -339,7 +332,7 @@ __global__ void __launch_bounds__(kSortThreads, 1)
         }
         cluster_sync_all();
         int all = sum, before = 0;
-        if (ctas > 1 && d < bins) {
+        if (d < bins) {
             int v[kSortCtas];
 #pragma unroll
             for (int r = 0; r < kSortCtas; ++r) v[r] = remote_int(peer_addr(smem_addr(&total[d]), (uint32_t)r));
@@ -381,7 +374,6 @@ __global__ void __launch_bounds__(kSortThreads, 1)
                 const int at = again ? place(dig) : dig >= 0 ? mine_hist[dig] + mine_place[32 * j + lane] : 0;
                 if (dig < 0) continue;
                 to[at] = p;
-                if (pass == 0 && touched) touched[p.x] = 1;
             }
             __syncwarp();
         }
@@ -390,21 +382,76 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     if (rank == 0 && threadIdx.x == 0) order->valid = valid;
 }
 
+// By clusters 1.. of the sort's launch, while latency bounds the sort: which rows no id names, a bit a row for the
+// sums, and zeros into the first of them.  Each cluster has a run of rows; its CTAs mark what an eighth of the ids
+// name each, in shared memory, and put an eighth of the words together.  Rows of the first `fill` words of a CTA get
+// their zeros here, and bits that say so.  kFillBits rows at a time.
+constexpr int kFillBits = 1 << 18;  // 32 KB of bits
+
+template <typename Tt, int W>
+__device__ __forceinline__ void mark_and_fill(const int32_t* __restrict__ ids, int64_t n, int64_t first, Tt* table, int64_t rows,
+                                              int64_t cols, int64_t ld, int fill, uint32_t* named) {
+    extern __shared__ int shared[];
+    unsigned* marks = reinterpret_cast<unsigned*>(shared);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = (int)cluster_rank();
+    const int64_t clusters = gridDim.x / kSortCtas - 1, mine = blockIdx.x / kSortCtas - 1;
+    const int64_t per = ((rows + 31) / 32 + clusters - 1) / clusters * 32, last = (mine + 1) * per < rows ? (mine + 1) * per : rows;
+    for (int64_t r0 = mine * per; r0 < last; r0 += kFillBits) {
+        const int many = (int)(last - r0 < kFillBits ? last - r0 : kFillBits), words = (many + 31) / 32;
+        for (int i = threadIdx.x; i < words; i += kSortThreads) marks[i] = 0;
+        __syncthreads();
+        const int64_t base = first + r0, step = (int64_t)kSortCtas * kSortThreads;
+        for (int64_t i0 = (int64_t)rank * kSortThreads + threadIdx.x; i0 < n; i0 += 8 * step) {
+            int64_t r[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[j] = i0 + j * step < n ? (int64_t)ids[i0 + j * step] - base : -1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (r[j] >= 0 && r[j] < many) atomicOr(&marks[r[j] >> 5], 1u << (r[j] & 31));
+        }
+        cluster_sync_all();
+        // this CTA's words, of all eight CTAs' marks
+        const int share = (words + kSortCtas - 1) / kSortCtas, from = rank * share, end = min(words, from + share);
+        for (int w = from + warp; w < end; w += kSortWarps) {
+            const unsigned some = lane < kSortCtas ? (unsigned)remote_int(peer_addr(smem_addr(&marks[w]), (uint32_t)lane)) : 0u;
+            const unsigned bits = __reduce_or_sync(kAll, some);
+            if (lane == 0) named[(r0 >> 5) + w] = w - from < fill ? kAll : bits;
+        }
+        __syncwarp();
+        // zeros: the rows of the first words, a warp a row
+        for (int i = warp; i < 32 * min(fill, end - from); i += kSortWarps) {
+            const int w = from + (i >> 5), row = w * 32 + (i & 31);
+            const unsigned some = lane < kSortCtas ? (unsigned)remote_int(peer_addr(smem_addr(&marks[w]), (uint32_t)lane)) : 0u;
+            const unsigned bits = __reduce_or_sync(kAll, some);
+            if (row < many && !(bits >> (i & 31) & 1)) zero_row<Tt, W>(table + (r0 + row) * ld, cols, lane);
+        }
+        cluster_sync_all();  // the marks have been read
+    }
+}
+
+template <typename Tt, int W>
+__global__ void __launch_bounds__(kSortThreads, 1)
+    embed_sort_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t first, int64_t rows, int bits, int passes,
+                      int2* pairs, int2* other, EmbedOrder* order, Tt* table, int64_t cols, int64_t ld, int fill, uint32_t* named) {
+    chain_wait();
+    if (blockIdx.x < kSortCtas) sort_by_row(ids, n, first, rows, bits, passes, pairs, other, order);
+    else mark_and_fill<Tt, W>(ids, n, first, table, rows, cols, ld, fill, named);
+}
+
 // ---------------------------------------------------------------- sums
 //
 // The sorted places are cut into chunks.  A warp adds up kSpan columns of a chunk's
 // tokens, in order.  A row of at most kFew tokens is the business of the chunk that it begins in, wherever it ends; of a longer one that is cut,
 // the part behind a cut goes to heads[chunk] and the part before the first to tails[chunk],
-// and embed_join_kernel adds those up, in the order of the chunks.  Rows that no token
-// names are written as zeros beside, by warps of their own.
+// and embed_join_kernel adds those up, in the order of the chunks.
 struct EmbedSum {
     const int2* pairs;
     EmbedOrder* order;
     int* joins;               // the chunks that such rows begin in
-    const uint8_t* touched;  // NULL: rows without tokens are left as they are
     float* heads;             // [chunks][pitch]
     float* tails;
     int64_t rows, cols, ld, dout_ld, pitch;
+    const uint32_t* named;    // a bit a row that needs no zeros (any more)
     int chunk;
     int accumulate;
     float scale;
@@ -459,19 +506,6 @@ __device__ __forceinline__ void add_row(const EmbedSum& g, Tt* table, int row, i
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = g.accumulate ? fmaf(g.scale, v[i], o[i]) : g.scale * v[i];
     Part<Tt, W>::template store<false>(at, n - lane * W, o);
-}
-
-// A row of zeros, by a warp.
-template <typename Tt, int W>
-__device__ __forceinline__ void zero_row(Tt* row, int64_t cols, int lane) {
-    const float zero[8] = {};
-    if constexpr (W == 1 && sizeof(Tt) == 2) {
-        for (int64_t c = (uintptr_t)row & 2 ? -1 : 0; c < cols; c += kSpan) store_pairs<true>(row, c, cols, zero, lane);
-    } else {
-        int64_t c = 0;
-        for (; c + kSpan <= cols; c += kSpan) Part<Tt, W>::template store<true>(row + c + lane * W, 0, zero);
-        if (c < cols) Part<Tt, W>::template store<false>(row + c + lane * W, (int)(cols - c) - lane * W, zero);
-    }
 }
 
 // Length of the run of ones from bit 0 on.
@@ -553,14 +587,14 @@ __global__ void __launch_bounds__(kEmbedThreads, 2)
             }
         }
     }
+    // rows without tokens that the sort's launch has left, a warp four of them
     if (ACCUMULATE) return;
-    // rows without tokens, a warp four of them
     const int64_t groups = (g.rows + 3) / 4;
     for (job -= jobs; job < groups; job += step) {
-        const uint32_t named = reinterpret_cast<const uint32_t*>(g.touched)[job];
+        const uint32_t done = g.named[job >> 3] >> ((job & 7) * 4);
         for (int i = 0; i < 4; ++i) {
             const int64_t r = job * 4 + i;
-            if (r < g.rows && !(named >> (8 * i) & 1)) zero_row<Tt, W>(table + r * g.ld, g.cols, lane);
+            if (r < g.rows && !(done >> i & 1)) zero_row<Tt, W>(table + r * g.ld, g.cols, lane);
         }
     }
 }
@@ -717,9 +751,32 @@ static size_t sort_smem(int bits) {
     return (sizeof(int) * (kSortWarps + 1) << bits) + (size_t)kSortWarps * kSortHeld * (sizeof(int2) + sizeof(uint16_t));
 }
 
-int embed_init_device() {
-    const int most = (int)sort_smem(kSortBits);
-    cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+template <typename Tt, int W>
+static cudaError_t sort_attr(int* clusters) {
+    const size_t most = sort_smem(kSortBits);
+    cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel<Tt, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e != cudaSuccess || !clusters) return e;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(kSortCtas);
+    c.blockDim = dim3(kSortThreads);
+    c.dynamicSmemBytes = most;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kSortCtas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    c.attrs = &attr;
+    c.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(clusters, embed_sort_kernel<Tt, W>, &c);
+}
+
+int embed_init_device(int* clusters) {
+    cudaError_t e = sort_attr<float, 1>(clusters);
+    if (e == cudaSuccess) e = sort_attr<float, 2>(nullptr);
+    if (e == cudaSuccess) e = sort_attr<float, 4>(nullptr);
+    if (e == cudaSuccess) e = sort_attr<__nv_bfloat16, 1>(nullptr);
+    if (e == cudaSuccess) e = sort_attr<__nv_bfloat16, 2>(nullptr);
+    if (e == cudaSuccess) e = sort_attr<__nv_bfloat16, 4>(nullptr);
+    if (e == cudaSuccess) e = sort_attr<__nv_bfloat16, 8>(nullptr);
     return e == cudaSuccess ? 0 : set_cuda_error(e, "cudaFuncSetAttribute(embedding order)");
 }
 
@@ -752,25 +809,17 @@ int embed_launch(const void* table, int bf16, const EmbedArgs& a, const int32_t*
     DeviceState* ds = device_state();
     if (!ds) return -3;
     const int w = width(a.cols, {table, a.ld, bf16}, {out, a.out_ld, out_bf16});
-    EmbedLookup g;
-    g.rows = a.rows;
-    g.cols = a.cols;
-    g.ld = a.ld;
-    g.first = a.first;
-    g.out_ld = a.out_ld;
-    g.scale = a.scale;
-    g.tokens = (int)a.tokens;
-    g.spans = (int)((a.cols + (w == 1 && out_bf16) + kSpan - 1) / kSpan);  // pairs may begin a column before the row
-    const int blocks = (g.spans + kAhead - 1) / kAhead;
-    g.block = (g.spans + blocks - 1) / blocks;
-    g.times = kAhead / g.block;
-    const int64_t jobs = (a.tokens + g.times - 1) / g.times * ((g.spans + g.block - 1) / g.block);
-    const unsigned grid = up_to(jobs, kEmbedWarps, (int64_t)ds->sm_count * 8);
+    const int64_t jobs = a.tokens * ((a.cols + 1 + kSpan - 1) / kSpan);  // (one more column where pairs begin before a row)
+    // A dozen turns a warp where there are enough: 65536 x 8192 bf16 takes 282 us with as many CTAs as run at
+    // once, 261 with ten times as many, whose runs in memory are nearer together, and 320 with one for each turn.
+    const int64_t some = (int64_t)ds->sm_count * 8, dozen = jobs / (12 * kEmbedWarps * kAhead);
+    const unsigned grid = up_to(jobs, kEmbedWarps * kAhead, dozen > some ? dozen < (1 << 30) ? dozen : 1 << 30 : some);
     const cudaError_t e = by_types(bf16, out_bf16, w, [&](auto t, auto o, auto wide_of) {
         using Tt = decltype(t);
         using To = decltype(o);
         return launch_chained(embed_kernel<Tt, To, decltype(wide_of)::value>, dim3(grid), kEmbedThreads, 0, s, 1,
-                              static_cast<const Tt*>(table), ids, static_cast<To*>(out), g);
+                              static_cast<const Tt*>(table), a.rows, a.cols, a.ld, a.first, ids, a.tokens, a.scale,
+                              static_cast<To*>(out), a.out_ld);
     });
     if (e != cudaSuccess) return set_cuda_error(e, "embedding kernel launch");
     count_launch();
@@ -781,7 +830,7 @@ int embed_launch(const void* table, int bf16, const EmbedArgs& a, const int32_t*
 struct EmbedWork {
     int chunk, chunks;
     int64_t pitch;
-    size_t pairs, other, joins, touched, heads, tails, bytes;
+    size_t pairs, other, joins, named, heads, tails, bytes;
 };
 
 static EmbedWork embed_work(int64_t tokens, int64_t rows, int64_t cols) {
@@ -801,7 +850,7 @@ static EmbedWork embed_work(int64_t tokens, int64_t rows, int64_t cols) {
     w.pairs = part((size_t)tokens * sizeof(int2));
     w.other = part((size_t)tokens * sizeof(int2));
     w.joins = part((size_t)w.chunks * sizeof(int));
-    w.touched = part((size_t)rows);
+    w.named = part((size_t)(rows + 31) / 32 * sizeof(uint32_t));
     w.heads = part((size_t)w.chunks * (size_t)w.pitch * sizeof(float));
     w.tails = part((size_t)w.chunks * (size_t)w.pitch * sizeof(float));
     w.bytes = at;
@@ -819,12 +868,10 @@ int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, c
     int2* pairs = reinterpret_cast<int2*>(base + w.pairs);
     EmbedOrder* order = reinterpret_cast<EmbedOrder*>(base);
     int* joins = reinterpret_cast<int*>(base + w.joins);
-    uint8_t* touched = accumulate ? nullptr : base + w.touched;
     EmbedSum g;
     g.pairs = pairs;
     g.order = order;
     g.joins = joins;
-    g.touched = touched;
     g.heads = reinterpret_cast<float*>(base + w.heads);
     g.tails = reinterpret_cast<float*>(base + w.tails);
     g.rows = a.rows;
@@ -854,10 +901,22 @@ int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, c
     while (bits < 31 && ((int64_t)1 << bits) < a.rows) ++bits;
     const int passes = (bits + kSortBits - 1) / kSortBits;
     bits = (bits + passes - 1) / passes;
-    const int ctas = a.tokens <= 4 * kSortThreads ? 1 : kSortCtas;
-    cudaError_t e = launch_chained(embed_sort_kernel, dim3(ctas), kSortThreads, sort_smem(bits), s,
-                                   (unsigned)ctas, ids, a.tokens, a.first, a.rows, bits, passes, pairs,
-                                   reinterpret_cast<int2*>(base + w.other), order, touched);
+    // Beside the cluster that sorts, as many others as run at once find the rows without tokens, and write
+    // zeros into as many of them, by words of 32 rows a CTA, as the sort leaves time for, at 4.5 TB/s (40009 tokens of
+    // 50021 x 1347 fp32: 104 us with none, 98 this way).
+    const int64_t words = (a.rows + 31) / 32, room = ds->embed_clusters > 1 ? ds->embed_clusters - 1 : 1;
+    const int64_t clusters = accumulate ? 0 : words < room ? words : room;
+    const double sort_us = 10.0 + 2.5e-4 * (double)a.tokens, word_bytes = 32.0 * (double)a.cols * (bf16 ? 2 : 4);
+    const double fill = clusters ? sort_us * 4.5e6 / word_bytes / (double)(clusters * kSortCtas) + 0.5 : 0;
+    uint32_t* named = reinterpret_cast<uint32_t*>(base + w.named);
+    g.named = named;
+    const unsigned ctas = (unsigned)(kSortCtas * (1 + clusters));
+    cudaError_t e = by_types(bf16, bf16, wide, [&](auto t, auto, auto wide_of) {
+        using Tt = decltype(t);
+        return launch_chained(embed_sort_kernel<Tt, decltype(wide_of)::value>, dim3(ctas), kSortThreads, sort_smem(bits), s, kSortCtas,
+                              ids, a.tokens, a.first, a.rows, bits, passes, pairs, reinterpret_cast<int2*>(base + w.other), order,
+                              static_cast<Tt*>(table), a.cols, a.ld, fill < kFillBits ? (int)fill : kFillBits, named);
+    });
     if (e != cudaSuccess) return set_cuda_error(e, "embedding order kernel launch");
     count_launch();
     const unsigned grid = up_to(w.chunks * spans + zeros, kEmbedWarps, most);
