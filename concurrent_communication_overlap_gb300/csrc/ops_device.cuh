@@ -26,9 +26,11 @@ enum OpsWaitSite : int {
 // chain_wait, every access to global memory after it, since chain_wait returns
 // only when the kernel before has ended and its writes are visible.  It also lets
 // the next chained kernel start.
+__device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void chain_ready() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void chain_wait() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    chain_next();
+    chain_ready();
 }
 
 // cluster: CTAs of a cluster (1: none, or the kernel's own).

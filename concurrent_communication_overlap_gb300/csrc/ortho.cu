@@ -8,8 +8,7 @@
 // which nearly cancel, are never rounded apart.
 //
 // The norm and the conversion are two passes over U; a step is three products by one kernel:
-//   A = X X^T and P = a I + b A + c A A   symmetric: tiles on and above the diagonal alone, each
-//                                         written twice;
+//   A = X X^T and P = a I + b A + c A A   symmetric: tiles on and above the diagonal alone;
 //   X <- P X.
 // Operands lie in memory as they are, along K or across it; the tensor cores take either.
 #include "ops_device.cuh"
@@ -17,6 +16,8 @@
 #include "ortho_plan.h"
 
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 namespace c3 {
 
@@ -40,6 +41,7 @@ struct OrthoIn {
     int power;  // 2^power: X's first scale
     float* sums;
     float* scale;
+    int* counts;  // of the products' parts, to be zero before the first
     __half* out;
     int64_t pitch;
 };
@@ -57,6 +59,8 @@ __global__ void __launch_bounds__(kOrthoThreads) ortho_norm_kernel(OrthoIn g) {
     const int64_t spans = (g.cols + kOrthoSpan - 1) / kOrthoSpan, jobs = g.rows * spans;
     constexpr int U = kOrthoSpan / (32 * W);
     chain_wait();
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < kOrthoRuns * 16; i += kOrthoThreads) g.counts[i] = 0;
     for (int64_t i = blockIdx.x; i < (int64_t)g.count * g.parts; i += gridDim.x) {
         const int64_t m = i / g.parts, p = i - m * g.parts;
         const T* x = static_cast<const T*>(g.x) + m * g.rows * g.ld;
@@ -175,6 +179,8 @@ constexpr int kGK = 64;         // K of a stage: 128 bytes
 constexpr int kGSmemLimit = 232448;
 constexpr int kGGroupM = 16;
 
+enum { kAlong = 0, kAcross = 1, kUpper = 2 };
+
 enum OrthoWaitSite : int {
     kSiteOrthoProducer = 16,
     kSiteOrthoMma = 17,
@@ -185,16 +191,19 @@ enum OrthoWaitSite : int {
 // out = alpha A B^T (times scale[m] `times` times) + beta mat + diag I, rounded to fp16 or bf16.
 struct OrthoProduct {
     void* out;
-    const __half* mat;   // NULL, or fp16 at the output's place (fp16 outputs)
     const float* scale;
-    int64_t ld, stride;  // of out, and from one matrix to the next
-    int64_t store_cols;  // columns that may be written
+    int64_t ld, stride;  // of out, and from one matrix to the next (no tensor map)
     int M, N, num_kb, count;
     int bf16, times;
-    int width;           // bytes that rows of out are aligned to
+    int mat;             // beta mat is added: fp16 at the output's place (outputs that are fp16 too)
+    int boxes;           // out has a tensor map, boxes of 32 rows x 64 columns
+    int width;           // bytes that rows of out are aligned to (no tensor map)
     float alpha, beta, diag;
     OrthoTiles tiles;    // symmetric: tiles above the diagonal
-    int64_t per_matrix;  // tiles of one matrix
+    int per_matrix;      // tiles of one matrix
+    OrthoSplit cut;
+    float* parts;        // [runs][2][2 CTAs][8 warps][pieces][8][32 lanes] float4: sums of parts of tiles
+    int* counts;         // [split][16]: parts that are there, by CTA and warp; all zero between products
 };
 
 template <int NT>
@@ -202,7 +211,7 @@ struct OrthoCfg {
     static constexpr uint32_t kABytes = 128 * 128;
     static constexpr uint32_t kBBytes = NT / 2 * 128;
     static constexpr uint32_t kStage = kABytes + kBBytes;
-    static constexpr uint32_t kStaging = kGEpiWarps * 2048;
+    static constexpr uint32_t kStaging = kGEpiWarps * 2 * 4096;  // a warp: two boxes of 32 rows x 64 columns
     static constexpr int kExtra = 1024 + 512 + (int)kStaging;
     static constexpr int kFit = (kGSmemLimit - kExtra) / (int)kStage;
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
@@ -240,29 +249,78 @@ struct OrthoTile {
 };
 
 template <int NT>
-__device__ __forceinline__ OrthoTile ortho_tile(const OrthoProduct& g, int64_t t) {
+__device__ __forceinline__ OrthoTile ortho_tile(const OrthoProduct& g, int t) {
     OrthoTile r;
-    r.m = (int)(t / g.per_matrix);
-    int64_t in = t - r.m * g.per_matrix;
+    r.m = g.count == 1 ? 0 : t / g.per_matrix;
+    const int in = t - r.m * g.per_matrix;
     if (g.tiles.skip) {
         int i = 0;
         while (i + 1 < g.tiles.rows && g.tiles.before(i + 1) <= in) ++i;
         r.row = i * 256;
-        r.col = (int)(in - g.tiles.before(i) + (int64_t)g.tiles.skip * i) * NT;
+        r.col = (in - g.tiles.before(i) + g.tiles.skip * i) * NT;
         return r;
     }
-    const int64_t per = (int64_t)kGGroupM * g.tiles.cols;
-    const int grp = (int)(in / per), first = grp * kGGroupM;
+    if (g.tiles.rows <= kGGroupM) {
+        r.col = in / g.tiles.rows;
+        r.row = (in - r.col * g.tiles.rows) * 256;
+        r.col *= NT;
+        return r;
+    }
+    const int per = kGGroupM * g.tiles.cols;
+    const int grp = in / per, first = grp * kGGroupM;
     const int gm = min(g.tiles.rows - first, kGGroupM);
-    const int at = (int)(in - grp * per);
+    const int at = in - grp * per;
     r.row = (first + at % gm) * 256;
     r.col = at / gm * NT;
     return r;
 }
 
-template <int NT, bool ACROSS_A, bool ACROSS_B>
+// Whether a K block of a symmetric operand's rows, which begin at `row` of a tile, lies below the diagonal's blocks.
+__device__ __forceinline__ bool mirrored(int kb, int row) { return kb * kGK / 256 < row / 256; }
+
+// A pair's i-th piece of work: the parts of tiles of its run, then whole tiles.
+struct OrthoWorkItem {
+    int tile;  // -1: no more
+    int kb0, kb1;
+};
+__device__ __forceinline__ OrthoWorkItem ortho_item(const OrthoSplit& s, int pair, int pairs, int i) {
+    OrthoWorkItem w;
+    const int whole = s.tiles - s.split;
+    if (pair < s.runs) {
+        const unsigned b0 = s.begin(pair), b1 = s.begin(pair + 1), t0 = b0 / (unsigned)s.num_kb;
+        const int parts = (t0 + 1) * (unsigned)s.num_kb < b1 ? 2 : 1;  // a run is no longer than a tile
+        if (i < parts) {
+            const unsigned first = (t0 + i) * (unsigned)s.num_kb, last = first + (unsigned)s.num_kb;
+            w.tile = whole + (int)t0 + i;
+            w.kb0 = (int)((b0 > first ? b0 : first) - first);
+            w.kb1 = (int)((b1 < last ? b1 : last) - first);
+            return w;
+        }
+        i -= parts;
+    }
+    const int64_t t = pair + (int64_t)i * pairs;
+    w.tile = t < whole ? (int)t : -1;
+    w.kb0 = 0;
+    w.kb1 = s.num_kb;
+    return w;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+template <int NT, int A_IS, int B_IS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
-    ortho_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, OrthoProduct g,
+    ortho_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap acrossA, const __grid_constant__ CUtensorMap acrossB,
+                         const __grid_constant__ CUtensorMap tmMat, const __grid_constant__ CUtensorMap tmOut, OrthoProduct g,
                          DevStatus* st) {
     using Cfg = OrthoCfg<NT>;
     constexpr int S = Cfg::kStages;
@@ -272,14 +330,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     uint8_t* gbase = smem_raw + (base - raw);
     const uint32_t staging = base + S * Cfg::kStage;
     uint64_t* bars = reinterpret_cast<uint64_t*>(gbase + S * Cfg::kStage + Cfg::kStaging);
-    // stage full [0, S), empty [S, 2S), accumulator full 2S.., empty 2S+2.., drain 2S+4
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+    // stage full [0, S), empty [S, 2S), accumulator full 2S.., empty 2S+2.., drain 2S+4, a warp's boxes
+    // of the added matrix 2S+5 + 2 warp ..
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 2 * kGEpiWarps);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     auto bar = [&](int i) { return smem_addr(&bars[i]); };
-    const int TFULL = 2 * S, TEMPTY = 2 * S + 2, DRAIN = 2 * S + 4;
+    const int TFULL = 2 * S, TEMPTY = 2 * S + 2, DRAIN = 2 * S + 4, BOX = 2 * S + 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
 
+    chain_next();
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         for (int i = 0; i < S; ++i) {
@@ -291,9 +351,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             mbar_init(bar(TEMPTY + b), 2 * kGEpiWarps);
         }
         mbar_init(bar(DRAIN), 1);
+        for (int b = 0; b < 2 * kGEpiWarps; ++b) mbar_init(bar(BOX + b), 1);
         fence_barrier_init();
-        prefetch_tensormap(&tmA);
-        prefetch_tensormap(&tmB);
+        if (A_IS != kAcross) prefetch_tensormap(&tmA);
+        if (A_IS != kAlong) prefetch_tensormap(&acrossA);
+        if (B_IS != kAcross) prefetch_tensormap(&tmB);
+        if (B_IS != kAlong) prefetch_tensormap(&acrossB);
+        if (g.mat) prefetch_tensormap(&tmMat);
+        if (g.boxes) prefetch_tensormap(&tmOut);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_slot))
@@ -304,9 +369,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     __syncthreads();
     cluster_sync_all();  // both CTAs' barriers are ready before either signals the other's
     tc_fence_after();
-    chain_wait();
+    // (The MMA warp waits for no other grid: it reads shared memory alone.)
     const uint32_t tmem = *tmem_slot;
-    const int64_t total = g.per_matrix * g.count, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -314,10 +379,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int64_t t = first; ok && t < total; t += step) {
-                const OrthoTile tile = ortho_tile<NT>(g, t);
+            for (int i = 0; ok; ++i) {
+                const OrthoWorkItem item = ortho_item(g.cut, pair, pairs, i);
+                if (item.tile < 0) break;
+                const OrthoTile tile = ortho_tile<NT>(g, item.tile);
+                if (i == 0) chain_ready();
                 const int arow = tile.row + (int)rank * 128, brow = tile.col + (int)rank * (NT / 2);
-                for (int kb = 0; kb < g.num_kb; ++kb) {
+                for (int kb = item.kb0; kb < item.kb1; ++kb) {
                     if (!mbar_wait_cluster(bar(S + stage), phase ^ 1u, abort_flag)) {
                         report_error(st, -4, kSiteOrthoProducer);
                         ok = false;
@@ -326,16 +394,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                     const uint32_t sa = base + (uint32_t)stage * Cfg::kStage, sb = sa + Cfg::kABytes;
                     const uint32_t full = leader_addr(bar(stage));
                     if (rank == 0) mbar_arrive_expect_tx(bar(stage), 2 * Cfg::kStage);
-                    if constexpr (ACROSS_A) {
-                        tma_load_3d_pair(sa, &tmA, full, arow, kb * kGK, tile.m, pol_a);
-                        tma_load_3d_pair(sa + 8192, &tmA, full, arow + 64, kb * kGK, tile.m, pol_a);
+                    if (A_IS == kAcross || (A_IS == kUpper && mirrored(kb, tile.row))) {
+                        tma_load_3d_pair(sa, &acrossA, full, arow, kb * kGK, tile.m, pol_a);
+                        tma_load_3d_pair(sa + 8192, &acrossA, full, arow + 64, kb * kGK, tile.m, pol_a);
                     } else {
                         tma_load_3d_pair(sa, &tmA, full, kb * kGK, arow, tile.m, pol_a);
                     }
-                    if constexpr (ACROSS_B) {
+                    if (B_IS == kAcross || (B_IS == kUpper && mirrored(kb, tile.col))) {
 #pragma unroll
                         for (int j = 0; j < NT / 128; ++j)
-                            tma_load_3d_pair(sb + j * 8192, &tmB, full, brow + j * 64, kb * kGK, tile.m, pol_b);
+                            tma_load_3d_pair(sb + j * 8192, &acrossB, full, brow + j * 64, kb * kGK, tile.m, pol_b);
                     } else {
                         tma_load_3d_pair(sb, &tmB, full, kb * kGK, brow, tile.m, pol_b);
                     }
@@ -356,36 +424,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     } else if (warp == 1) {
         if (rank == 0) {
             const uint32_t lead = elect_lane();
-            // D fp32, A and B fp16, which lie along K or across it, N >> 3, M >> 4
-            const uint32_t idesc = (1u << 4) | ((ACROSS_A ? 1u : 0u) << 15) | ((ACROSS_B ? 1u : 0u) << 16) |
-                                   ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
-            const uint64_t a0 = ACROSS_A ? across_desc(base) : along_desc(base);
-            const uint64_t b0 = ACROSS_B ? across_desc(base + Cfg::kABytes) : along_desc(base + Cfg::kABytes);
-            // 16 of K: 32 bytes along a line, or two atoms
-            constexpr uint32_t ka = ACROSS_A ? 2048 >> 4 : 2, kb16 = ACROSS_B ? 2048 >> 4 : 2;
-            int stage = 0, local = 0;
+            // D fp32, A and B fp16, N >> 3, M >> 4; bits 15 and 16 say that A, B lie across
+            const uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+            const uint64_t a_along = along_desc(base), a_across = across_desc(base);
+            const uint64_t b_along = along_desc(base + Cfg::kABytes), b_across = across_desc(base + Cfg::kABytes);
+            int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int64_t t = first; ok && t < total; t += step, ++local) {
+            for (int local = 0; ok; ++local) {
+                const OrthoWorkItem item = ortho_item(g.cut, pair, pairs, local);
+                if (item.tile < 0) break;
                 const int buf = local & 1;
                 if (!mbar_wait_cluster(bar(TEMPTY + buf), ((uint32_t)(local >> 1) & 1u) ^ 1u, abort_flag)) {
                     report_error(st, -4, kSiteOrthoMma);
                     break;
                 }
                 tc_fence_after();
+                const OrthoTile tile = ortho_tile<NT>(g, item.tile);
                 const uint32_t d = tmem + (uint32_t)(buf * NT);
-                for (int kb = 0; kb < g.num_kb; ++kb) {
+                for (int kb = item.kb0; kb < item.kb1; ++kb) {
                     if (!mbar_wait_cluster(bar(stage), phase, abort_flag)) {
                         report_error(st, -4, kSiteOrthoMma);
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t ad = a0 + (uint64_t)((uint32_t)stage * (Cfg::kStage >> 4));
-                    const uint64_t bd = b0 + (uint64_t)((uint32_t)stage * (Cfg::kStage >> 4));
+                    const bool ta = A_IS == kAcross || (A_IS == kUpper && mirrored(kb, tile.row));
+                    const bool tb = B_IS == kAcross || (B_IS == kUpper && mirrored(kb, tile.col));
+                    const uint64_t at = (uint64_t)((uint32_t)stage * (Cfg::kStage >> 4));
+                    const uint64_t ad = (ta ? a_across : a_along) + at, bd = (tb ? b_across : b_along) + at;
+                    // 16 of K: 32 bytes along a line, or two atoms
+                    const uint32_t ka = ta ? 2048 >> 4 : 2, kb16 = tb ? 2048 >> 4 : 2;
+                    const uint32_t id = idesc | (ta ? 1u << 15 : 0u) | (tb ? 1u << 16 : 0u);
 #pragma unroll
                     for (int k = 0; k < kGK / 16; ++k)
-                        mma_pair(lead, d, ad + (uint64_t)(k * ka), bd + (uint64_t)(k * kb16), idesc, k > 0 ? 1u : (uint32_t)(kb > 0));
+                        mma_pair(lead, d, ad + (uint64_t)(k * ka), bd + (uint64_t)(k * kb16), id, k > 0 ? 1u : (uint32_t)(kb > item.kb0));
                     commit_pair(lead, bar(S + stage));
                     if (++stage == S) {
                         stage = 0;
@@ -401,78 +474,168 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         }
     } else {
         const int q = warp & 3, half = (warp - 2) >> 2;
-        const uint32_t blk = staging + (uint32_t)(warp - 2) * 2048u;
-        constexpr int kPieces = NT / 64;  // of 32 columns: half of the tile's
-        int local = 0;
-        for (int64_t t = first; t < total; t += step, ++local) {
-            const OrthoTile tile = ortho_tile<NT>(g, t);
+        const uint32_t box0 = staging + (uint32_t)(warp - 2) * 8192u;
+        constexpr int kRounds = NT / 128;  // of 64 columns: half of the tile's
+        chain_ready();
+        uint32_t mat_phase = 0;
+        for (int local = 0;; ++local) {
+            const OrthoWorkItem item = ortho_item(g.cut, pair, pairs, local);
+            if (item.tile < 0) break;
+            const OrthoTile tile = ortho_tile<NT>(g, item.tile);
             const int buf = local & 1;
+            const int row0 = tile.row + (int)rank * 128 + q * 32, col0 = tile.col + half * (NT / 2);
+            const bool cut = item.kb1 - item.kb0 < g.num_kb;
+            const int place = item.tile - (g.cut.tiles - g.cut.split);  // among the cut tiles
+            int run0 = 0, run1 = 0;                                     // the runs that have parts of the tile
+            // What is added, on its way while the products run: into the boxes that the results go out from.
+            auto fetch = [&] {
+                if (lane == 0) {
+                    bulk_wait_read<0>();
+#pragma unroll
+                    for (int rd = 0; rd < kRounds; ++rd) {
+                        const uint32_t b = bar(BOX + (warp - 2) * 2 + rd);
+                        mbar_arrive_expect_tx(b, 4096);
+                        tma_load_3d(box0 + (uint32_t)rd * 4096u, &tmMat, b, col0 + rd * 64, row0, tile.m);
+                    }
+                }
+                __syncwarp();
+            };
+            if (g.mat && !cut) fetch();
             const bool ready = mbar_wait_cluster(bar(TFULL + buf), (uint32_t)(local >> 1) & 1u, abort_flag);
             if (!__all_sync(kAll, ready)) {
                 report_error(st, -4, kSiteOrthoEpilogue);
+                volatile int no_abort = 0;  // what is on its way into the boxes has to land before the CTA ends
+                for (int rd = 0; g.mat && !cut && rd < kRounds; ++rd) mbar_wait(bar(BOX + (warp - 2) * 2 + rd), mat_phase, &no_abort);
                 break;
             }
             tc_fence_after();
-            const int row0 = tile.row + (int)rank * 128 + q * 32, col0 = tile.col + half * (NT / 2);
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * NT + half * (NT / 2));
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(leader_addr(bar(TEMPTY + buf)));
+            };
+            // this warp's place in the part that `run` has of the tile
+            auto part_of = [&](int run) {
+                const int which = run == run0 ? place - (int)(g.cut.begin(run) / (unsigned)g.num_kb) : 0;
+                return reinterpret_cast<float4*>(g.parts) + (((run * 2 + which) * 2 + (int)rank) * kGEpiWarps + (warp - 2)) * (kRounds * 512) + lane;
+            };
+            if (cut) {
+                run0 = g.cut.run_of((unsigned)place * (unsigned)g.num_kb);
+                run1 = g.cut.run_of((unsigned)(place + 1) * (unsigned)g.num_kb - 1);
+                float4* mine = part_of(pair);
+#pragma unroll 1
+                for (int p = 0; p < 2 * kRounds; ++p) {
+                    uint32_t r[32];
+                    tmem_ld32(taddr + (uint32_t)(p * 32), r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        __stcg(mine + (p * 8 + j) * 32, make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                                                    __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
+                }
+                release();
+                __threadfence();
+                __syncwarp();
+                int there = 0;
+                int* count = g.counts + place * 16 + (int)rank * kGEpiWarps + (warp - 2);
+                if (lane == 0) {
+                    there = atomicAdd(count, 1);
+                    if (there == run1 - run0) *count = 0;  // the last: nobody else comes
+                }
+                if (__shfl_sync(kAll, there, 0) != run1 - run0) continue;
+                __threadfence();
+                if (g.mat) fetch();
+            }
             float alpha = g.alpha;
             for (int i = 0; i < g.times; ++i) alpha *= g.scale[tile.m];
-            uint16_t* out = static_cast<uint16_t*>(g.out) + tile.m * g.stride;
-            const int64_t place = tile.m * g.stride + (int64_t)(row0 + lane) * g.ld;
-            // Read out and rounded first: the accumulator is free again before anything is stored.
-            uint32_t v[kPieces][16];
-#pragma unroll
-            for (int p = 0; p < kPieces; ++p) {
-                const int c0 = col0 + p * 32;
-                uint32_t r[32];
-                tmem_ld32(taddr + (uint32_t)(p * 32), r);
-                uint4 old[4];
+            // 64 columns at a time, and 32 of them, in loops that are left rolled: what spills here goes all the way to L2,
+            // since shared memory leaves L1 next to nothing (1.3 KB of spills took the experts' 684 us to 1198).
+#pragma unroll 1
+            for (int rd = 0; rd < kRounds; ++rd) {
+                const uint32_t box = box0 + (uint32_t)rd * 4096u;
                 if (g.mat) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        old[j] = row0 + lane < g.M && c0 + 8 * j < g.store_cols
-                                     ? *reinterpret_cast<const uint4*>(g.mat + place + c0 + 8 * j)
-                                     : make_uint4(0, 0, 0, 0);
+                    const bool in = mbar_wait(bar(BOX + (warp - 2) * 2 + rd), mat_phase, abort_flag);
+                    if (!__all_sync(kAll, in)) report_error(st, -4, kSiteOrthoEpilogue);
+                } else {
+                    if (lane == 0) bulk_wait_read<kRounds - 1>();  // what the box held a tile ago has left it
+                    __syncwarp();
                 }
-                tmem_ld_wait();
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const int p = 2 * rd + h, c0 = col0 + p * 32;
+                    uint32_t r[32];
+                    if (cut) {  // the parts in order, whoever adds them up
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float x = alpha * __uint_as_float(r[2 * j]), y = alpha * __uint_as_float(r[2 * j + 1]);
-                    if (g.mat) {
-                        const uint32_t w = j % 4 == 0 ? old[j / 4].x : j % 4 == 1 ? old[j / 4].y : j % 4 == 2 ? old[j / 4].z : old[j / 4].w;
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-                        x = fmaf(g.beta, f.x, x);
-                        y = fmaf(g.beta, f.y, y);
-                        if (row0 + lane == c0 + 2 * j) x += g.diag;
-                        if (row0 + lane == c0 + 2 * j + 1) y += g.diag;
-                    }
-                    if (g.bf16) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-                        v[p][j] = *reinterpret_cast<const uint32_t*>(&h);
+                        for (int j = 0; j < 32; ++j) r[j] = 0;
+#pragma unroll 1
+                        for (int run = run0; run <= run1; ++run) {
+                            const float4* from = part_of(run) + p * 256;
+                            float4 t[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) t[j] = __ldcg(from + j * 32);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + t[j].x);
+                                r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + t[j].y);
+                                r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + t[j].z);
+                                r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + t[j].w);
+                            }
+                        }
                     } else {
-                        const __half2 h = __floats2half2_rn(x, y);
-                        v[p][j] = *reinterpret_cast<const uint32_t*>(&h);
+                        tmem_ld32(taddr + (uint32_t)(p * 32), r);
+                        tmem_ld_wait();
+                        if (p + 1 == 2 * kRounds) release();
+                    }
+                    // lane's row of the box: 16-byte chunk j at j ^ (row % 8), as the tensor maps have it
+                    const uint32_t line = box + (uint32_t)lane * 128u;
+                    uint32_t v[16];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t o[4] = {0, 0, 0, 0};
+                        if (g.mat) ld_shared_v4(line + (uint32_t)(((4 * h + j) ^ (lane & 7)) << 4), o);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int i = 4 * j + k;
+                            float a = alpha * __uint_as_float(r[2 * i]), b = alpha * __uint_as_float(r[2 * i + 1]);
+                            if (g.mat) {
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
+                                a = fmaf(g.beta, f.x, a);
+                                b = fmaf(g.beta, f.y, b);
+                                if (row0 + lane == c0 + 2 * i) a += g.diag;
+                                if (row0 + lane == c0 + 2 * i + 1) b += g.diag;
+                            }
+                            if (g.bf16) {
+                                const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+                                v[i] = *reinterpret_cast<const uint32_t*>(&x);
+                            } else {
+                                const __half2 x = __floats2half2_rn(a, b);
+                                v[i] = *reinterpret_cast<const uint32_t*>(&x);
+                            }
+                        }
+                    }
+                    if (g.boxes) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            st_shared_v4(line + (uint32_t)(((4 * h + j) ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    } else {
+                        store_piece<uint16_t>(v, box, lane, g.width, static_cast<uint16_t*>(g.out) + tile.m * g.stride, row0, g.M - row0, c0,
+                                              g.N, g.ld);
+                    }
+                }
+                if (g.boxes) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (row0 < g.M && col0 + rd * 64 < g.N) tma_store_3d(&tmOut, box, col0 + rd * 64, row0, tile.m);
+                        bulk_commit();
                     }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(leader_addr(bar(TEMPTY + buf)));
-#pragma unroll
-            for (int p = 0; p < kPieces; ++p) {
-                const int c0 = col0 + p * 32;
-                if (g.tiles.skip && c0 < row0) continue;  // below the diagonal: another piece's mirror image
-                store_piece<uint16_t>(v[p], blk, lane, g.width, out, row0, g.M - row0, c0, (int)g.store_cols, g.ld);
-                if (g.tiles.skip && c0 > row0 && row0 + lane < g.M) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        uint16_t* to = out + (int64_t)(c0 + 2 * j) * g.ld + row0 + lane;
-                        if (c0 + 2 * j < g.N) to[0] = (uint16_t)v[p][j];
-                        if (c0 + 2 * j + 1 < g.N) to[g.ld] = (uint16_t)(v[p][j] >> 16);
-                    }
-                }
-            }
+            if (g.mat) mat_phase ^= 1u;
         }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -485,33 +648,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 
 // ---------------------------------------------------------------- host side
 
-template <typename F>
+template <int NT, typename F>
 static int each_product(F f) {
-    int rc = f(ortho_product_kernel<256, false, false>, OrthoCfg<256>::kSmem);
-    if (!rc) rc = f(ortho_product_kernel<256, true, true>, OrthoCfg<256>::kSmem);
-    if (!rc) rc = f(ortho_product_kernel<256, false, true>, OrthoCfg<256>::kSmem);
-    if (!rc) rc = f(ortho_product_kernel<128, false, false>, OrthoCfg<128>::kSmem);
-    if (!rc) rc = f(ortho_product_kernel<128, true, true>, OrthoCfg<128>::kSmem);
-    if (!rc) rc = f(ortho_product_kernel<128, false, true>, OrthoCfg<128>::kSmem);
+    const int smem = OrthoCfg<NT>::kSmem;
+    int rc = f(ortho_product_kernel<NT, kAlong, kAlong>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kAcross, kAcross>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kUpper, kUpper>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kUpper, kAcross>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kAlong, kUpper>, smem);
     return rc;
 }
 
 int ortho_init_device() {
-    return each_product([](auto kernel, int smem) {
+    auto allow = [](auto kernel, int smem) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         return e == cudaSuccess ? 0 : set_cuda_error(e, "cudaFuncSetAttribute(orthogonalisation)");
-    });
+    };
+    const int rc = each_product<256>(allow);
+    return rc ? rc : each_product<128>(allow);
 }
 
-// fp16 matrices [count][rows][pitch], in boxes of 64 columns x box_rows.  What lies past a matrix reads as zeros.
-static int ortho_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t pitch, int count, int box_rows) {
+// fp16 or bf16 matrices [count][rows][pitch], in boxes of 64 columns x box_rows.  What lies past a matrix reads as zeros.
+static int ortho_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t pitch, int count, int box_rows, bool bf16) {
     EncodeTiledFn fn = tensor_map_encode();
     if (!fn) return set_error(-3, "cuTensorMapEncodeTiled entry point unavailable");
     cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
     cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)(rows * pitch) * 2};
     cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
+    CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? 0 : set_error(-3, "cuTensorMapEncodeTiled (orthogonalisation) failed");
@@ -555,6 +720,7 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
     in.power = step[0].x;
     in.sums = reinterpret_cast<float*>(base + w.sums);
     in.scale = reinterpret_cast<float*>(base + w.scale);
+    in.counts = reinterpret_cast<int*>(base + w.counts);
     in.out = reinterpret_cast<__half*>(base + w.x0);
     in.pitch = w.xpitch;
     // a part has at least 32 rows' worth of work for its warps, and every SM has a part
@@ -577,41 +743,55 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
     const bool narrow = num_r * ((cols + 255) / 256) * count < cap / 2;
     const int nt = narrow ? 128 : 256;
     auto blocks = [](int64_t n, int by) { return (int)((n + by - 1) / by); };
-    auto product = [&](bool across_a, bool across_b, const CUtensorMap& a, const CUtensorMap& b, OrthoProduct& g) -> int {
-        g.per_matrix = g.tiles.skip ? g.tiles.total() : (int64_t)g.tiles.rows * g.tiles.cols;
-        const int64_t tiles = g.per_matrix * count, pairs = cap / 2;
-        const dim3 ctas((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
-        auto go = [&](auto kernel, int smem) { return launch_chained(kernel, ctas, kGThreads, smem, s, 1, a, b, g, ds->status); };
-        cudaError_t err;
-        if (narrow) {
-            const int sm = OrthoCfg<128>::kSmem;
-            err = across_a ? go(ortho_product_kernel<128, true, true>, sm)
-                           : across_b ? go(ortho_product_kernel<128, false, true>, sm) : go(ortho_product_kernel<128, false, false>, sm);
-        } else {
-            const int sm = OrthoCfg<256>::kSmem;
-            err = across_a ? go(ortho_product_kernel<256, true, true>, sm)
-                           : across_b ? go(ortho_product_kernel<256, false, true>, sm) : go(ortho_product_kernel<256, false, false>, sm);
-        }
+    __half* X[2] = {reinterpret_cast<__half*>(base + w.x0), reinterpret_cast<__half*>(base + w.x1)};
+    __half* G = reinterpret_cast<__half*>(base + w.g);
+    __half* P = reinterpret_cast<__half*>(base + w.p);
+    CUtensorMap xm[2][3], gm[3], pm[3], om;  // boxes of 128, 64 and 32 rows; of the output
+    // (A box's last 16-byte unit of a row is written whole.  What so lies behind rows of X, A and P are zeros, of
+    // operands' rows that do not exist.)
+    const bool boxes = (uintptr_t)out % 16 == 0 && out_ld % 8 == 0 && cols % 8 == 0;
+    int rc = 0;
+    for (int j = 0; j < 3 && !rc; ++j) {
+        const int box = 128 >> j;
+        for (int i = 0; i < 2 && !rc; ++i) rc = ortho_map(&xm[i][j], X[i], rows, cols, w.xpitch, count, box, false);
+        if (!rc) rc = ortho_map(&gm[j], G, m, m, w.gpitch, count, box, false);
+        if (!rc) rc = ortho_map(&pm[j], P, m, m, w.gpitch, count, box, false);
+    }
+    if (!rc) rc = boxes ? ortho_map(&om, out, rows, cols, out_ld, count, 32, true) : 0;
+    if (!boxes) om = xm[0][2];
+    if (rc) return rc;
+
+    // Which product: an operand's two maps are its boxes of 128 and of 64 rows.
+    enum { kGramWide, kGramTall, kPoly, kApplyWide, kApplyTall };
+    auto product = [&](int which, const CUtensorMap (&a)[3], const CUtensorMap (&b)[3], const CUtensorMap& to, OrthoProduct& g) -> int {
+        const int64_t all = g.tiles.total() * count;
+        if (all > 0x7FFFFFFF) return set_error(-5, "orthogonalisation: more than 2^31 tiles");
+        g.per_matrix = (int)g.tiles.total();
+        const int tiles = (int)all, pairs = cap / 2;
+        g.cut = ortho_split(tiles, g.num_kb, pairs);
+        g.parts = reinterpret_cast<float*>(base + w.parts);
+        g.counts = in.counts;
+        const int some = tiles < g.cut.runs ? g.cut.runs : tiles;
+        const dim3 ctas((unsigned)(2 * (some < pairs ? some : pairs)));
+        auto by_width = [&](auto nt_of) {
+            constexpr int NT = decltype(nt_of)::value;
+            auto go = [&](auto kernel) {
+                // A along K in boxes of 128 rows, B in boxes of NT / 2; either across K in boxes of 64
+                return launch_chained(kernel, ctas, kGThreads, OrthoCfg<NT>::kSmem, s, 1, a[0], b[NT == 128], a[1], b[1], gm[2], to, g, ds->status);
+            };
+            switch (which) {
+                case kGramWide: return go(ortho_product_kernel<NT, kAlong, kAlong>);
+                case kGramTall: return go(ortho_product_kernel<NT, kAcross, kAcross>);
+                case kPoly: return go(ortho_product_kernel<NT, kUpper, kUpper>);
+                case kApplyWide: return go(ortho_product_kernel<NT, kUpper, kAcross>);
+                default: return go(ortho_product_kernel<NT, kAlong, kUpper>);
+            }
+        };
+        const cudaError_t err = narrow ? by_width(std::integral_constant<int, 128>()) : by_width(std::integral_constant<int, 256>());
         if (err != cudaSuccess) return set_cuda_error(err, "orthogonalisation: product kernel launch");
         count_launch();
         return 0;
     };
-    __half* X[2] = {reinterpret_cast<__half*>(base + w.x0), reinterpret_cast<__half*>(base + w.x1)};
-    __half* G = reinterpret_cast<__half*>(base + w.g);
-    __half* P = reinterpret_cast<__half*>(base + w.p);
-    // In boxes of 128 and of 64 rows: A along K; B along K in boxes of nt / 2; either across K in boxes of 64.
-    CUtensorMap x128[2], x64[2], g128, g64, p128, p64;
-    int rc = 0;
-    for (int i = 0; i < 2 && !rc; ++i) {
-        rc = ortho_map(&x128[i], X[i], rows, cols, w.xpitch, count, 128);
-        if (!rc) rc = ortho_map(&x64[i], X[i], rows, cols, w.xpitch, count, 64);
-    }
-    if (!rc) rc = ortho_map(&g128, G, m, m, w.gpitch, count, 128);
-    if (!rc) rc = ortho_map(&g64, G, m, m, w.gpitch, count, 64);
-    if (!rc) rc = ortho_map(&p128, P, m, m, w.gpitch, count, 128);
-    if (!rc) rc = ortho_map(&p64, P, m, m, w.gpitch, count, 64);
-    if (rc) return rc;
-
     for (int i = 0; i < steps; ++i) {
         const OrthoStep& t = step[i];
         const int now = i & 1;
@@ -620,29 +800,24 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
         g.scale = in.scale;
         g.count = count;
         // A = X X^T (X^T X): the stored 2^x X give 2^2x of it
-        g.out = G;
-        g.ld = g.store_cols = w.gpitch;
-        g.stride = m * w.gpitch;
+        g.boxes = 1;
         g.M = g.N = (int)m;
         g.num_kb = blocks(tall ? rows : cols, kGK);
-        g.width = 16;
         g.times = i == 0 ? 2 : 0;
         g.alpha = two(t.g - 2 * t.x);
         g.tiles = OrthoTiles{blocks(m, 256), blocks(m, nt), 256 / nt};
-        rc = tall ? product(true, true, x64[now], x64[now], g) : product(false, false, x128[now], narrow ? x64[now] : x128[now], g);
-        if (rc) return rc;
+        if ((rc = product(tall ? kGramTall : kGramWide, xm[now], xm[now], gm[2], g))) return rc;
         // P = a I + b A + c A A
-        g.out = P;
-        g.mat = G;
+        g.mat = 1;
         g.num_kb = blocks(m, kGK);
         g.times = 0;
         g.alpha = t.c * two(t.p - 2 * t.g);
         g.beta = t.b * two(t.p - t.g);
         g.diag = t.a * two(t.p);
-        if ((rc = product(false, false, g128, narrow ? g64 : g128, g))) return rc;
+        if ((rc = product(kPoly, gm, gm, pm[2], g))) return rc;
         // X <- P X (X P)
         const bool last = i + 1 == steps;
-        g.mat = nullptr;
+        g.mat = 0;
         g.M = (int)rows;
         g.N = (int)cols;
         g.times = i == 0 ? 1 : 0;
@@ -650,18 +825,15 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
         g.bf16 = last;
         g.tiles = OrthoTiles{(int)num_r, blocks(cols, nt), 0};
         if (last) {
+            g.boxes = boxes;
             g.out = out;
             g.ld = out_ld;
             g.stride = rows * out_ld;
-            g.store_cols = cols;
             const uintptr_t bits = (uintptr_t)out | (uintptr_t)(2 * out_ld) | (uintptr_t)(2 * cols);
-            g.width = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
-        } else {
-            g.out = X[now ^ 1];
-            g.ld = g.store_cols = w.xpitch;
-            g.stride = rows * w.xpitch;
+            g.width = bits % 4 == 0 ? 4 : 2;
         }
-        rc = tall ? product(false, false, x128[now], narrow ? p64 : p128, g) : product(false, true, p128, x64[now], g);
+        const CUtensorMap& to = last ? om : xm[now ^ 1][2];
+        rc = tall ? product(kApplyTall, xm[now], pm, to, g) : product(kApplyWide, pm, xm[now], to, g);
         if (rc) return rc;
     }
     return 0;

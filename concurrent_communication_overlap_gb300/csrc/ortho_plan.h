@@ -71,18 +71,56 @@ struct OrthoTiles {
 #ifdef __CUDACC__
     __host__ __device__
 #endif
-    int64_t before(int i) const { return (int64_t)i * cols - (int64_t)skip * i * (i - 1) / 2; }
+    int before(int i) const { return i * cols - skip * (i * (i - 1) / 2); }
     int64_t total() const {
-        int64_t t = 0;
-        for (int i = 0; i < rows; ++i) t += cols - (int64_t)skip * i > 0 ? cols - (int64_t)skip * i : 0;
-        return t;
+        return skip ? (int64_t)rows * cols - (int64_t)skip * rows * (rows - 1) / 2 : (int64_t)rows * cols;
     }
 };
+
+// How a product's tiles are dealt out to pairs of SMs.  Whole turns of all pairs take whole tiles; the
+// `split` tiles left over are laid end to end, by K blocks, and cut into as many runs as `runs` says, a pair each.
+// A tile that several runs have a part of is put together from their fp32 sums by whoever comes last.
+constexpr int kOrthoRuns = 80;  // at most: each has room for two parts of tiles
+
+struct OrthoSplit {
+    int tiles;        // of the product
+    int split, runs;  // 0: none
+    int num_kb;       // at most 2^18, so that 80 x 80 of them have 32-bit numbers
+#ifdef __CUDACC__
+    __host__ __device__
+#endif
+    unsigned begin(int run) const { return (unsigned)run * (unsigned)split * (unsigned)num_kb / (unsigned)runs; }
+    // The run that has a K block.
+#ifdef __CUDACC__
+    __host__ __device__
+#endif
+    int run_of(unsigned block) const { return (int)(((block + 1) * (unsigned)runs - 1) / ((unsigned)split * (unsigned)num_kb)); }
+};
+
+// In K blocks of a tile (0.27 us where 256 x 256 tiles are fed from L2): a part costs 5 to write and read back, the
+// meeting 8.  The tiles left over take a whole one's time; cut, their share of the runs' and the parts' of one tile.
+inline OrthoSplit ortho_split(int tiles, int num_kb, int pairs) {
+    OrthoSplit s{tiles, 0, 0, num_kb};
+    const int left = tiles % pairs;
+    if (left == 0 || num_kb <= 16) return s;
+    const int64_t most = pairs < kOrthoRuns ? pairs : kOrthoRuns, blocks = (int64_t)left * num_kb;
+    int64_t best = num_kb - 2;
+    for (int64_t runs = left + 1; runs <= most && runs <= 8 * left; ++runs) {
+        const int64_t each = (blocks + runs - 1) / runs, parts = (runs + left - 1) / left + (runs % left ? 1 : 0);
+        const int64_t cost = each + 5 * parts + 8;
+        if (each >= 4 && cost < best) {
+            best = cost;
+            s.split = left;
+            s.runs = (int)runs;
+        }
+    }
+    return s;
+}
 
 // The workspace: where each part begins, in bytes; pitches in elements.
 struct OrthoWork {
     int64_t xpitch, gpitch, short_side;
-    size_t scale, sums, x0, x1, g, p, bytes;
+    size_t scale, sums, counts, x0, x1, g, p, parts, bytes;
 };
 
 constexpr int kOrthoParts = 512;  // partial sums of a matrix's norm at most
@@ -90,8 +128,8 @@ constexpr int kOrthoParts = 512;  // partial sums of a matrix's norm at most
 inline OrthoWork ortho_work(int64_t rows, int64_t cols, int count) {
     OrthoWork w;
     w.short_side = rows < cols ? rows : cols;
-    w.xpitch = (cols + 7) / 8 * 8;
-    w.gpitch = (w.short_side + 7) / 8 * 8;
+    w.xpitch = (cols + 15) / 16 * 16;  // rows of whole 32-byte sectors
+    w.gpitch = (w.short_side + 15) / 16 * 16;
     size_t at = 0;
     auto part = [&](size_t bytes) {
         const size_t from = at;
@@ -100,12 +138,15 @@ inline OrthoWork ortho_work(int64_t rows, int64_t cols, int count) {
     };
     w.scale = part((size_t)count * sizeof(float));
     w.sums = part((size_t)count * kOrthoParts * 3 * sizeof(float));
+    w.counts = part((size_t)kOrthoRuns * 16 * sizeof(int));
     const size_t x = (size_t)count * (size_t)rows * (size_t)w.xpitch * 2;
     const size_t g = (size_t)count * (size_t)w.short_side * (size_t)w.gpitch * 2;
     w.x0 = part(x);
     w.x1 = part(x);
     w.g = part(g);
     w.p = part(g);
+    // (no product of fewer K blocks is cut)
+    w.parts = part(rows > 1024 || cols > 1024 ? (size_t)kOrthoRuns * 2 * 256 * 256 * sizeof(float) : 0);
     w.bytes = at;
     return w;
 }

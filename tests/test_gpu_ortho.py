@@ -122,6 +122,21 @@ def test_error_before_the_output_is_rounded(c3):  # noqa: F811
         assert both ** 2 - own ** 2 <= (3.4445 * F) ** 2 * 5, (rows, cols, own, both)
 
 
+@pytest.mark.parametrize("ty,count,rows,cols,budget", [
+    (1, 1, 200, 9000, 0), (1, 1, 9000, 200, 0), (0, 1, 1500, 2100, 0), (1, 1, 2100, 1500, 0), (1, 2, 300, 4000, 0),
+    (1, 3, 1100, 1090, 0), (0, 1, 64, 20011, 0), (1, 1, 700, 3000, 20), (1, 1, 3000, 700, 34), (1, 1, 2600, 2700, 0)])
+def test_products_that_are_cut_along_k(c3, ty, count, rows, cols, budget):  # noqa: F811
+    """Long sums and few tiles: parts of a tile from several pairs, put together by the last; the same bits every time."""
+    rng = np.random.default_rng(rows * 5 + cols)
+    x = torch.from_numpy(momentum(rng, count, rows, cols)).cuda().to(TD[ty])
+    out = run(c3, x, ty, count, rows, cols, [QUINTIC] * 3, sm_budget=budget)
+    c3.c3_status_check()
+    for i in range(count):
+        assert relative(out[i], oracle(x[i].double(), [QUINTIC] * 3)) <= 3.4445 * F * 3 + H
+    for _ in range(5):
+        assert torch.equal(run(c3, x, ty, count, rows, cols, [QUINTIC] * 3, sm_budget=budget), out)
+
+
 def test_singular_values_near_one(c3):  # noqa: F811
     rng = np.random.default_rng(4)
     q, _ = np.linalg.qr(rng.standard_normal((300, 200)))

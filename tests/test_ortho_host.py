@@ -24,11 +24,12 @@ def c3():
 def test_workspace_sizes(c3):
     size = c3.c3_orthogonalize_bytes
     assert size(-1, 8) == size(8, -1) == size(8, 8, -1) == size(1 << 25, 8) == size(8, 1 << 25) == size(8, 8, 65536) == 0
-    # two fp16 copies of x and two square matrices on the shorter side, rows of whole 16 bytes
-    for m, n, k in ((1, 1, 1), (5, 9, 3), (300, 77, 2), (4096, 4096, 1)):
+    # two fp16 copies of x and two square matrices on the shorter side, rows of whole 32 bytes
+    for m, n, k in ((1, 1, 1), (5, 9, 3), (300, 77, 2), (1024, 1000, 7), (4096, 4096, 1)):
         s = min(m, n)
-        need = k * (2 * m * -(-n // 8) * 16 + 2 * s * -(-s // 8) * 16)
-        assert need <= size(m, n, k) <= need + k * 512 * 12 + 4 * k + 2048, (m, n, k)
+        need = k * (2 * m * -(-n // 16) * 32 + 2 * s * -(-s // 16) * 32)
+        parts = 160 * 256 * 256 * 4 if max(m, n) > 1024 else 0  # fp32 sums of parts of products
+        assert need + parts <= size(m, n, k) <= need + parts + k * 512 * 12 + 4 * k + 80 * 64 + 2048, (m, n, k)
 
 
 def test_refusals(c3):
@@ -63,6 +64,16 @@ int main(int n, char** v) {
     const c3::OrthoTiles t{atoi(v[2]), atoi(v[3]), atoi(v[4])};
     printf("%lld", (long long)t.total());
     for (int i = 0; i <= t.rows; ++i) printf(" %lld", (long long)t.before(i));
+    return 0;
+  }
+  if (v[1][0] == 's') {
+    const c3::OrthoSplit s = c3::ortho_split(atoll(v[2]), atoi(v[3]), atoll(v[4]));
+    printf("%d %d\n", s.split, s.runs);
+    if (s.runs) {
+      for (int r = 0; r <= s.runs; ++r) printf("%lld ", (long long)s.begin(r));
+      printf("\n");
+      for (long long u = 0; u < (long long)s.split * s.num_kb; ++u) printf("%d ", s.run_of(u));
+    }
     return 0;
   }
   float c[c3::kOrthoSteps][3];
@@ -118,3 +129,21 @@ def test_tiles_cover_the_upper_triangle_once(plan, n, width):
         seen.add((i, t - before[i] + skip * i))
     want = {(i, j) for i in range(rows) for j in range(cols) if (j + 1) * width > i * 256}
     assert seen == want and total == len(want)
+
+
+@pytest.mark.parametrize("tiles,num_kb,pairs", [
+    (21, 79, 76), (1, 100, 76), (5, 17, 76), (136, 64, 76), (256, 64, 76), (77, 200, 76), (3584, 128, 76), (75, 300, 76),
+    (12, 40, 8), (7, 1000, 3), (2, 26, 1), (152, 500, 76), (40, 260, 64), (3, 16, 76), (90, 33, 128)])
+def test_a_products_tiles_are_dealt_out_once(plan, tiles, num_kb, pairs):
+    """Every K block of every tile goes to one pair, no run is longer than a tile, and the runs that a block's tile is
+    put together from are those that have a part of it."""
+    out = plan("s", tiles, num_kb, pairs).split("\n")
+    split, runs = map(int, out[0].split())
+    assert split == 0 or (split == tiles % pairs and split < runs <= min(pairs, 80) and num_kb > 16)
+    begin = list(map(int, out[1].split()))
+    if not split:
+        return
+    assert begin[0] == 0 and begin[-1] == split * num_kb and len(begin) == runs + 1
+    assert all(4 <= b - a <= num_kb for a, b in zip(begin, begin[1:]))
+    owner = list(map(int, out[2].split()))
+    assert owner == [max(q for q in range(runs) if begin[q] <= u) for u in range(split * num_kb)]
