@@ -52,12 +52,44 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// A warp's pieces of kOrthoSpan columns, `step` apart, as rows and spans.
+struct OrthoWalk {
+    int64_t row;
+    int span, spans, span_step;
+    int64_t row_step;
+    __device__ __forceinline__ OrthoWalk(int64_t at, int64_t step, int64_t width) {
+        spans = (int)((width + kOrthoSpan - 1) / kOrthoSpan);
+        row = at / spans;
+        span = (int)(at - row * spans);
+        row_step = step / spans;
+        span_step = (int)(step - row_step * spans);
+    }
+    __device__ __forceinline__ void next() {
+        row += row_step;
+        span += span_step;
+        if (span >= spans) span -= spans, ++row;
+    }
+};
+constexpr int kOrthoAhead = 4;  // pieces of which a warp has the loads in flight
+
+// The warp's values of a piece, 8 a lane.
+template <typename T, int W>
+__device__ __forceinline__ void load_piece(const OrthoIn& g, const T* x, const OrthoWalk& at, int lane, float (&v)[8]) {
+    const int64_t c0 = (int64_t)at.span * kOrthoSpan + lane * W;
+    const T* from = x + at.row * g.ld + c0;
+#pragma unroll
+    for (int u = 0; u < 8 / W; ++u) {
+        float t[W] = {};
+        if (at.row < g.rows && c0 + 32 * W * u < g.cols) load_w<W>(from + 32 * W * u, t);
+#pragma unroll
+        for (int k = 0; k < W; ++k) v[u * W + k] = t[k];
+    }
+}
+
 template <typename T, int W>
 __global__ void __launch_bounds__(kOrthoThreads) ortho_norm_kernel(OrthoIn g) {
     __shared__ float part[3][kOrthoWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t spans = (g.cols + kOrthoSpan - 1) / kOrthoSpan, jobs = g.rows * spans;
-    constexpr int U = kOrthoSpan / (32 * W);
     chain_wait();
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < kOrthoRuns * 16; i += kOrthoThreads) g.counts[i] = 0;
@@ -65,20 +97,18 @@ __global__ void __launch_bounds__(kOrthoThreads) ortho_norm_kernel(OrthoIn g) {
         const int64_t m = i / g.parts, p = i - m * g.parts;
         const T* x = static_cast<const T*>(g.x) + m * g.rows * g.ld;
         float low = 0.0f, mid = 0.0f, high = 0.0f;
-#pragma unroll 4
-        for (int64_t job = p * kOrthoWarps + warp; job < jobs; job += (int64_t)g.parts * kOrthoWarps) {
-            const int64_t r = job / spans, c0 = (job - r * spans) * kOrthoSpan + lane * W;
-            float v[U][W] = {};
+        OrthoWalk at(p * kOrthoWarps + warp, (int64_t)g.parts * kOrthoWarps, g.cols);
+        while (at.row < g.rows) {
+            float v[kOrthoAhead][8];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (c0 + 32 * W * u < g.cols) load_w<W>(x + r * g.ld + c0 + 32 * W * u, v[u]);
+            for (int a = 0; a < kOrthoAhead; ++a, at.next()) load_piece<T, W>(g, x, at, lane, v[a]);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int a = 0; a < kOrthoAhead; ++a)
 #pragma unroll
-                for (int k = 0; k < W; ++k) {
-                    const float l = v[u][k] * kTiny, h = v[u][k] * kHuge;
+                for (int k = 0; k < 8; ++k) {
+                    const float l = v[a][k] * kTiny, h = v[a][k] * kHuge;
                     low = fmaf(l, l, low);
-                    mid = fmaf(v[u][k], v[u][k], mid);
+                    mid = fmaf(v[a][k], v[a][k], mid);
                     high = fmaf(h, h, high);
                 }
         }
@@ -104,8 +134,6 @@ template <typename T, int W>
 __global__ void __launch_bounds__(kOrthoThreads) ortho_convert_kernel(OrthoIn g) {
     __shared__ float factors[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t spans = (g.pitch + kOrthoSpan - 1) / kOrthoSpan, jobs = g.rows * spans;
-    constexpr int U = kOrthoSpan / (32 * W);
     chain_wait();
     for (int64_t i = blockIdx.x; i < (int64_t)g.count * g.parts; i += gridDim.x) {
         const int64_t m = i / g.parts, p = i - m * g.parts;
@@ -137,29 +165,33 @@ __global__ void __launch_bounds__(kOrthoThreads) ortho_convert_kernel(OrthoIn g)
         const float f0 = factors[0], f1 = factors[1];
         const T* x = static_cast<const T*>(g.x) + m * g.rows * g.ld;
         __half* out = g.out + m * g.rows * g.pitch;
-#pragma unroll 2
-        for (int64_t job = p * kOrthoWarps + warp; job < jobs; job += (int64_t)g.parts * kOrthoWarps) {
-            const int64_t r = job / spans, c0 = (job - r * spans) * kOrthoSpan + lane * W;
-            float v[U][W] = {};
+        OrthoWalk at(p * kOrthoWarps + warp, (int64_t)g.parts * kOrthoWarps, g.pitch);
+        while (at.row < g.rows) {
+            float v[2][8];
+            OrthoWalk to = at;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (c0 + 32 * W * u < g.cols) load_w<W>(x + r * g.ld + c0 + 32 * W * u, v[u]);
+            for (int a = 0; a < 2; ++a, at.next()) load_piece<T, W>(g, x, at, lane, v[a]);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t c = c0 + 32 * W * u;
-                if (c >= g.pitch) continue;
-                __half* to = out + r * g.pitch + c;
-                if constexpr (W == 1) {
-                    *to = __float2half_rn(v[u][0] * f0 * f1);
-                } else {
-                    uint32_t h[W / 2];
+            for (int a = 0; a < 2; ++a, to.next()) {
+                if (to.row >= g.rows) break;
+                const int64_t c0 = (int64_t)to.span * kOrthoSpan + lane * W;
 #pragma unroll
-                    for (int k = 0; k < W / 2; ++k) {
-                        const __half2 t = __floats2half2_rn(v[u][2 * k] * f0 * f1, v[u][2 * k + 1] * f0 * f1);
-                        h[k] = *reinterpret_cast<const uint32_t*>(&t);
+                for (int u = 0; u < 8 / W; ++u) {
+                    const int64_t c = c0 + 32 * W * u;
+                    if (c >= g.pitch) continue;
+                    __half* h = out + to.row * g.pitch + c;
+                    if constexpr (W == 1) {
+                        *h = __float2half_rn(v[a][u] * f0 * f1);
+                    } else {
+                        uint32_t w[W / 2];
+#pragma unroll
+                        for (int k = 0; k < W / 2; ++k) {
+                            const __half2 t = __floats2half2_rn(v[a][u * W + 2 * k] * f0 * f1, v[a][u * W + 2 * k + 1] * f0 * f1);
+                            w[k] = *reinterpret_cast<const uint32_t*>(&t);
+                        }
+                        if constexpr (W == 8) *reinterpret_cast<uint4*>(h) = make_uint4(w[0], w[1], w[2], w[3]);
+                        else *reinterpret_cast<uint32_t*>(h) = w[0];
                     }
-                    if constexpr (W == 8) *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
-                    else *reinterpret_cast<uint32_t*>(to) = h[0];
                 }
             }
         }
@@ -500,27 +532,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 }
                 __syncwarp();
             };
-            if (g.mat && !cut) fetch();
-            const bool ready = mbar_wait_cluster(bar(TFULL + buf), (uint32_t)(local >> 1) & 1u, abort_flag);
-            if (!__all_sync(kAll, ready)) {
-                report_error(st, -4, kSiteOrthoEpilogue);
-                volatile int no_abort = 0;  // what is on its way into the boxes has to land before the CTA ends
-                for (int rd = 0; g.mat && !cut && rd < kRounds; ++rd) mbar_wait(bar(BOX + (warp - 2) * 2 + rd), mat_phase, &no_abort);
-                break;
-            }
-            tc_fence_after();
-            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * NT + half * (NT / 2));
             auto release = [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(leader_addr(bar(TEMPTY + buf)));
+            };
+            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * NT + half * (NT / 2));
+            // The tile's sums are there.
+            auto sums_ready = [&] {
+                const bool ready = mbar_wait_cluster(bar(TFULL + buf), (uint32_t)(local >> 1) & 1u, abort_flag);
+                if (!__all_sync(kAll, ready)) {
+                    report_error(st, -4, kSiteOrthoEpilogue);
+                    volatile int no_abort = 0;  // what is on its way into the boxes has to land before the CTA ends
+                    for (int rd = 0; g.mat && !cut && rd < kRounds; ++rd) mbar_wait(bar(BOX + (warp - 2) * 2 + rd), mat_phase, &no_abort);
+                    return false;
+                }
+                tc_fence_after();
+                return true;
             };
             // this warp's place in the part that `run` has of the tile
             auto part_of = [&](int run) {
                 const int which = run == run0 ? place - (int)(g.cut.begin(run) / (unsigned)g.num_kb) : 0;
                 return reinterpret_cast<float4*>(g.parts) + (((run * 2 + which) * 2 + (int)rank) * kGEpiWarps + (warp - 2)) * (kRounds * 512) + lane;
             };
+            if (g.mat && !cut) fetch();
             if (cut) {
+                if (!sums_ready()) break;
                 run0 = g.cut.run_of((unsigned)place * (unsigned)g.num_kb);
                 run1 = g.cut.run_of((unsigned)(place + 1) * (unsigned)g.num_kb - 1);
                 float4* mine = part_of(pair);
@@ -551,10 +588,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             for (int i = 0; i < g.times; ++i) alpha *= g.scale[tile.m];
             // 64 columns at a time, and 32 of them, in loops that are left rolled: what spills here goes all the way to L2,
             // since shared memory leaves L1 next to nothing (1.3 KB of spills took the experts' 684 us to 1198).
+            //
+            // The first tile is preceded by a round on nothing, which stores nothing: the warps would wait for the tile's sums,
+            // and so they bring the round's instructions in meanwhile (a product of a small matrix is a chain of first times).
+            // Not where the boxes are already being filled.
+            bool ok = true;
 #pragma unroll 1
-            for (int rd = 0; rd < kRounds; ++rd) {
-                const uint32_t box = box0 + (uint32_t)rd * 4096u;
-                if (g.mat) {
+            for (int rd = local == 0 && !cut && !g.mat ? -1 : 0; rd < kRounds; ++rd) {
+                if (rd == 0 && !cut) {
+                    ok = sums_ready();
+                    if (!ok) break;
+                }
+                const uint32_t box = box0 + (uint32_t)(rd < 0 ? 0 : rd) * 4096u;
+                if (rd < 0) {
+                } else if (g.mat) {
                     const bool in = mbar_wait(bar(BOX + (warp - 2) * 2 + rd), mat_phase, abort_flag);
                     if (!__all_sync(kAll, in)) report_error(st, -4, kSiteOrthoEpilogue);
                 } else {
@@ -569,23 +616,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) r[j] = 0;
 #pragma unroll 1
-                        for (int run = run0; run <= run1; ++run) {
-                            const float4* from = part_of(run) + p * 256;
-                            float4 t[8];
+                        for (int run = run0; run <= run1; run += 2) {
+                            float4 t[2][8];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) t[j] = __ldcg(from + j * 32);
+                            for (int k = 0; k < 2; ++k) {
+                                const float4* from = part_of(run + k) + p * 256;
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + t[j].x);
-                                r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + t[j].y);
-                                r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + t[j].z);
-                                r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + t[j].w);
+                                for (int j = 0; j < 8; ++j) t[k][j] = run + k <= run1 ? __ldcg(from + j * 32) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                             }
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + t[k][j].x);
+                                    r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + t[k][j].y);
+                                    r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + t[k][j].z);
+                                    r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + t[k][j].w);
+                                }
                         }
-                    } else {
+                    } else if (rd >= 0) {
                         tmem_ld32(taddr + (uint32_t)(p * 32), r);
                         tmem_ld_wait();
                         if (p + 1 == 2 * kRounds) release();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = 0;
                     }
                     // lane's row of the box: 16-byte chunk j at j ^ (row % 8), as the tensor maps have it
                     const uint32_t line = box + (uint32_t)lane * 128u;
@@ -618,7 +673,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             st_shared_v4(line + (uint32_t)(((4 * h + j) ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                    } else {
+                    } else if (rd >= 0) {
                         store_piece<uint16_t>(v, box, lane, g.width, static_cast<uint16_t*>(g.out) + tile.m * g.stride, row0, g.M - row0, c0,
                                               g.N, g.ld);
                     }
@@ -626,12 +681,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 if (g.boxes) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
+                    if (lane == 0 && rd >= 0) {
                         if (row0 < g.M && col0 + rd * 64 < g.N) tma_store_3d(&tmOut, box, col0 + rd * 64, row0, tile.m);
                         bulk_commit();
                     }
                 }
             }
+            if (!ok) break;
             if (g.mat) mat_phase ^= 1u;
         }
         if (lane == 0) bulk_wait_all();
@@ -639,7 +695,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();  // nothing of this CTA's is signalled or read by the other any more
+    cluster_meet();  // nothing of this CTA's is signalled or read by the other any more
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");

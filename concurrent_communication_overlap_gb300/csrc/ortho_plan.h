@@ -97,17 +97,21 @@ struct OrthoSplit {
     int run_of(unsigned block) const { return (int)(((block + 1) * (unsigned)runs - 1) / ((unsigned)split * (unsigned)num_kb)); }
 };
 
-// In K blocks of a tile (0.27 us where 256 x 256 tiles are fed from L2): a part costs 5 to write and read back, the
-// meeting 8.  The tiles left over take a whole one's time; cut, their share of the runs' and the parts' of one tile.
+constexpr int kOrthoFewest = 8;  // K blocks of a tile that is cut, at least
+
+// The tiles left over would take a whole one's time; cut, their share of the runs'.  In K blocks (0.27 to 0.34 us
+// for 256 x 256 tiles), a part costs 4 or 5 to write and read back, which stops its pair's next tile where it has one,
+// and where no whole tiles hide it the meeting another 8.  (16 matrices of 1024 x 2048: 8 of 160 tiles of 32 blocks are
+// left; in 64 parts the product took 50 us, whole 36.)
 inline OrthoSplit ortho_split(int tiles, int num_kb, int pairs) {
     OrthoSplit s{tiles, 0, 0, num_kb};
     const int left = tiles % pairs;
-    if (left == 0 || num_kb <= 16) return s;
+    if (left == 0 || num_kb < kOrthoFewest) return s;
     const int64_t most = pairs < kOrthoRuns ? pairs : kOrthoRuns, blocks = (int64_t)left * num_kb;
     int64_t best = num_kb - 2;
     for (int64_t runs = left + 1; runs <= most && runs <= 8 * left; ++runs) {
         const int64_t each = (blocks + runs - 1) / runs, parts = (runs + left - 1) / left + (runs % left ? 1 : 0);
-        const int64_t cost = each + 5 * parts + 8;
+        const int64_t cost = each + (tiles > pairs ? 4 * parts : 5 * parts + 8);
         if (each >= 4 && cost < best) {
             best = cost;
             s.split = left;
@@ -146,7 +150,7 @@ inline OrthoWork ortho_work(int64_t rows, int64_t cols, int count) {
     w.g = part(g);
     w.p = part(g);
     // (no product of fewer K blocks is cut)
-    w.parts = part(rows > 1024 || cols > 1024 ? (size_t)kOrthoRuns * 2 * 256 * 256 * sizeof(float) : 0);
+    w.parts = part(rows > (kOrthoFewest - 1) * 64 || cols > (kOrthoFewest - 1) * 64 ? (size_t)kOrthoRuns * 2 * 256 * 256 * sizeof(float) : 0);
     w.bytes = at;
     return w;
 }
