@@ -25,13 +25,14 @@ constexpr unsigned kAll = 0xffffffffu;
 
 // ---------------------------------------------------------------- norm and conversion
 
-constexpr int kOrthoThreads = 1024;
+constexpr int kOrthoThreads = 512;  // two CTAs an SM
 constexpr int kOrthoWarps = kOrthoThreads / 32;
 constexpr int kOrthoSpan = 256;
 
-// Squares of values are summed three times, times 2^-140, 1 and 2^140: whatever the magnitudes, one of
-// the sums neither overflows nor loses what matters.
+// Sums of squares are fp32 within a CTA, where their total is far from both ends of fp32's range, and fp64 between
+// CTAs.  A CTA whose total is not (or is no number) adds its squares up again times 2^-140 and 2^140.
 constexpr float kTiny = 8.470329472543003e-22f, kHuge = 1.1805916207174113e21f;  // 2^-70, 2^70
+constexpr double kTwo140 = 2.0 * 1180591620717411303424.0 * 590295810358705651712.0;
 
 struct OrthoIn {
     const void* x;
@@ -39,7 +40,7 @@ struct OrthoIn {
     int count, parts;
     double eps;
     int power;  // 2^power: X's first scale
-    float* sums;
+    double* sums;
     float* scale;
     int* counts;  // of the products' parts, to be zero before the first
     __half* out;
@@ -87,8 +88,8 @@ __device__ __forceinline__ void load_piece(const OrthoIn& g, const T* x, const O
 }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kOrthoThreads) ortho_norm_kernel(OrthoIn g) {
-    __shared__ float part[3][kOrthoWarps];
+__global__ void __launch_bounds__(kOrthoThreads, 2) ortho_norm_kernel(OrthoIn g) {
+    __shared__ float part[kOrthoWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     chain_wait();
     if (blockIdx.x == 0)
@@ -96,34 +97,34 @@ __global__ void __launch_bounds__(kOrthoThreads) ortho_norm_kernel(OrthoIn g) {
     for (int64_t i = blockIdx.x; i < (int64_t)g.count * g.parts; i += gridDim.x) {
         const int64_t m = i / g.parts, p = i - m * g.parts;
         const T* x = static_cast<const T*>(g.x) + m * g.rows * g.ld;
-        float low = 0.0f, mid = 0.0f, high = 0.0f;
-        OrthoWalk at(p * kOrthoWarps + warp, (int64_t)g.parts * kOrthoWarps, g.cols);
-        while (at.row < g.rows) {
-            float v[kOrthoAhead][8];
+        // the CTA's sum of squares of what `scaled` makes of the values
+        auto squares = [&](auto scaled) {
+            float sum = 0.0f;
+            OrthoWalk at(p * kOrthoWarps + warp, (int64_t)g.parts * kOrthoWarps, g.cols);
+            while (at.row < g.rows) {
+                float v[kOrthoAhead][8];
 #pragma unroll
-            for (int a = 0; a < kOrthoAhead; ++a, at.next()) load_piece<T, W>(g, x, at, lane, v[a]);
+                for (int a = 0; a < kOrthoAhead; ++a, at.next()) load_piece<T, W>(g, x, at, lane, v[a]);
 #pragma unroll
-            for (int a = 0; a < kOrthoAhead; ++a)
+                for (int a = 0; a < kOrthoAhead; ++a)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float l = v[a][k] * kTiny, h = v[a][k] * kHuge;
-                    low = fmaf(l, l, low);
-                    mid = fmaf(v[a][k], v[a][k], mid);
-                    high = fmaf(h, h, high);
-                }
-        }
-        float s[3] = {low, mid, high};
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            s[k] = warp_sum(s[k]);
-            if (lane == 0) part[k][warp] = s[k];
-        }
-        __syncthreads();
-        if (warp < 3) {
-            const float t = warp_sum(part[warp][lane]);
-            if (lane == 0) g.sums[(m * g.parts + p) * 3 + warp] = t;
-        }
-        __syncthreads();
+                    for (int k = 0; k < 8; ++k) {
+                        const float t = scaled(v[a][k]);
+                        sum = fmaf(t, t, sum);
+                    }
+            }
+            sum = warp_sum(sum);
+            if (lane == 0) part[warp] = sum;
+            __syncthreads();
+            sum = warp_sum(lane < kOrthoWarps ? part[lane] : 0.0f);
+            __syncthreads();
+            return sum;
+        };
+        const float sum = squares([](float v) { return v; });
+        double total = sum;
+        if (!(sum < 1e36f)) total = (double)squares([](float v) { return v * kTiny; }) * kTwo140;
+        else if (sum < 1e-18f) total = (double)squares([](float v) { return v * kHuge; }) / kTwo140;
+        if (threadIdx.x == 0) g.sums[m * g.parts + p] = total;
     }
 }
 
@@ -131,31 +132,24 @@ __global__ void __launch_bounds__(kOrthoThreads) ortho_norm_kernel(OrthoIn g) {
 // division, 2^e / (|U| + eps) in (1, 2], goes to scale[m] and into the first step's products.  A NaN or an
 // infinity makes the whole matrix NaN.
 template <typename T, int W>
-__global__ void __launch_bounds__(kOrthoThreads) ortho_convert_kernel(OrthoIn g) {
+__global__ void __launch_bounds__(kOrthoThreads, 2) ortho_convert_kernel(OrthoIn g) {
     __shared__ float factors[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     chain_wait();
     for (int64_t i = blockIdx.x; i < (int64_t)g.count * g.parts; i += gridDim.x) {
         const int64_t m = i / g.parts, p = i - m * g.parts;
         if (warp == 0) {
-            float s[3] = {};
-#pragma unroll 4
-            for (int j = lane; j < g.parts; j += 32)
+            double sum = 0.0;
+            for (int j = lane; j < g.parts; j += 32) sum += g.sums[m * g.parts + j];
 #pragma unroll
-                for (int k = 0; k < 3; ++k) s[k] += g.sums[(m * g.parts + j) * 3 + k];
-#pragma unroll
-            for (int k = 0; k < 3; ++k) s[k] = warp_sum(s[k]);
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
             if (lane == 0) {
-                const double one = 2.0 * 1180591620717411303424.0 * 590295810358705651712.0;  // 2^140
-                double sum = s[1];
-                if (!(sum < 1e36)) sum = s[0] * one;
-                else if (sum < 1e-18) sum = s[2] / one;
                 const double r = sqrt(sum) + g.eps;
                 int e = 0;
                 const double f = frexp(r, &e);
                 const bool fine = isfinite(r);
-                // two factors: one alone may leave fp32's range
-                const int half = fine ? (g.power - e) / 2 : 0;
+                // two factors where one alone may leave fp32's range
+                const int half = !fine ? 0 : abs(g.power - e) < 120 ? g.power - e : (g.power - e) / 2;
                 factors[0] = fine ? (r > 0 ? (float)ldexp(1.0, half) : 0.0f) : __int_as_float(0x7fc00000);
                 factors[1] = fine ? (float)ldexp(1.0, g.power - e - half) : 0.0f;
                 if (p == 0) g.scale[m] = fine && r > 0 ? (float)(1.0 / f) : 1.0f;
@@ -171,6 +165,10 @@ __global__ void __launch_bounds__(kOrthoThreads) ortho_convert_kernel(OrthoIn g)
             OrthoWalk to = at;
 #pragma unroll
             for (int a = 0; a < 2; ++a, at.next()) load_piece<T, W>(g, x, at, lane, v[a]);
+            if (f1 != 1.0f) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k / 8][k % 8] *= f1;
+            }
 #pragma unroll
             for (int a = 0; a < 2; ++a, to.next()) {
                 if (to.row >= g.rows) break;
@@ -181,12 +179,12 @@ __global__ void __launch_bounds__(kOrthoThreads) ortho_convert_kernel(OrthoIn g)
                     if (c >= g.pitch) continue;
                     __half* h = out + to.row * g.pitch + c;
                     if constexpr (W == 1) {
-                        *h = __float2half_rn(v[a][u] * f0 * f1);
+                        *h = __float2half_rn(v[a][u] * f0);
                     } else {
                         uint32_t w[W / 2];
 #pragma unroll
                         for (int k = 0; k < W / 2; ++k) {
-                            const __half2 t = __floats2half2_rn(v[a][u * W + 2 * k] * f0 * f1, v[a][u * W + 2 * k + 1] * f0 * f1);
+                            const __half2 t = __floats2half2_rn(v[a][u * W + 2 * k] * f0, v[a][u * W + 2 * k + 1] * f0);
                             w[k] = *reinterpret_cast<const uint32_t*>(&t);
                         }
                         if constexpr (W == 8) *reinterpret_cast<uint4*>(h) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -774,7 +772,7 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
     in.count = count;
     in.eps = eps;
     in.power = step[0].x;
-    in.sums = reinterpret_cast<float*>(base + w.sums);
+    in.sums = reinterpret_cast<double*>(base + w.sums);
     in.scale = reinterpret_cast<float*>(base + w.scale);
     in.counts = reinterpret_cast<int*>(base + w.counts);
     in.out = reinterpret_cast<__half*>(base + w.x0);

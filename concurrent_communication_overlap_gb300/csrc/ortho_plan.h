@@ -141,7 +141,7 @@ inline OrthoWork ortho_work(int64_t rows, int64_t cols, int count) {
         return from;
     };
     w.scale = part((size_t)count * sizeof(float));
-    w.sums = part((size_t)count * kOrthoParts * 3 * sizeof(float));
+    w.sums = part((size_t)count * kOrthoParts * sizeof(double));
     w.counts = part((size_t)kOrthoRuns * 16 * sizeof(int));
     const size_t x = (size_t)count * (size_t)rows * (size_t)w.xpitch * 2;
     const size_t g = (size_t)count * (size_t)w.short_side * (size_t)w.gpitch * 2;

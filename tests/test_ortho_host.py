@@ -29,7 +29,7 @@ def test_workspace_sizes(c3):
         s = min(m, n)
         need = k * (2 * m * -(-n // 16) * 32 + 2 * s * -(-s // 16) * 32)
         parts = 160 * 256 * 256 * 4 if max(m, n) > 448 else 0  # fp32 sums of parts of products
-        assert need + parts <= size(m, n, k) <= need + parts + k * 512 * 12 + 4 * k + 80 * 64 + 2048, (m, n, k)
+        assert need + parts <= size(m, n, k) <= need + parts + k * 512 * 8 + 4 * k + 80 * 64 + 2048, (m, n, k)
 
 
 def test_refusals(c3):
