@@ -792,10 +792,6 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
     if (e != cudaSuccess) return set_cuda_error(e, "orthogonalisation: norm kernel launch");
     count_launch();
 
-    const int64_t num_r = (rows + 255) / 256;
-    // Narrower tiles where wider ones would leave SMs idle.
-    const bool narrow = num_r * ((cols + 255) / 256) * count < cap / 2;
-    const int nt = narrow ? 128 : 256;
     auto blocks = [](int64_t n, int by) { return (int)((n + by - 1) / by); };
     __half* X[2] = {reinterpret_cast<__half*>(base + w.x0), reinterpret_cast<__half*>(base + w.x1)};
     __half* G = reinterpret_cast<__half*>(base + w.g);
@@ -816,16 +812,17 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
     if (rc) return rc;
 
     // Which product: an operand's two maps are its boxes of 128 and of 64 rows.
-    enum { kGramWide, kGramTall, kPoly, kApplyWide, kApplyTall };
+    enum { kGramWide, kGramTall, kPoly, kApplyWide, kApplyTall };  // the first three symmetric
     auto product = [&](int which, const CUtensorMap (&a)[3], const CUtensorMap (&b)[3], const CUtensorMap& to, OrthoProduct& g) -> int {
-        const int64_t all = g.tiles.total() * count;
-        if (all > 0x7FFFFFFF) return set_error(-5, "orthogonalisation: more than 2^31 tiles");
-        g.per_matrix = (int)g.tiles.total();
-        const int tiles = (int)all, pairs = cap / 2;
-        g.cut = ortho_split(tiles, g.num_kb, pairs);
+        const int pairs = cap / 2;
+        const OrthoPlan plan = ortho_plan(g.M, g.N, which <= kPoly, g.num_kb, count, pairs);
+        if (plan.total > 0x7FFFFFFF) return set_error(-5, "orthogonalisation: more than 2^31 tiles");
+        g.tiles = plan.tiles;
+        g.per_matrix = (int)plan.tiles.total();
+        g.cut = plan.cut;
         g.parts = reinterpret_cast<float*>(base + w.parts);
         g.counts = in.counts;
-        const int some = tiles < g.cut.runs ? g.cut.runs : tiles;
+        const int some = g.cut.tiles < g.cut.runs ? g.cut.runs : g.cut.tiles;
         const dim3 ctas((unsigned)(2 * (some < pairs ? some : pairs)));
         auto by_width = [&](auto nt_of) {
             constexpr int NT = decltype(nt_of)::value;
@@ -841,7 +838,7 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
                 default: return go(ortho_product_kernel<NT, kAlong, kUpper>);
             }
         };
-        const cudaError_t err = narrow ? by_width(std::integral_constant<int, 128>()) : by_width(std::integral_constant<int, 256>());
+        const cudaError_t err = plan.nt == 128 ? by_width(std::integral_constant<int, 128>()) : by_width(std::integral_constant<int, 256>());
         if (err != cudaSuccess) return set_cuda_error(err, "orthogonalisation: product kernel launch");
         count_launch();
         return 0;
@@ -859,7 +856,6 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
         g.num_kb = blocks(tall ? rows : cols, kGK);
         g.times = i == 0 ? 2 : 0;
         g.alpha = two(t.g - 2 * t.x);
-        g.tiles = OrthoTiles{blocks(m, 256), blocks(m, nt), 256 / nt};
         if ((rc = product(tall ? kGramTall : kGramWide, xm[now], xm[now], gm[2], g))) return rc;
         // P = a I + b A + c A A
         g.mat = 1;
@@ -877,7 +873,6 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
         g.times = i == 0 ? 1 : 0;
         g.alpha = last ? scale * two(-t.p - t.x) : two(t.next - t.p - t.x);
         g.bf16 = last;
-        g.tiles = OrthoTiles{(int)num_r, blocks(cols, nt), 0};
         if (last) {
             g.boxes = boxes;
             g.out = out;

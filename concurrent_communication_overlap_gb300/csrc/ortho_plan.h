@@ -99,26 +99,49 @@ struct OrthoSplit {
 
 constexpr int kOrthoFewest = 8;  // K blocks of a tile that is cut, at least
 
-// The tiles left over would take a whole one's time; cut, their share of the runs'.  In K blocks (0.27 to 0.34 us
-// for 256 x 256 tiles), a part costs 4 or 5 to write and read back, which stops its pair's next tile where it has one,
-// and where no whole tiles hide it the meeting another 8.  (16 matrices of 1024 x 2048: 8 of 160 tiles of 32 blocks are
-// left; in 64 parts the product took 50 us, whole 36.)
-inline OrthoSplit ortho_split(int tiles, int num_kb, int pairs) {
-    OrthoSplit s{tiles, 0, 0, num_kb};
-    const int left = tiles % pairs;
-    if (left == 0 || num_kb < kOrthoFewest) return s;
-    const int64_t most = pairs < kOrthoRuns ? pairs : kOrthoRuns, blocks = (int64_t)left * num_kb;
-    int64_t best = num_kb - 2;
-    for (int64_t runs = left + 1; runs <= most && runs <= 8 * left; ++runs) {
-        const int64_t each = (blocks + runs - 1) / runs, parts = (runs + left - 1) / left + (runs % left ? 1 : 0);
-        const int64_t cost = each + (tiles > pairs ? 4 * parts : 5 * parts + 8);
-        if (each >= 4 && cost < best) {
-            best = cost;
-            s.split = left;
-            s.runs = (int)runs;
+// Which tiles a product has, 256 x 256 or 256 x 128, and how they are dealt out.
+struct OrthoPlan {
+    int nt;
+    OrthoTiles tiles;  // of one matrix
+    int64_t total;     // of all matrices; the cut holds for 2^31 at most
+    OrthoSplit cut;
+    double us;         // what the turns of the busiest pair are taken to cost
+};
+
+// A K block takes 0.3 us in tiles of 256 x 256 and 0.2 in tiles of 256 x 128, which bring in three quarters of the
+// bytes for half the products (0.27 to 0.34 and 0.2 measured).  Tiles left over by whole turns of all pairs would take a
+// whole one's time; cut, their share of the runs' and what their parts cost to write and read back: of 256 x 256, 1.2 us
+// a part, which stops its pair's next tile where it has one, and where no whole tiles hide it 2.4 us for the meeting.
+// (16 matrices of 1024 x 2048: 8 of 160 tiles of 32 blocks are left; in 64 parts the product took 50 us, whole 36.)
+inline OrthoPlan ortho_plan_of(int64_t M, int64_t N, bool symmetric, int num_kb, int count, int pairs, int nt) {
+    OrthoPlan p;
+    p.nt = nt;
+    p.tiles = OrthoTiles{(int)((M + 255) / 256), (int)((N + nt - 1) / nt), symmetric ? 256 / nt : 0};
+    p.total = p.tiles.total() * count;
+    p.cut = OrthoSplit{(int)p.total, 0, 0, num_kb};
+    const double block = nt == 256 ? 0.3 : 0.2, part = nt == 256 ? 1.2 : 0.6;
+    const int64_t left = p.total % pairs, turns = p.total / pairs;
+    double last = left ? num_kb * block : 0;
+    if (left && num_kb >= kOrthoFewest) {
+        const int64_t most = pairs < kOrthoRuns ? pairs : kOrthoRuns, blocks = left * num_kb;
+        for (int64_t runs = left + 1; runs <= most && runs <= 8 * left; ++runs) {
+            const int64_t each = (blocks + runs - 1) / runs, parts = (runs + left - 1) / left + (runs % left ? 1 : 0);
+            const double us = (double)each * block + (double)parts * part + (turns ? 0 : 2.4);
+            if (each >= 4 && us < last - 0.5) {
+                last = us;
+                p.cut.split = (int)left;
+                p.cut.runs = (int)runs;
+            }
         }
     }
-    return s;
+    p.us = (double)turns * num_kb * block + last;
+    return p;
+}
+
+inline OrthoPlan ortho_plan(int64_t M, int64_t N, bool symmetric, int num_kb, int count, int pairs) {
+    const OrthoPlan wide = ortho_plan_of(M, N, symmetric, num_kb, count, pairs, 256);
+    const OrthoPlan narrow = ortho_plan_of(M, N, symmetric, num_kb, count, pairs, 128);
+    return narrow.us < wide.us ? narrow : wide;
 }
 
 // The workspace: where each part begins, in bytes; pitches in elements.

@@ -67,12 +67,13 @@ int main(int n, char** v) {
     return 0;
   }
   if (v[1][0] == 's') {
-    const c3::OrthoSplit s = c3::ortho_split(atoll(v[2]), atoi(v[3]), atoll(v[4]));
-    printf("%d %d\n", s.split, s.runs);
+    const c3::OrthoPlan p = c3::ortho_plan(atoll(v[2]), atoll(v[3]), atoi(v[4]) != 0, atoi(v[5]), atoi(v[6]), atoi(v[7]));
+    const c3::OrthoSplit& s = p.cut;
+    printf("%d %lld %d %d\n", p.nt, (long long)p.total, s.split, s.runs);
     if (s.runs) {
       for (int r = 0; r <= s.runs; ++r) printf("%lld ", (long long)s.begin(r));
       printf("\n");
-      for (long long u = 0; u < (long long)s.split * s.num_kb; ++u) printf("%d ", s.run_of(u));
+      for (long long u = 0; u < (long long)s.split * s.num_kb; ++u) printf("%d ", s.run_of((unsigned)u));
     }
     return 0;
   }
@@ -131,19 +132,30 @@ def test_tiles_cover_the_upper_triangle_once(plan, n, width):
     assert seen == want and total == len(want)
 
 
-@pytest.mark.parametrize("tiles,num_kb,pairs", [
-    (21, 79, 76), (1, 100, 76), (5, 17, 76), (136, 64, 76), (256, 64, 76), (77, 200, 76), (3584, 128, 76), (75, 300, 76),
-    (12, 40, 8), (7, 1000, 3), (2, 26, 1), (152, 500, 76), (40, 260, 64), (3, 16, 76), (90, 33, 128)])
-def test_a_products_tiles_are_dealt_out_once(plan, tiles, num_kb, pairs):
-    """Every K block of every tile goes to one pair, no run is longer than a tile, and the runs that a block's tile is
-    put together from are those that have a part of it."""
-    out = plan("s", tiles, num_kb, pairs).split("\n")
-    split, runs = map(int, out[0].split())
-    assert split == 0 or (split == tiles % pairs and split < runs <= min(pairs, 80) and num_kb >= 8)
-    begin = list(map(int, out[1].split()))
+# M, N, symmetric, K blocks, matrices, pairs and what the plan is to be: tiles' width, whether some are cut
+PLANS = [
+    (1347, 1347, 1, 79, 1, 76, 128, True), (5003, 1347, 0, 22, 1, 76, 256, False), (200, 200, 1, 141, 1, 76, 128, True),
+    (4096, 4096, 1, 64, 1, 76, 256, False), (4096, 4096, 0, 64, 1, 76, 256, True), (1024, 1024, 1, 32, 16, 76, 256, True),
+    (256, 640, 0, 4, 1, 76, 128, False), (256, 256, 1, 10, 1, 76, 128, False), (8192, 28672, 0, 128, 1, 76, 256, True),
+    (1024, 1024, 1, 16, 1, 76, 128, False), (3000, 700, 0, 11, 1, 17, 256, False), (700, 700, 1, 47, 1, 17, 128, False),
+    (700, 700, 1, 79, 1, 76, 128, True), (300, 5000, 0, 500, 3, 1, 256, False), (2600, 2700, 0, 41, 1, 76, 256, True),
+    (1, 1, 1, 3, 1, 76, 128, False)]
+
+
+@pytest.mark.parametrize("M,N,sym,num_kb,count,pairs,nt,cut", PLANS)
+def test_a_products_tiles_are_dealt_out_once(plan, M, N, sym, num_kb, count, pairs, nt, cut):
+    """Every K block of every tile that is left over goes to one pair, no run is longer than a tile, and the runs that
+    a block's tile is put together from are those that have a part of it."""
+    out = plan("s", M, N, sym, num_kb, count, pairs).split("\n")
+    got_nt, total, split, runs = map(int, out[0].split())
+    rows, cols = -(-M // 256), -(-N // got_nt)
+    assert total == count * (sum(cols - 256 // got_nt * i for i in range(rows)) if sym else rows * cols)
+    assert (got_nt, runs > 0) == (nt, cut)
+    assert split == 0 or (split == total % pairs and split < runs <= min(pairs, 80) and num_kb >= 8)
     if not split:
         return
+    begin = list(map(int, out[1].split()))
     assert begin[0] == 0 and begin[-1] == split * num_kb and len(begin) == runs + 1
-    assert all(4 <= b - a <= num_kb for a, b in zip(begin, begin[1:]))
+    assert all(3 <= b - a <= num_kb for a, b in zip(begin, begin[1:]))
     owner = list(map(int, out[2].split()))
     assert owner == [max(q for q in range(runs) if begin[q] <= u) for u in range(split * num_kb)]
