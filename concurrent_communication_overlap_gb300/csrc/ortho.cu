@@ -218,14 +218,14 @@ enum OrthoWaitSite : int {
     kSiteOrthoDrain = 19,
 };
 
-// out = alpha A B^T (times scale[m] `times` times) + beta mat + diag I, rounded to fp16 or bf16.
+// out = alpha A B^T (times scale[m] `times` times), rounded to fp16 or bf16; of two operands that are kUpper
+// + beta mat + diag I, mat fp16 of the output's shape.
 struct OrthoProduct {
     void* out;
     const float* scale;
     int64_t ld, stride;  // of out, and from one matrix to the next (no tensor map)
     int M, N, num_kb, count;
     int bf16, times;
-    int mat;             // beta mat is added: fp16 at the output's place (outputs that are fp16 too)
     int boxes;           // out has a tensor map, boxes of 32 rows x 64 columns
     int width;           // bytes that rows of out are aligned to (no tensor map)
     float alpha, beta, diag;
@@ -354,6 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                          DevStatus* st) {
     using Cfg = OrthoCfg<NT>;
     constexpr int S = Cfg::kStages;
+    constexpr bool kMat = A_IS == kUpper && B_IS == kUpper;  // beta mat + diag I is added
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -387,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         if (A_IS != kAlong) prefetch_tensormap(&acrossA);
         if (B_IS != kAcross) prefetch_tensormap(&tmB);
         if (B_IS != kAlong) prefetch_tensormap(&acrossB);
-        if (g.mat) prefetch_tensormap(&tmMat);
+        if (kMat) prefetch_tensormap(&tmMat);
         if (g.boxes) prefetch_tensormap(&tmOut);
     }
     if (warp == 1) {
@@ -542,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 if (!__all_sync(kAll, ready)) {
                     report_error(st, -4, kSiteOrthoEpilogue);
                     volatile int no_abort = 0;  // what is on its way into the boxes has to land before the CTA ends
-                    for (int rd = 0; g.mat && !cut && rd < kRounds; ++rd) mbar_wait(bar(BOX + (warp - 2) * 2 + rd), mat_phase, &no_abort);
+                    for (int rd = 0; kMat && !cut && rd < kRounds; ++rd) mbar_wait(bar(BOX + (warp - 2) * 2 + rd), mat_phase, &no_abort);
                     return false;
                 }
                 tc_fence_after();
@@ -553,7 +554,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 const int which = run == run0 ? place - (int)(g.cut.begin(run) / (unsigned)g.num_kb) : 0;
                 return reinterpret_cast<float4*>(g.parts) + (((run * 2 + which) * 2 + (int)rank) * kGEpiWarps + (warp - 2)) * (kRounds * 512) + lane;
             };
-            if (g.mat && !cut) fetch();
+            if (kMat && !cut) fetch();
             if (cut) {
                 if (!sums_ready()) break;
                 run0 = g.cut.run_of((unsigned)place * (unsigned)g.num_kb);
@@ -580,7 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 }
                 if (__shfl_sync(kAll, there, 0) != run1 - run0) continue;
                 __threadfence();
-                if (g.mat) fetch();
+                if (kMat) fetch();
             }
             float alpha = g.alpha;
             for (int i = 0; i < g.times; ++i) alpha *= g.scale[tile.m];
@@ -592,14 +593,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             // Not where the boxes are already being filled.
             bool ok = true;
 #pragma unroll 1
-            for (int rd = local == 0 && !cut && !g.mat ? -1 : 0; rd < kRounds; ++rd) {
+            for (int rd = local == 0 && !cut && !kMat ? -1 : 0; rd < kRounds; ++rd) {
                 if (rd == 0 && !cut) {
                     ok = sums_ready();
                     if (!ok) break;
                 }
                 const uint32_t box = box0 + (uint32_t)(rd < 0 ? 0 : rd) * 4096u;
                 if (rd < 0) {
-                } else if (g.mat) {
+                } else if (kMat) {
                     const bool in = mbar_wait(bar(BOX + (warp - 2) * 2 + rd), mat_phase, abort_flag);
                     if (!__all_sync(kAll, in)) report_error(st, -4, kSiteOrthoEpilogue);
                 } else {
@@ -642,29 +643,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                     }
                     // lane's row of the box: 16-byte chunk j at j ^ (row % 8), as the tensor maps have it
                     const uint32_t line = box + (uint32_t)lane * 128u;
-                    uint32_t v[16];
+                    if constexpr (kMat) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t o[4] = {0, 0, 0, 0};
-                        if (g.mat) ld_shared_v4(line + (uint32_t)(((4 * h + j) ^ (lane & 7)) << 4), o);
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t o[4];
+                            ld_shared_v4(line + (uint32_t)(((4 * h + j) ^ (lane & 7)) << 4), o);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int i = 4 * j + k;
-                            float a = alpha * __uint_as_float(r[2 * i]), b = alpha * __uint_as_float(r[2 * i + 1]);
-                            if (g.mat) {
+                            for (int k = 0; k < 4; ++k) {
                                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
-                                a = fmaf(g.beta, f.x, a);
-                                b = fmaf(g.beta, f.y, b);
-                                if (row0 + lane == c0 + 2 * i) a += g.diag;
-                                if (row0 + lane == c0 + 2 * i + 1) b += g.diag;
+                                const int i = 8 * j + 2 * k;
+                                r[i] = __float_as_uint(fmaf(g.beta, f.x, alpha * __uint_as_float(r[i])));
+                                r[i + 1] = __float_as_uint(fmaf(g.beta, f.y, alpha * __uint_as_float(r[i + 1])));
                             }
-                            if (g.bf16) {
-                                const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
-                                v[i] = *reinterpret_cast<const uint32_t*>(&x);
-                            } else {
-                                const __half2 x = __floats2half2_rn(a, b);
-                                v[i] = *reinterpret_cast<const uint32_t*>(&x);
-                            }
+                        }
+                        if (row0 == c0) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j == lane) r[j] = __float_as_uint(__uint_as_float(r[j]) + g.diag);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(alpha * __uint_as_float(r[j]));
+                    }
+                    uint32_t v[16];
+                    if (!kMat && g.bf16) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                            v[j] = *reinterpret_cast<const uint32_t*>(&x);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const __half2 x = __floats2half2_rn(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                            v[j] = *reinterpret_cast<const uint32_t*>(&x);
                         }
                     }
                     if (g.boxes) {
@@ -686,7 +698,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 }
             }
             if (!ok) break;
-            if (g.mat) mat_phase ^= 1u;
+            if (kMat) mat_phase ^= 1u;
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
@@ -858,7 +870,6 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
         g.alpha = two(t.g - 2 * t.x);
         if ((rc = product(tall ? kGramTall : kGramWide, xm[now], xm[now], gm[2], g))) return rc;
         // P = a I + b A + c A A
-        g.mat = 1;
         g.num_kb = blocks(m, kGK);
         g.times = 0;
         g.alpha = t.c * two(t.p - 2 * t.g);
@@ -867,7 +878,6 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
         if ((rc = product(kPoly, gm, gm, pm[2], g))) return rc;
         // X <- P X (X P)
         const bool last = i + 1 == steps;
-        g.mat = 0;
         g.M = (int)rows;
         g.N = (int)cols;
         g.times = i == 0 ? 1 : 0;
