@@ -313,10 +313,11 @@ struct OrthoWorkItem {
     int tile;  // -1: no more
     int kb0, kb1;
 };
+template <bool CUT>
 __device__ __forceinline__ OrthoWorkItem ortho_item(const OrthoSplit& s, int pair, int pairs, int i) {
     OrthoWorkItem w;
     const int whole = s.tiles - s.split;
-    if (pair < s.runs) {
+    if (CUT && pair < s.runs) {
         const unsigned b0 = s.begin(pair), b1 = s.begin(pair + 1), t0 = b0 / (unsigned)s.num_kb;
         const int parts = (t0 + 1) * (unsigned)s.num_kb < b1 ? 2 : 1;  // a run is no longer than a tile
         if (i < parts) {
@@ -346,7 +347,8 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
                  : "memory");
 }
 
-template <int NT, int A_IS, int B_IS>
+// CUT: some tiles are cut along K (else g.cut has none, and the code for it is left out).
+template <int NT, int A_IS, int B_IS, bool CUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     ortho_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap acrossA, const __grid_constant__ CUtensorMap acrossB,
@@ -355,6 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     using Cfg = OrthoCfg<NT>;
     constexpr int S = Cfg::kStages;
     constexpr bool kMat = A_IS == kUpper && B_IS == kUpper;  // beta mat + diag I is added
+    constexpr bool kBoxes = kMat || A_IS == B_IS;            // a symmetric product, whose output has a tensor map
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -389,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         if (B_IS != kAcross) prefetch_tensormap(&tmB);
         if (B_IS != kAlong) prefetch_tensormap(&acrossB);
         if (kMat) prefetch_tensormap(&tmMat);
-        if (g.boxes) prefetch_tensormap(&tmOut);
+        if (kBoxes || g.boxes) prefetch_tensormap(&tmOut);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_slot))
@@ -411,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             uint32_t phase = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
-                const OrthoWorkItem item = ortho_item(g.cut, pair, pairs, i);
+                const OrthoWorkItem item = ortho_item<CUT>(g.cut, pair, pairs, i);
                 if (item.tile < 0) break;
                 const OrthoTile tile = ortho_tile<NT>(g, item.tile);
                 if (i == 0) chain_ready();
@@ -463,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             uint32_t phase = 0;
             bool ok = true;
             for (int local = 0; ok; ++local) {
-                const OrthoWorkItem item = ortho_item(g.cut, pair, pairs, local);
+                const OrthoWorkItem item = ortho_item<CUT>(g.cut, pair, pairs, local);
                 if (item.tile < 0) break;
                 const int buf = local & 1;
                 if (!mbar_wait_cluster(bar(TEMPTY + buf), ((uint32_t)(local >> 1) & 1u) ^ 1u, abort_flag)) {
@@ -510,12 +513,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         chain_ready();
         uint32_t mat_phase = 0;
         for (int local = 0;; ++local) {
-            const OrthoWorkItem item = ortho_item(g.cut, pair, pairs, local);
+            const OrthoWorkItem item = ortho_item<CUT>(g.cut, pair, pairs, local);
             if (item.tile < 0) break;
             const OrthoTile tile = ortho_tile<NT>(g, item.tile);
             const int buf = local & 1;
             const int row0 = tile.row + (int)rank * 128 + q * 32, col0 = tile.col + half * (NT / 2);
-            const bool cut = item.kb1 - item.kb0 < g.num_kb;
+            const bool cut = CUT && item.kb1 - item.kb0 < g.num_kb;
             const int place = item.tile - (g.cut.tiles - g.cut.split);  // among the cut tiles
             int run0 = 0, run1 = 0;                                     // the runs that have parts of the tile
             // What is added, on its way while the products run: into the boxes that the results go out from.
@@ -555,7 +558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 return reinterpret_cast<float4*>(g.parts) + (((run * 2 + which) * 2 + (int)rank) * kGEpiWarps + (warp - 2)) * (kRounds * 512) + lane;
             };
             if (kMat && !cut) fetch();
-            if (cut) {
+            if (CUT && cut) {
                 if (!sums_ready()) break;
                 run0 = g.cut.run_of((unsigned)place * (unsigned)g.num_kb);
                 run1 = g.cut.run_of((unsigned)(place + 1) * (unsigned)g.num_kb - 1);
@@ -611,7 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 for (int h = 0; h < 2; ++h) {
                     const int p = 2 * rd + h, c0 = col0 + p * 32;
                     uint32_t r[32];
-                    if (cut) {  // the parts in order, whoever adds them up
+                    if (CUT && cut) {  // the parts in order, whoever adds them up
 #pragma unroll
                         for (int j = 0; j < 32; ++j) r[j] = 0;
 #pragma unroll 1
@@ -679,16 +682,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                             v[j] = *reinterpret_cast<const uint32_t*>(&x);
                         }
                     }
-                    if (g.boxes) {
+                    if (kBoxes || g.boxes) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             st_shared_v4(line + (uint32_t)(((4 * h + j) ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                    } else if (rd >= 0) {
+                    } else if (rd >= 0 && !kBoxes) {
                         store_piece<uint16_t>(v, box, lane, g.width, static_cast<uint16_t*>(g.out) + tile.m * g.stride, row0, g.M - row0, c0,
                                               g.N, g.ld);
                     }
                 }
-                if (g.boxes) {
+                if (kBoxes || g.boxes) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && rd >= 0) {
@@ -714,14 +717,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 
 // ---------------------------------------------------------------- host side
 
-template <int NT, typename F>
+template <int NT, bool CUT, typename F>
 static int each_product(F f) {
     const int smem = OrthoCfg<NT>::kSmem;
-    int rc = f(ortho_product_kernel<NT, kAlong, kAlong>, smem);
-    if (!rc) rc = f(ortho_product_kernel<NT, kAcross, kAcross>, smem);
-    if (!rc) rc = f(ortho_product_kernel<NT, kUpper, kUpper>, smem);
-    if (!rc) rc = f(ortho_product_kernel<NT, kUpper, kAcross>, smem);
-    if (!rc) rc = f(ortho_product_kernel<NT, kAlong, kUpper>, smem);
+    int rc = f(ortho_product_kernel<NT, kAlong, kAlong, CUT>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kAcross, kAcross, CUT>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kUpper, kUpper, CUT>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kUpper, kAcross, CUT>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kAlong, kUpper, CUT>, smem);
     return rc;
 }
 
@@ -730,8 +733,11 @@ int ortho_init_device() {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         return e == cudaSuccess ? 0 : set_cuda_error(e, "cudaFuncSetAttribute(orthogonalisation)");
     };
-    const int rc = each_product<256>(allow);
-    return rc ? rc : each_product<128>(allow);
+    int rc = each_product<256, false>(allow);
+    if (!rc) rc = each_product<256, true>(allow);
+    if (!rc) rc = each_product<128, false>(allow);
+    if (!rc) rc = each_product<128, true>(allow);
+    return rc;
 }
 
 // fp16 or bf16 matrices [count][rows][pitch], in boxes of 64 columns x box_rows.  What lies past a matrix reads as zeros.
@@ -836,21 +842,23 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
         g.counts = in.counts;
         const int some = g.cut.tiles < g.cut.runs ? g.cut.runs : g.cut.tiles;
         const dim3 ctas((unsigned)(2 * (some < pairs ? some : pairs)));
-        auto by_width = [&](auto nt_of) {
+        auto by_form = [&](auto nt_of, auto cut_of) {
             constexpr int NT = decltype(nt_of)::value;
+            constexpr bool CUT = decltype(cut_of)::value;
             auto go = [&](auto kernel) {
                 // A along K in boxes of 128 rows, B in boxes of NT / 2; either across K in boxes of 64
                 return launch_chained(kernel, ctas, kGThreads, OrthoCfg<NT>::kSmem, s, 1, a[0], b[NT == 128], a[1], b[1], gm[2], to, g, ds->status);
             };
             switch (which) {
-                case kGramWide: return go(ortho_product_kernel<NT, kAlong, kAlong>);
-                case kGramTall: return go(ortho_product_kernel<NT, kAcross, kAcross>);
-                case kPoly: return go(ortho_product_kernel<NT, kUpper, kUpper>);
-                case kApplyWide: return go(ortho_product_kernel<NT, kUpper, kAcross>);
-                default: return go(ortho_product_kernel<NT, kAlong, kUpper>);
+                case kGramWide: return go(ortho_product_kernel<NT, kAlong, kAlong, CUT>);
+                case kGramTall: return go(ortho_product_kernel<NT, kAcross, kAcross, CUT>);
+                case kPoly: return go(ortho_product_kernel<NT, kUpper, kUpper, CUT>);
+                case kApplyWide: return go(ortho_product_kernel<NT, kUpper, kAcross, CUT>);
+                default: return go(ortho_product_kernel<NT, kAlong, kUpper, CUT>);
             }
         };
-        const cudaError_t err = plan.nt == 128 ? by_width(std::integral_constant<int, 128>()) : by_width(std::integral_constant<int, 256>());
+        auto by_cut = [&](auto nt_of) { return g.cut.runs ? by_form(nt_of, std::true_type()) : by_form(nt_of, std::false_type()); };
+        const cudaError_t err = plan.nt == 128 ? by_cut(std::integral_constant<int, 128>()) : by_cut(std::integral_constant<int, 256>());
         if (err != cudaSuccess) return set_cuda_error(err, "orthogonalisation: product kernel launch");
         count_launch();
         return 0;
