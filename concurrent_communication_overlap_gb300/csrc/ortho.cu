@@ -221,12 +221,11 @@ enum OrthoWaitSite : int {
 // out = alpha A B^T (times scale[m] `times` times), rounded to fp16 or bf16; of two operands that are kUpper
 // + beta mat + diag I, mat fp16 of the output's shape.
 struct OrthoProduct {
-    void* out;
+    void* out;           // NULL: it has a tensor map, of boxes of 32 rows x 64 columns
     const float* scale;
     int64_t ld, stride;  // of out, and from one matrix to the next (no tensor map)
     int M, N, num_kb, count;
     int bf16, times;
-    int boxes;           // out has a tensor map, boxes of 32 rows x 64 columns
     int width;           // bytes that rows of out are aligned to (no tensor map)
     float alpha, beta, diag;
     OrthoTiles tiles;    // symmetric: tiles above the diagonal
@@ -347,8 +346,9 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
                  : "memory");
 }
 
-// CUT: some tiles are cut along K (else g.cut has none, and the code for it is left out).
-template <int NT, int A_IS, int B_IS, bool CUT>
+// CUT: some tiles are cut along K (else g.cut has none); BOXES: the output has a tensor map.  What a product does not
+// need is left out of its code.
+template <int NT, int A_IS, int B_IS, bool CUT, bool BOXES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     ortho_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap acrossA, const __grid_constant__ CUtensorMap acrossB,
@@ -357,7 +357,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     using Cfg = OrthoCfg<NT>;
     constexpr int S = Cfg::kStages;
     constexpr bool kMat = A_IS == kUpper && B_IS == kUpper;  // beta mat + diag I is added
-    constexpr bool kBoxes = kMat || A_IS == B_IS;            // a symmetric product, whose output has a tensor map
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -392,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         if (B_IS != kAcross) prefetch_tensormap(&tmB);
         if (B_IS != kAlong) prefetch_tensormap(&acrossB);
         if (kMat) prefetch_tensormap(&tmMat);
-        if (kBoxes || g.boxes) prefetch_tensormap(&tmOut);
+        if (BOXES) prefetch_tensormap(&tmOut);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_slot))
@@ -682,16 +681,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                             v[j] = *reinterpret_cast<const uint32_t*>(&x);
                         }
                     }
-                    if (kBoxes || g.boxes) {
+                    if (BOXES) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             st_shared_v4(line + (uint32_t)(((4 * h + j) ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                    } else if (rd >= 0 && !kBoxes) {
+                    } else if (rd >= 0) {
                         store_piece<uint16_t>(v, box, lane, g.width, static_cast<uint16_t*>(g.out) + tile.m * g.stride, row0, g.M - row0, c0,
                                               g.N, g.ld);
                     }
                 }
-                if (kBoxes || g.boxes) {
+                if (BOXES) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && rd >= 0) {
@@ -720,11 +719,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 template <int NT, bool CUT, typename F>
 static int each_product(F f) {
     const int smem = OrthoCfg<NT>::kSmem;
-    int rc = f(ortho_product_kernel<NT, kAlong, kAlong, CUT>, smem);
-    if (!rc) rc = f(ortho_product_kernel<NT, kAcross, kAcross, CUT>, smem);
-    if (!rc) rc = f(ortho_product_kernel<NT, kUpper, kUpper, CUT>, smem);
-    if (!rc) rc = f(ortho_product_kernel<NT, kUpper, kAcross, CUT>, smem);
-    if (!rc) rc = f(ortho_product_kernel<NT, kAlong, kUpper, CUT>, smem);
+    int rc = f(ortho_product_kernel<NT, kAlong, kAlong, CUT, true>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kAcross, kAcross, CUT, true>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kUpper, kUpper, CUT, true>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kUpper, kAcross, CUT, true>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kAlong, kUpper, CUT, true>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kUpper, kAcross, CUT, false>, smem);
+    if (!rc) rc = f(ortho_product_kernel<NT, kAlong, kUpper, CUT, false>, smem);
     return rc;
 }
 
@@ -850,11 +851,13 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
                 return launch_chained(kernel, ctas, kGThreads, OrthoCfg<NT>::kSmem, s, 1, a[0], b[NT == 128], a[1], b[1], gm[2], to, g, ds->status);
             };
             switch (which) {
-                case kGramWide: return go(ortho_product_kernel<NT, kAlong, kAlong, CUT>);
-                case kGramTall: return go(ortho_product_kernel<NT, kAcross, kAcross, CUT>);
-                case kPoly: return go(ortho_product_kernel<NT, kUpper, kUpper, CUT>);
-                case kApplyWide: return go(ortho_product_kernel<NT, kUpper, kAcross, CUT>);
-                default: return go(ortho_product_kernel<NT, kAlong, kUpper, CUT>);
+                case kGramWide: return go(ortho_product_kernel<NT, kAlong, kAlong, CUT, true>);
+                case kGramTall: return go(ortho_product_kernel<NT, kAcross, kAcross, CUT, true>);
+                case kPoly: return go(ortho_product_kernel<NT, kUpper, kUpper, CUT, true>);
+                case kApplyWide:
+                    return g.out ? go(ortho_product_kernel<NT, kUpper, kAcross, CUT, false>) : go(ortho_product_kernel<NT, kUpper, kAcross, CUT, true>);
+                default:
+                    return g.out ? go(ortho_product_kernel<NT, kAlong, kUpper, CUT, false>) : go(ortho_product_kernel<NT, kAlong, kUpper, CUT, true>);
             }
         };
         auto by_cut = [&](auto nt_of) { return g.cut.runs ? by_form(nt_of, std::true_type()) : by_form(nt_of, std::false_type()); };
@@ -871,7 +874,6 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
         g.scale = in.scale;
         g.count = count;
         // A = X X^T (X^T X): the stored 2^x X give 2^2x of it
-        g.boxes = 1;
         g.M = g.N = (int)m;
         g.num_kb = blocks(tall ? rows : cols, kGK);
         g.times = i == 0 ? 2 : 0;
@@ -891,8 +893,7 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
         g.times = i == 0 ? 1 : 0;
         g.alpha = last ? scale * two(-t.p - t.x) : two(t.next - t.p - t.x);
         g.bf16 = last;
-        if (last) {
-            g.boxes = boxes;
+        if (last && !boxes) {
             g.out = out;
             g.ld = out_ld;
             g.stride = rows * out_ld;
