@@ -213,6 +213,24 @@ __device__ __forceinline__ void zero_row(Tt* row, int64_t cols, int lane) {
     }
 }
 
+// What a warp clears at once: up to four rows' kZeroBytes.
+constexpr int kZeroBytes = 4096;
+template <typename Tt>
+struct ZeroPieces {
+    int64_t blocks;  // pieces of a row
+    __device__ __forceinline__ explicit ZeroPieces(int64_t cols) : blocks((cols + kCols - 1) / kCols) {}
+    static constexpr int kCols = kZeroBytes / (int)sizeof(Tt);
+    // rows 4 group .. 4 group + 3 but for those whose bit is set in `skip`
+    template <int W>
+    __device__ __forceinline__ void clear(Tt* table, int64_t rows, int64_t cols, int64_t ld, int64_t group, int64_t block, uint32_t skip,
+                                          int lane) const {
+        const int64_t c = block * kCols, n = cols - c < kCols ? cols - c : kCols;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i)
+            if (group * 4 + i < rows && !(skip >> i & 1)) zero_row<Tt, W>(table + (group * 4 + i) * ld + c, n, lane);
+    }
+};
+
 // ---------------------------------------------------------------- order of the tokens by row
 //
 // A stable radix sort of (row, token) by row, least digit first, by one cluster in one
@@ -589,13 +607,11 @@ __global__ void __launch_bounds__(kEmbedThreads, 2)
     }
     // rows without tokens that the sort's launch has left, a warp four of them
     if (ACCUMULATE) return;
-    const int64_t groups = (g.rows + 3) / 4;
-    for (job -= jobs; job < groups; job += step) {
-        const uint32_t done = g.named[job >> 3] >> ((job & 7) * 4);
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = job * 4 + i;
-            if (r < g.rows && !(done >> i & 1)) zero_row<Tt, W>(table + r * g.ld, g.cols, lane);
-        }
+    const ZeroPieces<Tt> zero(g.cols);
+    const int64_t pieces = (g.rows + 3) / 4 * zero.blocks;
+    for (job -= jobs; job < pieces; job += step) {
+        const int64_t group = job / zero.blocks;
+        zero.template clear<W>(table, g.rows, g.cols, g.ld, group, job - group * zero.blocks, g.named[group >> 3] >> ((group & 7) * 4), lane);
     }
 }
 
@@ -653,7 +669,9 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(Tt* __restric
 // Few tokens: one launch.  Every CTA has all ids in shared memory; a warp takes a token and kSpan
 // columns, adds up all tokens of its row if it is the first of them, and warps left over write the
 // rows that no id names.
-constexpr int kFewTokens = 256;
+// The more tokens, the longer every warp looks for its row's: 512 tokens into 50000 x 512 fp32 take 18.4 us, 28.0 sorted;
+// 2048 37.4 and 32.4.  And all may be of one row, which one warp a span then adds up.
+constexpr int kFewTokens = 512;
 
 template <typename Td, typename Tt, int W>
 __global__ void __launch_bounds__(kEmbedThreads)
@@ -664,15 +682,10 @@ __global__ void __launch_bounds__(kEmbedThreads)
     const int lane = threadIdx.x & 31;
     const int64_t spans = (g.cols + kSpan - 1) / kSpan, jobs = tokens * spans;
     const int64_t step = (int64_t)gridDim.x * kEmbedWarps;
-    static_assert(kFewTokens <= kEmbedThreads, "a thread a token");
     chain_wait();
-    {
-        int k = -1;
-        if ((int)threadIdx.x < tokens) {
-            const int64_t r = (int64_t)ids[threadIdx.x] - first;
-            if (r >= 0 && r < g.rows) k = (int)r;
-        }
-        keys[threadIdx.x] = k;
+    for (int i = threadIdx.x; i < tokens; i += kEmbedThreads) {
+        const int64_t r = (int64_t)ids[i] - first;
+        keys[i] = r >= 0 && r < g.rows ? (int)r : -1;
     }
     __syncthreads();
     int64_t job = (int64_t)blockIdx.x * kEmbedWarps + (threadIdx.x >> 5);
@@ -714,16 +727,14 @@ __global__ void __launch_bounds__(kEmbedThreads)
         add_row<Tt, W>(g, table, row, c0, n, acc, lane);
     }
     if (g.accumulate) return;
-    const int64_t groups = (g.rows + 3) / 4;
-    for (job -= jobs; job < groups; job += step) {
+    const ZeroPieces<Tt> zero(g.cols);
+    const int64_t pieces = (g.rows + 3) / 4 * zero.blocks;
+    for (job -= jobs; job < pieces; job += step) {
+        const int64_t group = job / zero.blocks;
         unsigned bits = 0;
         for (int j = lane; j < tokens; j += 32)
-            if (keys[j] >> 2 == job) bits |= 1u << (keys[j] & 3);
-        bits = __reduce_or_sync(kAll, bits);
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = job * 4 + i;
-            if (r < g.rows && !(bits >> i & 1)) zero_row<Tt, W>(table + r * g.ld, g.cols, lane);
-        }
+            if (keys[j] >> 2 == group) bits |= 1u << (keys[j] & 3);
+        zero.template clear<W>(table, g.rows, g.cols, g.ld, group, job - group * zero.blocks, __reduce_or_sync(kAll, bits), lane);
     }
 }
 
@@ -882,7 +893,7 @@ int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, c
     g.chunk = w.chunk;
     g.accumulate = accumulate;
     g.scale = a.scale;
-    const int64_t spans = (a.cols + kSpan - 1) / kSpan, zeros = accumulate ? 0 : (a.rows + 3) / 4;
+    const int64_t spans = (a.cols + kSpan - 1) / kSpan, zeros = accumulate ? 0 : (a.rows + 3) / 4 * ((a.cols * (bf16 ? 2 : 4) + kZeroBytes - 1) / kZeroBytes);
     const int64_t most = (int64_t)ds->sm_count * 8;
     const int wide = width(a.cols, {dout, a.out_ld, dout_bf16}, {table, a.ld, bf16});
     if (a.tokens <= kFewTokens) {
