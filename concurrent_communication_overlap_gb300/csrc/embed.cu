@@ -124,6 +124,10 @@ __device__ __forceinline__ void store_pairs(__nv_bfloat16* row, int64_t c0, int6
 // out[t] = scale * table[ids[t] - first], zeros where that is no row.  A warp takes kAhead pieces
 // of kSpan columns, of one token or of several, whose loads are all in flight before the first is used.
 //
+// Bytes bound it: 65536 tokens x 8192 bf16 take 259 us, 5.5 TB/s of what has to be read and written; tokens
+// of a power law name a row again after more than L2 holds, so that memory gives more.  10007 x 2051
+// fp32 to bf16, most tokens another shard's, take 14.4 us (floor 6.7), bound by issue and by latency.
+//
 // Rows of bf16 of odd length: pieces of a row that begins at no multiple of 4 bytes begin one column
 // before, so that pairs of values are aligned where they are stored.
 constexpr int kAhead = 2;  // 4 (100 registers): 10007 x 2051 fp32 to bf16 18.4 us, 2: 14.9
@@ -238,6 +242,10 @@ struct ZeroPieces {
 //   start[digit] + (of the CTAs before) + (of the warps before) + (before it in its warp),
 // whole-number sums, so that the order does not depend on timing.  Tokens without a row
 // in the table drop out in the first pass.
+//
+// Latency bounds it, a step after the other: 16384 tokens of 131072 rows take 14 us in two passes of
+// 512 bins, of which loads, votes and counts are 2.6 a pass, the meeting of the CTAs and the sums over
+// the bins 2.6, and placing them, with the fence behind it, 2.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortBits = 10;  // a digit at most: a thread a bin in the scans
@@ -459,9 +467,14 @@ __global__ void __launch_bounds__(kSortThreads, 1)
 // ---------------------------------------------------------------- sums
 //
 // The sorted places are cut into chunks.  A warp adds up kSpan columns of a chunk's
-// tokens, in order.  A row of at most kFew tokens is the business of the chunk that it begins in, wherever it ends; of a longer one that is cut,
-// the part behind a cut goes to heads[chunk] and the part before the first to tails[chunk],
-// and embed_join_kernel adds those up, in the order of the chunks.
+// tokens, in order.  A row of at most kFew tokens is the business of the chunk that it begins
+// in, wherever it ends; of a longer one that is cut, the part behind a cut goes to
+// heads[chunk] and the part before the first to tails[chunk], and embed_join_kernel adds
+// those up, in the order of the chunks.  (With every row cut at chunks of 16 the joins of 40009
+// tokens of a power law took 48 us, these 7.)  Eight tokens' rows are in flight a warp, four and
+// the table's where it is added to, whose loads one after the other took 28 us of 53.
+//
+// Bytes bound it: 16384 x 8192 bf16 into 131072 rows 376 us at 6.3 TB/s, of 397 in all.
 struct EmbedSum {
     const int2* pairs;
     EmbedOrder* order;
@@ -667,19 +680,24 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(Tt* __restric
 }
 
 // Few tokens: one launch.  Every CTA has all ids in shared memory; a warp takes a token and kSpan
-// columns, adds up all tokens of its row if it is the first of them, and warps left over write the
-// rows that no id names.
-// The more tokens, the longer every warp looks for its row's: 512 tokens into 50000 x 512 fp32 take 18.4 us, 28.0 sorted;
-// 2048 37.4 and 32.4.  And all may be of one row, which one warp a span then adds up.
-constexpr int kFewTokens = 512;
+// columns and adds up all tokens of its row, if it is the first of them.  A row of more than kAlone tokens
+// (padding that has an id, say) is left for all the CTA's warps, which add up an eighth of the tokens each; the eighths
+// meet in shared memory, in order.  Rows that no id names are cleared by what follows.
+//
+// The more tokens, the longer every warp looks for its row's: 512 tokens into 50000 x 512 fp32 take 18.8 us, 28.4 sorted;
+// 2048 37.4 and 32.4; 1024 into 9000 x 1001 bf16 14.6 and 23.1, into 6250 x 4096 fp32, of 16 spans, 30.8 and 28.9.
+constexpr int kFewTokens = 1024, kFewJobs = 8192;
+constexpr int kAlone = 32;
 
 template <typename Td, typename Tt, int W>
 __global__ void __launch_bounds__(kEmbedThreads)
     embed_few_kernel(const Td* __restrict__ dout, const int32_t* __restrict__ ids, int tokens, int64_t first,
                      Tt* __restrict__ table, EmbedSum g) {
     __shared__ int keys[kFewTokens];
+    __shared__ float part[kEmbedWarps][8][32];
+    __shared__ int crowd[kEmbedWarps];  // each warp's token whose row has many, or -1
     constexpr int B = 4;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t spans = (g.cols + kSpan - 1) / kSpan, jobs = tokens * spans;
     const int64_t step = (int64_t)gridDim.x * kEmbedWarps;
     chain_wait();
@@ -688,48 +706,83 @@ __global__ void __launch_bounds__(kEmbedThreads)
         keys[i] = r >= 0 && r < g.rows ? (int)r : -1;
     }
     __syncthreads();
-    int64_t job = (int64_t)blockIdx.x * kEmbedWarps + (threadIdx.x >> 5);
-    for (; job < jobs; job += step) {
-        const int t = (int)(job / spans);
-        const int64_t c0 = (job - t * spans) * kSpan;
-        const int n = (int)(g.cols - c0 < kSpan ? g.cols - c0 : kSpan);
-        const int row = keys[t];
-        if (row < 0) continue;
-        bool earlier = false;
-        for (int j = lane; j < t; j += 32) earlier |= keys[j] == row;
-        if (__any_sync(kAll, earlier)) continue;
-        float acc[8] = {};
-        for (int j0 = t & ~31; j0 < tokens; j0 += 32) {
-            unsigned same = __ballot_sync(kAll, j0 + lane < tokens && keys[(j0 + lane) & (kFewTokens - 1)] == row);
-            while (same) {
-                Part<Td, W> raw[B];
-                const Td* from[B];
-                unsigned left = same;
+    int64_t job0 = (int64_t)blockIdx.x * kEmbedWarps;
+    for (; job0 < jobs; job0 += step) {
+        auto token = [&](int w) { return (int)((job0 + w) / spans); };
+        const int t = job0 + warp < jobs ? token(warp) : 0;
+        int row = job0 + warp < jobs ? keys[t] : -1, many = 0;
+        for (int j0 = 0; row >= 0 && j0 < tokens; j0 += 32) {
+            const unsigned same = __ballot_sync(kAll, j0 + lane < tokens && keys[(j0 + lane) & (kFewTokens - 1)] == row);
+            const unsigned earlier = j0 + 32 <= t ? kAll : j0 <= t ? (1u << (t - j0)) - 1 : 0u;
+            if (same & earlier) row = -1;  // not the first
+            many += __popc(same);
+        }
+        const bool alone = row >= 0 && many <= kAlone;
+        if (lane == 0) crowd[warp] = row >= 0 && !alone ? t : -1;
+        // turn 0: a warp's own; then the crowds of all warps, one after the other
+#pragma unroll 1
+        for (int turn = 0; turn <= kEmbedWarps; ++turn) {
+            const int per = (tokens + kEmbedWarps - 1) / kEmbedWarps;
+            int from = t, to = alone ? tokens : 0, w = warp;
+            if (turn > 0) {
+                if (turn == 1) __syncthreads();
+                w = turn - 1;
+                if (crowd[w] < 0) continue;
+                row = keys[crowd[w]];
+                from = warp * per;
+                to = min(tokens, from + per);
+            }
+            const int64_t c0 = (job0 + w - token(w) * spans) * kSpan;
+            const int n = (int)(g.cols - c0 < kSpan ? g.cols - c0 : kSpan);
+            float acc[8] = {};
+            for (int j0 = from; j0 < to; j0 += 32) {
+                unsigned same = __ballot_sync(kAll, j0 + lane < to && keys[(j0 + lane) & (kFewTokens - 1)] == row);
+                while (same) {
+                    Part<Td, W> raw[B];
+                    const Td* at[B];
+                    unsigned left = same;
 #pragma unroll
-                for (int b = 0; b < B; ++b) {
-                    from[b] = nullptr;
-                    if (!left) continue;
-                    from[b] = dout + (int64_t)(j0 + __ffs(left) - 1) * g.dout_ld + c0;
-                    left &= left - 1;
-                    raw[b].template load<false>(from[b] + lane * W, n - lane * W);
-                }
-                same = left;
+                    for (int b = 0; b < B; ++b) {
+                        at[b] = nullptr;
+                        if (!left) continue;
+                        at[b] = dout + (int64_t)(j0 + __ffs(left) - 1) * g.dout_ld + c0;
+                        left &= left - 1;
+                        raw[b].template load<false>(at[b] + lane * W, n - lane * W);
+                    }
+                    same = left;
 #pragma unroll
-                for (int b = 0; b < B; ++b) {
-                    if (!from[b]) break;
-                    float v[8];
-                    raw[b].values(v);
+                    for (int b = 0; b < B; ++b) {
+                        if (!at[b]) break;
+                        float v[8];
+                        raw[b].values(v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[i] += v[i];
+                        for (int i = 0; i < 8; ++i) acc[i] += v[i];
+                    }
                 }
             }
+            if (turn > 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) part[warp][i][lane] = acc[i];
+                __syncthreads();
+                if (warp == 0) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        acc[i] = 0.0f;
+#pragma unroll
+                        for (int x = 0; x < kEmbedWarps; ++x) acc[i] += part[x][i][lane];
+                    }
+                }
+            }
+            if (turn == 0 ? alone : warp == 0) add_row<Tt, W>(g, table, row, c0, n, acc, lane);
+            if (turn > 0) __syncthreads();
         }
-        add_row<Tt, W>(g, table, row, c0, n, acc, lane);
+        __syncthreads();  // `crowd` has been read
     }
+    int64_t job = job0 + warp;  // past the sums' jobs, whose number is made up to whole CTAs
     if (g.accumulate) return;
     const ZeroPieces<Tt> zero(g.cols);
     const int64_t pieces = (g.rows + 3) / 4 * zero.blocks;
-    for (job -= jobs; job < pieces; job += step) {
+    for (job -= (jobs + kEmbedWarps - 1) / kEmbedWarps * kEmbedWarps; job < pieces; job += step) {
         const int64_t group = job / zero.blocks;
         unsigned bits = 0;
         for (int j = lane; j < tokens; j += 32)
@@ -896,8 +949,8 @@ int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, c
     const int64_t spans = (a.cols + kSpan - 1) / kSpan, zeros = accumulate ? 0 : (a.rows + 3) / 4 * ((a.cols * (bf16 ? 2 : 4) + kZeroBytes - 1) / kZeroBytes);
     const int64_t most = (int64_t)ds->sm_count * 8;
     const int wide = width(a.cols, {dout, a.out_ld, dout_bf16}, {table, a.ld, bf16});
-    if (a.tokens <= kFewTokens) {
-        const unsigned grid = up_to(a.tokens * spans + zeros, kEmbedWarps, most);
+    if (a.tokens <= kFewTokens && a.tokens * spans <= kFewJobs) {
+        const unsigned grid = up_to((a.tokens * spans + kEmbedWarps - 1) / kEmbedWarps * kEmbedWarps + zeros, kEmbedWarps, most);
         const cudaError_t e = by_types(dout_bf16, bf16, wide, [&](auto d, auto t, auto wide_of) {
             using Td = decltype(d);
             using Tt = decltype(t);
@@ -913,8 +966,9 @@ int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, c
     const int passes = (bits + kSortBits - 1) / kSortBits;
     bits = (bits + passes - 1) / passes;
     // Beside the cluster that sorts, as many others as run at once find the rows without tokens, and write
-    // zeros into as many of them, by words of 32 rows a CTA, as the sort leaves time for, at 4.5 TB/s (40009 tokens of
-    // 50021 x 1347 fp32: 104 us with none, 98 this way).
+    // zeros zeros into as many of them, by words of 32 rows a CTA, as the sort leaves time for, at 4.5 TB/s (40009 tokens
+    // of 50021 x 1347 fp32: 104 us with none, 98 this way; all of them there, 104, and 429 in place of 400 for
+    // 16384 x 8192 bf16, whose reads then come after the zeros and not beside them).
     const int64_t words = (a.rows + 31) / 32, room = ds->embed_clusters > 1 ? ds->embed_clusters - 1 : 1;
     const int64_t clusters = accumulate ? 0 : words < room ? words : room;
     const double sort_us = 10.0 + 2.5e-4 * (double)a.tokens, word_bytes = 32.0 * (double)a.cols * (bf16 ? 2 : 4);

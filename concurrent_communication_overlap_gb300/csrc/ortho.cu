@@ -2,10 +2,10 @@
 //   X = U / (|U|_F + eps);   X <- (a I + b X X^T + c (X X^T)^2) X, some times;   out = scale X
 // (the transposed products where U is tall, so that the square matrices have the short side).
 //
-// Iterates are fp16 times powers of two (ortho_plan.h): the tensor cores' bf16 rate with 11 bits
-// instead of 8.  Five steps end 1.2e-3 off (2-norm, relative, a random
-// 1024 x 1024), below a bf16 output's own rounding (1.7e-3); eight times that, as bf16 would have it, is above.  The polynomial is one matrix, its multiple of I included: a X and (b A + c A^2) X,
-// which nearly cancel, are never rounded apart.
+// Iterates are fp16 times powers of two (ortho_plan.h): the tensor cores' bf16 rate with 11 bits instead
+// of 8.  Five steps end 1.2e-3 off (2-norm, relative, a random 1024 x 1024), below a bf16 output's own
+// rounding, 1.7e-3; eight times that, as bf16 would have it, is above.  The polynomial is one matrix, its
+// multiple of I included: a X and (b A + c A^2) X, which nearly cancel, are never rounded apart.
 //
 // The norm and the conversion are two passes over U; a step is three products by one kernel:
 //   A = X X^T and P = a I + b A + c A A   symmetric: tiles on and above the diagonal alone;
@@ -201,8 +201,24 @@ __global__ void __launch_bounds__(kOrthoThreads, 2) ortho_convert_kernel(OrthoIn
 //
 // A cluster of two CTAs shares a tile of 256 x NT (tcgen05.mma, cta_group::2): each brings in half of
 // A's rows and half of B's and holds the accumulators of its own 128 rows, two sets of them, so that
-// the read-out of a tile hides behind the next.  ACROSS_A, ACROSS_B: the operand lies with its rows
-// (the output's rows or columns) along memory and K across it.
+// the read-out of a tile hides behind the next.  How an operand lies, A_IS and B_IS:
+//   kAlong   K along memory;
+//   kAcross  its rows (the output's rows or columns) along memory and K across it;
+//   kUpper   symmetric, K along memory, and only blocks of 256 x 256 on and above the diagonal are there:
+//            those below are read across, from their mirror image.
+// So a symmetric product writes each of its tiles once.  (Written twice, turned over by way of shared
+// memory, which the tensor cores need, 16 matrices of 1024 x 2048 took 830 us, and 684 turned over by
+// 2-byte stores.)
+//
+// Results leave by TMA, boxes of 32 rows x 64 columns, and what is added to them comes in the same way into
+// the same boxes: lanes that stored whole 32-byte sectors of their own rows kept the load and store units
+// busy for longer than the products (648 us against 618).
+//
+// What bounds it: the tensor cores, and power, where matrices are large (4096 x 4096, under ncu: tensor pipe
+// 80, 75 and 84% of the cycles in a step's three products; 8192 x 28672: 1.6 PFLOP/s of those that have
+// to be done, 20.0 to 20.8 ms); what one SM can bring in, 60 bytes a cycle, for one tile, 0.27 us a K block of
+// 256 x 256; and a launch's way from the last store before it to its own first one, 4.6 us, for
+// matrices of one tile (256 x 640: 78 us for 17 launches).
 constexpr int kGThreads = 320;  // producer, MMA, and the epilogue's eight warps
 constexpr int kGEpiWarps = 8;
 constexpr int kGK = 64;         // K of a stage: 128 bytes
@@ -587,8 +603,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             }
             float alpha = g.alpha;
             for (int i = 0; i < g.times; ++i) alpha *= g.scale[tile.m];
-            // 64 columns at a time, and 32 of them, in loops that are left rolled: what spills here goes all the way to L2,
-            // since shared memory leaves L1 next to nothing (1.3 KB of spills took the experts' 684 us to 1198).
+            // 64 columns at a time, and 32 of them, in loops that are left rolled: short code, which a chain of small products
+            // fetches again and again (both halves unrolled: 256 x 640 116 us against 103), and no spills, which go all the
+            // way to L2, since shared memory leaves L1 next to nothing (1.3 KB: 16 x 1024 x 2048 1198 us against 684).
             //
             // The first tile is preceded by a round on nothing, which stores nothing: the warps would wait for the tile's sums,
             // and so they bring the round's instructions in meanwhile (a product of a small matrix is a chain of first times).

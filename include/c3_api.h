@@ -760,7 +760,8 @@ int c3_moe_combine_backward(const void *dout, int dout_type, const void *y, int 
  * and the orthogonalisation of an update, which needs the whole matrix
  * (c3_allgather).  The conventions of the operators above hold.  A workspace
  * is scratch of one call at a time: calls that may overlap on the GPU, and
- * graphs that may run side by side, need one each.
+ * graphs that may run side by side, need one each.  The library's first call on
+ * a device sets it up and must come before a stream is captured.
  * ------------------------------------------------------------------------ */
 
 /*

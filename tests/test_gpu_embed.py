@@ -154,7 +154,9 @@ def check_gradient(c3, dt, tt, tokens, rows, cols, pad, off, first, kind, accumu
     (1, 1, 1, 0, 0, 0, "any"), (1, 1000, 8, 0, 0, 3, "any"), (2, 1, 8, 0, 0, 0, "one"), (7, 33, 255, 0, 0, 2, "padded"),
     (8, 3, 256, 0, 0, 0, "any"), (9, 40, 257, 3, 1, 5, "padded"), (31, 1025, 520, 0, 4, 0, "any"),
     (33, 1024, 40, 2, 2, 9, "hot"), (64, 64, 1030, 0, 0, 0, "one"), (100, 500, 2048, 8, 8, 100, "padded"),
-    (257, 5000, 2, 0, 0, 0, "hot"), (300, 7, 513, 0, 0, 0, "none"), (0, 9, 12, 1, 0, 0, "any")])
+    (257, 5000, 2, 0, 0, 0, "hot"), (300, 7, 513, 0, 0, 0, "none"), (0, 9, 12, 1, 0, 0, "any"),
+    (1024, 700, 257, 0, 0, 4, "hot"), (1023, 5, 48, 0, 0, 0, "one"), (1025, 100, 56, 0, 0, 0, "hot"),
+    (600, 33, 2050, 0, 0, 0, "padded"), (1000, 20, 8, 0, 0, 0, "any")])
 def test_gradient(c3, dt, tt, tokens, rows, cols, pad, off, first, kind, accumulate):  # noqa: F811
     check_gradient(c3, dt, tt, tokens, rows, cols, pad, off, first, kind, accumulate)
 
