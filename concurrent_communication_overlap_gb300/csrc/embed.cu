@@ -966,7 +966,7 @@ int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, c
     const int passes = (bits + kSortBits - 1) / kSortBits;
     bits = (bits + passes - 1) / passes;
     // Beside the cluster that sorts, as many others as run at once find the rows without tokens, and write
-    // zeros zeros into as many of them, by words of 32 rows a CTA, as the sort leaves time for, at 4.5 TB/s (40009 tokens
+    // zeros into as many of them, by words of 32 rows a CTA, as the sort leaves time for, at 4.5 TB/s (40009 tokens
     // of 50021 x 1347 fp32: 104 us with none, 98 this way; all of them there, 104, and 429 in place of 400 for
     // 16384 x 8192 bf16, whose reads then come after the zeros and not beside them).
     const int64_t words = (a.rows + 31) / 32, room = ds->embed_clusters > 1 ? ds->embed_clusters - 1 : 1;
