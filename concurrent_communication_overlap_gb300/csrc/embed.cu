@@ -250,7 +250,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortBits = 10;  // a digit at most: a thread a bin in the scans
 constexpr int kSortCtas = 8;
-constexpr int kFew = 32;       // tokens of a row that is never cut: a chunk's length at least, a warp's lanes at most
+constexpr int kFew = 32;       // tokens of a row that is never cut: a warp's lanes
 constexpr int kSortHeld = 256;  // pairs a warp holds in shared memory: up to 65536 tokens are read once a pass
 
 // What the sort leaves for the sums.
@@ -462,6 +462,85 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     chain_wait();
     if (blockIdx.x < kSortCtas) sort_by_row(ids, n, first, rows, bits, passes, pairs, other, order);
     else mark_and_fill<Tt, W>(ids, n, first, table, rows, cols, ld, fill, named);
+}
+
+// ---------------------------------------------------------------- order of some thousands of tokens
+//
+// Up to kRankTokens tokens every SM has all rows in shared memory and counts: a token's place is the number of tokens
+// of lower rows, and of its own row before it.  That is n^2 comparisons in place of the sort's chain of latencies: gradients
+// of 4096 tokens into 30000 x 100 bf16 take 22.5 us this way and 26.1 sorted, of 2048 19.1 and 23.6, but of 8192 29.9
+// and 26.0.  Each CTA then finds which of its share of the rows are named, and clears some, as the sort's clusters do.
+constexpr int kRankTokens = 4096;
+constexpr int kRankRows = 1 << 16;  // of a CTA's rows at a time: 8 KB of bits
+
+template <typename Tt, int W>
+__global__ void __launch_bounds__(kSortThreads, 1)
+    embed_rank_kernel(const int32_t* __restrict__ ids, int n, int64_t first, int64_t rows, int2* pairs, EmbedOrder* order,
+                      Tt* table, int64_t cols, int64_t ld, int fill, uint32_t* named) {
+    __shared__ __align__(16) int keys[kRankTokens];
+    __shared__ unsigned marks[kRankRows / 32];
+    constexpr int kNone = 0x7FFFFFFF;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int chunks = (n + 127) / 128;
+    chain_wait();
+    for (int i = threadIdx.x; i < chunks * 128; i += kSortThreads) {
+        const int64_t r = i < n ? (int64_t)ids[i] - first : -1;
+        keys[i] = r >= 0 && r < rows ? (int)r : kNone;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && warp == 0) {
+        int valid = 0;
+        for (int i = lane; i < n; i += 32) valid += keys[i] != kNone;
+        valid = __reduce_add_sync(kAll, valid);
+        if (lane == 0) {
+            order->valid = valid;
+            order->joins = 0;
+        }
+    }
+    for (int i = (int)blockIdx.x * kSortWarps + warp; i < n; i += (int)gridDim.x * kSortWarps) {
+        const int key = keys[i];
+        if (key == kNone) continue;
+        int below = 0;
+        const int4* k4 = reinterpret_cast<const int4*>(keys) + lane;
+        int c = 0;
+#pragma unroll 4
+        for (; c < i / 128; ++c) {
+            const int4 k = k4[c * 32];
+            below += (k.x <= key) + (k.y <= key) + (k.z <= key) + (k.w <= key);
+        }
+        {
+            const int4 k = k4[c * 32];
+            const int j = c * 128 + lane * 4;
+            below += (k.x < key + (j < i)) + (k.y < key + (j + 1 < i)) + (k.z < key + (j + 2 < i)) + (k.w < key + (j + 3 < i));
+        }
+#pragma unroll 4
+        for (++c; c < chunks; ++c) {
+            const int4 k = k4[c * 32];
+            below += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
+        }
+        below = __reduce_add_sync(kAll, below);
+        if (lane == 0) pairs[below] = make_int2(key, i);
+    }
+    if (!named) return;
+    const int64_t words = (rows + 31) / 32, share = (words + gridDim.x - 1) / gridDim.x;
+    const int64_t last = (blockIdx.x + 1) * share < words ? (blockIdx.x + 1) * share : words;
+    for (int64_t w0 = blockIdx.x * share; w0 < last; w0 += kRankRows / 32) {
+        const int many = (int)(last - w0 < kRankRows / 32 ? last - w0 : kRankRows / 32);
+        for (int w = threadIdx.x; w < many; w += kSortThreads) marks[w] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += kSortThreads) {
+            const int64_t r = (int64_t)keys[i] - w0 * 32;
+            if (keys[i] != kNone && r >= 0 && r < many * 32) atomicOr(&marks[r >> 5], 1u << (r & 31));
+        }
+        __syncthreads();
+        const int clear = min(fill, many);
+        for (int w = threadIdx.x; w < many; w += kSortThreads) named[w0 + w] = w < clear ? kAll : marks[w];
+        for (int i = warp; i < 32 * clear; i += kSortWarps) {
+            const int64_t row = w0 * 32 + i;
+            if (row < rows && !(marks[i >> 5] >> (i & 31) & 1)) zero_row<Tt, W>(table + row * ld, cols, lane);
+        }
+        __syncthreads();
+    }
 }
 
 // ---------------------------------------------------------------- sums
@@ -900,9 +979,11 @@ struct EmbedWork {
 static EmbedWork embed_work(int64_t tokens, int64_t rows, int64_t cols) {
     EmbedWork w;
     const int64_t spans = (cols + kSpan - 1) / kSpan;
-    w.chunk = kFew;
+    // Enough for every warp that runs at once to have two, down to 8 tokens: a chunk's rows are written one after the
+    // other (2048 tokens into 9000 x 1001 bf16: chunks of 32 20.8 us in all).  Above 32 tokens more of them cost less.
+    w.chunk = 8;
+    while ((tokens + w.chunk - 1) / w.chunk * spans > (w.chunk < 32 ? 4864 : 16384) && w.chunk < (1 << 20)) w.chunk *= 2;
     static_assert(kFew == 32, "a warp's votes find a short row's ends");
-    while ((tokens + w.chunk - 1) / w.chunk * spans > 16384 && w.chunk < (1 << 20)) w.chunk *= 2;
     w.chunks = (int)((tokens + w.chunk - 1) / w.chunk);
     w.pitch = (cols + 7) / 8 * 8;
     size_t at = 256;
@@ -961,26 +1042,33 @@ int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, c
         count_launch();
         return 0;
     }
+    // Beside the tokens' order the first launch finds the rows without tokens, and writes zeros into as many of them,
+    // by words of 32 rows a CTA, as the order leaves time for, at 4.5 TB/s (40009 tokens of 50021 x 1347 fp32:
+    // 104 us with none, 98 this way; all of them there, 104, and 429 in place of 400 for 16384 x 8192 bf16, whose reads
+    // then come after the zeros and not beside them).
+    const bool rank = a.tokens <= kRankTokens;
+    const int64_t words = (a.rows + 31) / 32, room = rank ? ds->sm_count : ds->embed_clusters > 1 ? ds->embed_clusters - 1 : 1;
+    const int64_t clusters = accumulate || rank ? 0 : words < room ? words : room;
+    const double order_us = rank ? 2.0 + 4e-4 * (double)a.tokens : 10.0 + 2.5e-4 * (double)a.tokens;
+    const double word_bytes = 32.0 * (double)a.cols * (bf16 ? 2 : 4), beside = (double)(rank ? room : room * kSortCtas);
+    const double clear = order_us * 4.5e6 / word_bytes / beside + 0.5;
+    const int fill = clear < kFillBits ? (int)clear : kFillBits;
+    uint32_t* named = accumulate ? nullptr : reinterpret_cast<uint32_t*>(base + w.named);
+    g.named = named;
     int bits = 1;
     while (bits < 31 && ((int64_t)1 << bits) < a.rows) ++bits;
     const int passes = (bits + kSortBits - 1) / kSortBits;
     bits = (bits + passes - 1) / passes;
-    // Beside the cluster that sorts, as many others as run at once find the rows without tokens, and write
-    // zeros into as many of them, by words of 32 rows a CTA, as the sort leaves time for, at 4.5 TB/s (40009 tokens
-    // of 50021 x 1347 fp32: 104 us with none, 98 this way; all of them there, 104, and 429 in place of 400 for
-    // 16384 x 8192 bf16, whose reads then come after the zeros and not beside them).
-    const int64_t words = (a.rows + 31) / 32, room = ds->embed_clusters > 1 ? ds->embed_clusters - 1 : 1;
-    const int64_t clusters = accumulate ? 0 : words < room ? words : room;
-    const double sort_us = 10.0 + 2.5e-4 * (double)a.tokens, word_bytes = 32.0 * (double)a.cols * (bf16 ? 2 : 4);
-    const double fill = clusters ? sort_us * 4.5e6 / word_bytes / (double)(clusters * kSortCtas) + 0.5 : 0;
-    uint32_t* named = reinterpret_cast<uint32_t*>(base + w.named);
-    g.named = named;
-    const unsigned ctas = (unsigned)(kSortCtas * (1 + clusters));
     cudaError_t e = by_types(bf16, bf16, wide, [&](auto t, auto, auto wide_of) {
         using Tt = decltype(t);
-        return launch_chained(embed_sort_kernel<Tt, decltype(wide_of)::value>, dim3(ctas), kSortThreads, sort_smem(bits), s, kSortCtas,
-                              ids, a.tokens, a.first, a.rows, bits, passes, pairs, reinterpret_cast<int2*>(base + w.other), order,
-                              static_cast<Tt*>(table), a.cols, a.ld, fill < kFillBits ? (int)fill : kFillBits, named);
+        constexpr int W = decltype(wide_of)::value;
+        Tt* to = static_cast<Tt*>(table);
+        if (rank)
+            return launch_chained(embed_rank_kernel<Tt, W>, dim3((unsigned)room), kSortThreads, 0, s, 1, ids, a.tokens, a.first, a.rows, pairs,
+                                  order, to, a.cols, a.ld, fill, named);
+        return launch_chained(embed_sort_kernel<Tt, W>, dim3((unsigned)(kSortCtas * (1 + clusters))), kSortThreads, sort_smem(bits), s,
+                              kSortCtas, ids, a.tokens, a.first, a.rows, bits, passes, pairs, reinterpret_cast<int2*>(base + w.other),
+                              order, to, a.cols, a.ld, fill, named);
     });
     if (e != cudaSuccess) return set_cuda_error(e, "embedding order kernel launch");
     count_launch();

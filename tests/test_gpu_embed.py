@@ -162,7 +162,8 @@ def test_gradient(c3, dt, tt, tokens, rows, cols, pad, off, first, kind, accumul
 
 
 @pytest.mark.parametrize("tokens,rows,cols,kind", [
-    (4095, 1000, 24, "any"), (4096, 1023, 8, "hot"), (4097, 1024, 8, "padded"), (5000, 1025, 40, "one"),
+    (2000, 70000, 520, "padded"), (3000, 2500000, 2, "hot"), (4096, 5000, 300, "hot"), (4097, 5000, 300, "hot"),
+    (4000, 1, 16, "one"), (3001, 77, 16, "none"), (1100, 33, 2304, "any"), (4095, 1000, 24, "any"), (4096, 1023, 8, "hot"), (4097, 1024, 8, "padded"), (5000, 1025, 40, "one"),
     (8191, 70001, 16, "any"), (20011, 50021, 24, "hot"), (70001, 131072, 8, "padded"), (66000, 40, 264, "any"),
     (65536, 3, 1040, "hot"), (33000, 1100000, 8, "any"), (300007, 600, 8, "hot"), (12345, 2000, 1347, "padded")])
 @pytest.mark.parametrize("accumulate", [False, True])
