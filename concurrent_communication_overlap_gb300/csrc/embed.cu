@@ -763,9 +763,9 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(Tt* __restric
 // (padding that has an id, say) is left for all the CTA's warps, which add up an eighth of the tokens each; the eighths
 // meet in shared memory, in order.  Rows that no id names are cleared by what follows.
 //
-// The more tokens, the longer every warp looks for its row's: 512 tokens into 50000 x 512 fp32 take 18.8 us, 28.4 sorted;
-// 2048 37.4 and 32.4; 1024 into 9000 x 1001 bf16 14.6 and 23.1, into 6250 x 4096 fp32, of 16 spans, 30.8 and 28.9.
-constexpr int kFewTokens = 1024, kFewJobs = 8192;
+// The more tokens and spans, the longer the warps look for their rows'.  This way and ordered first: 512 tokens into
+// 9000 x 1001 bf16 9.6 us and 11.2, 768 12.5 and 11.5; into 6250 x 4096 fp32, 16 spans, 256 18.3 and 19.8, 512 23.5 and 20.4.
+constexpr int kFewTokens = 512, kFewJobs = 4096;
 constexpr int kAlone = 32;
 
 template <typename Td, typename Tt, int W>
