@@ -13,6 +13,7 @@ constexpr int64_t kMaxRows = 0x7FFFFFFF;  // row numbers are 32-bit
 constexpr int kMaxTopk = 32;              // a warp's lanes
 constexpr int kMaxExperts = 1024;
 constexpr int64_t kMaxOrtho = 1 << 24;
+constexpr int64_t kMaxOrthoElements = (int64_t)1 << 40;
 
 static_assert(C3_TILE_ROWS == kTileRows, "tile rows");
 
@@ -329,8 +330,9 @@ int c3_embed_backward(const void* dout, int dout_type, int64_t dout_ld, const in
 
 static int check_ortho(int64_t rows, int64_t cols, int count) {
     if (rows < 0 || cols < 0 || count < 0) return set_error(C3_EINVAL, "negative rows, cols or count");
-    // (sizes of workspaces, 2 bytes an element, stay within 64 bits)
     if (rows > kMaxOrtho || cols > kMaxOrtho || count > 65535) return set_error(C3_EUNSUP, "above 2^24 rows or columns, or 65535 matrices");
+    // so that sizes of workspaces stay within 64 bits
+    if (rows && cols && count > kMaxOrthoElements / (rows * cols)) return set_error(C3_EUNSUP, "above 2^40 elements");
     return C3_OK;
 }
 

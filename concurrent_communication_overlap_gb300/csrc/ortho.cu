@@ -835,7 +835,8 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
     CUtensorMap xm[2][3], gm[3], pm[3], om;  // boxes of 128, 64 and 32 rows; of the output
     // (A box's last 16-byte unit of a row is written whole.  What so lies behind rows of X, A and P are zeros, of
     // operands' rows that do not exist.)
-    const bool boxes = (uintptr_t)out % 16 == 0 && out_ld % 8 == 0 && cols % 8 == 0;
+    // (a map's strides are below 2^40 bytes)
+    const bool boxes = (uintptr_t)out % 16 == 0 && out_ld % 8 == 0 && cols % 8 == 0 && out_ld < ((int64_t)1 << 39) / rows;
     int rc = 0;
     for (int j = 0; j < 3 && !rc; ++j) {
         const int box = 128 >> j;

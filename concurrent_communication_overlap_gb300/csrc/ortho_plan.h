@@ -54,7 +54,6 @@ inline bool ortho_steps(const float (*coeffs)[3], int steps, OrthoStep* out) {
         s.x = ortho_power(top);
         s.g = ortho_power(q);
         s.p = ortho_power(pmax);
-        // values rounded to 11 bits are up to 2^-11 off what the bound was found for, four times over
         // values rounded to 11 bits are up to 2^-11 off, four times over, what the bound was found for
         top = 1.002 * smax;
         if (!(top <= kOrthoMost) || !(pmax <= kOrthoMost)) return false;

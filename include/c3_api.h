@@ -807,14 +807,15 @@ int c3_embed_backward(const void *dout, int dout_type, int64_t dout_ld, const in
  *   out     bf16 [count][rows][cols], row distance out_ld, matrices rows * out_ld
  *           apart; may be x itself, at the same distances, where x is bf16
  *   work    at least c3_orthogonalize_bytes(rows, cols, count) bytes, device, 256-byte
- *           aligned, scratch (about four times x's elements in bytes, and twice that
- *           of the square matrices on the shorter side)
+ *           aligned, scratch (four bytes for each of x's elements and for each of the
+ *           square matrices' on the shorter side, and 42 MB for parts of products
+ *           where a side is above 448)
  *   sm_budget  as for c3_gemm, but 0 or at least 2: products run on pairs of SMs
  * Iterates and the matrices between are fp16 times powers of two, products are
  * accumulated in fp32: before its rounding to bf16, which is 1.7e-3 off in the 2-norm,
- * the result of five steps was 1.2e-3 off the exact one for a random 1024 x 1024.  Matrices are independent; one with a
- * NaN or an infinity becomes NaN, one of zeros stays zeros.  rows, cols at most
- * 2^24.  c3_orthogonalize_bytes is host only: 0 for bad arguments.
+ * the result of five steps was 1.2e-3 off the exact one for a random 1024 x 1024.
+ * Matrices are independent; one with a NaN or an infinity becomes NaN, one of zeros stays zeros.  rows, cols at most
+ * 2^24, all matrices 2^40 elements.  c3_orthogonalize_bytes is host only: 0 for bad arguments.
  */
 size_t c3_orthogonalize_bytes(int64_t rows, int64_t cols, int count);
 int c3_orthogonalize(const void *x, int type, int64_t rows, int64_t cols, int64_t ld, int count, const float *coeffs,

@@ -171,6 +171,13 @@ def test_gradient_of_many_tokens(c3, tokens, rows, cols, kind, accumulate):  # n
     check_gradient(c3, 1, 0, tokens, rows, cols, 0, 0, 11, kind, accumulate)
 
 
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("tokens,rows,cols,kind", [(1, 3, 1050001, "any"), (40, 2, 1048600, "one"), (5, 600, 700001, "padded")])
+def test_gradient_of_long_rows(c3, tokens, rows, cols, kind, accumulate):  # noqa: F811
+    """Few tokens of so many columns that they are put in order first."""
+    check_gradient(c3, 1, 1, tokens, rows, cols, 0, 0, 11, kind, accumulate)
+
+
 def test_gradient_of_infinities(c3):  # noqa: F811
     """An infinity or a NaN stays in its row and column."""
     dout = torch.zeros(40, 16, device="cuda")

@@ -223,6 +223,18 @@ def test_budgets_change_nothing(c3, budget):  # noqa: F811
     c3.c3_status_check()
 
 
+def test_distance_that_nothing_is_read_at(c3):  # noqa: F811
+    """A single row's distance to a next one may be any, also one that a tensor map cannot hold."""
+    rng = np.random.default_rng(2)
+    x = torch.from_numpy(momentum(rng, 1, 1, 264)).cuda().to(torch.bfloat16)
+    for ld in (264, 1 << 38, 1 << 39, 1 << 42):
+        out = torch.full((264,), 7.0, dtype=torch.bfloat16, device="cuda")
+        c3.c3_orthogonalize(x, 1, 1, 264, out, torch.empty(c3.c3_orthogonalize_bytes(1, 264), dtype=torch.uint8, device="cuda"),
+                            [QUINTIC], ld=ld, out_ld=ld)
+        assert relative(out.view(1, 264), oracle(x[0].double(), [QUINTIC])) <= 3.4445 * F * 3 ** 0.5 + H
+    c3.c3_status_check()
+
+
 def test_past_32_bits(c3):  # noqa: F811
     """A stack of matrices whose elements pass 2^31, one step each."""
     count, rows, cols = 17, 8192, 16384  # 2.28 G elements

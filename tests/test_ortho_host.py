@@ -45,6 +45,11 @@ def test_refusals(c3):
         assert c3.c3_last_error()
     for kw in (dict(rows=1 << 25), dict(cols=1 << 25, ld=1 << 25, out_ld=1 << 25), dict(count=65536)):
         assert f(**kw) == c3.C3_EUNSUP, kw
+    # sizes whose workspace would pass 64 bits, and the first above the limit
+    for m, n, k in ((1 << 24, 1 << 24, 65535), (1 << 24, 1 << 24, 1), (1 << 20, 1 << 20, 2), (1 << 16, (1 << 24) - 1, 2)):
+        assert f(rows=m, cols=n, count=k, nbytes=2 ** 64 - 1) == c3.C3_EUNSUP, (m, n, k)
+        assert c3.c3_orthogonalize_bytes(m, n, k) == 0
+    assert c3.c3_orthogonalize_bytes(1 << 20, 1 << 20) > 1 << 43
     for kw in (dict(x=P + 2), dict(x=P + 1, type=1), dict(out=P + 1), dict(work=P + 16)):
         assert f(**kw) == c3.C3_EALIGN, kw
     for kw in (dict(rows=0), dict(cols=0), dict(count=0)):
