@@ -73,21 +73,73 @@ struct OrthoWalk {
 };
 constexpr int kOrthoAhead = 4;  // pieces of which a warp has the loads in flight
 
-// The warp's values of a piece, 8 a lane.
-template <typename T, int W>
-__device__ __forceinline__ void load_piece(const OrthoIn& g, const T* x, const OrthoWalk& at, int lane, float (&v)[8]) {
-    const int64_t c0 = (int64_t)at.span * kOrthoSpan + lane * W;
-    const T* from = x + at.row * g.ld + c0;
-#pragma unroll
-    for (int u = 0; u < 8 / W; ++u) {
-        float t[W] = {};
-        if (at.row < g.rows && c0 + 32 * W * u < g.cols) load_w<W>(from + 32 * W * u, t);
-#pragma unroll
-        for (int k = 0; k < W; ++k) v[u * W + k] = t[k];
-    }
-}
+// A lane's eight values of a piece, as they are loaded and not looked at: many are in flight at once.
+//   kWhole    rows are whole, aligned units of eight neighbours;
+//   kShifted  bf16: the two aligned units that a lane's eight neighbours lie in, shifted when they are there, and at a
+//             row's ends, where a unit has other values too, one by one;
+//   kSingles  fp32: one by one, 32 apart (shifted, 5003 x 1347 took 268 us in all, this way 260).
+// (35 M bf16 in rows of 4321: norm and conversion 62 and 65 us with loads and stores of single values, 29 and 43 this way.)
+enum { kWhole = 0, kShifted = 1, kSingles = 2 };
+template <typename T, int FORM>
+struct OrthoPiece {
+    static_assert(FORM == kWhole || (sizeof(T) == 2) == (FORM == kShifted), "form");
+    uint32_t w[FORM == kWhole && sizeof(T) == 2 ? 4 : 8];
+    int shift;  // kShifted: by how many values, or -1: one in each word
 
-template <typename T, int W>
+    __device__ __forceinline__ void load(const OrthoIn& g, const T* x, const OrthoWalk& at, int lane) {
+        const int64_t c = (int64_t)at.span * kOrthoSpan + lane * (FORM == kSingles ? 1 : 8);
+        const T* from = x + at.row * g.ld + c;
+        const bool there = at.row < g.rows && c < g.cols;
+        if constexpr (FORM == kSingles) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = there && c + 32 * i < g.cols ? __float_as_uint(from[32 * i]) : 0;
+            return;
+        }
+        shift = FORM == kWhole ? 0 : (int)((uintptr_t)from % 16 / sizeof(T));
+        if constexpr (FORM == kShifted) {
+            if (c < shift || c - shift + (shift ? 16 : 8) > g.cols) {
+                shift = -1;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = there && c + i < g.cols ? reinterpret_cast<const uint16_t*>(from)[i] : 0;
+                return;
+            }
+        }
+        const uint4* unit = reinterpret_cast<const uint4*>(from - shift);
+#pragma unroll
+        for (int k = 0; k < (int)(sizeof(w) / 16); ++k) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (there && (FORM == kWhole || k == 0 || shift)) u = unit[k];
+            w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+            return;
+        } else {
+            if constexpr (FORM == kShifted) {
+                if (shift < 0) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i] << 16);
+                    return;
+                }
+#pragma unroll
+                for (int by = 2; by > 0; by /= 2)
+                    if (shift & (2 * by)) {
+#pragma unroll
+                        for (int i = 0; i + by < 8; ++i) w[i] = w[i + by];
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (shift & 1) * 16);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        }
+    }
+};
+
+template <typename T, int FORM>
 __global__ void __launch_bounds__(kOrthoThreads, 2) ortho_norm_kernel(OrthoIn g) {
     __shared__ float part[kOrthoWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -102,16 +154,19 @@ __global__ void __launch_bounds__(kOrthoThreads, 2) ortho_norm_kernel(OrthoIn g)
             float sum = 0.0f;
             OrthoWalk at(p * kOrthoWarps + warp, (int64_t)g.parts * kOrthoWarps, g.cols);
             while (at.row < g.rows) {
-                float v[kOrthoAhead][8];
+                OrthoPiece<T, FORM> piece[kOrthoAhead];
 #pragma unroll
-                for (int a = 0; a < kOrthoAhead; ++a, at.next()) load_piece<T, W>(g, x, at, lane, v[a]);
+                for (int a = 0; a < kOrthoAhead; ++a, at.next()) piece[a].load(g, x, at, lane);
 #pragma unroll
-                for (int a = 0; a < kOrthoAhead; ++a)
+                for (int a = 0; a < kOrthoAhead; ++a) {
+                    float v[8];
+                    piece[a].values(v);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const float t = scaled(v[a][k]);
+                        const float t = scaled(v[k]);
                         sum = fmaf(t, t, sum);
                     }
+                }
             }
             sum = warp_sum(sum);
             if (lane == 0) part[warp] = sum;
@@ -131,7 +186,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 2) ortho_norm_kernel(OrthoIn g)
 // X = U 2^-e in fp16, where 2^e is the power of two above |U| + eps: exact for bf16.  What is left of the
 // division, 2^e / (|U| + eps) in (1, 2], goes to scale[m] and into the first step's products.  A NaN or an
 // infinity makes the whole matrix NaN.
-template <typename T, int W>
+template <typename T, int FORM>
 __global__ void __launch_bounds__(kOrthoThreads, 2) ortho_convert_kernel(OrthoIn g) {
     __shared__ float factors[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -161,35 +216,40 @@ __global__ void __launch_bounds__(kOrthoThreads, 2) ortho_convert_kernel(OrthoIn
         __half* out = g.out + m * g.rows * g.pitch;
         OrthoWalk at(p * kOrthoWarps + warp, (int64_t)g.parts * kOrthoWarps, g.pitch);
         while (at.row < g.rows) {
-            float v[2][8];
+            OrthoPiece<T, FORM> piece[2];
             OrthoWalk to = at;
 #pragma unroll
-            for (int a = 0; a < 2; ++a, at.next()) load_piece<T, W>(g, x, at, lane, v[a]);
-            if (f1 != 1.0f) {
-#pragma unroll
-                for (int k = 0; k < 16; ++k) v[k / 8][k % 8] *= f1;
-            }
+            for (int a = 0; a < 2; ++a, at.next()) piece[a].load(g, x, at, lane);
 #pragma unroll
             for (int a = 0; a < 2; ++a, to.next()) {
                 if (to.row >= g.rows) break;
-                const int64_t c0 = (int64_t)to.span * kOrthoSpan + lane * W;
+                float v[8];
+                piece[a].values(v);
+                if (f1 != 1.0f) {
 #pragma unroll
-                for (int u = 0; u < 8 / W; ++u) {
-                    const int64_t c = c0 + 32 * W * u;
-                    if (c >= g.pitch) continue;
-                    __half* h = out + to.row * g.pitch + c;
-                    if constexpr (W == 1) {
-                        *h = __float2half_rn(v[a][u] * f0);
-                    } else {
-                        uint32_t w[W / 2];
+                    for (int k = 0; k < 8; ++k) v[k] *= f1;
+                }
+                // kSingles: lanes of a pair trade half their values, so that each has pairs of neighbours
+                const bool odd = lane & 1;
+                uint32_t w[4];
 #pragma unroll
-                        for (int k = 0; k < W / 2; ++k) {
-                            const __half2 t = __floats2half2_rn(v[a][u * W + 2 * k] * f0, v[a][u * W + 2 * k + 1] * f0);
-                            w[k] = *reinterpret_cast<const uint32_t*>(&t);
-                        }
-                        if constexpr (W == 8) *reinterpret_cast<uint4*>(h) = make_uint4(w[0], w[1], w[2], w[3]);
-                        else *reinterpret_cast<uint32_t*>(h) = w[0];
+                for (int k = 0; k < 4; ++k) {
+                    float lo = v[2 * k] * f0, hi = v[2 * k + 1] * f0;
+                    if constexpr (FORM == kSingles) {
+                        const float got = __shfl_xor_sync(kAll, odd ? lo : hi, 1);
+                        (odd ? lo : hi) = got;
                     }
+                    const __half2 t = __floats2half2_rn(lo, hi);
+                    w[k] = *reinterpret_cast<const uint32_t*>(&t);
+                }
+                const int64_t c = (int64_t)to.span * kOrthoSpan + (FORM == kSingles ? (odd ? 32 : 0) + (lane & ~1) : lane * 8);
+                __half* h = out + to.row * g.pitch + c;
+                if constexpr (FORM == kSingles) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (c + 64 * k < g.pitch) *reinterpret_cast<uint32_t*>(h + 64 * k) = w[k];
+                } else {
+                    if (c < g.pitch) *reinterpret_cast<uint4*>(h) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
         }
@@ -256,7 +316,10 @@ struct OrthoCfg {
     static constexpr uint32_t kABytes = 128 * 128;
     static constexpr uint32_t kBBytes = NT / 2 * 128;
     static constexpr uint32_t kStage = kABytes + kBBytes;
-    static constexpr uint32_t kStaging = kGEpiWarps * 2 * 4096;  // a warp: two boxes of 32 rows x 64 columns
+    // Boxes of 32 rows x 64 columns a warp, all of a tile's.  (One, and a sixth stage in its place: 5 x 1605 x 4321 922 us
+    // against 889, 16 x 1024 x 2048 540 against 558.)
+    static constexpr int kBoxes = NT / 128;
+    static constexpr uint32_t kStaging = kGEpiWarps * kBoxes * 4096;
     static constexpr int kExtra = 1024 + 512 + (int)kStaging;
     static constexpr int kFit = (kGSmemLimit - kExtra) / (int)kStage;
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
@@ -370,9 +433,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                          const __grid_constant__ CUtensorMap acrossA, const __grid_constant__ CUtensorMap acrossB,
                          const __grid_constant__ CUtensorMap tmMat, const __grid_constant__ CUtensorMap tmOut, OrthoProduct g,
                          DevStatus* st) {
+    constexpr bool kMat = A_IS == kUpper && B_IS == kUpper;  // beta mat + diag I is added
     using Cfg = OrthoCfg<NT>;
     constexpr int S = Cfg::kStages;
-    constexpr bool kMat = A_IS == kUpper && B_IS == kUpper;  // beta mat + diag I is added
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -523,7 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         }
     } else {
         const int q = warp & 3, half = (warp - 2) >> 2;
-        const uint32_t box0 = staging + (uint32_t)(warp - 2) * 8192u;
+        const uint32_t box0 = staging + (uint32_t)(warp - 2) * (Cfg::kBoxes * 4096u);
         constexpr int kRounds = NT / 128;  // of 64 columns: half of the tile's
         chain_ready();
         uint32_t mat_phase = 0;
@@ -623,7 +686,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                     const bool in = mbar_wait(bar(BOX + (warp - 2) * 2 + rd), mat_phase, abort_flag);
                     if (!__all_sync(kAll, in)) report_error(st, -4, kSiteOrthoEpilogue);
                 } else {
-                    if (lane == 0) bulk_wait_read<kRounds - 1>();  // what the box held a tile ago has left it
+                    if (lane == 0) bulk_wait_read<Cfg::kBoxes - 1>();  // what the box held has left it
                     __syncwarp();
                 }
 #pragma unroll 1
@@ -735,7 +798,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 
 template <int NT, bool CUT, typename F>
 static int each_product(F f) {
-    const int smem = OrthoCfg<NT>::kSmem;
+    constexpr int smem = OrthoCfg<NT>::kSmem;
     int rc = f(ortho_product_kernel<NT, kAlong, kAlong, CUT, true>, smem);
     if (!rc) rc = f(ortho_product_kernel<NT, kAcross, kAcross, CUT, true>, smem);
     if (!rc) rc = f(ortho_product_kernel<NT, kUpper, kUpper, CUT, true>, smem);
@@ -775,16 +838,16 @@ static int ortho_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols
 size_t ortho_bytes(int64_t rows, int64_t cols, int count) { return ortho_work(rows, cols, count).bytes; }
 
 template <typename T>
-static cudaError_t ortho_in(int w, unsigned grid, cudaStream_t s, const OrthoIn& in) {
+static cudaError_t ortho_in(bool whole, unsigned grid, cudaStream_t s, const OrthoIn& in) {
     auto go = [&](auto norm, auto convert) {
         cudaError_t e = launch_chained(norm, dim3(grid), kOrthoThreads, 0, s, 1, in);
         if (e != cudaSuccess) return e;
         count_launch();
         return launch_chained(convert, dim3(grid), kOrthoThreads, 0, s, 1, in);
     };
-    return w == 8   ? go(ortho_norm_kernel<T, 8>, ortho_convert_kernel<T, 8>)
-           : w == 2 ? go(ortho_norm_kernel<T, 2>, ortho_convert_kernel<T, 2>)
-                    : go(ortho_norm_kernel<T, 1>, ortho_convert_kernel<T, 1>);
+    constexpr int kElse = sizeof(T) == 2 ? kShifted : kSingles;
+    return whole ? go(ortho_norm_kernel<T, kWhole>, ortho_convert_kernel<T, kWhole>)
+                 : go(ortho_norm_kernel<T, kElse>, ortho_convert_kernel<T, kElse>);
 }
 
 int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld, int count, const float (*coeffs)[3], int steps,
@@ -819,12 +882,9 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
     in.parts = (int)(most < want ? most : want);
     if (in.parts > kOrthoParts) in.parts = kOrthoParts;
     const int64_t all = (int64_t)in.parts * count, fit = sm_budget > 0 && cap < ds->sm_count ? cap : 2 * (int64_t)cap;
-    const int size = bf16 ? 2 : 4;
-    const int64_t unit8 = 8 * size < 16 ? 8 * size : 16;
-    auto fits = [&](int64_t bytes) { return (uintptr_t)x % bytes == 0 && ld * size % bytes == 0; };
-    const int wide = cols % 8 == 0 && fits(unit8) ? 8 : cols % 2 == 0 && fits(2 * size) ? 2 : 1;
+    const bool whole = cols % 8 == 0 && (uintptr_t)x % 16 == 0 && ld % (bf16 ? 8 : 4) == 0;
     const unsigned grid = (unsigned)(all < fit ? all : fit);
-    cudaError_t e = bf16 ? ortho_in<__nv_bfloat16>(wide, grid, s, in) : ortho_in<float>(wide, grid, s, in);
+    cudaError_t e = bf16 ? ortho_in<__nv_bfloat16>(whole, grid, s, in) : ortho_in<float>(whole, grid, s, in);
     if (e != cudaSuccess) return set_cuda_error(e, "orthogonalisation: norm kernel launch");
     count_launch();
 

@@ -223,6 +223,24 @@ def test_budgets_change_nothing(c3, budget):  # noqa: F811
     c3.c3_status_check()
 
 
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("cols", [1, 7, 8, 9, 15, 16, 17, 31, 33, 255, 257, 520, 777])
+def test_rows_that_begin_anywhere(c3, ty, cols):  # noqa: F811
+    """The one step X <- 1 X, where every value is the division by the norm alone: f for the conversion of fp32 (bf16 is
+    exact), h for the output and 2^-20 for the norm, value by value.  What lies around the rows is NaN."""
+    rng = np.random.default_rng(cols)
+    rows = 5
+    for off in range(9):
+        for pad in (0, 1, 6, 8):
+            g = Guarded((2 * rows * (cols + pad) + off,), TD[ty], float("nan"))
+            x = g.t[off:].view(2, rows, cols + pad)[:, :, :cols]
+            x.copy_(torch.from_numpy(rng.uniform(1, 2, (2, rows, cols)) * rng.choice([-1, 1], (2, rows, cols))))
+            out = run(c3, g.t[off:], ty, 2, rows, cols, [(1, 0, 0)], ld=cols + pad)
+            ref = x.double() / (torch.linalg.vector_norm(x.double(), dim=(1, 2), keepdim=True) + 1e-7)
+            assert ((out.double() - ref).abs() <= (H + 2.0 ** -20 + (0 if ty else F)) * ref.abs()).all(), (off, pad)
+    c3.c3_status_check()
+
+
 def test_distance_that_nothing_is_read_at(c3):  # noqa: F811
     """A single row's distance to a next one may be any, also one that a tensor map cannot hold."""
     rng = np.random.default_rng(2)
