@@ -709,9 +709,17 @@ __global__ void __launch_bounds__(kEmbedThreads, 2)
 
 // The rows that were cut: tails[c] + heads[c + 1] + ... .  A CTA takes a row and kSpan columns; its warps
 // add up consecutive parts, and the warps' sums meet in shared memory, in order.
-template <typename Tt, int W>
-__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(Tt* __restrict__ table, EmbedSum g) {
-    __shared__ float part[kEmbedWarps][8][32];
+//
+// Latency bounds it.  Rows of up to kJoinSpans spans: 16 warps a row and four parts in flight each, since few rows make few
+// CTAs (32768 tokens of a power law, 256 columns: 36 us in all, and 43 with 8 warps; one row for all of them 67 and
+// 170).  Longer rows: 8 warps and eight parts, of which more rows run at once (16384 x 8192 bf16 391 us, and 400 with 16
+// warps; 32768 x 4096 129 and 136; 2048 columns 80 either way).  Told to leave room for a second CTA or none, the
+// compiler took 120 registers in place of 48 to 73 for the latter, and 32768 x 4096 133 us.
+constexpr int kJoinSpans = 8;
+template <typename Tt, int W, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 2 : 0) embed_join_kernel(Tt* __restrict__ table, EmbedSum g) {
+    constexpr int B = WARPS == 16 ? 4 : 8;  // parts in flight
+    __shared__ float part[WARPS][8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t spans = (g.cols + kSpan - 1) / kSpan;
     chain_wait();
@@ -720,25 +728,31 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(Tt* __restric
         const int64_t at = job / spans, c = (job - at * spans) * kSpan, ch = g.joins[at];
         const int n = (int)(g.cols - c < kSpan ? g.cols - c : kSpan);
         const int row = g.pairs[(ch + 1) * g.chunk].x;
-        int parts = 1;
-        for (;; parts += 32) {  // how many chunks begin with the row
-            const int64_t p = (ch + parts + lane) * g.chunk;
-            const int more = run_of(__ballot_sync(kAll, p < valid && g.pairs[p < valid ? p : 0].x == row));
-            if (more < 32) {
-                parts += more;
-                break;
+        // how many chunks begin with the row: the next 32 first, then by steps that bring what is left down to a 32nd
+        auto begins = [&](int64_t k) {
+            const int64_t p = (ch + k) * g.chunk;
+            return p < valid && g.pairs[p].x == row;
+        };
+        int more = run_of(__ballot_sync(kAll, begins(1 + lane))), parts = 1 + more;
+        if (more == 32) {
+            int left = (int)((valid - 1) / g.chunk - ch) - 32;  // chunks behind those
+            while (left > 0) {
+                const int apart = (left + 31) / 32, probe = (lane + 1) * apart;
+                more = run_of(__ballot_sync(kAll, probe <= left && begins(parts - 1 + probe)));
+                parts += more * apart;
+                left = min(left - more * apart, apart - 1);
             }
         }
-        const int per = (parts + kEmbedWarps - 1) / kEmbedWarps, to = min(parts, (warp + 1) * per);
+        const int per = (parts + WARPS - 1) / WARPS, to = min(parts, (warp + 1) * per);
         float acc[8] = {};
 #pragma unroll 1
-        for (int k0 = warp * per; k0 < to; k0 += 4) {
-            float v[4][8];
+        for (int k0 = warp * per; k0 < to; k0 += B) {
+            float v[B][8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < B; ++j)
                 Parked<W>::load((k0 + j ? g.heads : g.tails) + (ch + k0 + j) * g.pitch + c + lane * W, k0 + j < to ? n - lane * W : 0, v[j]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < B; ++j)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[i] += v[j][i];
         }
@@ -750,7 +764,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(Tt* __restric
             for (int i = 0; i < 8; ++i) {
                 acc[i] = 0.0f;
 #pragma unroll
-                for (int x = 0; x < kEmbedWarps; ++x) acc[i] += part[x][i][lane];
+                for (int x = 0; x < WARPS; ++x) acc[i] += part[x][i][lane];
             }
             add_row<Tt, W>(g, table, row, c, n, acc, lane);
         }
@@ -1084,7 +1098,8 @@ int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, c
         const cudaError_t err = accumulate ? sum(embed_sum_kernel<Td, Tt, W, true>) : sum(embed_sum_kernel<Td, Tt, W, false>);
         if (err != cudaSuccess || join_grid == 0) return err;
         count_launch();
-        return launch_chained(embed_join_kernel<Tt, W>, dim3(join_grid), kEmbedThreads, 0, s, 1, static_cast<Tt*>(table), g);
+        if (spans <= kJoinSpans) return launch_chained(embed_join_kernel<Tt, W, 16>, dim3(join_grid), 512, 0, s, 1, static_cast<Tt*>(table), g);
+        return launch_chained(embed_join_kernel<Tt, W, 8>, dim3(join_grid), 256, 0, s, 1, static_cast<Tt*>(table), g);
     });
     if (e != cudaSuccess) return set_cuda_error(e, "embedding gradient kernel launch");
     count_launch();

@@ -171,6 +171,13 @@ def test_gradient_of_many_tokens(c3, tokens, rows, cols, kind, accumulate):  # n
     check_gradient(c3, 1, 0, tokens, rows, cols, 0, 0, 11, kind, accumulate)
 
 
+@pytest.mark.parametrize("tokens", [513, 520, 768, 769, 1025, 8439, 8448, 8449, 8456, 38912, 38913])
+@pytest.mark.parametrize("kind,cols", [("one", 8), ("hot", 8), ("one", 2500)])
+def test_gradient_of_rows_cut_into_many_parts(c3, tokens, kind, cols):  # noqa: F811
+    """Around the numbers of parts at which their count takes another turn: 1 + 32, 1 + 32 + 32, 1 + 32 + 1024 of 8 tokens."""
+    check_gradient(c3, 0, 0, tokens, 90, cols, 0, 0, 3, kind, True)
+
+
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("tokens,rows,cols,kind", [(1, 3, 1050001, "any"), (40, 2, 1048600, "one"), (5, 600, 700001, "padded")])
 def test_gradient_of_long_rows(c3, tokens, rows, cols, kind, accumulate):  # noqa: F811
