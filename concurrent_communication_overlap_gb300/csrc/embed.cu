@@ -713,9 +713,9 @@ __global__ void __launch_bounds__(kEmbedThreads, 2)
 // Latency bounds it.  Rows of up to kJoinSpans spans: 16 warps a row and four parts in flight each, since few rows make few
 // CTAs (32768 tokens of a power law, 256 columns: 36 us in all, and 43 with 8 warps; one row for all of them 67 and
 // 170).  Longer rows: 8 warps and eight parts, of which more rows run at once (16384 x 8192 bf16 391 us, and 400 with 16
-// warps; 32768 x 4096 129 and 136; 2048 columns 80 either way).  Told to leave room for a second CTA or none, the
+// warps; 32768 x 4096 129 and 136; 1024 columns 55 and 54, 2048 81 either way).  Told to leave room for a second CTA or none, the
 // compiler took 120 registers in place of 48 to 73 for the latter, and 32768 x 4096 133 us.
-constexpr int kJoinSpans = 8;
+constexpr int kJoinSpans = 4;
 template <typename Tt, int W, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 2 : 0) embed_join_kernel(Tt* __restrict__ table, EmbedSum g) {
     constexpr int B = WARPS == 16 ? 4 : 8;  // parts in flight
