@@ -481,7 +481,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     __syncthreads();
     cluster_sync_all();  // both CTAs' barriers are ready before either signals the other's
     tc_fence_after();
-    // (The MMA warp waits for no other grid: it reads shared memory alone.)
     const uint32_t tmem = *tmem_slot;
     const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
 
@@ -543,6 +542,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
+            // It reads shared memory alone, but its waits have a limit, which must not run while the kernels before do:
+            // these may take seconds, on few SMs.
+            chain_ready();
             for (int local = 0; ok; ++local) {
                 const OrthoWorkItem item = ortho_item<CUT>(g.cut, pair, pairs, local);
                 if (item.tile < 0) break;

@@ -284,3 +284,31 @@ def test_an_injected_launch_failure_is_reported(c3):  # noqa: F811
     assert e.value.status == c3.C3_ECUDA and "injected" in str(e.value)
     run(c3, x, 1, 1, 8, 8, [QUINTIC])
     c3.c3_status_check()
+
+
+def blocks_of(count, rows, cols, seed):
+    """A matrix of zeros but for two blocks that share no rows or columns, and where they are."""
+    x = torch.zeros(count, rows, cols, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    at = [(slice(0, 300), slice(cols - 200, cols)), (slice(rows - 100, rows), slice(0, 50))]
+    for r, c in at:
+        x[:, r, c] = torch.randn(count, r.stop - r.start, c.stop - c.start, generator=gen, device="cuda").to(torch.bfloat16)
+    return x, at
+
+
+def test_a_chain_longer_than_a_waits_limit(c3):  # noqa: F811
+    """Products on one pair of SMs that take several seconds together: the limit of a wait in a later product does not run
+    while the earlier ones do."""
+    rows, cols, steps = 16384, 20480, 6  # 1.25e14 operations at some 2.5e13 a second and pair
+    x, at = blocks_of(1, rows, cols, 3)
+    out = run(c3, x, 1, 1, rows, cols, [QUINTIC] * steps, sm_budget=2)
+    c3.c3_status_check()
+    norm = torch.linalg.vector_norm(x[0].double()) + float(np.float32(1e-7))
+    for r, c in at:  # each block is a product of its own, with the whole matrix's norm
+        u = x[0, r, c].double() / norm
+        for a, b, q in np.asarray([QUINTIC] * steps, np.float32).astype(np.float64):
+            g = u @ u.T
+            u = a * u + (b * g + q * (g @ g)) @ u
+        assert relative(out[0, r, c], u) <= 3.4445 * F * (3 * steps) ** 0.5 + H
+        out[0, r, c] = 0
+    assert not out.any()
