@@ -40,6 +40,7 @@ struct OrthoIn {
     int count, parts;
     double eps;
     int power;  // 2^power: X's first scale
+    int early;  // the next kernel may start beside this one
     double* sums;
     float* scale;
     int* counts;  // of the products' parts, to be zero before the first
@@ -143,7 +144,8 @@ template <typename T, int FORM>
 __global__ void __launch_bounds__(kOrthoThreads, 2) ortho_norm_kernel(OrthoIn g) {
     __shared__ float part[kOrthoWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    chain_wait();
+    if (g.early) chain_next();
+    chain_ready();
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < kOrthoRuns * 16; i += kOrthoThreads) g.counts[i] = 0;
     for (int64_t i = blockIdx.x; i < (int64_t)g.count * g.parts; i += gridDim.x) {
@@ -190,7 +192,8 @@ template <typename T, int FORM>
 __global__ void __launch_bounds__(kOrthoThreads, 2) ortho_convert_kernel(OrthoIn g) {
     __shared__ float factors[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    chain_wait();
+    if (g.early) chain_next();
+    chain_ready();
     for (int64_t i = blockIdx.x; i < (int64_t)g.count * g.parts; i += gridDim.x) {
         const int64_t m = i / g.parts, p = i - m * g.parts;
         if (warp == 0) {
@@ -302,6 +305,7 @@ struct OrthoProduct {
     int64_t ld, stride;  // of out, and from one matrix to the next (no tensor map)
     int M, N, num_kb, count;
     int bf16, times;
+    int early;           // the next kernel may start beside this one
     int width;           // bytes that rows of out are aligned to (no tensor map)
     float alpha, beta, diag;
     OrthoTiles tiles;    // symmetric: tiles above the diagonal
@@ -451,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
 
-    chain_next();
+    if (g.early) chain_next();
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         for (int i = 0; i < S; ++i) {
@@ -873,6 +877,10 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
     in.count = count;
     in.eps = eps;
     in.power = step[0].x;
+    // Under a budget no kernel starts beside the one before, on SMs that are left to others: one product after the
+    // other would wait there with all of an SM's shared memory (20 SMs, 8192 x 8192: a product of 0.1 ms on the
+    // other 132 took 3.6 ms).
+    in.early = cap == ds->sm_count;
     in.sums = reinterpret_cast<double*>(base + w.sums);
     in.scale = reinterpret_cast<float*>(base + w.scale);
     in.counts = reinterpret_cast<int*>(base + w.counts);
@@ -953,6 +961,7 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
         OrthoProduct g{};
         g.scale = in.scale;
         g.count = count;
+        g.early = in.early;
         // A = X X^T (X^T X): the stored 2^x X give 2^2x of it
         g.M = g.N = (int)m;
         g.num_kb = blocks(tall ? rows : cols, kGK);

@@ -6,6 +6,8 @@ and f |P| and its own sums' m 2^-23 |c| |A| |A|; the result by dP |X| + |P| dX a
 for fp32 inputs and 0 for bf16, and by h of itself.  Several steps, in the 2-norm: three roundings a step of f at most
 each, independent of one another, each carried on by a factor of at most 3.4445, the quintic's steepest slope on the
 singular values that it leaves: 3.4445 f sqrt(3 steps), and h for the output."""
+import time
+
 import numpy as np
 import pytest
 
@@ -312,3 +314,34 @@ def test_a_chain_longer_than_a_waits_limit(c3):  # noqa: F811
         assert relative(out[0, r, c], u) <= 3.4445 * F * (3 * steps) ** 0.5 + H
         out[0, r, c] = 0
     assert not out.any()
+
+
+def test_a_budget_leaves_the_other_sms_free(c3):  # noqa: F811
+    """A product on 132 SMs beside an orthogonalisation on 20: it waits for none of the 15 products there, which take 37 ms.
+    (Where the later of them stood on other SMs already, waiting, it took 30 times its time alone.)"""
+    n, m = 8192, 4096
+    x = torch.ones(n, n, dtype=torch.bfloat16, device="cuda")
+    out, work = torch.empty_like(x), torch.empty(c3.c3_orthogonalize_bytes(n, n), dtype=torch.uint8, device="cuda")
+    a, product = torch.ones(m, m, dtype=torch.bfloat16, device="cuda"), torch.empty(m, m, device="cuda")
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def timed():
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record(two)
+        c3.c3_gemm(a, a, product, m, m, m, sm_budget=132, stream=two)
+        end.record(two)
+        return begin, end
+
+    alone, beside = [], []
+    for _ in range(6):
+        torch.cuda.synchronize()
+        begin, end = timed()
+        torch.cuda.synchronize()
+        alone.append(begin.elapsed_time(end))
+        c3.c3_orthogonalize(x, 1, n, n, out, work, [QUINTIC] * 5, sm_budget=20, stream=one)
+        time.sleep(0.003)
+        begin, end = timed()
+        torch.cuda.synchronize()
+        beside.append(begin.elapsed_time(end))
+    c3.c3_status_check()
+    assert min(beside) < 6 * min(alone), (alone, beside)
