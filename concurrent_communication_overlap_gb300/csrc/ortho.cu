@@ -546,9 +546,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            // It reads shared memory alone, but its waits have a limit, which must not run while the kernels before do:
-            // these may take seconds, on few SMs.
-            chain_ready();
             for (int local = 0; ok; ++local) {
                 const OrthoWorkItem item = ortho_item<CUT>(g.cut, pair, pairs, local);
                 if (item.tile < 0) break;
@@ -560,6 +557,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 tc_fence_after();
                 const OrthoTile tile = ortho_tile<NT>(g, item.tile);
                 const uint32_t d = tmem + (uint32_t)(buf * NT);
+                // It reads shared memory alone, but its waits have a limit, which must not run while the kernels before
+                // do: these may take seconds, on few SMs.  (The waits above end at once the first time.)
+                if (local == 0) chain_ready();
                 for (int kb = item.kb0; kb < item.kb1; ++kb) {
                     if (!mbar_wait_cluster(bar(stage), phase, abort_flag)) {
                         report_error(st, -4, kSiteOrthoMma);
