@@ -30,9 +30,10 @@ constexpr int kOrthoWarps = kOrthoThreads / 32;
 constexpr int kOrthoSpan = 256;
 
 // Sums of squares are fp32 within a CTA, where their total is far from both ends of fp32's range, and fp64 between
-// CTAs.  A CTA whose total is not (or is no number) adds its squares up again times 2^-140 and 2^140.
-constexpr float kTiny = 8.470329472543003e-22f, kHuge = 1.1805916207174113e21f;  // 2^-70, 2^70
-constexpr double kTwo140 = 2.0 * 1180591620717411303424.0 * 590295810358705651712.0;
+// CTAs.  A CTA whose total is not (or is no number) adds its squares up again times 2^-180 or 2^180: 2^38 values below 2^128
+// stay below 2^114 that way, squares of 2^-149 are 2^-118, and what a sum of 1e36 or 1e-18 consists of lies between.
+constexpr float kTiny = 8.077935669463161e-28f, kHuge = 1.2379400392853803e27f;  // 2^-90, 2^90
+constexpr double kTwo180 = (double)kHuge * (double)kHuge;
 
 struct OrthoIn {
     const void* x;
@@ -179,8 +180,8 @@ __global__ void __launch_bounds__(kOrthoThreads, 2) ortho_norm_kernel(OrthoIn g)
         };
         const float sum = squares([](float v) { return v; });
         double total = sum;
-        if (!(sum < 1e36f)) total = (double)squares([](float v) { return v * kTiny; }) * kTwo140;
-        else if (sum < 1e-18f) total = (double)squares([](float v) { return v * kHuge; }) / kTwo140;
+        if (!(sum < 1e36f)) total = (double)squares([](float v) { return v * kTiny; }) * kTwo180;
+        else if (sum < 1e-18f) total = (double)squares([](float v) { return v * kHuge; }) / kTwo180;
         if (threadIdx.x == 0) g.sums[m * g.parts + p] = total;
     }
 }

@@ -345,3 +345,28 @@ def test_a_budget_leaves_the_other_sms_free(c3):  # noqa: F811
         beside.append(begin.elapsed_time(end))
     c3.c3_status_check()
     assert min(beside) < 6 * min(alone), (alone, beside)
+
+
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("rows,cols,value", [(1024, 4096, 3e38), (4096, 1000, -2.5e38), (300, 70, 3e38), (512, 1031, 2.0 ** 127),
+                                             (64, 64, 2.0 ** -133), (1024, 2048, 2.0 ** -126), (30, 20, 2.0 ** -60)])
+def test_many_values_at_the_ends_of_the_range(c3, ty, rows, cols, value):  # noqa: F811
+    """Finite matrices whose squares' sums neither fp32 nor one of its halves' ranges holds.  eps = 0."""
+    rng = np.random.default_rng(rows)
+    sign = torch.from_numpy(rng.choice([-1.0, 1.0], (1, rows, 1)) * rng.choice([-1.0, 1.0], (1, 1, cols))).cuda()
+    x = (sign * value).float().to(TD[ty])
+    out = run(c3, x, ty, 1, rows, cols, [QUINTIC] * 3, eps=0.0)
+    c3.c3_status_check()
+    # one singular value, 1 after the norm: three steps of the polynomial on it, and the vectors' product
+    assert relative(out[0], oracle(x[0].double(), [QUINTIC] * 3, eps=0.0)) <= 3.4445 * F * 3 + H
+
+
+def test_subnormal_numbers_of_every_size(c3):  # noqa: F811
+    """fp32's smallest numbers, exact in fp64 (the sum of squares below is 2^-298 times a whole number)."""
+    rng = np.random.default_rng(1)
+    for power in (-149, -148, -145, -140):
+        x = torch.from_numpy(rng.integers(-3, 4, (1, 90, 130)) * 2.0 ** power).cuda().float()
+        assert x.double().abs().max() == 3 * 2.0 ** power
+        out = run(c3, x, 0, 1, 90, 130, [QUINTIC] * 5, eps=0.0)
+        assert relative(out[0], oracle(x[0].double(), [QUINTIC] * 5, eps=0.0)) <= 3.4445 * F * 15 ** 0.5 + H
+    c3.c3_status_check()
