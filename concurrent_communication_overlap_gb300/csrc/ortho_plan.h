@@ -38,14 +38,14 @@ inline bool ortho_steps(const float (*coeffs)[3], int steps, OrthoStep* out) {
         auto image = [&](double t) { return std::sqrt(t) * poly(t); };
         double pmax = std::fmax(poly(0), poly(q)), smax = image(q);
         if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < q) pmax = std::fmax(pmax, poly(-b / (2 * c)));
-        // a + 3 b t + 5 c t^2 = 0, t = s^2
+        // a + 3 b t + 5 c t^2 = 0, t = s^2, by way of the root that does not cancel: the other would be lost where
+        // c is tiny beside b
         const double disc = 9 * b * b - 20 * a * c;
         double roots[2] = {-1, -1};
-        if (c != 0 && disc >= 0) {
-            roots[0] = (-3 * b + std::sqrt(disc)) / (10 * c);
-            roots[1] = (-3 * b - std::sqrt(disc)) / (10 * c);
-        } else if (c == 0 && b != 0) {
-            roots[0] = -a / (3 * b);
+        if (disc >= 0) {
+            const double h = -(3 * b + std::copysign(std::sqrt(disc), b)) / 2;
+            if (c != 0) roots[0] = h / (5 * c);
+            if (h != 0) roots[1] = a / h;
         }
         for (double t : roots)
             if (t > 0 && t < q) smax = std::fmax(smax, image(t));

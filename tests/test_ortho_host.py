@@ -164,3 +164,11 @@ def test_a_products_tiles_are_dealt_out_once(plan, M, N, sym, num_kb, count, pai
     assert all(3 <= b - a <= num_kb for a, b in zip(begin, begin[1:]))
     owner = list(map(int, out[2].split()))
     assert owner == [max(q for q in range(runs) if begin[q] <= u) for u in range(split * num_kb)]
+
+
+@pytest.mark.parametrize("coeffs", [
+    [(3, -3, c), (1.5, -0.5, 0)] for c in (1e-16, -1e-16, 1e-12, 1e-7, -1e-7, 1e-30, 1e-38)] + [
+    [(1e-30, -3, 1e-16), (5, 1, 1)], [(3, -3e-16, -3), (1, 0, 0)], [(2, 0, -1), (1, 0, 0)], [(-3, 3, -1e-16), (1, 0, 0)]])
+def test_powers_where_a_coefficient_is_tiny_beside_the_others(plan, coeffs):
+    """The polynomial's turning points, of which an equation's textbook roots lose one there."""
+    test_powers_keep_every_matrix_within_fp16(plan, coeffs)
