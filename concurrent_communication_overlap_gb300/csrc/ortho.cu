@@ -887,11 +887,12 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
     in.counts = reinterpret_cast<int*>(base + w.counts);
     in.out = reinterpret_cast<__half*>(base + w.x0);
     in.pitch = w.xpitch;
-    // a part has at least 32 rows' worth of work for its warps, and every SM has a part
+    // parts of a norm: no more than give each warp a span of columns; over all matrices two an SM of the budget, rounded
+    // up to whole ones for each matrix
     const int64_t jobs = rows * ((cols + kOrthoSpan - 1) / kOrthoSpan), most = (jobs + kOrthoWarps - 1) / kOrthoWarps;
     const int64_t want = (2 * (int64_t)cap + count - 1) / count;
     in.parts = (int)(most < want ? most : want);
-    if (in.parts > kOrthoParts) in.parts = kOrthoParts;
+    if (in.parts > ortho_parts(count)) in.parts = ortho_parts(count);
     const int64_t all = (int64_t)in.parts * count, fit = sm_budget > 0 && cap < ds->sm_count ? cap : 2 * (int64_t)cap;
     const bool whole = cols % 8 == 0 && (uintptr_t)x % 16 == 0 && ld % (bf16 ? 8 : 4) == 0;
     const unsigned grid = (unsigned)(all < fit ? all : fit);

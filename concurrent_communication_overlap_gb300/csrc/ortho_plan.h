@@ -149,7 +149,10 @@ struct OrthoWork {
     size_t scale, sums, counts, x0, x1, g, p, parts, bytes;
 };
 
-constexpr int kOrthoParts = 512;  // partial sums of a matrix's norm at most
+// Partial sums of a matrix's norm, at most: 512 for one matrix, and as many for all of a stack together, rounded up to
+// whole ones for each.  (512 a matrix were 268 MB for 65535 of any size.)
+constexpr int kOrthoParts = 512;
+inline int ortho_parts(int count) { return count ? (kOrthoParts + count - 1) / count : 0; }
 
 inline OrthoWork ortho_work(int64_t rows, int64_t cols, int count) {
     OrthoWork w;
@@ -163,7 +166,7 @@ inline OrthoWork ortho_work(int64_t rows, int64_t cols, int count) {
         return from;
     };
     w.scale = part((size_t)count * sizeof(float));
-    w.sums = part((size_t)count * kOrthoParts * sizeof(double));
+    w.sums = part((size_t)count * (size_t)ortho_parts(count) * sizeof(double));
     w.counts = part((size_t)kOrthoRuns * 16 * sizeof(int));
     const size_t x = (size_t)count * (size_t)rows * (size_t)w.xpitch * 2;
     const size_t g = (size_t)count * (size_t)w.short_side * (size_t)w.gpitch * 2;

@@ -807,9 +807,10 @@ int c3_embed_backward(const void *dout, int dout_type, int64_t dout_ld, const in
  *   out     bf16 [count][rows][cols], row distance out_ld, matrices rows * out_ld
  *           apart; may be x itself, at the same distances, where x is bf16
  *   work    at least c3_orthogonalize_bytes(rows, cols, count) bytes, device, 256-byte
- *           aligned, scratch (four bytes for each of x's elements and for each of the
- *           square matrices' on the shorter side, and 42 MB for parts of products
- *           where a side is above 448)
+ *           aligned, scratch: with m the shorter side and rows filled up to multiples of
+ *           16 elements, four bytes for each element of x and of an m x m matrix; where a
+ *           side is above 448, 42 MB for parts of products, whether or not the call has
+ *           any; and at most 12 bytes a matrix and 12 KB besides
  *   sm_budget  as for c3_gemm, but 0 or at least 2: products run on pairs of SMs
  * Iterates and the matrices between are fp16 times powers of two, products are
  * accumulated in fp32: before its rounding to bf16, which is 1.7e-3 off in the 2-norm,

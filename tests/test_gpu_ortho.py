@@ -370,3 +370,8 @@ def test_subnormal_numbers_of_every_size(c3):  # noqa: F811
         out = run(c3, x, 0, 1, 90, 130, [QUINTIC] * 5, eps=0.0)
         assert relative(out[0], oracle(x[0].double(), [QUINTIC] * 5, eps=0.0)) <= 3.4445 * F * 15 ** 0.5 + H
     c3.c3_status_check()
+
+
+@pytest.mark.parametrize("ty,count,rows,cols", [(1, 700, 20, 33), (0, 513, 65, 17), (1, 300, 130, 258)])
+def test_stacks_of_many_small_matrices(c3, ty, count, rows, cols):  # noqa: F811
+    test_several_steps(c3, ty, count, rows, cols, 0, 0, 4)

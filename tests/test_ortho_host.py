@@ -172,3 +172,13 @@ def test_a_products_tiles_are_dealt_out_once(plan, M, N, sym, num_kb, count, pai
 def test_powers_where_a_coefficient_is_tiny_beside_the_others(plan, coeffs):
     """The polynomial's turning points, of which an equation's textbook roots lose one there."""
     test_powers_keep_every_matrix_within_fp16(plan, coeffs)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (8, 8, 65535), (5, 9, 3), (300, 77, 511), (300, 77, 512), (300, 77, 513), (449, 3, 1),
+                                   (2, 448, 40000), (4096, 4096, 1)])
+def test_workspace_is_what_the_header_says(c3, m, n, k):
+    s, up = min(m, n), lambda v: -(-v // 16) * 16
+    need = 4 * k * (m * up(n) + s * up(s)) + (160 * 256 * 256 * 4 if max(m, n) > 448 else 0)
+    # sums: 8 bytes each, at most 512 and one more a matrix; 4 bytes a matrix, 5120 of counts, eight parts' roundings to 256
+    assert need <= c3.c3_orthogonalize_bytes(m, n, k) <= need + 12 * k + 4096 + 5120 + 8 * 256
+    assert c3.c3_orthogonalize_bytes(m, n, 0) < need + (8 << 10)
