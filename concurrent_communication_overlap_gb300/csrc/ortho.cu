@@ -298,7 +298,7 @@ enum OrthoWaitSite : int {
     kSiteOrthoDrain = 19,
 };
 
-// out = alpha A B^T (times scale[m] `times` times), rounded to fp16 or bf16; of two operands that are kUpper
+// out = alpha A B^T (times scale[m] `times` times), rounded to fp16, or times scale_out to bf16; of two operands that are kUpper
 // + beta mat + diag I, mat fp16 of the output's shape.
 struct OrthoProduct {
     void* out;           // NULL: it has a tensor map, of boxes of 32 rows x 64 columns
@@ -309,6 +309,7 @@ struct OrthoProduct {
     int early;           // the next kernel may start beside this one
     int width;           // bytes that rows of out are aligned to (no tensor map)
     float alpha, beta, diag;
+    float scale_out;     // of the bf16 output, besides alpha
     OrthoTiles tiles;    // symmetric: tiles above the diagonal
     int per_matrix;      // tiles of one matrix
     OrthoSplit cut;
@@ -758,7 +759,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                     if (!kMat && g.bf16) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                            const __nv_bfloat162 x = __floats2bfloat162_rn(g.scale_out * __uint_as_float(r[2 * j]), g.scale_out * __uint_as_float(r[2 * j + 1]));
                             v[j] = *reinterpret_cast<const uint32_t*>(&x);
                         }
                     } else {
@@ -982,7 +983,9 @@ int ortho_launch(const void* x, int bf16, int64_t rows, int64_t cols, int64_t ld
         g.M = (int)rows;
         g.N = (int)cols;
         g.times = i == 0 ? 1 : 0;
-        g.alpha = last ? scale * two(-t.p - t.x) : two(t.next - t.p - t.x);
+        // (one factor of both would be subnormal, and lose digits, for a scale below 2^-103)
+        g.alpha = two((last ? 0 : t.next) - t.p - t.x);
+        g.scale_out = scale;
         g.bf16 = last;
         if (last && !boxes) {
             g.out = out;

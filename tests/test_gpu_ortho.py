@@ -375,3 +375,17 @@ def test_subnormal_numbers_of_every_size(c3):  # noqa: F811
 @pytest.mark.parametrize("ty,count,rows,cols", [(1, 700, 20, 33), (0, 513, 65, 17), (1, 300, 130, 258)])
 def test_stacks_of_many_small_matrices(c3, ty, count, rows, cols):  # noqa: F811
     test_several_steps(c3, ty, count, rows, cols, 0, 0, 4)
+
+
+def test_output_scales_near_the_ends_of_the_range(c3):  # noqa: F811
+    """Powers of two on top of a scale change no digit of what stays a normal bf16 number."""
+    rng = np.random.default_rng(12)
+    for rows, cols, steps in ((8, 8, 1), (8, 12, 5), (300, 5, 2)):
+        x = torch.from_numpy(momentum(rng, 1, rows, cols)).cuda().to(torch.bfloat16)
+        one = run(c3, x, 1, 1, rows, cols, [QUINTIC] * steps, scale=1.37).double()
+        for power in (-60, -100, -108, -114, -120, 100, 120):
+            out = run(c3, x, 1, 1, rows, cols, [QUINTIC] * steps, scale=1.37 * 2.0 ** power).double()
+            normal = one.abs() * 2.0 ** power >= 2.0 ** -126
+            assert normal.any() and torch.equal(out[normal], one[normal] * 2.0 ** power), (rows, cols, power)
+            assert ((out - one * 2.0 ** power).abs()[~normal] <= 2.0 ** -133).all()
+    c3.c3_status_check()
