@@ -482,9 +482,19 @@ def _work_bytes(work, nbytes):
     return 0 if work is None else work.numel() * work.element_size()
 
 
+def _ids(ids, tokens, where):
+    """Address of the tokens' ids: an address, or a tensor, which has to be what the library reads (else C3Error)."""
+    if hasattr(ids, "dtype"):
+        if str(ids.dtype) != "torch.int32" or not ids.is_contiguous() or ids.numel() < tokens:
+            raise C3Error(C3_EINVAL, where, f"ids must be int32, contiguous and at least {tokens}: "
+                                            f"got {ids.dtype}, shape {tuple(ids.shape)}, strides {ids.stride()}")
+    return _ptr(ids)
+
+
 def c3_embed(table, type, rows, cols, ids, tokens, out, out_type, scale=1.0, first=0, ld=None, out_ld=None, stream=None,
              check=True):
-    rc = _lib.c3_embed(_ptr(table), type, rows, cols, cols if ld is None else ld, first, _ptr(ids), tokens, scale, _ptr(out),
+    at = _ids(ids, tokens, "c3_embed")
+    rc = _lib.c3_embed(_ptr(table), type, rows, cols, cols if ld is None else ld, first, at, tokens, scale, _ptr(out),
                        out_type, cols if out_ld is None else out_ld, _stream(stream))
     return _done(rc, "c3_embed", check)
 
@@ -496,7 +506,8 @@ def c3_embed_backward_bytes(tokens, rows, cols):
 def c3_embed_backward(dout, dout_type, ids, tokens, dtable, type, rows, cols, work, scale=1.0, first=0, accumulate=False,
                       dout_ld=None, ld=None, work_bytes=None, stream=None, check=True):
     """work: a tensor (its size is taken from it) or an address with work_bytes."""
-    rc = _lib.c3_embed_backward(_ptr(dout), dout_type, cols if dout_ld is None else dout_ld, _ptr(ids), tokens, first, scale,
+    at = _ids(ids, tokens, "c3_embed_backward")
+    rc = _lib.c3_embed_backward(_ptr(dout), dout_type, cols if dout_ld is None else dout_ld, at, tokens, first, scale,
                                 int(accumulate), _ptr(dtable), type, rows, cols, cols if ld is None else ld, _ptr(work),
                                 _work_bytes(work, work_bytes), _stream(stream))
     return _done(rc, "c3_embed_backward", check)

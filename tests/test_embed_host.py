@@ -54,3 +54,18 @@ def test_gradient_refusals(c3):
     assert f(rows=0, table=None, work=None) == c3.C3_OK
     assert f(cols=0, table=None, work=None) == c3.C3_OK
     assert f(tokens=0, accumulate=True, table=None, work=None, ids=None, dout=None) == c3.C3_OK
+
+
+def test_ids_of_another_type_or_with_gaps_are_refused(c3):
+    """PyTorch's whole numbers are 64-bit unless told otherwise; read as int32 they would be twice as many ids."""
+    torch = pytest.importorskip("torch")
+    for ids in (torch.zeros(4, dtype=torch.int64), torch.zeros(4), torch.zeros(8, dtype=torch.int32)[::2],
+                torch.zeros(4, dtype=torch.int16), torch.zeros(4, 2, dtype=torch.int32).T, torch.zeros(3, dtype=torch.int32)):
+        with pytest.raises(c3.C3Error) as e:
+            c3.c3_embed(P, 0, 8, 4, ids, 4, P, 0)
+        assert e.value.status == c3.C3_EINVAL and "ids" in str(e.value)
+        with pytest.raises(c3.C3Error) as e:
+            c3.c3_embed_backward(P, 0, ids, 4, P, 0, 8, 4, P, work_bytes=1 << 20)
+        assert e.value.status == c3.C3_EINVAL and "ids" in str(e.value)
+    # what is given is looked at whether or not a call has anything to do with it
+    assert c3.c3_embed(P, 0, 8, 0, torch.zeros(2, 2, dtype=torch.int32), 4, P, 0) == c3.C3_OK
