@@ -25,7 +25,9 @@ enum OpsWaitSite : int {
 // stream still runs: its own set-up (barriers, TMEM, tensor maps) comes before
 // chain_wait, every access to global memory after it, since chain_wait returns
 // only when the kernel before has ended and its writes are visible.  It also lets
-// the next chained kernel start.
+// the next chained kernel start (chain_next), which products under a budget of SMs
+// leave out: what starts early waits on SMs that the budget leaves to others.  No
+// wait with a time limit may begin before chain_ready.
 __device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void chain_ready() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void chain_wait() {
