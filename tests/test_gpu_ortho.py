@@ -389,3 +389,19 @@ def test_output_scales_near_the_ends_of_the_range(c3):  # noqa: F811
             assert normal.any() and torch.equal(out[normal], one[normal] * 2.0 ** power), (rows, cols, power)
             assert ((out - one * 2.0 ** power).abs()[~normal] <= 2.0 ** -133).all()
     c3.c3_status_check()
+
+
+@pytest.mark.parametrize("ty,count,rows,cols", [(0, 1, 1024, 1024), (0, 1, 5003, 1347), (0, 1, 256, 640), (0, 2, 700, 3000),
+                                                (1, 4, 512, 1024), (1, 1, 256, 640), (1, 1, 2100, 1500)])
+def test_error_before_the_output_is_rounded_of_both_types(c3, ty, count, rows, cols):  # noqa: F811
+    """As above, over types, stacks, odd sizes and sums that are cut: fp32 inputs have one rounding more, 3 * 5 + 1 of them, each
+    f / sqrt(3) in the square mean and carried on by at most 3.4445.  Matrices between in bf16 would be off eight times as far."""
+    rng = np.random.default_rng(rows)
+    x = torch.from_numpy(momentum(rng, count, rows, cols, rank=8, strong=1.0)).cuda().to(TD[ty])
+    out = run(c3, x, ty, count, rows, cols, [QUINTIC] * 5)
+    for i in range(count):
+        ref = oracle(x[i].double(), [QUINTIC] * 5)
+        own, both = relative(ref.to(torch.bfloat16).double(), ref), relative(out[i], ref)
+        print(ty, rows, cols, own, both, max(0.0, both ** 2 - own ** 2) ** 0.5)
+        assert both ** 2 - own ** 2 <= (3.4445 * F) ** 2 * 16 / 3
+    c3.c3_status_check()
