@@ -482,13 +482,21 @@ def _work_bytes(work, nbytes):
     return 0 if work is None else work.numel() * work.element_size()
 
 
+_int32 = None  # torch.int32, once a call has come with it (this module does not import torch)
+
+
 def _ids(ids, tokens, where):
     """Address of the tokens' ids: an address, or a tensor, which has to be what the library reads (else C3Error)."""
-    if hasattr(ids, "dtype"):
-        if str(ids.dtype) != "torch.int32" or not ids.is_contiguous() or ids.numel() < tokens:
-            raise C3Error(C3_EINVAL, where, f"ids must be int32, contiguous and at least {tokens}: "
-                                            f"got {ids.dtype}, shape {tuple(ids.shape)}, strides {ids.stride()}")
-    return _ptr(ids)
+    global _int32
+    if ids is None or isinstance(ids, int):
+        return ids
+    dtype = ids.dtype
+    if dtype is not _int32 and str(dtype) == "torch.int32":
+        _int32 = dtype
+    if dtype is not _int32 or not ids.is_contiguous() or ids.numel() < tokens:
+        raise C3Error(C3_EINVAL, where, f"ids must be int32, contiguous and at least {tokens}: "
+                                        f"got {dtype}, shape {tuple(ids.shape)}, strides {ids.stride()}")
+    return ids.data_ptr()
 
 
 def c3_embed(table, type, rows, cols, ids, tokens, out, out_type, scale=1.0, first=0, ld=None, out_ld=None, stream=None,
