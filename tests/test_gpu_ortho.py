@@ -405,3 +405,24 @@ def test_error_before_the_output_is_rounded_of_both_types(c3, ty, count, rows, c
         print(ty, rows, cols, own, both, max(0.0, both ** 2 - own ** 2) ** 0.5)
         assert both ** 2 - own ** 2 <= (3.4445 * F) ** 2 * 16 / 3
     c3.c3_status_check()
+
+
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("rows,cols,rank", [(256, 640, 1), (640, 256, 3), (1024, 1024, 30)])
+def test_matrices_of_low_rank(c3, ty, rows, cols, rank):  # noqa: F811
+    """Directions that a matrix does not have: the roundings' noise there grows like the smallest singular values do, by the
+    first coefficient a step.  In the Frobenius norm, of f |X| at most each and independent of one another: one of the
+    conversion (none for bf16), three a step, each carried on by a for each step that is left."""
+    rng = np.random.default_rng(rank)
+    x = rng.standard_normal((1, rows, rank)) @ rng.standard_normal((1, rank, cols))
+    x = torch.from_numpy(x).cuda().to(TD[ty])
+    out = run(c3, x, ty, 1, rows, cols, [QUINTIC] * 5)
+    noise = 0.0 if ty else 1.0  # in units of f^2
+    for k in range(1, 6):
+        norm = float(torch.linalg.vector_norm(oracle(x[0].double(), [QUINTIC] * k)))
+        noise = noise * 3.4445 ** 2 + 3 * norm ** 2
+    ref = oracle(x[0].double(), [QUINTIC] * 5)
+    off = float(torch.linalg.vector_norm(out[0].double() - ref))
+    print(ty, rows, cols, rank, off, F * noise ** 0.5, off / norm)
+    assert off <= F * noise ** 0.5 + H * norm
+    c3.c3_status_check()
