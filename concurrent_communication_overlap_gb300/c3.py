@@ -490,13 +490,12 @@ def _ids(ids, tokens, where):
     global _int32
     if ids is None or isinstance(ids, int):
         return ids
-    dtype = ids.dtype
-    if dtype is not _int32 and str(dtype) == "torch.int32":
-        _int32 = dtype
-    if dtype is not _int32 or not ids.is_contiguous() or ids.numel() < tokens:
-        raise C3Error(C3_EINVAL, where, f"ids must be int32, contiguous and at least {tokens}: "
-                                        f"got {dtype}, shape {tuple(ids.shape)}, strides {ids.stride()}")
-    return ids.data_ptr()
+    if ids.dtype is not _int32 and str(ids.dtype) == "torch.int32":
+        _int32 = ids.dtype
+    if ids.dtype is _int32 and ids.numel() >= tokens and ids.is_contiguous():
+        return ids.data_ptr()
+    raise C3Error(C3_EINVAL, where, f"ids must be int32, contiguous and at least {tokens}: "
+                                    f"got {ids.dtype}, shape {tuple(ids.shape)}, strides {ids.stride()}")
 
 
 def c3_embed(table, type, rows, cols, ids, tokens, out, out_type, scale=1.0, first=0, ld=None, out_ld=None, stream=None,
@@ -504,7 +503,7 @@ def c3_embed(table, type, rows, cols, ids, tokens, out, out_type, scale=1.0, fir
     at = _ids(ids, tokens, "c3_embed")
     rc = _lib.c3_embed(_ptr(table), type, rows, cols, cols if ld is None else ld, first, at, tokens, scale, _ptr(out),
                        out_type, cols if out_ld is None else out_ld, _stream(stream))
-    return _done(rc, "c3_embed", check)
+    return rc if rc == C3_OK else _done(rc, "c3_embed", check)
 
 
 def c3_embed_backward_bytes(tokens, rows, cols):
@@ -518,7 +517,7 @@ def c3_embed_backward(dout, dout_type, ids, tokens, dtable, type, rows, cols, wo
     rc = _lib.c3_embed_backward(_ptr(dout), dout_type, cols if dout_ld is None else dout_ld, at, tokens, first, scale,
                                 int(accumulate), _ptr(dtable), type, rows, cols, cols if ld is None else ld, _ptr(work),
                                 _work_bytes(work, work_bytes), _stream(stream))
-    return _done(rc, "c3_embed_backward", check)
+    return rc if rc == C3_OK else _done(rc, "c3_embed_backward", check)
 
 
 def c3_orthogonalize_bytes(rows, cols, count=1):
