@@ -124,9 +124,10 @@ __device__ __forceinline__ void store_pairs(__nv_bfloat16* row, int64_t c0, int6
 // out[t] = scale * table[ids[t] - first], zeros where that is no row.  A warp takes kAhead pieces
 // of kSpan columns, of one token or of several, whose loads are all in flight before the first is used.
 //
-// Bytes bound it: 65536 tokens x 8192 bf16 take 259 us, 5.5 TB/s of what has to be read and written; tokens
+// Bytes bound it: 65536 tokens x 8192 bf16 take 261 us, 5.4 TB/s of what has to be read and written; tokens
 // of a power law name a row again after more than L2 holds, so that memory gives more.  10007 x 2051
-// fp32 to bf16, most tokens another shard's, take 14.4 us (floor 6.7), bound by issue and by latency.
+// fp32 to bf16, most tokens another shard's, take 14.5 us (floor 6.7): nine rows of ten are zeros, which go by 4-byte
+// stores and with the address arithmetic of rows that hold something.
 //
 // Rows of bf16 of odd length: pieces of a row that begins at no multiple of 4 bytes begin one column
 // before, so that pairs of values are aligned where they are stored.
@@ -712,7 +713,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 2)
 //
 // Latency bounds it.  Rows of up to kJoinSpans spans: 16 warps a row and four parts in flight each, since few rows make few
 // CTAs (32768 tokens of a power law, 256 columns: 36 us in all, and 43 with 8 warps; one row for all of them 67 and
-// 170).  Longer rows: 8 warps and eight parts, of which more rows run at once (16384 x 8192 bf16 391 us, and 400 with 16
+// 170).  Longer rows: 8 warps and eight parts, of which more rows run at once (16384 x 8192 bf16 9 us less in all than with 16
 // warps; 32768 x 4096 129 and 136; 1024 columns 55 and 54, 2048 81 either way).  Told to leave room for a second CTA or none, the
 // compiler took 120 registers in place of 48 to 73 for the latter, and 32768 x 4096 133 us.
 constexpr int kJoinSpans = 4;
@@ -995,8 +996,9 @@ static EmbedWork embed_work(int64_t tokens, int64_t rows, int64_t cols) {
     const int64_t spans = (cols + kSpan - 1) / kSpan;
     // Enough for every warp that runs at once to have two, down to 8 tokens: a chunk's rows are written one after the
     // other (2048 tokens into 9000 x 1001 bf16: chunks of 32 20.8 us in all).  Above 32 tokens more of them cost less.
+    constexpr int64_t kEnough = 32 * 152, kMost = 16384;  // 152 SMs of two CTAs of eight warps
     w.chunk = 8;
-    while ((tokens + w.chunk - 1) / w.chunk * spans > (w.chunk < 32 ? 4864 : 16384) && w.chunk < (1 << 20)) w.chunk *= 2;
+    while ((tokens + w.chunk - 1) / w.chunk * spans > (w.chunk < 32 ? kEnough : kMost) && w.chunk < (1 << 20)) w.chunk *= 2;
     static_assert(kFew == 32, "a warp's votes find a short row's ends");
     w.chunks = (int)((tokens + w.chunk - 1) / w.chunk);
     w.pitch = (cols + 7) / 8 * 8;
@@ -1058,7 +1060,7 @@ int embed_backward_launch(const void* dout, int dout_bf16, const EmbedArgs& a, c
     }
     // Beside the tokens' order the first launch finds the rows without tokens, and writes zeros into as many of them,
     // by words of 32 rows a CTA, as the order leaves time for, at 4.5 TB/s (40009 tokens of 50021 x 1347 fp32:
-    // 104 us with none, 98 this way; all of them there, 104, and 429 in place of 400 for 16384 x 8192 bf16, whose reads
+    // 104 us with none, 98 this way; all of them there, 104, and 29 us more for 16384 x 8192 bf16, whose reads
     // then come after the zeros and not beside them).
     const bool rank = a.tokens <= kRankTokens;
     const int64_t words = (a.rows + 31) / 32, room = rank ? ds->sm_count : ds->embed_clusters > 1 ? ds->embed_clusters - 1 : 1;
